@@ -20,6 +20,8 @@ _lock = threading.Lock()
 _lib = None
 
 ATTN_F32, ATTN_F16, ATTN_BF16 = 0, 1, 2
+KV8_INT8, KV8_E4M3 = 0, 1
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 MASK_NONE, MASK_CAUSAL, MASK_KEY_PADDING = 0, 1, 2
 
 
@@ -46,6 +48,18 @@ class MlaShape(ctypes.Structure):
     """attn_mla_shape_t."""
     _fields_ = [(n, ctypes.c_int32) for n in ("num_seqs", "num_queries", "H", "R", "Pd", "page_size",
                                                "num_pages", "max_pages", "max_queries")]
+
+
+class Kv8Cache(ctypes.Structure):
+    """attn_kv8_cache_t."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "Hkv", "D", "group", "format")]
+
+
+class RopeShape(ctypes.Structure):
+    """attn_rope_shape_t."""
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "S", "Hq", "Hk", "D", "rot")] +
+                [(n, ctypes.c_int64 * 3) for n in ("q_strides", "k_strides", "q_out_strides", "k_out_strides")] +
+                [("pos_batch_stride", ctypes.c_int64)])
 
 
 def library_path() -> str:
@@ -128,6 +142,22 @@ def _open(path):
     lib.attn_paged_mla_bwd_workspace_bytes.argtypes = [ctypes.POINTER(MlaShape),
                                                        ctypes.POINTER(ctypes.c_size_t)]
     lib.attn_paged_mla_bwd_workspace_bytes.restype = ctypes.c_int
+    pi64 = ctypes.POINTER(ctypes.c_int64)
+    lib.attn_kv8_write.argtypes = [ctypes.POINTER(Kv8Cache), ctypes.c_int, ctypes.c_int, ctypes.c_int, vp, vp, pi64,
+                                   pi64, vp, vp, vp, ctypes.c_int, vp, vp, vp, vp, vp]
+    lib.attn_kv8_write.restype = ctypes.c_int
+    lib.attn_kv8_read.argtypes = [ctypes.POINTER(Kv8Cache), ctypes.c_int, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp,
+                                  vp, vp, vp, vp, ctypes.c_int, vp, vp, vp]
+    lib.attn_kv8_read.restype = ctypes.c_int
+    lib.attn_paged_kv8_fwd.argtypes = [ctypes.POINTER(PagedShape), ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp, vp,
+                                       vp, vp, vp, ctypes.c_int, ctypes.c_float, ctypes.c_int, vp, ctypes.c_size_t,
+                                       vp, vp, vp]
+    lib.attn_paged_kv8_fwd.restype = ctypes.c_int
+    lib.attn_paged_kv8_workspace_bytes.argtypes = [ctypes.POINTER(PagedShape), ctypes.POINTER(ctypes.c_size_t)]
+    lib.attn_paged_kv8_workspace_bytes.restype = ctypes.c_int
+    lib.attn_rope.argtypes = [ctypes.POINTER(RopeShape), vp, vp, vp, vp, ctypes.c_int, ctypes.c_int, ctypes.c_float,
+                              ctypes.c_int, vp, vp, vp]
+    lib.attn_rope.restype = ctypes.c_int
     lib.attn_fwd_host.argtypes = [ctypes.POINTER(Shape), vp, vp, vp, ctypes.c_int, vp, vp, ctypes.c_float,
                                   ctypes.c_int, vp, ctypes.c_size_t, vp, vp]
     lib.attn_fwd_host.restype = ctypes.c_int
@@ -682,3 +712,300 @@ def paged_mla_bwd(q, qp, latent, kpos, block_table, seq_lens, q_offsets, dout, *
                                             ptr(lse), ptr(workspace), need, ptr(dq), ptr(dqp), ptr(dlat), ptr(dkp),
                                             stream.cuda_stream or None))
     return dq, dqp, dlat, dkp
+
+
+# ------------------------------------------------------------------ 8-bit paged cache
+def _on(dev):
+    """The library launches on the current device: make it the tensors' own."""
+    import torch
+    if dev.type != "cuda":
+        raise AttnError(f"tensors must be on a CUDA device, not {dev}")
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _stream(stream, dev, made=()):
+    """Handle of ``stream`` (None: the current one). Tensors made here for a call
+    on another stream than the current one are kept until that stream is done."""
+    import torch
+    cur = torch.cuda.current_stream(dev)
+    if stream is None or stream.cuda_stream == cur.cuda_stream:
+        return cur.cuda_stream or None
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream or None
+
+
+def _ints(dev, **tensors):
+    import torch
+    for name, (t, shape) in tensors.items():
+        if t is not None and (t.dtype != torch.int32 or t.device != dev or t.shape != shape
+                              or not t.is_contiguous()):
+            raise AttnError(f"{name} must be a contiguous int32 {list(shape)} tensor on {dev}")
+
+
+def _kv8_check(dev, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, offsets, offsets_name):
+    """Checks an 8-bit cache and its metadata; its C description and the number of sequences."""
+    import torch
+    fmt = KV8_INT8 if k_cache.dtype == torch.int8 else KV8_E4M3 if k_cache.dtype == torch.float8_e4m3fn else None
+    if fmt is None or k_cache.dim() != 4 or k_cache.device != dev or not k_cache.is_contiguous():
+        raise AttnError(f"k_cache must be a contiguous int8 or float8_e4m3fn [pages, page_size, Hkv, D] tensor on {dev}")
+    pages, P, H, D = k_cache.shape
+    if (v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape or v_cache.device != dev
+            or not v_cache.is_contiguous()):
+        raise AttnError("v_cache must be a contiguous tensor like k_cache")
+    if (k_scale.dim() != 3 or k_scale.shape[0] != pages or k_scale.shape[1] != H or k_scale.shape[2] < 1
+            or P % k_scale.shape[2]):
+        raise AttnError("k_scale must be [pages, Hkv, page_size / group], group a divisor of page_size")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t.dtype != torch.float32 or t.shape != k_scale.shape or t.device != dev or not t.is_contiguous():
+            raise AttnError(f"{name} must be a contiguous float32 {list(k_scale.shape)} tensor on {dev}")
+    ns = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    if block_table.dim() != 2:
+        raise AttnError("block_table must be int32 [num_seqs, max_pages]")
+    _ints(dev, block_table=(block_table, (ns, block_table.shape[1])), seq_lens=(seq_lens, (ns,)),
+          **{offsets_name: (offsets, (ns + 1,))})
+    return Kv8Cache(pages, P, H, D, P // k_scale.shape[2], fmt), ns
+
+
+def kv8_write(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, tok_offsets, *, stream=None):
+    """Quantise the newest tokens of every sequence into an 8-bit paged cache, in place (attn_kv8_write).
+
+    k, v [tokens, Hkv, D] float32, float16 or bfloat16: packed tokens, rows
+    tok_offsets[s] .. tok_offsets[s+1]-1 the last ones of sequence s, whose
+    length seq_lens[s] counts them. A head's D elements lie side by side; tokens
+    and heads may be strided (slices of a fused projection). k_cache, v_cache
+    [pages, page_size, Hkv, D] int8 or float8_e4m3fn; k_scale, v_scale float32
+    [pages, Hkv, page_size / group], one scale for every ``group`` consecutive
+    tokens of a head; block_table int32 [num_seqs, max_pages]; seq_lens int32
+    [num_seqs]; tok_offsets int32 [num_seqs + 1]. A group that an earlier call
+    began keeps its scale or gets a larger one, with its codes brought to it.
+    """
+    dev = k.device
+    shape, ns = _kv8_check(dev, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, tok_offsets, "tok_offsets")
+    for name, t in (("k", k), ("v", v)):
+        if t.dim() != 3 or t.device != dev or t.dtype != k.dtype or t.shape != k.shape:
+            raise AttnError(f"{name} must be a [tokens, Hkv, D] tensor on {dev}, k and v alike")
+        if t.shape[2] > 1 and t.stride(2) != 1:
+            raise AttnError(f"the last dimension of {name} must be contiguous")
+    if k.shape[1] != shape.Hkv or k.shape[2] != shape.D:
+        raise AttnError("k and v must have the cache's Hkv and D")
+    i64 = ctypes.c_int64 * 2
+    with _on(dev):
+        check(load_library().attn_kv8_write(
+            shape, ns, block_table.shape[1], k.shape[0], k.data_ptr() or None, v.data_ptr() or None,
+            i64(k.stride(0), k.stride(1)), i64(v.stride(0), v.stride(1)), block_table.data_ptr() or None,
+            seq_lens.data_ptr() or None, tok_offsets.data_ptr() or None, _dtype_code(k), k_cache.data_ptr() or None,
+            v_cache.data_ptr() or None, k_scale.data_ptr() or None, v_scale.data_ptr() or None,
+            _stream(stream, dev)))
+
+
+def kv8_read(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, row_offsets, num_rows: int | None = None, *,
+             starts=None, dtype=None, k_out=None, v_out=None, stream=None):
+    """Values of an 8-bit paged cache as packed rows (attn_kv8_read).
+
+    Row row_offsets[s] + i of the result is token starts[s] + i of sequence s
+    (``starts`` int32 [num_seqs], None: from its first token), code * scale in
+    ``dtype`` (float32, float16 or bfloat16; default bfloat16, or that of
+    ``k_out``). ``num_rows`` is the number of rows (None: that of ``k_out``, or
+    read from row_offsets with a host sync). Tokens past a sequence's end and
+    pages outside the cache read as zeros; rows of no sequence are not written.
+    Returns k, v [num_rows, Hkv, D] (``k_out``/``v_out`` when given).
+    """
+    import torch
+
+    dev = k_cache.device
+    shape, ns = _kv8_check(dev, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, row_offsets, "row_offsets")
+    _ints(dev, starts=(starts, (ns,)))
+    like = k_out if k_out is not None else v_out
+    if num_rows is None:
+        num_rows = like.shape[0] if like is not None else int(row_offsets[-1].item())
+    if dtype is None:
+        dtype = like.dtype if like is not None else torch.bfloat16
+    size = (num_rows, shape.Hkv, shape.D)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None and (t.shape != size or t.dtype != dtype or t.device != dev or not t.is_contiguous()):
+            raise AttnError(f"{name} must be a contiguous {dtype} {list(size)} tensor on {dev}")
+    made = []
+    if k_out is None:
+        made.append(k_out := torch.empty(size, dtype=dtype, device=dev))
+    if v_out is None:
+        made.append(v_out := torch.empty(size, dtype=dtype, device=dev))
+    with _on(dev):
+        check(load_library().attn_kv8_read(
+            shape, ns, block_table.shape[1], num_rows, k_cache.data_ptr() or None, v_cache.data_ptr() or None,
+            k_scale.data_ptr() or None, v_scale.data_ptr() or None, block_table.data_ptr() or None,
+            seq_lens.data_ptr() or None, row_offsets.data_ptr() or None, starts.data_ptr() if starts is not None else None,
+            _dtype_code(k_out), k_out.data_ptr() or None, v_out.data_ptr() or None, _stream(stream, dev, made)))
+    return k_out, v_out
+
+
+def paged_kv8_workspace_bytes(shape: PagedShape) -> int:
+    """Workspace bytes attn_paged_kv8_fwd needs for ``shape``."""
+    n = ctypes.c_size_t(0)
+    check(load_library().attn_paged_kv8_workspace_bytes(shape, n))
+    return n.value
+
+
+def paged_kv8_fwd(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, q_offsets, *, positions=None,
+                  causal: bool = True, scale: float | None = None, max_queries: int | None = None,
+                  return_lse: bool = False, out=None, stream=None, workspace=None, lse_out=None):
+    """:func:`paged_fwd` over an 8-bit paged cache (attn_paged_kv8_fwd).
+
+    q [queries, Hq, D] float32, float16 or bfloat16; the cache, its scales and
+    block_table as for :func:`kv8_write`; the other arguments and the results as
+    for :func:`paged_fwd`. The kernel shares out the keys by itself, so there is
+    no ``num_splits``; its ``workspace`` (a CUDA uint8 tensor of
+    :func:`paged_kv8_workspace_bytes`) is allocated here when not given.
+    """
+    import torch
+
+    dev = q.device
+    if q.dim() != 3 or not q.is_contiguous():
+        raise AttnError("q must be a contiguous [queries, Hq, D] tensor")
+    cache, ns = _kv8_check(dev, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, q_offsets, "q_offsets")
+    nq, Hq, D = q.shape
+    if D != cache.D:
+        raise AttnError("q must have the cache's D")
+    _ints(dev, positions=(positions, (nq,)))
+    if max_queries is None:
+        max_queries = int((q_offsets[1:] - q_offsets[:-1]).max().item()) if ns else 0
+    made = []
+    if out is None:
+        made.append(out := torch.empty_like(q))
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+        raise AttnError("out must be a contiguous tensor like q")
+    lse = _lse_buffer(lse_out, (nq, Hq), dev) if return_lse else None
+    made.append(lse if lse_out is None else None)
+    shape = PagedShape(ns, nq, Hq, cache.Hkv, D, cache.page_size, cache.num_pages, block_table.shape[1], max_queries)
+    need = paged_kv8_workspace_bytes(shape)
+    if need and workspace is None:
+        made.append(workspace := torch.empty(need, dtype=torch.uint8, device=dev))
+    elif need and (workspace.device != dev or workspace.numel() * workspace.element_size() < need
+                   or not workspace.is_contiguous()):
+        raise AttnError(f"workspace must hold {need} contiguous bytes on q's device")
+    with _on(dev):
+        check(load_library().attn_paged_kv8_fwd(
+            shape, cache.group, cache.format, q.data_ptr() or None, k_cache.data_ptr() or None,
+            v_cache.data_ptr() or None, k_scale.data_ptr() or None, v_scale.data_ptr() or None,
+            block_table.data_ptr() or None, seq_lens.data_ptr() or None, q_offsets.data_ptr() or None,
+            positions.data_ptr() if positions is not None else None, 1 if causal else 0,
+            1.0 / math.sqrt(D) if scale is None else scale, _dtype_code(q), workspace.data_ptr() if need else None, need,
+            out.data_ptr() or None, lse.data_ptr() if lse is not None else None, _stream(stream, dev, made)))
+    return (out, lse) if return_lse else out
+
+
+# ------------------------------------------------------------------ rotary positions
+def rope_frequencies(rot: int, *, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original_positions: int = 4096, fast_turns: float = 32.0, slow_turns: float = 1.0):
+    """Angular frequencies of rotary positions: (float64 [rot / 2] host tensor, mscale).
+
+    Frequency i is base^(-2i / rot). ``scaling`` stretches them for contexts
+    ``factor`` times as long: "linear" divides every one by ``factor``; "ntk"
+    raises the base by factor^(rot / (rot - 2)), so that the slowest pair is
+    divided by ``factor`` and the fastest kept; "by_parts" keeps the pairs that
+    turn at least ``fast_turns`` times over ``original_positions``, divides those
+    of at most ``slow_turns`` and blends between, with mscale
+    0.1 ln(factor) + 1 (1 for the others).
+    """
+    import torch
+
+    if rot < 2 or rot % 2:
+        raise AttnError("rot must be even and at least 2")
+    if not (base > 0 and math.isfinite(base)) or not (factor >= 1 and math.isfinite(factor)):
+        raise AttnError("base must be positive and factor at least 1")
+    if scaling not in (None, "linear", "ntk", "by_parts"):
+        raise AttnError(f"unknown scaling {scaling!r}")
+    if scaling == "ntk" and rot > 2:
+        base *= factor ** (rot / (rot - 2))
+    w = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    if scaling == "linear":
+        w = w / factor
+    if scaling != "by_parts":
+        return w, 1.0
+    if not fast_turns > slow_turns:
+        raise AttnError("fast_turns must exceed slow_turns")
+    turns = original_positions * w / (2 * math.pi)
+    keep = ((turns - slow_turns) / (fast_turns - slow_turns)).clamp(0.0, 1.0)
+    return w * keep + w / factor * (1.0 - keep), 0.1 * math.log(factor) + 1.0
+
+
+def _rope(q, k, positions, inv_freq, layout, mscale, inverse, q_out, k_out, stream):
+    import torch
+
+    dev = q.device
+    if layout not in ("half", "interleaved"):
+        raise AttnError(f"layout must be 'half' or 'interleaved', not {layout!r}")
+    dim = q.dim()
+    if dim not in (3, 4):
+        raise AttnError("q must be [tokens, Hq, D] or [B, Hq, S, D]")
+    if k is None:
+        k_out = None
+    made = []
+    if q_out is None:
+        made.append(q_out := torch.empty(q.shape, dtype=q.dtype, device=dev))
+    if k is not None and k_out is None:
+        made.append(k_out := torch.empty(k.shape, dtype=k.dtype, device=dev))
+    tensors = [("q", q), ("q_out", q_out)] + ([("k", k), ("k_out", k_out)] if k is not None else [])
+    for name, t in tensors:
+        if t.dtype != q.dtype or t.device != dev or t.dim() != dim:
+            raise AttnError(f"{name} must be a {dim}-D {q.dtype} tensor on {dev}")
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise AttnError(f"the last dimension of {name} must be contiguous")
+    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
+        raise AttnError("q_out and k_out must be shaped like q and k")
+    # packed [tokens, H, D] is one batch; dense [B, H, S, D] has its heads outside its tokens
+    if dim == 3:
+        B, (S, Hq, D) = 1, q.shape
+        strides = lambda t: (0, t.stride(0), t.stride(1))  # noqa: E731
+        if k is not None and (k.shape[0] != S or k.shape[2] != D):
+            raise AttnError("k must be [tokens, Hk, D] with q's tokens and D")
+        if positions.shape != (S,):
+            raise AttnError("positions must be int32 [tokens]")
+    else:
+        B, Hq, S, D = q.shape
+        strides = lambda t: (t.stride(0), t.stride(2), t.stride(1))  # noqa: E731
+        if k is not None and (k.shape[0] != B or k.shape[2] != S or k.shape[3] != D):
+            raise AttnError("k must be [B, Hk, S, D] with q's B, S and D")
+        if positions.shape != (S,) and positions.shape != (B, S):
+            raise AttnError("positions must be int32 [S] or [B, S]")
+    if positions.dtype != torch.int32 or positions.device != dev or not positions.is_contiguous():
+        raise AttnError(f"positions must be a contiguous int32 tensor on {dev}")
+    if (inv_freq.dtype != torch.float64 or inv_freq.device != dev or inv_freq.dim() != 1
+            or not inv_freq.is_contiguous()):
+        raise AttnError(f"inv_freq must be a contiguous float64 [rot / 2] tensor on {dev}")
+    i64 = ctypes.c_int64 * 3
+    Hk = 0 if k is None else k.shape[1]
+    shape = RopeShape(B, S, Hq, Hk, D, 2 * inv_freq.shape[0], i64(*strides(q)), i64(*strides(k)) if Hk else i64(),
+                      i64(*strides(q_out)), i64(*strides(k_out)) if Hk else i64(), S if positions.dim() == 2 else 0)
+    with _on(dev):
+        check(load_library().attn_rope(
+            shape, q.data_ptr() or None, k.data_ptr() or None if Hk else None, positions.data_ptr() or None,
+            inv_freq.data_ptr() or None, ROPE_HALF if layout == "half" else ROPE_INTERLEAVED, inverse, mscale,
+            _dtype_code(q), q_out.data_ptr() or None, k_out.data_ptr() or None if Hk else None,
+            _stream(stream, dev, made)))
+    return q_out, k_out
+
+
+def rope(q, k, positions, inv_freq, *, layout: str = "half", mscale: float = 1.0, q_out=None, k_out=None,
+         stream=None):
+    """Rotary positions of queries and keys (attn_rope).
+
+    q [tokens, Hq, D] and k [tokens, Hk, D] (packed, as :func:`paged_fwd` and
+    :func:`kv8_write` take them) or [B, Hq, S, D] and [B, Hk, S, D] (dense, as
+    :func:`fwd`); k may be None. Any strides with the last dimension contiguous,
+    float32, float16 or bfloat16. positions int32 [tokens], [S] or [B, S];
+    inv_freq float64 [rot / 2] on the same device (:func:`rope_frequencies`),
+    which turns the first rot elements of each head. ``layout``: "half" pairs
+    element i with i + rot / 2, "interleaved" 2i with 2i + 1. ``q_out``/``k_out``
+    receive the results when given; they may be q and k themselves. Returns
+    (q_out, k_out).
+    """
+    return _rope(q, k, positions, inv_freq, layout, mscale, 0, q_out, k_out, stream)
+
+
+def rope_bwd(dq, dk, positions, inv_freq, *, layout: str = "half", mscale: float = 1.0, q_out=None, k_out=None,
+             stream=None):
+    """Gradients of :func:`rope` with respect to q and k, from those of its outputs
+    (the turn by the opposite angle, same mscale); arguments as for :func:`rope`."""
+    return _rope(dq, dk, positions, inv_freq, layout, mscale, 1, q_out, k_out, stream)

@@ -1,0 +1,310 @@
+// attn_rope.cu - rotary positions of queries and keys, and their gradient.
+//
+// Pair i of a head (elements i and i + rot/2, or 2i and 2i + 1) is turned by
+// the angle a = position * inv_freq[i] and multiplied by mscale; elements from
+// `rot` on are copied. The turn is linear and orthogonal up to mscale, so the
+// gradient is the turn by -a with the same factor (inverse = 1).
+//
+// Angles: of a far position only the fraction of a turn matters, and fp32
+// loses it (position 10^6 leaves an error of 0.06 rad). inv_freq / 2 pi is
+// taken once as a 64-bit fraction of a turn, F = frac(f) 2^64; position * F
+// modulo 2^64 is then the exact fraction of the product, for every int32
+// position, and its upper 32 bits as a signed number are the angle in half
+// turns, in [-1, 1), which sincospi takes without any range reduction. The
+// rounding of f to double leaves position * 2^-53 of a turn.
+//
+// Bytes: every element is read once and written once, and nothing else counts:
+// the angles of a token are computed once for all its heads, in shared memory.
+// A thread moves 16-byte vectors.
+#include <math.h>
+
+#include <algorithm>
+
+#include "attn.h"
+#include "params.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace rope {
+
+constexpr int THREADS = 256;
+
+struct Side {  // queries or keys
+  const void* in;
+  void* out;
+  int H, copy_tail;
+  int64_t ib, it, ih, ob, ot, oh;  // batch, token and head strides (elements)
+};
+
+struct Params {
+  int B, S, D, rot;
+  int64_t pos_batch;  // 0 or S: one row of positions for all, or one each
+  const int32_t* pos;
+  const double* freq;
+  float mscale;
+  int inverse, tok;  // tok: tokens of a CTA
+  Side a, b;
+};
+
+template <int DT> struct Elem;
+template <> struct Elem<0> { using T = float; static constexpr int VEC = 4; };
+template <> struct Elem<1> { using T = __half; static constexpr int VEC = 8; };
+template <> struct Elem<2> { using T = __nv_bfloat16; static constexpr int VEC = 8; };
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f(float& y, float x) { y = x; }
+__device__ __forceinline__ void from_f(__half& y, float x) { y = __float2half_rn(x); }
+__device__ __forceinline__ void from_f(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
+
+// N elements moved as one access (16 bytes, or one element).
+template <typename T, int N>
+struct alignas(N * sizeof(T)) Vec {
+  T x[N];
+};
+
+// Items of a head: pairs of vectors (halves) or single vectors (interleaved),
+// then the vectors of the copied tail. N = 1: elements instead of vectors
+// (interleaved: pairs), for rows that 16-byte accesses do not fit.
+template <int DT, bool HALVES, int N>
+__device__ __forceinline__ void side(const Params& p, const Side& s, const float2* cs, int64_t tok0, int ntok) {
+  using T = typename Elem<DT>::T;
+  using V = Vec<T, N>;
+  const int half = p.rot >> 1;
+  const int turn = HALVES ? half / N : (N > 1 ? p.rot / N : half);
+  const int items = turn + (s.copy_tail ? (p.D - p.rot) / N : 0);
+  const int per = items < THREADS ? THREADS / items : 1;  // heads side by side in the CTA
+  const int h0 = items < THREADS ? threadIdx.x / items : 0;
+  if (h0 >= per) return;
+  const int rows = ntok * s.H;
+  for (int item = threadIdx.x - h0 * items; item < items; item += THREADS) {
+    for (int r = h0; r < rows; r += per) {
+      const int t = r / s.H, h = r - t * s.H;
+      const int64_t g = tok0 + t, b = g / p.S, q = g - b * p.S;
+      const T* in = static_cast<const T*>(s.in) + b * s.ib + q * s.it + h * s.ih;
+      T* out = static_cast<T*>(s.out) + b * s.ob + q * s.ot + h * s.oh;
+      const float2* c = cs + t * half;
+      if (item >= turn) {
+        const int i = p.rot + (item - turn) * N;
+        *reinterpret_cast<V*>(out + i) = *reinterpret_cast<const V*>(in + i);
+      } else if constexpr (HALVES) {
+        const int i = item * N;
+        V x = *reinterpret_cast<const V*>(in + i), y = *reinterpret_cast<const V*>(in + half + i);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const float u = to_f(x.x[k]), v = to_f(y.x[k]);
+          const float2 w = c[i + k];
+          from_f(x.x[k], u * w.x - v * w.y);
+          from_f(y.x[k], v * w.x + u * w.y);
+        }
+        *reinterpret_cast<V*>(out + i) = x;
+        *reinterpret_cast<V*>(out + half + i) = y;
+      } else {
+        constexpr int M = N > 1 ? N : 2;
+        const int i = item * M;
+        Vec<T, M> x;
+        if constexpr (N > 1) {
+          x = *reinterpret_cast<const V*>(in + i);
+        } else {
+          x.x[0] = in[i];
+          x.x[1] = in[i + 1];
+        }
+#pragma unroll
+        for (int k = 0; k < M; k += 2) {
+          const float u = to_f(x.x[k]), v = to_f(x.x[k + 1]);
+          const float2 w = c[(i + k) >> 1];
+          from_f(x.x[k], u * w.x - v * w.y);
+          from_f(x.x[k + 1], v * w.x + u * w.y);
+        }
+        if constexpr (N > 1) {
+          *reinterpret_cast<V*>(out + i) = x;
+        } else {
+          out[i] = x.x[0];
+          out[i + 1] = x.x[1];
+        }
+      }
+    }
+  }
+}
+
+template <int DT, bool HALVES, int N>
+__global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ Params p) {
+  extern __shared__ float2 cs[];  // [tok][rot / 2] cos, sin times mscale
+  const int half = p.rot >> 1;
+  const int64_t total = static_cast<int64_t>(p.B) * p.S;
+  const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tok;
+  const int ntok = static_cast<int>(min(static_cast<int64_t>(p.tok), total - tok0));
+  for (int i = threadIdx.x; i < half; i += THREADS) {
+    constexpr double INV_2PI = 0.15915494309189533577;
+    const double f = __ldg(p.freq + i) * INV_2PI;
+    const uint64_t F = __double2ull_rd((f - floor(f)) * 18446744073709551616.0);
+    for (int t = 0; t < ntok; ++t) {
+      const int64_t g = tok0 + t, b = g / p.S;
+      const int64_t pos = __ldg(p.pos + b * p.pos_batch + (g - b * p.S));
+      const int32_t top = static_cast<int32_t>(static_cast<uint32_t>((static_cast<uint64_t>(pos) * F) >> 32));
+      float sn, cn;
+      sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31
+      cs[t * half + i] = make_float2(cn * p.mscale, (p.inverse ? -sn : sn) * p.mscale);
+    }
+  }
+  __syncthreads();
+  side<DT, HALVES, N>(p, p.a, cs, tok0, ntok);
+  if (p.b.H > 0) side<DT, HALVES, N>(p, p.b, cs, tok0, ntok);
+}
+
+template <int DT>
+cudaError_t launch_dt(const Params& p, bool halves, bool vec, dim3 grid, cudaStream_t st) {
+  constexpr int N = Elem<DT>::VEC;
+  const size_t smem = static_cast<size_t>(p.tok) * (p.rot / 2) * sizeof(float2);
+  if (halves) {
+    if (vec) rope_kernel<DT, true, N><<<grid, THREADS, smem, st>>>(p);
+    else rope_kernel<DT, true, 1><<<grid, THREADS, smem, st>>>(p);
+  } else {
+    if (vec) rope_kernel<DT, false, N><<<grid, THREADS, smem, st>>>(p);
+    else rope_kernel<DT, false, 1><<<grid, THREADS, smem, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace rope
+}  // namespace attn
+
+namespace {
+
+using attn::rope::Params;
+using attn::rope::Side;
+
+struct Span {  // what a strided tensor may touch, in bytes
+  uintptr_t p;
+  int64_t token, row, all;  // token stride, extent of one token's heads, extent of everything
+};
+
+Span span_of(const void* p, int64_t B, int64_t S, int64_t H, int64_t D, const int64_t* st, int es) {
+  Span s;
+  s.p = reinterpret_cast<uintptr_t>(p);
+  s.token = st[1] * es;
+  s.row = ((H - 1) * st[2] + D) * es;
+  s.all = ((B - 1) * st[0] + (S - 1) * st[1] + (H - 1) * st[2] + D) * es;
+  return s;
+}
+
+// Whether two strided tensors may share an element. Slices of one fused
+// projection interleave without sharing any: tokens the same stride apart
+// (batches too, as multiples of it), and rows that lie apart modulo it.
+bool spans_meet(const Span& a, const Span& b, bool batches_fit) {
+  if (a.p + a.all <= b.p || b.p + b.all <= a.p) return false;
+  if (batches_fit && a.token == b.token && a.token > 0 && a.row <= a.token && b.row <= a.token) {
+    const int64_t diff = static_cast<int64_t>(b.p) - static_cast<int64_t>(a.p);
+    const int64_t d = ((diff % a.token) + a.token) % a.token;
+    if (d >= a.row && d + b.row <= a.token) return false;
+  }
+  return true;
+}
+
+// No two (batch, token, head) rows of a written tensor may share an element:
+// the axes, from the smallest stride up, each step over what lies below.
+bool rows_apart(int64_t B, int64_t S, int64_t H, int64_t D, const int64_t* st) {
+  struct Axis { int64_t n, stride; } ax[3] = {{B, st[0]}, {S, st[1]}, {H, st[2]}};
+  std::sort(ax, ax + 3, [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
+  int64_t below = D;
+  for (const Axis& a : ax) {
+    if (a.n <= 1) continue;
+    if (a.stride < below) return false;
+    below = (a.n - 1) * a.stride + below;
+  }
+  return true;
+}
+
+}  // namespace
+
+extern "C" int attn_rope(const attn_rope_shape_t* shape, const void* q, const void* k, const int32_t* positions,
+                         const double* inv_freq, int layout, int inverse, float mscale, attn_dtype_t dtype,
+                         void* q_out, void* k_out, void* stream) {
+  if (!shape) return ATTN_ERR_NULL;
+  const attn_rope_shape_t s = *shape;
+  if (dtype != ATTN_F32 && dtype != ATTN_F16 && dtype != ATTN_BF16) return ATTN_ERR_DTYPE;
+  if (s.B < 0 || s.S < 0 || s.Hq <= 0 || s.Hk < 0 || s.D <= 0 || s.D > ATTN_ROPE_MAX_D || s.rot <= 0 ||
+      s.rot > s.D || (s.rot & 1) || (layout != ATTN_ROPE_HALF && layout != ATTN_ROPE_INTERLEAVED) ||
+      (inverse != 0 && inverse != 1) || (s.pos_batch_stride != 0 && s.pos_batch_stride != s.S))
+    return ATTN_ERR_SHAPE;
+  if (!isfinite(mscale)) return ATTN_ERR_SCALE;
+  const int nside = s.Hk > 0 ? 2 : 1;
+  const int64_t* st[4] = {s.q_strides, s.q_out_strides, s.k_strides, s.k_out_strides};
+  const int heads[4] = {s.Hq, s.Hq, s.Hk, s.Hk};
+  for (int i = 0; i < 2 * nside; ++i) {
+    for (int j = 0; j < 3; ++j)
+      if (st[i][j] < 0) return ATTN_ERR_SHAPE;
+    // extents stay far inside 64 bits
+    if (static_cast<double>(s.B) * st[i][0] + static_cast<double>(s.S) * st[i][1] +
+            static_cast<double>(heads[i]) * st[i][2] > 1e17)
+      return ATTN_ERR_SHAPE;
+  }
+  const int64_t tokens = static_cast<int64_t>(s.B) * s.S;
+  if (tokens == 0) return ATTN_OK;
+  if (tokens > 0x7fffffffLL || static_cast<int64_t>(std::max(s.Hq, s.Hk)) * 4 > 0x7fffffffLL) return ATTN_ERR_SHAPE;
+  if (!q || !q_out || !positions || !inv_freq || (s.Hk > 0 && (!k || !k_out))) return ATTN_ERR_NULL;
+  const int es = dtype == ATTN_F32 ? 4 : 2;
+  const void* ptr[4] = {q, q_out, k, k_out};
+  Span sp[4];
+  bool fit = true, vec = (s.D * es) % 16 == 0;
+  for (int i = 0; i < 2 * nside; ++i) {
+    if (reinterpret_cast<uintptr_t>(ptr[i]) % es) return ATTN_ERR_ALIGN;
+    if ((i & 1) && !rows_apart(s.B, s.S, heads[i], s.D, st[i])) return ATTN_ERR_OVERLAP;
+    sp[i] = span_of(ptr[i], s.B, s.S, heads[i], s.D, st[i], es);
+    fit = fit && (s.B == 1 || (st[i][1] > 0 && st[i][0] % st[i][1] == 0));
+    vec = vec && reinterpret_cast<uintptr_t>(ptr[i]) % 16 == 0;
+    const int n[3] = {s.B, s.S, heads[i]};
+    for (int j = 0; j < 3; ++j) vec = vec && (n[j] == 1 || (st[i][j] * es) % 16 == 0);
+  }
+  if ((reinterpret_cast<uintptr_t>(positions) & 3u) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u))
+    return ATTN_ERR_ALIGN;
+  bool in_place[2] = {false, false};
+  for (int i = 0; i < nside; ++i) {
+    in_place[i] = ptr[2 * i] == ptr[2 * i + 1];
+    for (int j = 0; j < 3; ++j) in_place[i] = in_place[i] && st[2 * i][j] == st[2 * i + 1][j];
+  }
+  Span meta[2];
+  const int64_t meta_bytes[2] = {(s.pos_batch_stride ? tokens : s.S) * 4, s.rot / 2 * 8};
+  for (int i = 0; i < 2; ++i) {
+    meta[i].p = reinterpret_cast<uintptr_t>(i == 0 ? static_cast<const void*>(positions) : inv_freq);
+    meta[i].token = 0;
+    meta[i].row = meta[i].all = meta_bytes[i];
+  }
+  for (int o = 1; o < 2 * nside; o += 2) {  // each output against every other tensor
+    for (int i = 0; i < 2 * nside; ++i)
+      if (i != o && !(i == o - 1 && in_place[o / 2]) && spans_meet(sp[o], sp[i], fit)) return ATTN_ERR_OVERLAP;
+    for (const Span& m : meta)
+      if (spans_meet(sp[o], m, false)) return ATTN_ERR_OVERLAP;
+  }
+
+  Params p{};
+  p.B = s.B;
+  p.S = s.S;
+  p.D = s.D;
+  p.rot = s.rot;
+  p.pos_batch = s.pos_batch_stride;
+  p.pos = positions;
+  p.freq = inv_freq;
+  p.mscale = mscale;
+  p.inverse = inverse;
+  auto make = [&](int i) {
+    const int64_t *a = st[2 * i], *b = st[2 * i + 1];
+    return Side{ptr[2 * i], const_cast<void*>(ptr[2 * i + 1]), heads[2 * i], in_place[i] ? 0 : 1,
+                a[0], a[1], a[2], b[0], b[1], b[2]};
+  };
+  p.a = make(0);
+  if (nside == 2) p.b = make(1);
+  const bool halves = layout == ATTN_ROPE_HALF;
+  const int n = dtype == ATTN_F32 ? 4 : 8;
+  vec = vec && (halves ? s.rot / 2 : s.rot) % n == 0 && (s.D - s.rot) % n == 0;
+  // a CTA takes 4 tokens when that still leaves several CTAs for each SM
+  p.tok = tokens >= 152 * 16 ? 4 : 1;
+  const dim3 grid(static_cast<unsigned>((tokens + p.tok - 1) / p.tok));
+  cudaError_t e;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (dtype == ATTN_F32) e = attn::rope::launch_dt<0>(p, halves, vec, grid, cs);
+  else if (dtype == ATTN_F16) e = attn::rope::launch_dt<1>(p, halves, vec, grid, cs);
+  else e = attn::rope::launch_dt<2>(p, halves, vec, grid, cs);
+  return e == cudaSuccess ? ATTN_OK : attn::record_cuda_error(e);
+}

@@ -4,7 +4,9 @@
  * splits and the log-sum-exp in attn_fwd_split, on host buffers in
  * attn_fwd_host), its backward (attn_bwd), attention and MLA over a paged
  * cache (attn_paged_fwd, attn_paged_mla) and their backward (attn_paged_bwd,
- * attn_paged_mla_bwd). Each entry below states its own definition and source.
+ * attn_paged_mla_bwd), a paged cache of 8-bit codes (attn_kv8_write,
+ * attn_kv8_read, attn_paged_kv8_fwd) and rotary positions (attn_rope). Each
+ * entry below states its own definition and source.
  *
  * The operation, per batch b, query head hq and query row i:
  *
@@ -416,6 +418,160 @@ ATTN_API int attn_paged_mla_bwd(const attn_mla_shape_t* shape,
  * layout of attn_paged_bwd_workspace_bytes with Hq = H). Returns ATTN_OK,
  * ATTN_ERR_NULL or ATTN_ERR_SHAPE. */
 ATTN_API int attn_paged_mla_bwd_workspace_bytes(const attn_mla_shape_t* shape, size_t* bytes);
+
+/* ------------------------------------------------------------ 8-bit paged cache
+ * (The pages have no counterpart: they describe caches of F32, F16 and BF16.)
+ *
+ * The paged cache of attn_paged_fwd with one byte per element and one float
+ * scale for every `group` consecutive tokens of a head:
+ *   k_cache, v_cache  [num_pages, page_size, Hkv, D]        codes
+ *   k_scale, v_scale  [num_pages, Hkv, page_size / group]   float
+ * Element d of key j of sequence s is code * scale, with
+ *   page = block_table[s][j / page_size], row = j % page_size,
+ *   code = k_cache[page][row][hk][d], scale = k_scale[page][hk][row / group].
+ * ATTN_KV8_INT8: codes are two's complement integers. ATTN_KV8_E4M3: 1 sign, 4
+ * exponent and 3 mantissa bits, bias 7, largest value 448; attn_kv8_write never
+ * makes the codes 0x7f and 0xff, and everything that reads them takes them for
+ * +-480. Scales are finite and >= 0, or NaN (a group that was given a NaN or an
+ * infinity: all of it reads as NaN). */
+enum { ATTN_KV8_INT8 = 0, ATTN_KV8_E4M3 = 1 };
+
+/* group: tokens of a scale, a divisor of page_size. D in {16, 32, 64, 128}. */
+typedef struct {
+  int32_t num_pages, page_size, Hkv, D, group, format;
+} attn_kv8_cache_t;
+
+/* attn_kv8_write - quantise the newest tokens of every sequence into the cache.
+ *
+ * k, v: `dtype` rows of num_tokens tokens, packed sequence by sequence: rows
+ *   tok_offsets[s] .. tok_offsets[s+1]-1 (offsets clamped to [0, num_tokens])
+ *   are the last n tokens of sequence s, positions L - n .. L - 1 with
+ *   L = seq_lens[s] (clamped to [0, max_pages * page_size]) counting them, the
+ *   rule of attn_paged_fwd; where n > L the first n - L rows are not written.
+ *   k_strides, v_strides (host arrays): elements from token to token and from
+ *   head to head, so that k and v may be slices of one projection's output; the
+ *   D elements of a head lie side by side. Pointers aligned to their element;
+ *   rows on 16-byte boundaries (pointers multiples of 16 bytes, strides of 8
+ *   elements) load as vectors.
+ * For each group that receives tokens, with a = max |x| over the new tokens of
+ * a head in it, t = fl32(a / 127) (int8) or the least power of two that is at
+ * least a / 448 (e4m3), not below 2^-100:
+ *   - a group that begins with new tokens gets the scale S = t;
+ *   - one that begins with tokens of earlier calls keeps at least its scale,
+ *     S = max(S_old, t), and when it grows their codes c become the nearest
+ *     code of c * S_old / S (repeated growth rounds them repeatedly);
+ *   - new codes are the nearest code of x / S, ties to the even code, exactly.
+ * The codes and scales of groups without new tokens, and rows of a group past
+ * the last token, keep their bytes. A page that the table puts outside the
+ * cache is not written. A group may be written by one sequence in a call: where
+ * two sequences (or two blocks of one) name the same page, which one's values a
+ * shared group ends with is unspecified, so copy a shared page before
+ * appending to it. Not to be run at the same time as another call on the cache.
+ *
+ * Repeating a call leaves the cache as the first did. Asynchronous on `stream`,
+ * one kernel, no workspace, no atomics. Returns ATTN_OK or a negative
+ * ATTN_ERR_* code before any launch (ATTN_ERR_DTYPE also for the format). */
+ATTN_API int attn_kv8_write(const attn_kv8_cache_t* cache, int num_seqs, int max_pages, int num_tokens,
+                            const void* k, const void* v,
+                            const int64_t* k_strides, const int64_t* v_strides,
+                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* tok_offsets,
+                            attn_dtype_t dtype,
+                            void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                            void* stream);
+
+/* attn_kv8_read - values of cached tokens as packed rows.
+ *
+ * k_out, v_out [num_rows, Hkv, D] in `dtype` (16-byte aligned, contiguous): row
+ * row_offsets[s] + i is token starts[s] + i of sequence s (starts NULL: its
+ * token i), code * scale rounded once to `dtype`. A token before 0 or at or
+ * past seq_lens[s], or on a page outside the cache, reads as zeros; rows of no
+ * sequence (offsets clamped to [0, num_rows]) are not written. row_offsets does
+ * not decrease. The rows are dense: attn_fwd and attn_bwd take them after a
+ * transpose, and so does attn_kv8_write of another cache. Asynchronous on
+ * `stream`, one kernel. */
+ATTN_API int attn_kv8_read(const attn_kv8_cache_t* cache, int num_seqs, int max_pages, int num_rows,
+                           const void* k_cache, const void* v_cache,
+                           const float* k_scale, const float* v_scale,
+                           const int32_t* block_table, const int32_t* seq_lens, const int32_t* row_offsets,
+                           const int32_t* starts,
+                           attn_dtype_t dtype, void* k_out, void* v_out,
+                           void* stream);
+
+/* attn_paged_kv8_fwd - attn_paged_fwd over an 8-bit cache:
+ *   s_ij = scale * k_scale_j * (q_i . k_code_j),
+ *   out_i = sum_j softmax_j(s_i) * v_scale_j * v_code_j.
+ *
+ * shape, q, block_table, seq_lens, q_offsets, positions, causal, scale, dtype,
+ * out and lse are those of attn_paged_fwd, with the same rules (packed queries,
+ * the newest positions by default, rows that see no key NaN with lse -inf,
+ * pages outside the cache zero keys and values, query rows of no sequence not
+ * written); group and format are those of the cache, k_scale and v_scale its
+ * scales. Codes enter the products unrounded (every code is exact in F16 and
+ * BF16); scores, softmax statistics and outputs are summed in fp32, and the
+ * F16/BF16 kernels round p_j * v_scale_j to the type of q.
+ *
+ * workspace: attn_paged_kv8_workspace_bytes(shape) bytes (0 for some shapes),
+ * 16-byte aligned, caller-owned, disjoint from every other buffer, its contents
+ * of no meaning before or after; calls in flight at once need one each. The
+ * keys of a call with few rows are shared out over the GPU by the kernel
+ * itself, in a fixed order: repeated calls give identical bits. There is no
+ * backward; attn_kv8_read gives the rows that attn_bwd takes. Asynchronous on
+ * `stream`. Returns ATTN_OK or a negative ATTN_ERR_* code before any launch. */
+ATTN_API int attn_paged_kv8_fwd(const attn_paged_shape_t* shape, int group, int format,
+                                const void* q, const void* k_cache, const void* v_cache,
+                                const float* k_scale, const float* v_scale,
+                                const int32_t* block_table, const int32_t* seq_lens,
+                                const int32_t* q_offsets, const int32_t* positions,
+                                int causal, float scale, attn_dtype_t dtype,
+                                void* workspace, size_t workspace_bytes,
+                                void* out, float* lse,
+                                void* stream);
+
+/* attn_paged_kv8_workspace_bytes - workspace attn_paged_kv8_fwd needs for
+ * `shape` (every dtype, group and format). Returns ATTN_OK, ATTN_ERR_NULL,
+ * ATTN_ERR_SHAPE or ATTN_ERR_HEAD_DIM. */
+ATTN_API int attn_paged_kv8_workspace_bytes(const attn_paged_shape_t* shape, size_t* bytes);
+
+/* ------------------------------------------------------------ rotary positions
+ * Layouts of the pairs in the first `rot` elements of a head: pair i is
+ * elements i and i + rot/2 (HALF), or 2i and 2i + 1 (INTERLEAVED). */
+enum { ATTN_ROPE_HALF = 0, ATTN_ROPE_INTERLEAVED = 1 };
+#define ATTN_ROPE_MAX_D 512
+
+/* q [B, S, Hq, D] and k [B, S, Hk, D] by strides: elements from batch to batch,
+ * token to token and head to head, 0 or more each; a head's D elements lie side
+ * by side. Packed tokens are B = 1. Hk = 0: no keys (k, k_out and their strides
+ * are ignored). pos_batch_stride: S, or 0 when every batch has the same
+ * positions. rot: even, 2 .. D; the elements from rot on are copied. */
+typedef struct {
+  int32_t B, S, Hq, Hk, D, rot;
+  int64_t q_strides[3], k_strides[3], q_out_strides[3], k_out_strides[3];
+  int64_t pos_batch_stride;
+} attn_rope_shape_t;
+
+/* attn_rope - rotary positions of queries and keys, or (inverse = 1) their
+ * gradient. (The pages leave position encoding to the caller.)
+ *
+ * Pair i (x, y) of a token at position p becomes, with a = p * inv_freq[i],
+ *   (mscale (x cos a - y sin a), mscale (y cos a + x sin a));
+ * inverse = 1 turns by -a: the transposed map, which takes the gradient of the
+ * outputs to the gradient of the inputs (and, at mscale 1, undoes the turn).
+ * inv_freq: device double [rot/2], finite, so scaling for long contexts is a
+ * choice of frequencies and mscale. The fraction of a turn is computed in
+ * 64 bits: no loss at any int32 position. Products and sums in fp32, rounded
+ * once to `dtype`.
+ * positions: device int32 [S] or [B, S] (row stride pos_batch_stride).
+ * An output may be its own input (same pointer and strides), must have no two
+ * rows in the same place and may share no other element with any other
+ * argument; slices of one buffer that interleave by token are told apart.
+ * Pointers aligned to their element; rows on 16-byte boundaries move as vectors.
+ * Asynchronous on `stream`, one kernel. Returns ATTN_OK or a negative
+ * ATTN_ERR_* code before any launch (ATTN_ERR_SCALE: mscale not finite). */
+ATTN_API int attn_rope(const attn_rope_shape_t* shape, const void* q, const void* k,
+                       const int32_t* positions, const double* inv_freq,
+                       int layout, int inverse, float mscale, attn_dtype_t dtype,
+                       void* q_out, void* k_out,
+                       void* stream);
 
 /* Size of the device scratch array built into the library for
  * attn_fwd_split_noalloc (32 MiB per GPU that loads the library). */
