@@ -186,12 +186,27 @@ int check_shape(const attn_paged_shape_t& s) {
   return ATTN_OK;
 }
 
+// Shapes of the kernel that shares out the keys. Its token numbers (page *
+// page_size + row) are 32-bit.
+bool takes_decode(const attn_paged_shape_t& s) {
+  return (s.D == 64 || s.D == 128) && attn::kv8::decode_rows(s.max_queries, s.Hq / s.Hkv) && s.num_pages > 0 &&
+         static_cast<int64_t>(s.num_pages) * s.page_size <= 0x7fffffffLL && s.num_seqs > 0 && s.Hkv <= 65535 &&
+         static_cast<int64_t>(s.max_pages) * s.page_size <= 0x7fff0000LL;
+}
+
 }  // namespace
 
 extern "C" int attn_paged_kv8_workspace_bytes(const attn_paged_shape_t* shape, size_t* bytes) {
   if (!shape || !bytes) return ATTN_ERR_NULL;
   if (const int rc = check_shape(*shape)) return rc;
+  const attn_paged_shape_t& s = *shape;
   *bytes = 0;
+  if (takes_decode(s)) {
+    const int64_t rows = static_cast<int64_t>(s.max_queries) * (s.Hq / s.Hkv);
+    const attn::kv8::DecodeLayout lay{
+        2ll * s.Hkv * attn::kv8::decode_ranges(s.num_seqs, s.Hkv, s.max_pages, s.page_size), rows <= 8 ? 8 : rows <= 16 ? 16 : 32};
+    *bytes = static_cast<size_t>(lay.bytes(s.D));
+  }
   return ATTN_OK;
 }
 
@@ -275,6 +290,10 @@ extern "C" int attn_paged_kv8_fwd(const attn_paged_shape_t* shape, int group, in
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool i8 = format == ATTN_KV8_INT8;
   using namespace attn::kv8;
+  if (dtype != ATTN_F32 && takes_decode(s)) {
+    e = dtype == ATTN_BF16 ? launch_decode<true>(p, format, st) : launch_decode<false>(p, format, st);
+    return e == cudaSuccess ? ATTN_OK : attn::record_cuda_error(e);
+  }
 #define ATTN_FWD(DT) (i8 ? launch_simt<DT, FMT_INT8>(p, st) : launch_simt<DT, FMT_E4M3>(p, st))
   e = dtype == ATTN_F32 ? ATTN_FWD(0) : dtype == ATTN_F16 ? ATTN_FWD(1) : ATTN_FWD(2);
 #undef ATTN_FWD
