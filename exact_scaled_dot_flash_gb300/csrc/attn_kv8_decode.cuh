@@ -17,13 +17,16 @@
 //    two keys in one register, which the byte permutation of the conversion
 //    gives without an instruction of its own; P^T is S^T transposed, one
 //    movmatrix for 8 keys x 8 rows;
-//  - codes convert exactly: int8 by placing the byte under the exponent of 128
-//    (BF16, its sign bit apart) or 1024 (F16) and subtracting, e4m3 by moving
-//    its 7 low bits to the top of exponent and mantissa, which leaves a power of
-//    two (BF16: 2^-120, multiplied out; F16: 2^-8, folded into the scales);
+//  - the products are F16 whatever the type of q: every code is exact in F16, a
+//    BF16 query is brought to F16's range by a power of two for its row (what
+//    falls below 2^-24 there is 2^-40 of the row's largest element), and the
+//    probabilities get 11 bits instead of 8. Codes convert exactly: int8 by
+//    placing the byte, offset by 128, under the exponent of 1024 and
+//    subtracting; e4m3 by the conversion instruction;
 //  - k_scale enters the score in fp32, v_scale the probability before it is
-//    rounded to 16 bits. In F16 that product is kept within the type by dividing
-//    by a running power of two that is at least every v_scale seen;
+//    rounded: P' = p v_scale r, r a factor for the row that keeps the
+//    largest p v_scale so far near 1, so that what F16 loses below 2^-14 is
+//    small beside the largest term of the sum and not beside the largest scale;
 //  - the running maximum moves only when a score exceeds it by 2^8 (one vote a
 //    tile instead of a reduction).
 //
@@ -112,17 +115,11 @@ __device__ __forceinline__ Place locate(const FwdParams& p, int range, int range
 }
 
 // ------------------------------------------------------------------ operands
-template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  if constexpr (BF16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
@@ -131,39 +128,22 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
-// Two codes as a 16-bit pair: byte `i` of x in the low half, byte `j` of y in
-// the high half. F16 e4m3 pairs are 2^-8 of their values (CODE_SCALE).
-template <bool BF16, int FMT>
-__device__ __forceinline__ uint32_t pair(uint32_t x, uint32_t y, int i, int j) {
-  const uint32_t t = __byte_perm(x, y, i | (i << 4) | ((4 + j) << 8) | ((4 + j) << 12));
+// The 4 codes of a word as two F16 pairs: bytes 0, 1 and bytes 2, 3.
+template <int FMT>
+__device__ __forceinline__ void pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (FMT == FMT_INT8) {
-    if constexpr (BF16) {
-      const uint32_t low = (t & 0x007f007fu) | 0x43004300u, sign = (t & 0x00800080u) | 0x43004300u;  // 128 + b, 128 + 128 s
-      uint32_t r;
-      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(low), "r"(sign));
-      return r;
-    } else {
-      const uint32_t u = (t & 0x00ff00ffu) ^ 0x64806480u;  // 1024 + (c + 128)
-      uint32_t r;
-      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x64806480u));
-      return r;
-    }
-  } else if constexpr (BF16) {
-    const uint32_t u = (t & 0x80008000u) | ((t >> 4) & 0x07f007f0u);
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x7b807b80u));  // 2^120
-    return r;
+    const uint32_t u = w ^ 0x80808080u;  // c + 128
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);  // 1024 + (c + 128)
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
   } else {
-    return (t & 0x80008000u) | ((t >> 1) & 0x3f803f80u);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
   }
 }
 
-template <bool BF16, int FMT>
-__device__ __forceinline__ constexpr float code_scale() {
-  return !BF16 && FMT == FMT_E4M3 ? 256.f : 1.f;
-}
-
-// D / 8 bytes of one key that a lane holds of V, D / 4 of K (words)
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t* r, const uint8_t* at) {
   if constexpr (N == 2) {
@@ -175,18 +155,29 @@ __device__ __forceinline__ void load_words(uint32_t* r, const uint8_t* at) {
   }
 }
 
+// Power of two 2^e as fp32, e in [-126, 127].
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// A pair of outputs in the type of q.
+__device__ __forceinline__ uint32_t pack_out(bool bf16, float a, float b) {
+  return bf16 ? pack2<true>(a, b) : pack2<false>(a, b);
+}
+
 template <int D, int NT>
 struct Shared {
   static constexpr int ROW = D + 4;
   static constexpr int O = WARPS * 8 * NT * ROW * 4;  // partial outputs of the warps
   static constexpr int ML = WARPS * 8 * NT * 8;
-  static constexpr int Q = NT > 1 ? NT * (D / 16) * 32 * 8 : 0;  // query operands, in fragment order
-  static constexpr int BYTES = O + ML + Q;
+  static constexpr int QF = 8 * NT * 4;
+  static constexpr int Q = NT * (D / 16) * 32 * 8;  // query operands, in the lanes' order
+  static constexpr int BYTES = O + ML + QF + Q;
 };
 
-template <int D, bool BF16, int FMT, int NT>
+// Rows of a call: `rows` in all, in blockIdx.y groups of 8 NT; a slot of the
+// workspace holds all groups (slot_rows).
+template <int D, int FMT, int NT>
 __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
-    decode_kernel(const __grid_constant__ FwdParams p, int ranges, int64_t ml_offset) {
+    decode_kernel(const __grid_constant__ FwdParams p, int ranges, int slot_rows, int64_t ml_offset) {
   constexpr int KS = D / 16;    // 16-element steps of a head
   constexpr int KB = D / 64;    // 64-byte pieces of a key
   constexpr int VW = D / 32;    // words of V a lane holds of one key
@@ -195,20 +186,24 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
   extern __shared__ __align__(16) uint8_t smem[];
   float* const so = reinterpret_cast<float*>(smem);
   float2* const sml = reinterpret_cast<float2*>(smem + SH::O);
-  uint2* const sq = reinterpret_cast<uint2*>(smem + SH::O + SH::ML);
+  float* const sqf = reinterpret_cast<float*>(smem + SH::O + SH::ML);  // the rows' inverse powers of two
+  uint2* const sq = reinterpret_cast<uint2*>(smem + SH::O + SH::ML + SH::QF);
 
   const Cache& c = p.c;
   int* const status = c.status;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int h = blockIdx.x % c.Hkv, range = blockIdx.x / c.Hkv;
+  const int row_lo = blockIdx.y * ROWS;
   const int heads = p.Hq / c.Hkv;
-  const size_t step = static_cast<size_t>(c.Hkv) * D;  // bytes from token to token
+  const bool bf16 = p.bf16;
+  const int64_t step = static_cast<int64_t>(c.Hkv) * D;  // bytes from token to token
   const int64_t ntok = static_cast<int64_t>(c.num_pages) * c.page_size;
   const int64_t nscale = static_cast<int64_t>(c.num_pages) * c.Hkv * c.per;
   const int64_t nrows = static_cast<int64_t>(p.num_queries) * p.Hq;
-  const uint8_t* const kb = p.k_codes + h * D;
-  const uint8_t* const vb = p.v_codes + h * D;
+  const uint8_t* const kb = p.k_codes + h * D + t * 16;
+  const uint8_t* const vb = p.v_codes + h * D + g * (D / 8);
   const bool tiles_in_page = c.page_size % 16 == 0;
+  const int dblk = BLOCK_KEYS / c.page_size, drow = BLOCK_KEYS % c.page_size;
 
   int64_t u0, u1;
   const Place pl = locate(p, range, ranges, false, u0, u1);
@@ -223,58 +218,85 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
     const int take = static_cast<int>(min(static_cast<int64_t>(nb - b), u1 - u));
     const bool first = u == u0, whole = take == nb;
     u += take;
-    const int R = static_cast<int>(min(static_cast<int64_t>(nq) * heads, static_cast<int64_t>(ROWS)));
+    const int R = static_cast<int>(min(static_cast<int64_t>(nq) * heads - row_lo, static_cast<int64_t>(ROWS)));
+    if (R <= 0) continue;  // CTA-uniform
+    auto row_at = [&](int row) {  // row of the call's [queries, Hq]
+      const int q = (row_lo + row) / heads;
+      return static_cast<int64_t>(q_lo + q) * p.Hq + h * heads + (row_lo + row - q * heads);
+    };
 
     // ------------------------------------------------ query rows
-    uint32_t qf[NT == 1 ? KS : 1][2];
-    auto load_q = [&](int row, int piece, uint32_t (&r)[8]) {  // 16 elements at 64 piece + 16 t
-      uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-      if (row < R) {
-        const int64_t at = static_cast<int64_t>(q_lo + row / heads) * p.Hq + h * heads + row % heads;
-        if (in_bounds(status, at, nrows)) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at * D + piece * 64 + t * 16);
-          x = __ldg(src);
-          y = __ldg(src + 1);
-        }
-      }
-      r[0] = x.x; r[1] = x.y; r[2] = x.z; r[3] = x.w;
-      r[4] = y.x; r[5] = y.y; r[6] = y.z; r[7] = y.w;
-    };
-    if constexpr (NT == 1) {
+    // Row 8 w + g by warp w, its elements in the lanes' order: lane t holds
+    // elements 64 i + 16 t .. + 15, two registers for each of 4 steps.
+    if (warp < NT) {
+      uint32_t r[KB][8];
+      const int row = 8 * warp + g;
 #pragma unroll
       for (int i = 0; i < KB; ++i) {
-        uint32_t r[8];
-        load_q(g, i, r);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          qf[4 * i + k][0] = r[2 * k];
-          qf[4 * i + k][1] = r[2 * k + 1];
+        uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+        if (row < R) {
+          const int64_t at = row_at(row);
+          if (in_bounds(status, at, nrows)) {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at * D + i * 64 + t * 16);
+            x = __ldg(src);
+            y = __ldg(src + 1);
+          }
         }
+        r[i][0] = x.x; r[i][1] = x.y; r[i][2] = x.z; r[i][3] = x.w;
+        r[i][4] = y.x; r[i][5] = y.y; r[i][6] = y.z; r[i][7] = y.w;
       }
-    } else {
-      if (warp < NT) {
+      float back = 1.f;
+      if (bf16) {
+        float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < KB; ++i) {
-          uint32_t r[8];
-          load_q(8 * warp + g, i, r);
+        for (int i = 0; i < KB; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sq[(warp * KS + 4 * i + k) * 32 + lane] = make_uint2(r[2 * k], r[2 * k + 1]);
-        }
+          for (int k = 0; k < 8; ++k) {
+            const float lo = fabsf(__uint_as_float(r[i][k] << 16)), hi = fabsf(__uint_as_float(r[i][k] & 0xffff0000u));
+            top = fmaxf(top, fmaxf(lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f));
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // the largest element to [2^14, 2^15)
+        const int e = min(max(14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), -126), 126);
+        const float f = pow2(e);
+        back = pow2(-e);
+#pragma unroll
+        for (int i = 0; i < KB; ++i)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            r[i][k] = pack2<false>(__uint_as_float(r[i][k] << 16) * f, __uint_as_float(r[i][k] & 0xffff0000u) * f);
       }
-      __syncthreads();
+      if (t == 0) sqf[row] = back;
+#pragma unroll
+      for (int i = 0; i < KB; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sq[(warp * KS + 4 * i + k) * 32 + lane] = make_uint2(r[i][2 * k], r[i][2 * k + 1]);
     }
-    int lim[NT][2];  // last key that the lane's rows (8 i + 2 t, + 1) see
+    __syncthreads();
+    uint32_t qf[NT == 1 ? KS : 1][2];
+    if constexpr (NT == 1) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const uint2 w = sq[k * 32 + lane];
+        qf[k][0] = w.x;
+        qf[k][1] = w.y;
+      }
+    }
+    int lim[NT][2];     // last key that the lane's rows (8 i + 2 t, + 1) see
+    float back[NT][2];  // and their inverse powers of two
     int least = L - 1, most = -1;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int row = 8 * i + 2 * t + e;
+        back[i][e] = sqf[row];
         int x = -1;
         if (row < R) {
           x = L - 1;
           if (p.causal) {
-            const int q = row / heads;
+            const int q = (row_lo + row) / heads;
             const int pos = p.positions ? (in_bounds(status, q_lo + q, p.num_queries) ? __ldg(p.positions + q_lo + q) : -1)
                                         : L - nq + q;
             x = min(x, pos);
@@ -291,133 +313,116 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
     }
 
     // ------------------------------------------------ keys
-    float m[NT][2], l[NT][2], acc[KS][NT][4];
+    // Of a row: m the running maximum (log2 units), l the lane's part of the sum
+    // of p = 2^(x - m), acc the sum of P' = p v_scale r times the codes.
+    float m[NT][2], l[NT][2], r[NT][2], acc[KS][NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       m[i][0] = m[i][1] = -INFINITY;
       l[i][0] = l[i][1] = 0.f;
+      r[i][0] = r[i][1] = 1.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k) acc[k][i][0] = acc[k][i][1] = acc[k][i][2] = acc[k][i][3] = 0.f;
     }
-    float top = 1.17549435e-38f, itop = 8.5070592e37f;  // F16: the power of two that P' is relative to, its inverse
     // Lane (g, t): keys ka and ka + 2 of a tile in S^T; keys 4 t .. 4 t + 3 in V^T
     const int ka = 4 * (g >> 1) + (g & 1);
-    // token (page * page_size + row) of keys j and j + 2, -1 for zeros
-    auto tokens = [&](int key0, int& x, int& y) {
-      if (tiles_in_page) {
-        const int blk = key0 / c.page_size;
-        const int page = key0 < L ? page_of(c, s, blk) : -1;
-        const int base = page * c.page_size + (key0 - blk * c.page_size) + ka;
-        x = page >= 0 && key0 + ka < L ? base : -1;
-        y = page >= 0 && key0 + ka + 2 < L ? base + 2 : -1;
-      } else {
-        auto one = [&](int j) {
-          if (j >= L) return -1;
-          const int blk = j / c.page_size, page = page_of(c, s, blk);
-          return page >= 0 ? page * c.page_size + (j - blk * c.page_size) : -1;
-        };
-        x = one(key0 + ka);
-        y = one(key0 + ka + 2);
-      }
-    };
+    const int last_key = min(most + 1, (b + take) * BLOCK_KEYS);
+    int key0 = b * BLOCK_KEYS + warp * 16;
+    int blk = key0 / c.page_size, row0 = key0 - blk * c.page_size;  // of the tile to load next
     uint32_t kr[2][KB * 4], vr[4][VW];
     float ks[2], vs[2];
-    auto load_k = [&](int x, int y) {
+    int tok[2];  // tokens (page * page_size + row) of the lane's two keys, -1: zeros
+    auto load_k = [&](int key) {
+      int page[2], row[2];
+      page[0] = page[1] = page_of(c, s, blk);
+      row[0] = row0 + ka;
+      row[1] = row[0] + 2;
+      if (!tiles_in_page) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int more = row[e] / c.page_size;
+          row[e] -= more * c.page_size;
+          page[e] = key + ka + 2 * e < L ? page_of(c, s, blk + more) : -1;
+        }
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int tok = e ? y : x;
-        const bool ok = tok >= 0 && in_bounds(status, tok, ntok);
-        const uint8_t* at = kb + (ok ? static_cast<size_t>(tok) * step : 0) + t * 16;
+        tok[e] = page[e] * c.page_size + row[e];
+        const bool ok = page[e] >= 0 && key + ka + 2 * e < L && in_bounds(status, tok[e], ntok);
+        tok[e] = ok ? tok[e] : -1;
+        const uint8_t* at = kb + max(tok[e], 0) * step;
 #pragma unroll
         for (int i = 0; i < KB; ++i) load_words<4>(&kr[e][4 * i], at + 64 * i);
         ks[e] = vs[e] = 0.f;
         if (ok) {
-          const int page = tok / c.page_size;
-          const size_t si = scale_index(c, page, tok - page * c.page_size, h);
-          if (in_bounds(status, static_cast<int64_t>(si), nscale)) {
-            ks[e] = __ldg(p.k_scale + si) * (p.scale_log2 * code_scale<BF16, FMT>());
-            vs[e] = __ldg(p.v_scale + si) * code_scale<BF16, FMT>();
+          const int gi = c.group == 1 ? row[e] : static_cast<int>(__umulhi(static_cast<uint32_t>(row[e]), p.group_magic));
+          const int64_t si = (static_cast<int64_t>(page[e]) * c.Hkv + h) * c.per + gi;
+          if (in_bounds(status, si, nscale)) {
+            ks[e] = __ldg(p.k_scale + si);
+            vs[e] = __ldg(p.v_scale + si);
           }
         }
       }
     };
-    auto load_v = [&](int x, int y) {
+    auto load_v = [&]() {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int tok = __shfl_sync(0xffffffffu, i < 2 ? x : y, (2 * t + (i & 1)) * 4);
-        const bool ok = tok >= 0 && in_bounds(status, tok, ntok);
-        load_words<VW>(vr[i], vb + (ok ? static_cast<size_t>(tok) * step : 0) + g * (D / 8));
+        const int x = __shfl_sync(0xffffffffu, tok[i >> 1], (2 * t + (i & 1)) * 4);
+        load_words<VW>(vr[i], vb + max(x, 0) * step);
       }
     };
-    const int key_end = most + 1;
-    const int last_key = min(key_end, (b + take) * BLOCK_KEYS);
-    int key0 = b * BLOCK_KEYS + warp * 16;
-    int nx, ny;  // tokens of the tile to load next
     if (key0 < last_key) {
-      tokens(key0, nx, ny);
-      load_k(nx, ny);
-      load_v(nx, ny);
+      load_k(key0);
+      load_v();
     }
     for (; key0 < last_key; key0 += BLOCK_KEYS) {
       const bool more = key0 + BLOCK_KEYS < last_key;
-      if (more) tokens(key0 + BLOCK_KEYS, nx, ny);
       float sc[NT][4];
 #pragma unroll
       for (int i = 0; i < NT; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const uint32_t a0 = pair<BF16, FMT>(kr[0][k], kr[0][k], 0, 1), a1 = pair<BF16, FMT>(kr[1][k], kr[1][k], 0, 1);
-        const uint32_t a2 = pair<BF16, FMT>(kr[0][k], kr[0][k], 2, 3), a3 = pair<BF16, FMT>(kr[1][k], kr[1][k], 2, 3);
+        uint32_t a0, a1, a2, a3;
+        pairs<FMT>(kr[0][k], a0, a2);
+        pairs<FMT>(kr[1][k], a1, a3);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          uint32_t b0, b1;
           if constexpr (NT == 1) {
-            b0 = qf[k][0];
-            b1 = qf[k][1];
+            mma16816(sc[i], a0, a1, a2, a3, qf[k][0], qf[k][1]);
           } else {
             const uint2 w = sq[(i * KS + k) * 32 + lane];
-            b0 = w.x;
-            b1 = w.y;
+            mma16816(sc[i], a0, a1, a2, a3, w.x, w.y);
           }
-          mma16816<BF16>(sc[i], a0, a1, a2, a3, b0, b1);
         }
       }
-      const float k0 = ks[0], k1 = ks[1], v0 = vs[0], v1 = vs[1];
-      if (more) load_k(nx, ny);
+      const float k0 = ks[0] * p.scale_log2, k1 = ks[1] * p.scale_log2, v0 = vs[0], v1 = vs[1];
+      blk += dblk;
+      row0 += drow;
+      if (row0 >= c.page_size) {
+        row0 -= c.page_size;
+        ++blk;
+      }
+      if (more) load_k(key0 + BLOCK_KEYS);
 
-      // scores (log2 units) of keys key0 + ka and + 2
+      // keys key0 + ka (elements 0, 1: the lane's rows) and + 2 (elements 2, 3)
       const bool masked = key0 + 15 > least;
+      float z[NT][4], d[NT][2];  // P', and the tile's part of the sum
       bool grow = false;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        sc[i][0] *= k0;
-        sc[i][1] *= k0;
-        sc[i][2] *= k1;
-        sc[i][3] *= k1;
-        if (masked) {
+        d[i][0] = d[i][1] = 0.f;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (key0 + ka > lim[i][e]) sc[i][e] = -INFINITY;
-            if (key0 + ka + 2 > lim[i][e]) sc[i][2 + e] = -INFINITY;
-          }
+        for (int e = 0; e < 4; ++e) {
+          float x = sc[i][e] * (e < 2 ? k0 : k1) * back[i][e & 1];
+          if (masked && key0 + ka + (e & 2) > lim[i][e & 1]) x = -INFINITY;
+          sc[i][e] = x;
+          const float y = fast_exp2(x - (m[i][e & 1] == -INFINITY ? 0.f : m[i][e & 1]));
+          d[i][e & 1] += y;
+          z[i][e] = y * (e < 2 ? v0 : v1) * r[i][e & 1];
+          grow = grow || x > m[i][e & 1] + RESCALE_LOG2 || z[i][e] > 256.f;
         }
-        grow = grow || fmaxf(sc[i][0], sc[i][2]) > m[i][0] + RESCALE_LOG2 ||
-               fmaxf(sc[i][1], sc[i][3]) > m[i][1] + RESCALE_LOG2;
       }
-      if constexpr (!BF16) grow = grow || fmaxf(v0, v1) > top;
       if (__any_sync(0xffffffffu, grow)) {
-        float ratio = 1.f;
-        if constexpr (!BF16) {
-          float x = fmaxf(v0, v1);
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-          if (x > top) {  // the power of two above x (or 2^126)
-            const float n = __uint_as_float(min((__float_as_uint(x) & 0x7f800000u) + 0x00800000u, 0x7e800000u));
-            ratio = top / n;
-            top = n;
-            itop = 1.f / n;
-          }
-        }
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -426,41 +431,59 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
             const float n = fmaxf(m[i][e], x);
+            const float sub = n == -INFINITY ? 0.f : n;
             const float alpha = n == -INFINITY ? 1.f : fast_exp2(m[i][e] - n);
+            // the largest p v_scale of the tile, and the r that brings it to (1/2, 1];
+            // r may grow with m, as the old terms shrink, but not past what they allow
+            const float y0 = fast_exp2(sc[i][e] - sub), y1 = fast_exp2(sc[i][2 + e] - sub);
+            float w = fmaxf(y0 * v0, y1 * v1);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
+            const float same = fminf(r[i][e] / alpha, 1.2676506e30f);  // 2^100; keeps the accumulator's scale
+            const int ex = static_cast<int>(__float_as_uint(w) >> 23) - 127 + 1;  // w < 2^ex
+            const float want = pow2(min(max(-ex, -126), 100));
+            const float rn = w * same > 1.f ? want : same;
+            const float f = fminf(rn / r[i][e], 3e38f) * alpha;
             m[i][e] = n;
+            r[i][e] = rn;
             l[i][e] *= alpha;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-              acc[k][i][e] *= alpha * ratio;
-              acc[k][i][2 + e] *= alpha * ratio;
+              acc[k][i][e] *= f;
+              acc[k][i][2 + e] *= f;
             }
+            d[i][e] = y0 + y1;
+            z[i][e] = y0 * v0 * rn;
+            z[i][2 + e] = y1 * v1 * rn;
           }
       }
-      const float w0 = BF16 ? v0 : v0 * itop, w1 = BF16 ? v1 : v1 * itop;
       uint32_t pf[NT][2];
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        float x[4];
+        l[i][0] += d[i][0];
+        l[i][1] += d[i][1];
+        if (masked) {  // a masked key may have any scale
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float n = m[i][e & 1];
-          const float y = fast_exp2(sc[i][e] - (n == -INFINITY ? 0.f : n));
-          l[i][e & 1] += y;
-          // a masked key may have any scale
-          x[e] = masked && sc[i][e] == -INFINITY ? 0.f : y * (e < 2 ? w0 : w1);
+          for (int e = 0; e < 4; ++e) z[i][e] = sc[i][e] == -INFINITY ? 0.f : z[i][e];
         }
-        pf[i][0] = transpose8x8(pack2<BF16>(x[0], x[1]));
-        pf[i][1] = transpose8x8(pack2<BF16>(x[2], x[3]));
+        pf[i][0] = transpose8x8(pack2<false>(z[i][0], z[i][1]));
+        pf[i][1] = transpose8x8(pack2<false>(z[i][2], z[i][3]));
       }
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const int w = k / 2, o = (k & 1) * 2;  // bytes 2 k and 2 k + 1 of the lane's
-        const uint32_t a0 = pair<BF16, FMT>(vr[0][w], vr[1][w], o, o), a1 = pair<BF16, FMT>(vr[0][w], vr[1][w], o + 1, o + 1);
-        const uint32_t a2 = pair<BF16, FMT>(vr[2][w], vr[3][w], o, o), a3 = pair<BF16, FMT>(vr[2][w], vr[3][w], o + 1, o + 1);
+      for (int w = 0; w < VW; ++w) {
+        // keys 0, 1 and 2, 3 of the lane interleaved: two steps' operands
+        uint32_t a[2][4];
+        pairs<FMT>(__byte_perm(vr[0][w], vr[1][w], 0x5140), a[0][0], a[0][1]);
+        pairs<FMT>(__byte_perm(vr[2][w], vr[3][w], 0x5140), a[0][2], a[0][3]);
+        pairs<FMT>(__byte_perm(vr[0][w], vr[1][w], 0x7362), a[1][0], a[1][1]);
+        pairs<FMT>(__byte_perm(vr[2][w], vr[3][w], 0x7362), a[1][2], a[1][3]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) mma16816<BF16>(acc[k][i], a0, a1, a2, a3, pf[i][0], pf[i][1]);
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+            mma16816(acc[2 * w + k][i], a[k][0], a[k][1], a[k][2], a[k][3], pf[i][0], pf[i][1]);
       }
-      if (more) load_v(nx, ny);
+      if (more) load_v();
     }
 
     // ------------------------------------------------ the warps' parts
@@ -473,10 +496,10 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
         const int row = 8 * i + 2 * t + e;
         if (g == 0) sml[warp * ROWS + row] = make_float2(m[i][e], l[i][e]);
         float* const o = so + (warp * ROWS + row) * SH::ROW + g * (D / 8);
+        const float f = 1.f / r[i][e];
 #pragma unroll
         for (int k = 0; k < KS; ++k)
-          *reinterpret_cast<float2*>(o + 2 * k) = make_float2(BF16 ? acc[k][i][e] : acc[k][i][e] * top,
-                                                              BF16 ? acc[k][i][2 + e] : acc[k][i][2 + e] * top);
+          *reinterpret_cast<float2*>(o + 2 * k) = make_float2(acc[k][i][e] * f, acc[k][i][2 + e] * f);
       }
     __syncthreads();
     const int64_t slot = 2ll * blockIdx.x + (first ? 0 : 1);
@@ -501,14 +524,14 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
       if (whole) {
         const bool live = sum > 0.f;
         const float inv = live ? 1.f / sum : __int_as_float(0x7fc00000);
-        const int64_t at = static_cast<int64_t>(q_lo + row / heads) * p.Hq + h * heads + row % heads;
+        const int64_t at = row_at(row);
         if (!in_bounds(status, at, nrows)) continue;
         reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * D)[d4] =
-            make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+            make_uint2(pack_out(bf16, o.x * inv, o.y * inv), pack_out(bf16, o.z * inv, o.w * inv));
         if (p.lse && d4 == 0) p.lse[at] = live ? (M + log2f(sum)) * LN2 : (sum == 0.f ? -INFINITY : sum);
       } else {
-        const int64_t at = slot * ROWS + row;
-        if (!in_bounds(status, at, 2ll * ranges * c.Hkv * ROWS)) continue;
+        const int64_t at = slot * slot_rows + row_lo + row;
+        if (!in_bounds(status, at, 2ll * ranges * c.Hkv * slot_rows)) continue;
         reinterpret_cast<float4*>(p.ws)[at * (D / 4) + d4] = o;
         if (d4 == 0) reinterpret_cast<float2*>(static_cast<uint8_t*>(p.ws) + ml_offset)[at] = make_float2(M, sum);
       }
@@ -520,8 +543,8 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
 // A CTA (range, head; blockIdx.y: row) combines the parts of the sequence that
 // begins in the range and goes on past it: its own last slot, then the first
 // slot of the ranges after it.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(THREADS) merge_kernel(const __grid_constant__ FwdParams p, int ranges, int ROWS,
+template <int D>
+__global__ void __launch_bounds__(THREADS) merge_kernel(const __grid_constant__ FwdParams p, int ranges, int slot_rows,
                                                         int64_t ml_offset) {
   constexpr int G = D / 4;
   __shared__ float4 so[WARPS * 32 / G][G];
@@ -546,8 +569,8 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const __grid_constant__ 
   for (int r = range + part0; r <= last; r += parts) {
     const int64_t a = pl.total * r / ranges, b = pl.total * (r + 1) / ranges;
     if (a == b) continue;
-    const int64_t at = (2ll * (static_cast<int64_t>(r) * c.Hkv + h) + (r == range && pl.at > u0 ? 1 : 0)) * ROWS + row;
-    if (!in_bounds(c.status, at, 2ll * ranges * c.Hkv * ROWS)) continue;
+    const int64_t at = (2ll * (static_cast<int64_t>(r) * c.Hkv + h) + (r == range && pl.at > u0 ? 1 : 0)) * slot_rows + row;
+    if (!in_bounds(c.status, at, 2ll * ranges * c.Hkv * slot_rows)) continue;
     const float2 ml = wml[at];
     const float4 x = wo[at * G + g];
     const float n = fmaxf(M, ml.x);
@@ -574,43 +597,41 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const __grid_constant__ 
   const int64_t at = static_cast<int64_t>(q_lo + row / heads) * p.Hq + h * heads + row % heads;
   if (!in_bounds(c.status, at, static_cast<int64_t>(p.num_queries) * p.Hq)) return;
   reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * D)[g] =
-      make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+      make_uint2(pack_out(p.bf16, o.x * inv, o.y * inv), pack_out(p.bf16, o.z * inv, o.w * inv));
   if (p.lse && g == 0) p.lse[at] = live ? (M + log2f(sum)) * LN2 : (sum == 0.f ? -INFINITY : sum);
 }
 
-template <int D, bool BF16, int FMT, int NT>
-cudaError_t launch_nt(const FwdParams& p, int ranges, cudaStream_t st) {
-  auto kern = decode_kernel<D, BF16, FMT, NT>;
+template <int D, int FMT, int NT>
+cudaError_t launch_nt(const FwdParams& p, const DecodePlan& plan, cudaStream_t st) {
+  auto kern = decode_kernel<D, FMT, NT>;
   constexpr int smem = Shared<D, NT>::BYTES;
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const DecodeLayout lay{2ll * ranges * p.c.Hkv, 8 * NT};
-  const unsigned ctas = static_cast<unsigned>(ranges) * p.c.Hkv;
-  kern<<<ctas, THREADS, smem, st>>>(p, ranges, lay.ml_offset(D));
+  const unsigned ctas = static_cast<unsigned>(plan.ranges) * p.c.Hkv;
+  const int64_t ml = plan.ml_offset(p.c.Hkv, D);
+  kern<<<dim3(ctas, plan.row_groups), THREADS, smem, st>>>(p, plan.ranges, plan.slot_rows(), ml);
   e = cudaGetLastError();
-  if (e != cudaSuccess || ranges == 1) return e;
-  const int rows = min(p.max_queries * (p.Hq / p.c.Hkv), 8 * NT);
-  merge_kernel<D, BF16><<<dim3(ctas, rows), THREADS, 0, st>>>(p, ranges, 8 * NT, lay.ml_offset(D));
+  if (e != cudaSuccess || plan.ranges == 1) return e;
+  merge_kernel<D><<<dim3(ctas, plan.rows), THREADS, 0, st>>>(p, plan.ranges, plan.slot_rows(), ml);
   return cudaGetLastError();
 }
 
-template <int D, bool BF16, int FMT>
-cudaError_t launch_d(const FwdParams& p, int ranges, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(p.max_queries) * (p.Hq / p.c.Hkv);
-  if (rows <= 8) return launch_nt<D, BF16, FMT, 1>(p, ranges, st);
-  if (rows <= 16) return launch_nt<D, BF16, FMT, 2>(p, ranges, st);
-  return launch_nt<D, BF16, FMT, 4>(p, ranges, st);
+template <int D, int FMT>
+cudaError_t launch_d(const FwdParams& p, const DecodePlan& plan, cudaStream_t st) {
+  switch (plan.nt) {
+    case 1: return launch_nt<D, FMT, 1>(p, plan, st);
+    case 2: return launch_nt<D, FMT, 2>(p, plan, st);
+    case 3: return launch_nt<D, FMT, 3>(p, plan, st);
+    default: return launch_nt<D, FMT, 4>(p, plan, st);
+  }
 }
 
 }  // namespace dec
 
-template <bool BF16>
-cudaError_t launch_decode(const FwdParams& p, int fmt, cudaStream_t st) {
-  const int ranges = decode_ranges(p.c.num_seqs, p.c.Hkv, p.c.max_pages, p.c.page_size);
-  if (fmt == FMT_INT8)
-    return p.c.D == 128 ? dec::launch_d<128, BF16, FMT_INT8>(p, ranges, st) : dec::launch_d<64, BF16, FMT_INT8>(p, ranges, st);
-  return p.c.D == 128 ? dec::launch_d<128, BF16, FMT_E4M3>(p, ranges, st) : dec::launch_d<64, BF16, FMT_E4M3>(p, ranges, st);
+template <int FMT>
+cudaError_t launch_decode(const FwdParams& p, const DecodePlan& plan, cudaStream_t st) {
+  return p.c.D == 128 ? dec::launch_d<128, FMT>(p, plan, st) : dec::launch_d<64, FMT>(p, plan, st);
 }
 
 }  // namespace kv8

@@ -187,11 +187,16 @@ int check_shape(const attn_paged_shape_t& s) {
 }
 
 // Shapes of the kernel that shares out the keys. Its token numbers (page *
-// page_size + row) are 32-bit.
+// page_size + row) are 32-bit, its row / group a 32-bit multiplication.
 bool takes_decode(const attn_paged_shape_t& s) {
-  return (s.D == 64 || s.D == 128) && attn::kv8::decode_rows(s.max_queries, s.Hq / s.Hkv) && s.num_pages > 0 &&
-         static_cast<int64_t>(s.num_pages) * s.page_size <= 0x7fffffffLL && s.num_seqs > 0 && s.Hkv <= 65535 &&
+  const int64_t rows = static_cast<int64_t>(s.max_queries) * (s.Hq / s.Hkv);
+  return (s.D == 64 || s.D == 128) && rows > 0 && rows <= attn::kv8::DECODE_ROWS && s.num_pages > 0 && s.num_seqs > 0 &&
+         static_cast<int64_t>(s.num_pages) * s.page_size <= 0x7fffffffLL && s.page_size < 65536 && s.Hkv <= 65535 &&
          static_cast<int64_t>(s.max_pages) * s.page_size <= 0x7fff0000LL;
+}
+
+attn::kv8::DecodePlan plan_of(const attn_paged_shape_t& s) {
+  return attn::kv8::decode_plan(s.num_seqs, s.Hkv, s.Hq / s.Hkv, s.max_queries, s.max_pages, s.page_size);
 }
 
 }  // namespace
@@ -199,14 +204,7 @@ bool takes_decode(const attn_paged_shape_t& s) {
 extern "C" int attn_paged_kv8_workspace_bytes(const attn_paged_shape_t* shape, size_t* bytes) {
   if (!shape || !bytes) return ATTN_ERR_NULL;
   if (const int rc = check_shape(*shape)) return rc;
-  const attn_paged_shape_t& s = *shape;
-  *bytes = 0;
-  if (takes_decode(s)) {
-    const int64_t rows = static_cast<int64_t>(s.max_queries) * (s.Hq / s.Hkv);
-    const attn::kv8::DecodeLayout lay{
-        2ll * s.Hkv * attn::kv8::decode_ranges(s.num_seqs, s.Hkv, s.max_pages, s.page_size), rows <= 8 ? 8 : rows <= 16 ? 16 : 32};
-    *bytes = static_cast<size_t>(lay.bytes(s.D));
-  }
+  *bytes = takes_decode(*shape) ? static_cast<size_t>(plan_of(*shape).bytes(shape->Hkv, shape->D)) : 0;
   return ATTN_OK;
 }
 
@@ -276,6 +274,8 @@ extern "C" int attn_paged_kv8_fwd(const attn_paged_shape_t* shape, int group, in
   p.max_queries = s.max_queries;
   p.causal = causal;
   p.device = dev;
+  p.bf16 = dtype == ATTN_BF16;
+  p.group_magic = group > 1 ? static_cast<uint32_t>((1ull << 32) / group + 1) : 0u;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.q_offsets = q_offsets;
   p.positions = positions;
@@ -291,7 +291,8 @@ extern "C" int attn_paged_kv8_fwd(const attn_paged_shape_t* shape, int group, in
   const bool i8 = format == ATTN_KV8_INT8;
   using namespace attn::kv8;
   if (dtype != ATTN_F32 && takes_decode(s)) {
-    e = dtype == ATTN_BF16 ? launch_decode<true>(p, format, st) : launch_decode<false>(p, format, st);
+    const DecodePlan plan = plan_of(s);
+    e = i8 ? launch_decode<FMT_INT8>(p, plan, st) : launch_decode<FMT_E4M3>(p, plan, st);
     return e == cudaSuccess ? ATTN_OK : attn::record_cuda_error(e);
   }
 #define ATTN_FWD(DT) (i8 ? launch_simt<DT, FMT_INT8>(p, st) : launch_simt<DT, FMT_E4M3>(p, st))

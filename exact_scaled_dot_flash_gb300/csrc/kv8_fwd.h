@@ -9,6 +9,8 @@ namespace kv8 {
 struct FwdParams {
   Cache c;
   int Hq, num_queries, max_queries, causal, device;
+  bool bf16;                   // type of q and out in the 16-bit kernels (else F16)
+  uint32_t group_magic;        // row / group = umulhi(row, group_magic) for group > 1, row < 65536
   float scale_log2;            // scale * log2(e): scores are kept in the log2 domain
   const int32_t* q_offsets;    // [num_seqs + 1]
   const int32_t* positions;    // [num_queries] or nullptr (the newest tokens)
@@ -20,35 +22,42 @@ struct FwdParams {
   void* ws;
 };
 
-// Calls with at most this many rows (queries x heads) of a kv head share out
-// the keys (attn_kv8_decode.cuh).
-constexpr int DECODE_ROWS = 32;
-inline bool decode_rows(int max_queries, int heads) {
-  return static_cast<int64_t>(max_queries) * heads <= DECODE_ROWS;
-}
-
-// Ranges that the keys of a call are cut into, each for Hkv CTAs: two CTAs for
-// each of the 152 SMs (the kernel for 8 rows fits twice); with many heads four
-// waves of smaller ones, so that a last wave that is not full costs little;
-// never more than there can be blocks of 128 keys.
-inline int decode_ranges(int num_seqs, int Hkv, int max_pages, int page_size) {
-  const int64_t keys = static_cast<int64_t>(max_pages) * page_size;
-  const int64_t blocks = num_seqs * ((keys + 127) / 128 > 1 ? (keys + 127) / 128 : 1);
-  int64_t r = (Hkv > 16 ? 4 : 1) * 304 / Hkv;
-  if (r > blocks) r = blocks;
-  return static_cast<int>(r > 1 ? r : 1);
-}
-
-// Partials: CTA c (range, head) owns slots 2c (its first sequence) and 2c + 1
-// (its last), each rows x (D floats) and rows x (m, l).
-struct DecodeLayout {
-  int64_t slots, rows;
-  int64_t ml_offset(int D) const { return (slots * rows * D * 4 + 255) / 256 * 256; }
-  int64_t bytes(int D) const { return ml_offset(D) + slots * rows * 8; }
+// How a call with few rows is cut (attn_kv8_decode.cuh). A CTA takes up to 32
+// rows of a kv head (8 nt); more rows go to `row_groups` CTAs that read the same
+// codes (the second from L2).
+struct DecodePlan {
+  int rows = 0, row_groups = 0, nt = 0, ranges = 0;
+  int slot_rows() const { return row_groups * nt * 8; }
+  // Partials: CTA c (range, head) owns slots 2c (its first sequence) and 2c + 1
+  // (its last), each slot_rows x (D floats) and slot_rows x (m, l).
+  int64_t ml_offset(int Hkv, int D) const { return 2ll * ranges * Hkv * slot_rows() * D * 4; }
+  int64_t bytes(int Hkv, int D) const { return ml_offset(Hkv, D) + 2ll * ranges * Hkv * slot_rows() * 8; }
 };
 
-template <bool BF16>
-cudaError_t launch_decode(const FwdParams& p, int fmt, cudaStream_t st);
+// Calls with at most this many rows (queries x heads) of a kv head.
+constexpr int DECODE_ROWS = 64;
+
+// Ranges that the keys of a call are cut into, each for Hkv CTAs (and row
+// groups): as many CTAs as the 152 SMs hold at once, two each of the kernel for
+// 8 rows and one of the others; with many heads four waves of smaller ones, so
+// that a last wave that is not full costs little; never more ranges than there
+// can be blocks of 128 keys.
+inline DecodePlan decode_plan(int num_seqs, int Hkv, int heads, int max_queries, int max_pages, int page_size) {
+  DecodePlan d;
+  d.rows = static_cast<int>(static_cast<int64_t>(max_queries) * heads);
+  d.row_groups = (d.rows + 31) / 32;
+  d.nt = ((d.rows + d.row_groups - 1) / d.row_groups + 7) / 8;
+  const int64_t keys = static_cast<int64_t>(max_pages) * page_size;
+  const int64_t blocks = num_seqs * (keys > 128 ? (keys + 127) / 128 : 1);
+  const int64_t side = static_cast<int64_t>(Hkv) * d.row_groups;
+  int64_t r = (side > 16 ? 4 : 1) * (d.nt == 1 ? 304 : 152) / side;
+  if (r > blocks) r = blocks;
+  d.ranges = static_cast<int>(r > 1 ? r : 1);
+  return d;
+}
+
+template <int FMT>
+cudaError_t launch_decode(const FwdParams& p, const DecodePlan& plan, cudaStream_t st);
 
 }  // namespace kv8
 }  // namespace attn

@@ -499,3 +499,28 @@ def test_graph_and_streams(new):
     got = [step(caches[i], *args[i], stream=sides[i]) for i in range(2)]
     torch.cuda.synchronize()
     assert all(torch.equal(o, t) for i in range(2) for o, t in zip(got[i], want[i]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("new", [1, 33])
+def test_attention_over_small_and_large_codes(dtype, new):
+    import torch
+    # e4m3 codes below the format's normal range in one sequence, the largest in the other; queries
+    # whose rows differ by many powers of two
+    p = Problem(20, [200, 150], [new, new], dtype=dtype, fmt="e4m3", D=128, Hq=8, P=32, G=4)
+    r = np.random.RandomState(5)
+    for c in (p.kc, p.vc):
+        for s, codes in ((0, [0, 1, 2, 3, 7, 0x81, 0x87, 8]), (1, [0x7e, 0xfe, 0x78, 0xf0, 0x80])):
+            for b in p.table[s][p.table[s] >= 0]:
+                c[b] = r.choice(codes, c[b].shape)
+    p.ks[p.table[0, :7]] *= 2.0 ** 9
+    p.q = (p.q.double() * torch.from_numpy(0.2 * 2.0 ** r.randint(-12, 3, (p.tokens, 8, 1)))).to(p.q.dtype)
+    check_attention(p, attend(p, p.cache()), p.kc, p.ks, p.vc, p.vs)
+
+
+@pytest.mark.parametrize("heads,new", [(3, 3), (5, 2), (7, 5), (8, 7), (16, 4), (1, 20), (1, 60)])
+@pytest.mark.parametrize("H", [1, 3, 20])
+def test_attention_row_counts(heads, new, H):
+    # 9 .. 64 rows of a kv head, one and two groups of rows; heads that divide nothing; uneven lengths
+    p = Problem(21, [300, 64, 1000], [new, 1, new - 1], dtype="f16", fmt="int8", D=64, P=16, G=4, H=H, Hq=H * heads)
+    check_attention(p, attend(p, p.cache()), p.kc, p.ks, p.vc, p.vs)
