@@ -6,11 +6,12 @@
 // the copy bandwidth an SM is fed 21 bytes a cycle, and each byte has to become
 // a 16-bit operand, so what the kernel economises is instructions and
 // shared-memory traffic per byte:
-//  - the codes go from global memory to registers and, converted there, into
-//    mma.sync as the A operand (a 16-key tile of a warp); nothing is staged in
-//    shared memory (a tcgen05 operand would be written once and read twice, 6
-//    bytes of shared-memory traffic for a byte of cache) and a tile has 8
-//    columns for the query rows instead of 128;
+//  - a warp streams its own 16-key tiles through a ring of cp.async copies in
+//    shared memory (no barrier between warps), reads each code once into
+//    registers, converts it there and feeds it to mma.sync as the A operand: 2
+//    bytes of shared-memory traffic for a byte of cache (a 16-bit tcgen05 operand
+//    would be written once and read twice, 6 bytes of it), and 8 columns for the
+//    query rows instead of 128;
 //  - S^T = K Q^T (keys x rows), then O^T = V^T P^T. The order of the head's
 //    elements inside a 16-element step of S^T, and of the rows of O^T, is free,
 //    so that a lane's operands are 16 consecutive bytes of one key; V^T wants
@@ -144,15 +145,29 @@ __device__ __forceinline__ void pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
   }
 }
 
+// 16 or 4 bytes global -> shared; `bytes` of them (0: zeros are written).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t* r, const uint8_t* at) {
-  if constexpr (N == 2) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(at));
-    r[0] = u.x; r[1] = u.y;
-  } else {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(at));
-    r[0] = u.x; r[1] = u.y; r[2] = u.z; r[3] = u.w;
-  }
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Where 16-byte piece `c` of row r of a tile is kept (in pieces), so that the
+// lanes of a read fall on different banks: K is read as rows 4 (g/2) + g%2 and
+// pieces 4 i + t, V as rows 4 t + i and pieces (D 64: half pieces) g.
+template <int D>
+__device__ __forceinline__ int k_piece(int r, int c) {
+  return D == 128 ? r * 8 + (c ^ ((r & 1) << 2)) : r * 4 + c;
+}
+template <int D>
+__device__ __forceinline__ int v_piece(int r, int c) {
+  return D == 128 ? r * 8 + (c ^ ((r >> 1) & 6)) : ((r & ~1) | ((r ^ (r >> 2)) & 1)) * 4 + (c ^ ((r >> 2) & 2));
 }
 
 // Power of two 2^e as fp32, e in [-126, 127].
@@ -165,12 +180,16 @@ __device__ __forceinline__ uint32_t pack_out(bool bf16, float a, float b) {
 
 template <int D, int NT>
 struct Shared {
+  static constexpr int STAGES = NT == 1 ? 3 : 4;
+  static constexpr int TILE = 16 * D;                  // K or V codes of a tile
+  static constexpr int STAGE = 2 * TILE + 128;         // both, and 16 + 16 scales
+  static constexpr int RING = WARPS * STAGES * STAGE;
   static constexpr int ROW = D + 4;
-  static constexpr int O = WARPS * 8 * NT * ROW * 4;  // partial outputs of the warps
-  static constexpr int ML = WARPS * 8 * NT * 8;
-  static constexpr int QF = 8 * NT * 4;
-  static constexpr int Q = NT * (D / 16) * 32 * 8;  // query operands, in the lanes' order
-  static constexpr int BYTES = O + ML + QF + Q;
+  static constexpr int O = WARPS * 8 * NT * ROW * 4;   // partial outputs of the warps, in the ring's place
+  static constexpr int OFF_ML = RING > O ? RING : O;
+  static constexpr int OFF_QF = OFF_ML + WARPS * 8 * NT * 8;
+  static constexpr int OFF_Q = OFF_QF + 8 * NT * 4;    // query operands, in the lanes' order
+  static constexpr int BYTES = OFF_Q + NT * (D / 16) * 32 * 8;
 };
 
 // Rows of a call: `rows` in all, in blockIdx.y groups of 8 NT; a slot of the
@@ -185,9 +204,9 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
   using SH = Shared<D, NT>;
   extern __shared__ __align__(16) uint8_t smem[];
   float* const so = reinterpret_cast<float*>(smem);
-  float2* const sml = reinterpret_cast<float2*>(smem + SH::O);
-  float* const sqf = reinterpret_cast<float*>(smem + SH::O + SH::ML);  // the rows' inverse powers of two
-  uint2* const sq = reinterpret_cast<uint2*>(smem + SH::O + SH::ML + SH::QF);
+  float2* const sml = reinterpret_cast<float2*>(smem + SH::OFF_ML);
+  float* const sqf = reinterpret_cast<float*>(smem + SH::OFF_QF);  // the rows' inverse powers of two
+  uint2* const sq = reinterpret_cast<uint2*>(smem + SH::OFF_Q);
 
   const Cache& c = p.c;
   int* const status = c.status;
@@ -200,8 +219,12 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
   const int64_t ntok = static_cast<int64_t>(c.num_pages) * c.page_size;
   const int64_t nscale = static_cast<int64_t>(c.num_pages) * c.Hkv * c.per;
   const int64_t nrows = static_cast<int64_t>(p.num_queries) * p.Hq;
-  const uint8_t* const kb = p.k_codes + h * D + t * 16;
-  const uint8_t* const vb = p.v_codes + h * D + g * (D / 8);
+  constexpr int PIECES = D / 16;             // 16-byte pieces of a key
+  constexpr int RPC = 32 / PIECES;           // keys that one copy of the warp covers
+  const uint8_t* const kb = p.k_codes + h * D + lane % PIECES * 16;
+  const uint8_t* const vb = p.v_codes + h * D + lane % PIECES * 16;
+  uint8_t* const ring = smem + (threadIdx.x >> 5) * SH::STAGES * SH::STAGE;
+  const uint32_t ring_at = smem_u32(ring);
   const bool tiles_in_page = c.page_size % 16 == 0;
   const int dblk = BLOCK_KEYS / c.page_size, drow = BLOCK_KEYS % c.page_size;
 
@@ -328,55 +351,65 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
     const int ka = 4 * (g >> 1) + (g & 1);
     const int last_key = min(most + 1, (b + take) * BLOCK_KEYS);
     int key0 = b * BLOCK_KEYS + warp * 16;
-    int blk = key0 / c.page_size, row0 = key0 - blk * c.page_size;  // of the tile to load next
-    uint32_t kr[2][KB * 4], vr[4][VW];
-    float ks[2], vs[2];
-    int tok[2];  // tokens (page * page_size + row) of the lane's two keys, -1: zeros
-    auto load_k = [&](int key) {
-      int page[2], row[2];
-      page[0] = page[1] = page_of(c, s, blk);
-      row[0] = row0 + ka;
-      row[1] = row[0] + 2;
-      if (!tiles_in_page) {
+    // The tile to copy next; lane l has its key l % 16. The page is looked up
+    // one tile ahead of the copy.
+    int ckey = key0, blk = key0 / c.page_size, row0 = key0 - blk * c.page_size;
+    const int kl = lane & 15;
+    auto find_page = [&]() {
+      if (ckey + kl >= L) return -1;
+      return page_of(c, s, tiles_in_page ? blk : blk + (row0 + kl) / c.page_size);
+    };
+    int page = find_page();
+    auto copy_tile = [&](int stage) {
+      if (ckey < last_key) {
+        int row = row0 + kl;
+        if (!tiles_in_page) row %= c.page_size;
+        const int tok = page * c.page_size + row;
+        const bool ok = page >= 0 && in_bounds(status, tok, ntok);
+        const int mine = ok ? tok : 0;  // zeros by their scale
+        const int gi = c.group == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.group_magic));
+        const int64_t si = ok ? (static_cast<int64_t>(page) * c.Hkv + h) * c.per + gi : 0;
+        const bool sok = ok && in_bounds(status, si, nscale);
+        const uint32_t at = ring_at + stage * SH::STAGE;
+        copy4(at + 2 * SH::TILE + lane * 4, (lane < 16 ? p.k_scale : p.v_scale) + (sok ? si : 0), sok ? 4 : 0);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int more = row[e] / c.page_size;
-          row[e] -= more * c.page_size;
-          page[e] = key + ka + 2 * e < L ? page_of(c, s, blk + more) : -1;
+        for (int j = 0; j < 16 / RPC; ++j) {
+          const int r = RPC * j + lane / PIECES;
+          const int64_t off = __shfl_sync(0xffffffffu, mine, r) * step;
+          copy16(at + k_piece<D>(r, lane % PIECES) * 16, kb + off);
+          copy16(at + SH::TILE + v_piece<D>(r, lane % PIECES) * 16, vb + off);
         }
       }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        tok[e] = page[e] * c.page_size + row[e];
-        const bool ok = page[e] >= 0 && key + ka + 2 * e < L && in_bounds(status, tok[e], ntok);
-        tok[e] = ok ? tok[e] : -1;
-        const uint8_t* at = kb + max(tok[e], 0) * step;
-#pragma unroll
-        for (int i = 0; i < KB; ++i) load_words<4>(&kr[e][4 * i], at + 64 * i);
-        ks[e] = vs[e] = 0.f;
-        if (ok) {
-          const int gi = c.group == 1 ? row[e] : static_cast<int>(__umulhi(static_cast<uint32_t>(row[e]), p.group_magic));
-          const int64_t si = (static_cast<int64_t>(page[e]) * c.Hkv + h) * c.per + gi;
-          if (in_bounds(status, si, nscale)) {
-            ks[e] = __ldg(p.k_scale + si);
-            vs[e] = __ldg(p.v_scale + si);
-          }
-        }
+      copy_commit();
+      ckey += BLOCK_KEYS;
+      blk += dblk;
+      row0 += drow;
+      if (row0 >= c.page_size) {
+        row0 -= c.page_size;
+        ++blk;
       }
+      page = find_page();
     };
-    auto load_v = [&]() {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int x = __shfl_sync(0xffffffffu, tok[i >> 1], (2 * t + (i & 1)) * 4);
-        load_words<VW>(vr[i], vb + max(x, 0) * step);
-      }
-    };
-    if (key0 < last_key) {
-      load_k(key0);
-      load_v();
-    }
+    for (int i = 0; i < SH::STAGES - 1; ++i) copy_tile(i);
+    int stage = 0;
     for (; key0 < last_key; key0 += BLOCK_KEYS) {
-      const bool more = key0 + BLOCK_KEYS < last_key;
+      copy_wait<SH::STAGES - 2>();
+      __syncwarp();  // the tile's copies of every lane; and every lane is done with the tile before
+      copy_tile(stage == 0 ? SH::STAGES - 1 : stage - 1);
+      const uint8_t* const at = ring + stage * SH::STAGE;
+      stage = stage == SH::STAGES - 1 ? 0 : stage + 1;
+      const float* const scales = reinterpret_cast<const float*>(at + 2 * SH::TILE);
+      uint32_t kr[2][KB * 4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < KB; ++i) {
+          const uint4 x = reinterpret_cast<const uint4*>(at)[k_piece<D>(ka + 2 * e, 4 * i + t)];
+          kr[e][4 * i] = x.x; kr[e][4 * i + 1] = x.y; kr[e][4 * i + 2] = x.z; kr[e][4 * i + 3] = x.w;
+        }
+      const float k0 = scales[ka] * p.scale_log2, k1 = scales[ka + 2] * p.scale_log2;
+      const float v0 = scales[16 + ka], v1 = scales[16 + ka + 2];
       float sc[NT][4];
 #pragma unroll
       for (int i = 0; i < NT; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
@@ -395,15 +428,6 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
           }
         }
       }
-      const float k0 = ks[0] * p.scale_log2, k1 = ks[1] * p.scale_log2, v0 = vs[0], v1 = vs[1];
-      blk += dblk;
-      row0 += drow;
-      if (row0 >= c.page_size) {
-        row0 -= c.page_size;
-        ++blk;
-      }
-      if (more) load_k(key0 + BLOCK_KEYS);
-
       // keys key0 + ka (elements 0, 1: the lane's rows) and + 2 (elements 2, 3)
       const bool masked = key0 + 15 > least;
       float z[NT][4], d[NT][2];  // P', and the tile's part of the sum
@@ -469,6 +493,18 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
         pf[i][0] = transpose8x8(pack2<false>(z[i][0], z[i][1]));
         pf[i][1] = transpose8x8(pack2<false>(z[i][2], z[i][3]));
       }
+      uint32_t vr[4][VW];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* const va = at + SH::TILE;
+        if constexpr (D == 128) {
+          const uint4 x = reinterpret_cast<const uint4*>(va)[v_piece<D>(4 * t + i, g)];
+          vr[i][0] = x.x; vr[i][1] = x.y; vr[i][2] = x.z; vr[i][3] = x.w;
+        } else {
+          const uint2 x = reinterpret_cast<const uint2*>(va)[v_piece<D>(4 * t + i, g >> 1) * 2 + (g & 1)];
+          vr[i][0] = x.x; vr[i][1] = x.y;
+        }
+      }
 #pragma unroll
       for (int w = 0; w < VW; ++w) {
         // keys 0, 1 and 2, 3 of the lane interleaved: two steps' operands
@@ -483,8 +519,9 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
           for (int i = 0; i < NT; ++i)
             mma16816(acc[2 * w + k][i], a[k][0], a[k][1], a[k][2], a[k][3], pf[i][0], pf[i][1]);
       }
-      if (more) load_v();
     }
+    copy_wait<0>();
+    __syncthreads();  // the ring's place takes the warps' parts
 
     // ------------------------------------------------ the warps' parts
 #pragma unroll
