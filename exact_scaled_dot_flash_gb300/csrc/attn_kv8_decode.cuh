@@ -6,7 +6,7 @@
 // the copy bandwidth an SM is fed 21 bytes a cycle, and each byte has to become
 // a 16-bit operand, so what the kernel economises is instructions and
 // shared-memory traffic per byte:
-//  - a warp streams its own 16-key tiles through a ring of cp.async copies in
+//  - a warp streams its own 32-key tiles through two buffers of cp.async copies in
 //    shared memory (no barrier between warps), reads each code once into
 //    registers, converts it there and feeds it to mma.sync as the A operand: 2
 //    bytes of shared-memory traffic for a byte of cache (a 16-bit tcgen05 operand
@@ -25,13 +25,13 @@
 //    placing the byte, offset by 128, under the exponent of 1024 and
 //    subtracting; e4m3 by the conversion instruction;
 //  - k_scale enters the score in fp32, v_scale the probability before it is
-//    rounded: P' = p v_scale r, r a factor for the row that keeps the
-//    largest p v_scale so far near 1, so that what F16 loses below 2^-14 is
-//    small beside the largest term of the sum and not beside the largest scale;
-//  - the running maximum moves only when a score exceeds it by 2^8 (one vote a
-//    tile instead of a reduction).
+//    rounded. A row has one reference exponent for both: with y = 2^(x - ref),
+//    l = sum y and P' = y v_scale, and ref moves up when a P' passes 2^8 (one vote
+//    a tile instead of a reduction), to bring the largest p v_scale so far near 1.
+//    What F16 loses below 2^-14 is then small beside the largest term of the sum,
+//    whatever the scales of other keys.
 //
-// Work: the keys of all sequences, in blocks of 128 (16 a warp), are cut into
+// Work: the keys of all sequences, in blocks of 128 (32 a warp), are cut into
 // equal ranges, one for each group of Hkv CTAs (one CTA a head, side by side,
 // since their codes lie side by side). A CTA walks the sequences of its range;
 // a sequence wholly inside it is written out, a cut one as a partial (m, l, O)
@@ -45,11 +45,13 @@ namespace attn {
 namespace kv8 {
 namespace dec {
 
-constexpr int WARPS = 8;
+constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
-constexpr int BLOCK_KEYS = 16 * WARPS;
+constexpr int TILE_KEYS = 32;
+constexpr int BLOCK_KEYS = TILE_KEYS * WARPS;
 constexpr float LN2 = 0.6931471805599453f;
-constexpr float RESCALE_LOG2 = 8.0f;
+constexpr float Y_RANGE = 80.f;     // y <= 2^80: below it a row of tiny value scales still fills F16
+constexpr float UNSEEN = -1e30f;    // reference of a row without keys: its first one passes every range
 
 __device__ __forceinline__ int blocks_of(int nq, int L) {
   return nq > 0 ? max(1, (L + BLOCK_KEYS - 1) / BLOCK_KEYS) : 0;  // without keys: one, for the NaN rows
@@ -180,9 +182,9 @@ __device__ __forceinline__ uint32_t pack_out(bool bf16, float a, float b) {
 
 template <int D, int NT>
 struct Shared {
-  static constexpr int STAGES = NT == 1 ? 3 : 4;
-  static constexpr int TILE = 16 * D;                  // K or V codes of a tile
-  static constexpr int STAGE = 2 * TILE + 128;         // both, and 16 + 16 scales
+  static constexpr int STAGES = 2;
+  static constexpr int TILE = TILE_KEYS * D;           // K or V codes of a tile
+  static constexpr int STAGE = 2 * TILE + 8 * TILE_KEYS;  // both, and their scales
   static constexpr int RING = WARPS * STAGES * STAGE;
   static constexpr int ROW = D + 4;
   static constexpr int O = WARPS * 8 * NT * ROW * 4;   // partial outputs of the warps, in the ring's place
@@ -195,7 +197,7 @@ struct Shared {
 // Rows of a call: `rows` in all, in blockIdx.y groups of 8 NT; a slot of the
 // workspace holds all groups (slot_rows).
 template <int D, int FMT, int NT>
-__global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
     decode_kernel(const __grid_constant__ FwdParams p, int ranges, int slot_rows, int64_t ml_offset) {
   constexpr int KS = D / 16;    // 16-element steps of a head
   constexpr int KB = D / 64;    // 64-byte pieces of a key
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
   const int row_lo = blockIdx.y * ROWS;
   const int heads = p.Hq / c.Hkv;
   const bool bf16 = p.bf16;
-  const int64_t step = static_cast<int64_t>(c.Hkv) * D;  // bytes from token to token
+  const uint32_t step = static_cast<uint32_t>(c.Hkv) * D;  // bytes from token to token
   const int64_t ntok = static_cast<int64_t>(c.num_pages) * c.page_size;
   const int64_t nscale = static_cast<int64_t>(c.num_pages) * c.Hkv * c.per;
   const int64_t nrows = static_cast<int64_t>(p.num_queries) * p.Hq;
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
   const uint8_t* const vb = p.v_codes + h * D + lane % PIECES * 16;
   uint8_t* const ring = smem + (threadIdx.x >> 5) * SH::STAGES * SH::STAGE;
   const uint32_t ring_at = smem_u32(ring);
-  const bool tiles_in_page = c.page_size % 16 == 0;
+  const bool tiles_in_page = c.page_size % TILE_KEYS == 0;
   const int dblk = BLOCK_KEYS / c.page_size, drow = BLOCK_KEYS % c.page_size;
 
   int64_t u0, u1;
@@ -336,46 +338,45 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
     }
 
     // ------------------------------------------------ keys
-    // Of a row: m the running maximum (log2 units), l the lane's part of the sum
-    // of p = 2^(x - m), acc the sum of P' = p v_scale r times the codes.
-    float m[NT][2], l[NT][2], r[NT][2], acc[KS][NT][4];
+    // Of a row: y = 2^(x - ref) for a score x (log2 units), l the lane's part of
+    // the sum of y, acc the sum of P' = y v_scale times the codes.
+    float ref[NT][2], l[NT][2], acc[KS][NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      m[i][0] = m[i][1] = -INFINITY;
+      ref[i][0] = ref[i][1] = UNSEEN;
       l[i][0] = l[i][1] = 0.f;
-      r[i][0] = r[i][1] = 1.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k) acc[k][i][0] = acc[k][i][1] = acc[k][i][2] = acc[k][i][3] = 0.f;
     }
-    // Lane (g, t): keys ka and ka + 2 of a tile in S^T; keys 4 t .. 4 t + 3 in V^T
+    // Lane (g, t): keys ka and ka + 2 of each 16 of a tile in S^T, 4 t .. 4 t + 3 in V^T
     const int ka = 4 * (g >> 1) + (g & 1);
     const int last_key = min(most + 1, (b + take) * BLOCK_KEYS);
-    int key0 = b * BLOCK_KEYS + warp * 16;
-    // The tile to copy next; lane l has its key l % 16. The page is looked up
+    int key0 = b * BLOCK_KEYS + warp * TILE_KEYS;
+    // The tile to copy next; a lane has one of its keys. The page is looked up
     // one tile ahead of the copy.
     int ckey = key0, blk = key0 / c.page_size, row0 = key0 - blk * c.page_size;
-    const int kl = lane & 15;
     auto find_page = [&]() {
-      if (ckey + kl >= L) return -1;
-      return page_of(c, s, tiles_in_page ? blk : blk + (row0 + kl) / c.page_size);
+      if (ckey + lane >= L) return -1;
+      return page_of(c, s, tiles_in_page ? blk : blk + (row0 + lane) / c.page_size);
     };
     int page = find_page();
     auto copy_tile = [&](int stage) {
       if (ckey < last_key) {
-        int row = row0 + kl;
+        int row = row0 + lane;
         if (!tiles_in_page) row %= c.page_size;
         const int tok = page * c.page_size + row;
         const bool ok = page >= 0 && in_bounds(status, tok, ntok);
         const int mine = ok ? tok : 0;  // zeros by their scale
         const int gi = c.group == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.group_magic));
         const int64_t si = ok ? (static_cast<int64_t>(page) * c.Hkv + h) * c.per + gi : 0;
-        const bool sok = ok && in_bounds(status, si, nscale);
+        const int bytes = ok && in_bounds(status, si, nscale) ? 4 : 0;
         const uint32_t at = ring_at + stage * SH::STAGE;
-        copy4(at + 2 * SH::TILE + lane * 4, (lane < 16 ? p.k_scale : p.v_scale) + (sok ? si : 0), sok ? 4 : 0);
+        copy4(at + 2 * SH::TILE + lane * 4, p.k_scale + (bytes ? si : 0), bytes);
+        copy4(at + 2 * SH::TILE + 4 * TILE_KEYS + lane * 4, p.v_scale + (bytes ? si : 0), bytes);
 #pragma unroll
-        for (int j = 0; j < 16 / RPC; ++j) {
+        for (int j = 0; j < TILE_KEYS / RPC; ++j) {
           const int r = RPC * j + lane / PIECES;
-          const int64_t off = __shfl_sync(0xffffffffu, mine, r) * step;
+          const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, mine, r))) * step;
           copy16(at + k_piece<D>(r, lane % PIECES) * 16, kb + off);
           copy16(at + SH::TILE + v_piece<D>(r, lane % PIECES) * 16, vb + off);
         }
@@ -400,124 +401,156 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
       const uint8_t* const at = ring + stage * SH::STAGE;
       stage = stage == SH::STAGES - 1 ? 0 : stage + 1;
       const float* const scales = reinterpret_cast<const float*>(at + 2 * SH::TILE);
-      uint32_t kr[2][KB * 4];
+      float sc[2][NT][4], vs[2][2];
+      const bool masked = key0 + TILE_KEYS - 1 > least;
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int u = 0; u < 2; ++u) {  // 16 keys
+        uint32_t kr[2][KB * 4];
 #pragma unroll
-        for (int i = 0; i < KB; ++i) {
-          const uint4 x = reinterpret_cast<const uint4*>(at)[k_piece<D>(ka + 2 * e, 4 * i + t)];
-          kr[e][4 * i] = x.x; kr[e][4 * i + 1] = x.y; kr[e][4 * i + 2] = x.z; kr[e][4 * i + 3] = x.w;
-        }
-      const float k0 = scales[ka] * p.scale_log2, k1 = scales[ka + 2] * p.scale_log2;
-      const float v0 = scales[16 + ka], v1 = scales[16 + ka + 2];
-      float sc[NT][4];
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+          for (int i = 0; i < KB; ++i) {
+            const uint4 x = reinterpret_cast<const uint4*>(at)[k_piece<D>(16 * u + ka + 2 * e, 4 * i + t)];
+            kr[e][4 * i] = x.x; kr[e][4 * i + 1] = x.y; kr[e][4 * i + 2] = x.z; kr[e][4 * i + 3] = x.w;
+          }
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        uint32_t a0, a1, a2, a3;
-        pairs<FMT>(kr[0][k], a0, a2);
-        pairs<FMT>(kr[1][k], a1, a3);
+        for (int i = 0; i < NT; ++i) sc[u][i][0] = sc[u][i][1] = sc[u][i][2] = sc[u][i][3] = 0.f;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          if constexpr (NT == 1) {
-            mma16816(sc[i], a0, a1, a2, a3, qf[k][0], qf[k][1]);
-          } else {
-            const uint2 w = sq[(i * KS + k) * 32 + lane];
-            mma16816(sc[i], a0, a1, a2, a3, w.x, w.y);
+        for (int k = 0; k < KS; ++k) {
+          uint32_t a0, a1, a2, a3;
+          pairs<FMT>(kr[0][k], a0, a2);
+          pairs<FMT>(kr[1][k], a1, a3);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            if constexpr (NT == 1) {
+              mma16816(sc[u][i], a0, a1, a2, a3, qf[k][0], qf[k][1]);
+            } else {
+              const uint2 w = sq[(i * KS + k) * 32 + lane];
+              mma16816(sc[u][i], a0, a1, a2, a3, w.x, w.y);
+            }
           }
         }
-      }
-      // keys key0 + ka (elements 0, 1: the lane's rows) and + 2 (elements 2, 3)
-      const bool masked = key0 + 15 > least;
-      float z[NT][4], d[NT][2];  // P', and the tile's part of the sum
-      bool grow = false;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        d[i][0] = d[i][1] = 0.f;
+        for (int e = 0; e < 2; ++e) {
+          const float f = scales[16 * u + ka + 2 * e] * p.scale_log2;
+          vs[u][e] = scales[TILE_KEYS + 16 * u + ka + 2 * e];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = sc[i][e] * (e < 2 ? k0 : k1) * back[i][e & 1];
-          if (masked && key0 + ka + (e & 2) > lim[i][e & 1]) x = -INFINITY;
-          sc[i][e] = x;
-          const float y = fast_exp2(x - (m[i][e & 1] == -INFINITY ? 0.f : m[i][e & 1]));
-          d[i][e & 1] += y;
-          z[i][e] = y * (e < 2 ? v0 : v1) * r[i][e & 1];
-          grow = grow || x > m[i][e & 1] + RESCALE_LOG2 || z[i][e] > 256.f;
+          for (int i = 0; i < NT; ++i) {
+            sc[u][i][2 * e] *= f;
+            sc[u][i][2 * e + 1] *= f;
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key0 + 16 * u + ka + (e & 2) > lim[i][e & 1]) sc[u][i][e] = -INFINITY;
         }
       }
-      if (__any_sync(0xffffffffu, grow)) {
+      // y and P' against the rows' references
+      float z[2][NT][4], d[NT][2];
+      auto against = [&](int i) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+        for (int e = 0; e < 2; ++e) d[i][e] = 0.f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = fast_exp2(fmaf(sc[u][i][e], back[i][e & 1], -ref[i][e & 1]));
+            d[i][e & 1] += y;
+            z[u][i][e] = y * vs[u][e >> 1];
+          }
+      };
+      float big = 0.f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        against(i);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          big = fmax3(big, z[u][i][0], z[u][i][1]);
+          big = fmax3(big, z[u][i][2], z[u][i][3]);
+        }
+        // y itself past 2^88: value scales so small that P' does not show it
+        constexpr float DOWN = 8.271806125530277e-25f;  // 2^-80
+        big = fmax3(big, d[i][0] * DOWN, d[i][1] * DOWN);
+      }
+      if (__any_sync(0xffffffffu, big > 256.f)) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = fmaxf(sc[i][e], sc[i][2 + e]);
+            float x = fmaxf(fmaxf(sc[0][i][e], sc[0][i][2 + e]), fmaxf(sc[1][i][e], sc[1][i][2 + e]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-            const float n = fmaxf(m[i][e], x);
-            const float sub = n == -INFINITY ? 0.f : n;
-            const float alpha = n == -INFINITY ? 1.f : fast_exp2(m[i][e] - n);
-            // the largest p v_scale of the tile, and the r that brings it to (1/2, 1];
-            // r may grow with m, as the old terms shrink, but not past what they allow
-            const float y0 = fast_exp2(sc[i][e] - sub), y1 = fast_exp2(sc[i][2 + e] - sub);
-            float w = fmaxf(y0 * v0, y1 * v1);
+            const bool none = x == -INFINITY;
+            x = none ? 0.f : x * back[i][e];
+            float w = 0.f;  // the largest p v_scale of the tile, p relative to x
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int a = 0; a < 2; ++a)
+                w = fmaxf(w, fast_exp2(fmaf(sc[u][i][2 * a + e], back[i][e], -x)) * vs[u][a]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
-            const float same = fminf(r[i][e] / alpha, 1.2676506e30f);  // 2^100; keeps the accumulator's scale
-            const int ex = static_cast<int>(__float_as_uint(w) >> 23) - 127 + 1;  // w < 2^ex
-            const float want = pow2(min(max(-ex, -126), 100));
-            const float rn = w * same > 1.f ? want : same;
-            const float f = fminf(rn / r[i][e], 3e38f) * alpha;
-            m[i][e] = n;
-            r[i][e] = rn;
-            l[i][e] *= alpha;
+            // w < 2^ex
+            const int ex = static_cast<int>(__float_as_uint(w) >> 23) - 126;
+            const float n = none ? ref[i][e] : fmaxf(ref[i][e], x + fmaxf(static_cast<float>(ex), -Y_RANGE));
+            const float f = fast_exp2(ref[i][e] - n);
+            ref[i][e] = n;
+            l[i][e] *= f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
               acc[k][i][e] *= f;
               acc[k][i][2 + e] *= f;
             }
-            d[i][e] = y0 + y1;
-            z[i][e] = y0 * v0 * rn;
-            z[i][2 + e] = y1 * v1 * rn;
           }
+          against(i);
+        }
       }
-      uint32_t pf[NT][2];
+      uint32_t pf[2][NT][2];
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         l[i][0] += d[i][0];
         l[i][1] += d[i][1];
-        if (masked) {  // a masked key may have any scale
 #pragma unroll
-          for (int e = 0; e < 4; ++e) z[i][e] = sc[i][e] == -INFINITY ? 0.f : z[i][e];
+        for (int u = 0; u < 2; ++u) {
+          if (masked) {  // a masked key may have any scale
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[u][i][e] = sc[u][i][e] == -INFINITY ? 0.f : z[u][i][e];
+          }
+          pf[u][i][0] = transpose8x8(pack2<false>(z[u][i][0], z[u][i][1]));
+          pf[u][i][1] = transpose8x8(pack2<false>(z[u][i][2], z[u][i][3]));
         }
-        pf[i][0] = transpose8x8(pack2<false>(z[i][0], z[i][1]));
-        pf[i][1] = transpose8x8(pack2<false>(z[i][2], z[i][3]));
       }
-      uint32_t vr[4][VW];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int u = 0; u < 2; ++u) {
+        uint32_t vr[4][VW];
         const uint8_t* const va = at + SH::TILE;
-        if constexpr (D == 128) {
-          const uint4 x = reinterpret_cast<const uint4*>(va)[v_piece<D>(4 * t + i, g)];
-          vr[i][0] = x.x; vr[i][1] = x.y; vr[i][2] = x.z; vr[i][3] = x.w;
-        } else {
-          const uint2 x = reinterpret_cast<const uint2*>(va)[v_piece<D>(4 * t + i, g >> 1) * 2 + (g & 1)];
-          vr[i][0] = x.x; vr[i][1] = x.y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (D == 128) {
+            const uint4 x = reinterpret_cast<const uint4*>(va)[v_piece<D>(16 * u + 4 * t + i, g)];
+            vr[i][0] = x.x; vr[i][1] = x.y; vr[i][2] = x.z; vr[i][3] = x.w;
+          } else {
+            const uint2 x = reinterpret_cast<const uint2*>(va)[v_piece<D>(16 * u + 4 * t + i, g >> 1) * 2 + (g & 1)];
+            vr[i][0] = x.x; vr[i][1] = x.y;
+          }
         }
-      }
 #pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        // keys 0, 1 and 2, 3 of the lane interleaved: two steps' operands
-        uint32_t a[2][4];
-        pairs<FMT>(__byte_perm(vr[0][w], vr[1][w], 0x5140), a[0][0], a[0][1]);
-        pairs<FMT>(__byte_perm(vr[2][w], vr[3][w], 0x5140), a[0][2], a[0][3]);
-        pairs<FMT>(__byte_perm(vr[0][w], vr[1][w], 0x7362), a[1][0], a[1][1]);
-        pairs<FMT>(__byte_perm(vr[2][w], vr[3][w], 0x7362), a[1][2], a[1][3]);
+        for (int w = 0; w < VW; ++w) {
+          // keys 0, 1 and 2, 3 of the lane interleaved: two steps' operands
+          uint32_t a[2][4];
+          pairs<FMT>(__byte_perm(vr[0][w], vr[1][w], 0x5140), a[0][0], a[0][1]);
+          pairs<FMT>(__byte_perm(vr[2][w], vr[3][w], 0x5140), a[0][2], a[0][3]);
+          pairs<FMT>(__byte_perm(vr[0][w], vr[1][w], 0x7362), a[1][0], a[1][1]);
+          pairs<FMT>(__byte_perm(vr[2][w], vr[3][w], 0x7362), a[1][2], a[1][3]);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
-            mma16816(acc[2 * w + k][i], a[k][0], a[k][1], a[k][2], a[k][3], pf[i][0], pf[i][1]);
+            for (int i = 0; i < NT; ++i)
+              mma16816(acc[2 * w + k][i], a[k][0], a[k][1], a[k][2], a[k][3], pf[u][i][0], pf[u][i][1]);
+        }
       }
     }
     copy_wait<0>();
@@ -531,12 +564,11 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], o);
         const int row = 8 * i + 2 * t + e;
-        if (g == 0) sml[warp * ROWS + row] = make_float2(m[i][e], l[i][e]);
+        // a warp without keys has no reference
+        if (g == 0) sml[warp * ROWS + row] = make_float2(l[i][e] == 0.f ? -INFINITY : ref[i][e], l[i][e]);
         float* const o = so + (warp * ROWS + row) * SH::ROW + g * (D / 8);
-        const float f = 1.f / r[i][e];
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-          *reinterpret_cast<float2*>(o + 2 * k) = make_float2(acc[k][i][e] * f, acc[k][i][2 + e] * f);
+        for (int k = 0; k < KS; ++k) *reinterpret_cast<float2*>(o + 2 * k) = make_float2(acc[k][i][e], acc[k][i][2 + e]);
       }
     __syncthreads();
     const int64_t slot = 2ll * blockIdx.x + (first ? 0 : 1);

@@ -38,8 +38,8 @@ struct DecodePlan {
 constexpr int DECODE_ROWS = 64;
 
 // Ranges that the keys of a call are cut into, each for Hkv CTAs (and row
-// groups): as many CTAs as the 152 SMs hold at once, two each of the kernel for
-// 8 rows and one of the others; with many heads four waves of smaller ones, so
+// groups): as many CTAs as the 152 SMs hold at once, three each of the kernels for
+// 8 and 16 rows and two of the others; with many heads four waves of smaller ones, so
 // that a last wave that is not full costs little; never more ranges than there
 // can be blocks of 128 keys.
 inline DecodePlan decode_plan(int num_seqs, int Hkv, int heads, int max_queries, int max_pages, int page_size) {
@@ -50,7 +50,7 @@ inline DecodePlan decode_plan(int num_seqs, int Hkv, int heads, int max_queries,
   const int64_t keys = static_cast<int64_t>(max_pages) * page_size;
   const int64_t blocks = num_seqs * (keys > 128 ? (keys + 127) / 128 : 1);
   const int64_t side = static_cast<int64_t>(Hkv) * d.row_groups;
-  int64_t r = (side > 16 ? 4 : 1) * (d.nt == 1 ? 304 : 152) / side;
+  int64_t r = (side > 16 ? 4 : 1) * 152 * (d.nt <= 2 ? 3 : 2) / side;
   if (r > blocks) r = blocks;
   d.ranges = static_cast<int>(r > 1 ? r : 1);
   return d;
