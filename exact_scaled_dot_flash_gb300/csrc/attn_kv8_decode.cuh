@@ -32,8 +32,8 @@
 //    whatever the scales of other keys.
 //
 // Work: the keys of all sequences, in blocks of 128 (32 a warp), are cut into
-// equal ranges, one for each group of Hkv CTAs (one CTA a head, side by side,
-// since their codes lie side by side). A CTA walks the sequences of its range;
+// ranges, one for each group of Hkv CTAs (one CTA a head, side by side, since
+// their codes lie side by side). A CTA walks the sequences of its range;
 // a sequence wholly inside it is written out, a cut one as a partial (m, l, O)
 // that merge_kernel combines in order. Uneven lengths cost nothing and there
 // are no atomics.
@@ -63,21 +63,31 @@ __device__ __forceinline__ int blocks_of(const FwdParams& p, int s) {
   return blocks_of(hi - lo, seq_len(p.c, s));
 }
 
-// Where block u lies: sequence, block inside it; and the number of all blocks.
+// First block of range r (see DecodePlan): the first `large` ranges are LARGE
+// times the length of the others.
+__device__ __forceinline__ int64_t cut(int64_t total, int r, int ranges, int large) {
+  const int64_t at = r <= large ? static_cast<int64_t>(r) * DecodePlan::LARGE
+                                : static_cast<int64_t>(large) * DecodePlan::LARGE + (r - large);
+  const int64_t all = static_cast<int64_t>(large) * DecodePlan::LARGE + (ranges - large);
+  return total * at / all;
+}
+
+// Blocks of all sequences; the sequence s that the first or the last block of a
+// range lies in, and that sequence's first block.
 struct Place {
-  int64_t total;
-  int64_t at;  // first block of sequence s
+  int64_t total, at;
   int s;
 };
 
-// The whole CTA (THREADS threads) calls it. `range` of `ranges`; the first or
-// the last block of the range is located.
-__device__ __forceinline__ Place locate(const FwdParams& p, int range, int ranges, bool last, int64_t& u0, int64_t& u1) {
-  __shared__ int64_t warp_sum[WARPS];
+// The whole CTA (N threads) calls it.
+template <int N>
+__device__ __forceinline__ Place locate(const FwdParams& p, int range, int ranges, int large, bool last, int64_t& u0,
+                                        int64_t& u1) {
+  __shared__ int64_t warp_sum[N / 32];
   __shared__ int64_t found_at;
   __shared__ int found_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.c.num_seqs + THREADS - 1) / THREADS;
+  const int per = (p.c.num_seqs + N - 1) / N;
   const int s0 = min(tid * per, p.c.num_seqs), s1 = min(s0 + per, p.c.num_seqs);
   int64_t mine = 0;
   for (int s = s0; s < s1; ++s) mine += blocks_of(p, s);
@@ -95,12 +105,12 @@ __device__ __forceinline__ Place locate(const FwdParams& p, int range, int range
   __syncthreads();
   int64_t before = incl - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
+  for (int w = 0; w < N / 32; ++w) {
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
-  u0 = total * range / ranges;
-  u1 = total * (range + 1) / ranges;
+  u0 = cut(total, range, ranges, large);
+  u1 = cut(total, range + 1, ranges, large);
   const int64_t u = last ? u1 - 1 : u0;
   if (u >= before && u < before + mine) {
     int s = s0;
@@ -198,7 +208,7 @@ struct Shared {
 // workspace holds all groups (slot_rows).
 template <int D, int FMT, int NT>
 __global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
-    decode_kernel(const __grid_constant__ FwdParams p, int ranges, int slot_rows, int64_t ml_offset) {
+    decode_kernel(const __grid_constant__ FwdParams p, int ranges, int large, int slot_rows, int64_t ml_offset) {
   constexpr int KS = D / 16;    // 16-element steps of a head
   constexpr int KB = D / 64;    // 64-byte pieces of a key
   constexpr int VW = D / 32;    // words of V a lane holds of one key
@@ -231,7 +241,8 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
   const int dblk = BLOCK_KEYS / c.page_size, drow = BLOCK_KEYS % c.page_size;
 
   int64_t u0, u1;
-  const Place pl = locate(p, range, ranges, false, u0, u1);
+  const Place pl = locate<THREADS>(p, range, ranges, large, false, u0, u1);
+  asm volatile("griddepcontrol.launch_dependents;");  // merge_kernel may come up; it waits for this grid's end
   int s = pl.s;
   int b = static_cast<int>(u0 - pl.at);
   for (int64_t u = u0; u < u1; ++s, b = 0) {
@@ -609,65 +620,90 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
   }
 }
 
-// A CTA (range, head; blockIdx.y: row) combines the parts of the sequence that
-// begins in the range and goes on past it: its own last slot, then the first
-// slot of the ranges after it.
+// A CTA (range, head) combines the parts of the sequence that begins in the
+// range and goes on past it: its own last slot, then the first slot of the
+// ranges after it. D / 4 threads take a row; with few rows several such teams
+// share a row's parts, and their sums are added in order. Launched while the
+// decode kernel still runs; everything up to the wait needs nothing of it.
+constexpr int MERGE_THREADS = 256;
+
 template <int D>
-__global__ void __launch_bounds__(THREADS) merge_kernel(const __grid_constant__ FwdParams p, int ranges, int slot_rows,
-                                                        int64_t ml_offset) {
-  constexpr int G = D / 4;
-  __shared__ float4 so[WARPS * 32 / G][G];
-  __shared__ float2 sml[WARPS * 32 / G];
+__global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const __grid_constant__ FwdParams p, int ranges, int large,
+                                                              int slot_rows, int64_t ml_offset) {
+  constexpr int G = D / 4, TEAMS = MERGE_THREADS / G;
+  __shared__ float4 so[TEAMS][G];
+  __shared__ float2 sml[TEAMS];
   const Cache& c = p.c;
-  const int h = blockIdx.x % c.Hkv, range = blockIdx.x / c.Hkv, row = blockIdx.y;
+  const int h = blockIdx.x % c.Hkv, range = blockIdx.x / c.Hkv;
   int64_t u0, u1;
-  const Place pl = locate(p, range, ranges, true, u0, u1);
+  const Place pl = locate<MERGE_THREADS>(p, range, ranges, large, true, u0, u1);
   if (u1 <= u0 || pl.at < u0) return;  // CTA-uniform, as every return below
   int q_lo, q_hi;
   row_range(p.q_offsets, pl.s, p.num_queries, q_lo, q_hi);
   const int heads = p.Hq / c.Hkv;
   const int64_t end = pl.at + blocks_of(q_hi - q_lo, seq_len(c, pl.s));
-  if (end <= u1 || row >= static_cast<int64_t>(q_hi - q_lo) * heads) return;
-  int last = range;  // the range that holds the sequence's last block
-  while (pl.total * (last + 1) / ranges < end) ++last;
+  if (end <= u1) return;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(q_hi - q_lo) * heads, static_cast<int64_t>(slot_rows)));
+  int last = range, hi = ranges - 1;  // the range that holds block end - 1: the least with cut(last + 1) >= end
+  while (last < hi) {
+    const int mid = (last + hi) >> 1;
+    if (cut(pl.total, mid + 1, ranges, large) >= end) hi = mid;
+    else last = mid + 1;
+  }
+  const bool gaps = pl.total < (static_cast<int64_t>(large) * DecodePlan::LARGE + ranges - large);  // some ranges are empty
   const float4* const wo = static_cast<const float4*>(p.ws);
   const float2* const wml = reinterpret_cast<const float2*>(static_cast<const uint8_t*>(p.ws) + ml_offset);
-  const int g = threadIdx.x % G, part0 = threadIdx.x / G, parts = THREADS / G;
-  float M = -INFINITY, sum = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int r = range + part0; r <= last; r += parts) {
-    const int64_t a = pl.total * r / ranges, b = pl.total * (r + 1) / ranges;
-    if (a == b) continue;
-    const int64_t at = (2ll * (static_cast<int64_t>(r) * c.Hkv + h) + (r == range && pl.at > u0 ? 1 : 0)) * slot_rows + row;
-    if (!in_bounds(c.status, at, 2ll * ranges * c.Hkv * slot_rows)) continue;
-    const float2 ml = wml[at];
-    const float4 x = wo[at * G + g];
-    const float n = fmaxf(M, ml.x);
-    const float f = n == -INFINITY ? 0.f : fast_exp2(M - n), e = n == -INFINITY ? 0.f : fast_exp2(ml.x - n);
-    M = n;
-    sum = sum * f + ml.y * e;
-    o = make_float4(o.x * f + x.x * e, o.y * f + x.y * e, o.z * f + x.z * e, o.w * f + x.w * e);
+  const int g = threadIdx.x % G, team = threadIdx.x / G;
+  const int share = rows >= TEAMS ? 1 : TEAMS / rows;  // teams of a row
+  const int at_once = TEAMS / share;                   // rows side by side
+  const int64_t nslot = 2ll * ranges * c.Hkv * slot_rows, nrows = static_cast<int64_t>(p.num_queries) * p.Hq;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int row0 = 0; row0 < rows; row0 += at_once) {
+    const int row = row0 + team / share, part0 = team % share;
+    float M = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float2 ml, float4 x) {
+      const float n = fmaxf(M, ml.x);
+      const float f = n == -INFINITY ? 0.f : fast_exp2(M - n), e = n == -INFINITY ? 0.f : fast_exp2(ml.x - n);
+      M = n;
+      sum = sum * f + ml.y * e;
+      o = make_float4(o.x * f + x.x * e, o.y * f + x.y * e, o.z * f + x.z * e, o.w * f + x.w * e);
+    };
+    if (row < rows && team / share < at_once) {
+      constexpr int BATCH = 8;  // parts read together: each read is a trip to L2
+      for (int r0 = range + part0; r0 <= last; r0 += share * BATCH) {
+        float2 ml[BATCH];
+        float4 x[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+          const int r = r0 + k * share;
+          const int64_t at = (2ll * (static_cast<int64_t>(r) * c.Hkv + h) + (r == range && pl.at > u0 ? 1 : 0)) * slot_rows + row;
+          const bool part = r <= last && !(gaps && cut(pl.total, r, ranges, large) == cut(pl.total, r + 1, ranges, large)) &&
+                            in_bounds(c.status, at, nslot);
+          ml[k] = part ? wml[at] : make_float2(-INFINITY, 0.f);
+          x[k] = part ? wo[at * G + g] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) add(ml[k], x[k]);
+      }
+    }
+    if (share > 1) {
+      __syncthreads();
+      so[team][g] = o;
+      if (g == 0) sml[team] = make_float2(M, sum);
+      __syncthreads();
+      if (part0 == 0)
+        for (int i = 1; i < share; ++i) add(sml[min(team + i, TEAMS - 1)], so[min(team + i, TEAMS - 1)][g]);
+    }
+    if (row >= rows || part0 != 0 || team / share >= at_once) continue;
+    const bool live = sum > 0.f;
+    const float inv = live ? 1.f / sum : __int_as_float(0x7fc00000);
+    const int64_t at = static_cast<int64_t>(q_lo + row / heads) * p.Hq + h * heads + row % heads;
+    if (!in_bounds(c.status, at, nrows)) continue;
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * D)[g] =
+        make_uint2(pack_out(p.bf16, o.x * inv, o.y * inv), pack_out(p.bf16, o.z * inv, o.w * inv));
+    if (p.lse && g == 0) p.lse[at] = live ? (M + log2f(sum)) * LN2 : (sum == 0.f ? -INFINITY : sum);
   }
-  so[part0][g] = o;
-  if (g == 0) sml[part0] = make_float2(M, sum);
-  __syncthreads();
-  if (part0 != 0) return;
-  for (int i = 1; i < parts; ++i) {
-    const float2 ml = sml[i];
-    const float4 x = so[i][g];
-    const float n = fmaxf(M, ml.x);
-    const float f = n == -INFINITY ? 0.f : fast_exp2(M - n), e = n == -INFINITY ? 0.f : fast_exp2(ml.x - n);
-    M = n;
-    sum = sum * f + ml.y * e;
-    o = make_float4(o.x * f + x.x * e, o.y * f + x.y * e, o.z * f + x.z * e, o.w * f + x.w * e);
-  }
-  const bool live = sum > 0.f;
-  const float inv = live ? 1.f / sum : __int_as_float(0x7fc00000);
-  const int64_t at = static_cast<int64_t>(q_lo + row / heads) * p.Hq + h * heads + row % heads;
-  if (!in_bounds(c.status, at, static_cast<int64_t>(p.num_queries) * p.Hq)) return;
-  reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * D)[g] =
-      make_uint2(pack_out(p.bf16, o.x * inv, o.y * inv), pack_out(p.bf16, o.z * inv, o.w * inv));
-  if (p.lse && g == 0) p.lse[at] = live ? (M + log2f(sum)) * LN2 : (sum == 0.f ? -INFINITY : sum);
 }
 
 template <int D, int FMT, int NT>
@@ -679,11 +715,19 @@ cudaError_t launch_nt(const FwdParams& p, const DecodePlan& plan, cudaStream_t s
   if (e != cudaSuccess) return e;
   const unsigned ctas = static_cast<unsigned>(plan.ranges) * p.c.Hkv;
   const int64_t ml = plan.ml_offset(p.c.Hkv, D);
-  kern<<<dim3(ctas, plan.row_groups), THREADS, smem, st>>>(p, plan.ranges, plan.slot_rows(), ml);
+  kern<<<dim3(ctas, plan.row_groups), THREADS, smem, st>>>(p, plan.ranges, plan.large, plan.slot_rows(), ml);
   e = cudaGetLastError();
   if (e != cudaSuccess || plan.ranges == 1) return e;
-  merge_kernel<D><<<dim3(ctas, plan.rows), THREADS, 0, st>>>(p, plan.ranges, plan.slot_rows(), ml);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(MERGE_THREADS);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, p, plan.ranges, plan.large, plan.slot_rows(), ml);
 }
 
 template <int D, int FMT>

@@ -26,7 +26,8 @@ struct FwdParams {
 // rows of a kv head (8 nt); more rows go to `row_groups` CTAs that read the same
 // codes (the second from L2).
 struct DecodePlan {
-  int rows = 0, row_groups = 0, nt = 0, ranges = 0;
+  static constexpr int LARGE = 5;  // the first `large` ranges are this many times the others
+  int rows = 0, row_groups = 0, nt = 0, ranges = 0, large = 0;
   int slot_rows() const { return row_groups * nt * 8; }
   // Partials: CTA c (range, head) owns slots 2c (its first sequence) and 2c + 1
   // (its last), each slot_rows x (D floats) and slot_rows x (m, l).
@@ -38,10 +39,9 @@ struct DecodePlan {
 constexpr int DECODE_ROWS = 64;
 
 // Ranges that the keys of a call are cut into, each for Hkv CTAs (and row
-// groups): as many CTAs as the 152 SMs hold at once, three each of the kernels for
-// 8 and 16 rows and two of the others; with many heads four waves of smaller ones, so
-// that a last wave that is not full costs little; never more ranges than there
-// can be blocks of 128 keys.
+// groups): as many CTAs as the 152 SMs hold at once, three each of the kernels
+// for 8 and 16 rows, two of the others; never more ranges than there can be
+// blocks of 128 keys.
 inline DecodePlan decode_plan(int num_seqs, int Hkv, int heads, int max_queries, int max_pages, int page_size) {
   DecodePlan d;
   d.rows = static_cast<int>(static_cast<int64_t>(max_queries) * heads);
@@ -50,9 +50,12 @@ inline DecodePlan decode_plan(int num_seqs, int Hkv, int heads, int max_queries,
   const int64_t keys = static_cast<int64_t>(max_pages) * page_size;
   const int64_t blocks = num_seqs * (keys > 128 ? (keys + 127) / 128 : 1);
   const int64_t side = static_cast<int64_t>(Hkv) * d.row_groups;
-  int64_t r = (side > 16 ? 4 : 1) * 152 * (d.nt <= 2 ? 3 : 2) / side;
-  if (r > blocks) r = blocks;
-  d.ranges = static_cast<int>(r > 1 ? r : 1);
+  int64_t large = 152 * (d.nt <= 2 ? 3 : 2) / side;
+  if (large < 1) large = 1;
+  int64_t r = large;
+  if (r > blocks) large = r = blocks;  // few blocks: one each
+  d.ranges = static_cast<int>(r);
+  d.large = static_cast<int>(large);
   return d;
 }
 
