@@ -40,6 +40,7 @@
 #pragma once
 
 #include "kv8_fwd.h"
+#include "kv8_ops.cuh"
 
 namespace attn {
 namespace kv8 {
@@ -141,35 +142,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
-// The 4 codes of a word as two F16 pairs: bytes 0, 1 and bytes 2, 3.
-template <int FMT>
-__device__ __forceinline__ void pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (FMT == FMT_INT8) {
-    const uint32_t u = w ^ 0x80808080u;  // c + 128
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);  // 1024 + (c + 128)
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
-  } else {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-  }
-}
-
-// 16 or 4 bytes global -> shared; `bytes` of them (0: zeros are written).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Where 16-byte piece `c` of row r of a tile is kept (in pieces), so that the
 // lanes of a read fall on different banks: K is read as rows 4 (g/2) + g%2 and
 // pieces 4 i + t, V as rows 4 t + i and pieces (D 64: half pieces) g.
@@ -180,14 +152,6 @@ __device__ __forceinline__ int k_piece(int r, int c) {
 template <int D>
 __device__ __forceinline__ int v_piece(int r, int c) {
   return D == 128 ? r * 8 + (c ^ ((r >> 1) & 6)) : ((r & ~1) | ((r ^ (r >> 2)) & 1)) * 4 + (c ^ ((r >> 2) & 2));
-}
-
-// Power of two 2^e as fp32, e in [-126, 127].
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-
-// A pair of outputs in the type of q.
-__device__ __forceinline__ uint32_t pack_out(bool bf16, float a, float b) {
-  return bf16 ? pack2<true>(a, b) : pack2<false>(a, b);
 }
 
 template <int D, int NT>
@@ -288,15 +252,11 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
         for (int i = 0; i < KB; ++i)
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float lo = fabsf(__uint_as_float(r[i][k] << 16)), hi = fabsf(__uint_as_float(r[i][k] & 0xffff0000u));
-            top = fmaxf(top, fmaxf(lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f));
+            top = fmaxf(top, finite_top(r[i][k]));
           }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the largest element to [2^14, 2^15)
-        const int e = min(max(14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), -126), 126);
-        const float f = pow2(e);
-        back = pow2(-e);
+        const float f = f16_range(top, back);
 #pragma unroll
         for (int i = 0; i < KB; ++i)
 #pragma unroll

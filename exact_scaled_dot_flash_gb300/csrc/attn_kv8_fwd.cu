@@ -1,5 +1,6 @@
 // attn_kv8_fwd.cu - attention of packed queries over an 8-bit paged cache: the
-// entry point, and the fp32 FMA kernel that takes every call.
+// entry point, and the fp32 FMA kernel that takes the calls the tensor-core
+// kernels (attn_kv8_decode.cuh, attn_kv8_tc.cuh) do not: F32, D in {16, 32}.
 //
 // Per query row i (a query and a head) and visible key j of its sequence, with
 // the codes kc, vc and the scales ks, vs of the cache (kv8.cuh):
@@ -186,13 +187,17 @@ int check_shape(const attn_paged_shape_t& s) {
   return ATTN_OK;
 }
 
-// Shapes of the kernel that shares out the keys. Its token numbers (page *
-// page_size + row) are 32-bit, its row / group a 32-bit multiplication.
-bool takes_decode(const attn_paged_shape_t& s) {
-  const int64_t rows = static_cast<int64_t>(s.max_queries) * (s.Hq / s.Hkv);
-  return (s.D == 64 || s.D == 128) && rows > 0 && rows <= attn::kv8::DECODE_ROWS && s.num_pages > 0 && s.num_seqs > 0 &&
+// Shapes of the 16-bit kernels on the tensor cores. Their token numbers (page *
+// page_size + row) are 32-bit, their row / group a 32-bit multiplication.
+bool takes_tensor(const attn_paged_shape_t& s) {
+  return (s.D == 64 || s.D == 128) && s.max_queries > 0 && s.num_pages > 0 && s.num_seqs > 0 &&
          static_cast<int64_t>(s.num_pages) * s.page_size <= 0x7fffffffLL && s.page_size < 65536 && s.Hkv <= 65535 &&
          static_cast<int64_t>(s.max_pages) * s.page_size <= 0x7fff0000LL;
+}
+
+// The kernel that shares out the keys; the other tensor-core kernel takes the rest.
+bool takes_decode(const attn_paged_shape_t& s) {
+  return takes_tensor(s) && static_cast<int64_t>(s.max_queries) * (s.Hq / s.Hkv) <= attn::kv8::DECODE_ROWS;
 }
 
 attn::kv8::DecodePlan plan_of(const attn_paged_shape_t& s) {
@@ -293,6 +298,10 @@ extern "C" int attn_paged_kv8_fwd(const attn_paged_shape_t* shape, int group, in
   if (dtype != ATTN_F32 && takes_decode(s)) {
     const DecodePlan plan = plan_of(s);
     e = i8 ? launch_decode<FMT_INT8>(p, plan, st) : launch_decode<FMT_E4M3>(p, plan, st);
+    return e == cudaSuccess ? ATTN_OK : attn::record_cuda_error(e);
+  }
+  if (dtype != ATTN_F32 && takes_tensor(s)) {
+    e = i8 ? launch_tc<FMT_INT8>(p, st) : launch_tc<FMT_E4M3>(p, st);
     return e == cudaSuccess ? ATTN_OK : attn::record_cuda_error(e);
   }
 #define ATTN_FWD(DT) (i8 ? launch_simt<DT, FMT_INT8>(p, st) : launch_simt<DT, FMT_E4M3>(p, st))

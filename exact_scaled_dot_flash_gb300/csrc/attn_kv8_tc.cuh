@@ -1,0 +1,536 @@
+// attn_kv8_tc.cuh - attention over an 8-bit paged cache on the tcgen05 tensor
+// cores, for calls with many rows (prompts and chunks of prompts; F16/BF16, D in
+// {64, 128}, any page size).
+//
+// A CTA takes 256 packed rows (row = query * heads + head, the heads that share
+// a kv head) of one sequence and kv head, as two tiles of 128, over all keys
+// they see, 128 at a time:
+//  - warps 8-11 convert. Each thread copies its share of a tile's codes ahead of
+//    time (cp.async; it reads back only what it copied, so a page may end
+//    anywhere and no barrier is needed), and writes them as F16, exactly, in the
+//    128-byte swizzle that the tensor cores read; with K it leaves the tile's
+//    scales in shared memory. A converted tile serves 256 rows: 0.13 conversions
+//    for a multiply-add step of the tensor core's 256 x 16 rate;
+//  - warp 12 issues S = Q K^T and O += P V in the order S_0 PV_1 S_1 PV_0, so
+//    that each tile's softmax runs under the other's products;
+//  - warps 0-7 own a row a thread: x = S ks scale in fp32, y = 2^(x - ref),
+//    P = y vs rounded to F16 back into tensor memory, l += y. ref holds the
+//    row's largest score and the tile's largest value scale, and moves only when
+//    that passes it by 2^8.
+// The products are F16 for BF16 queries too: a row is brought into range by a
+// power of two (see attn_kv8_decode.cuh).
+// Bound: the tensor pipe's 2048 cycles for a tile of 256 x 128 x 128; the
+// softmax and the conversion together issue for some 1500 of them.
+#pragma once
+
+#include "kv8_fwd.h"
+#include "kv8_ops.cuh"
+
+namespace attn {
+namespace kv8 {
+namespace tc {
+
+constexpr int BM = 128, BN = 128, NQ = 2;
+constexpr int NUM_THREADS = 512;
+constexpr int WARP_CONV = 8, CONV_WARPS = 4, WARP_MMA = 12;
+constexpr int TMEM_COLS = 512;
+// 512 threads start with 128 registers each; 2 x 128 x 200 + 2 x 128 x 56 is the same sum
+constexpr int REG_SOFTMAX = 200, REG_OTHER = 56;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float RESCALE_LOG2 = 8.0f;
+constexpr float UNSEEN = -1e30f;
+
+template <int D>
+struct Cfg {
+  static constexpr int NCHUNK = D / 64;                // 64 elements: one 128-byte row of the swizzle
+  static constexpr int CHUNK_BYTES = BN * 128;
+  static constexpr int TILE_BYTES = NCHUNK * CHUNK_BYTES;
+  static constexpr int STAGES = 3;                     // converted tiles: K_j, V_j, K_j+1
+  static constexpr int RAW = 3;                        // tiles of codes on their way
+  static constexpr int RAW_BYTES = BN * D;
+  static constexpr int SCALE_BYTES = 2 * BN * 4 + 16;  // ks, vs, the warps' largest vs
+  static constexpr int OFF_KV = NQ * TILE_BYTES;
+  static constexpr int OFF_RAW = OFF_KV + STAGES * TILE_BYTES;
+  static constexpr int OFF_SCALE = OFF_RAW + RAW * RAW_BYTES;
+  static constexpr int OFF_BAR = OFF_SCALE + 2 * SCALE_BYTES;
+  static constexpr int BAR_FULL = 0, BAR_EMPTY = STAGES, BAR_Q = 2 * STAGES, BAR_S = BAR_Q + NQ;
+  static constexpr int BAR_P = BAR_S + NQ, BAR_O = BAR_P + NQ, BAR_DONE = BAR_O + NQ;
+  static constexpr int OFF_MISC = OFF_BAR + (BAR_DONE + 1) * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static_assert(SMEM_BYTES <= 227 * 1024);
+  static constexpr int KSTEPS_QK = D / 16, KSTEPS_PV = BN / 16;
+  static constexpr int COL_P = 64;
+};
+
+struct Work {
+  int s, hk, q_lo, nq, L;
+  int64_t row0;       // first packed row of the CTA
+  int n[NQ], nmax;    // key tiles of each row tile
+  int nfull[NQ];      // of which the first ones need no mask
+};
+
+__device__ __forceinline__ Work make_work(const FwdParams& p, int qblocks) {
+  Work w;
+  const int heads = p.Hq / p.c.Hkv;
+  int item = static_cast<int>(blockIdx.x);
+  w.hk = item % p.c.Hkv;
+  item /= p.c.Hkv;
+  // the last blocks of a sequence see the most keys and go first
+  w.row0 = static_cast<int64_t>(qblocks - 1 - item % qblocks) * NQ * BM;
+  w.s = item / qblocks;
+  int hi;
+  row_range(p.q_offsets, w.s, p.num_queries, w.q_lo, hi);
+  w.nq = hi - w.q_lo;
+  w.L = seq_len(p.c, w.s);
+  w.nmax = 0;
+#pragma unroll
+  for (int t = 0; t < NQ; ++t) {
+    const int64_t r0 = w.row0 + t * BM, rows = static_cast<int64_t>(w.nq) * heads;
+    w.n[t] = w.nfull[t] = 0;
+    if (r0 >= rows) continue;
+    int64_t most = w.L, least = w.L;
+    if (p.causal) {
+      if (p.positions) {
+        least = 0;  // any order: every tile is masked element by element
+      } else {
+        most = min(most, static_cast<int64_t>(w.L) - w.nq + min(static_cast<int64_t>(w.nq) - 1, (r0 + BM - 1) / heads) + 1);
+        least = min(least, static_cast<int64_t>(w.L) - w.nq + r0 / heads + 1);
+      }
+    }
+    w.n[t] = most > 0 ? static_cast<int>((most + BN - 1) / BN) : 0;
+    w.nfull[t] = least > 0 ? static_cast<int>(least / BN) : 0;
+    w.nmax = max(w.nmax, w.n[t]);
+  }
+  return w;
+}
+
+// Byte of 16-byte piece `c` (8 elements) of row r in a swizzled tile.
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+  return (c >> 3) * (BN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constant__ FwdParams p, int qblocks) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_u32(smem);
+  auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Cache& c = p.c;
+  int* const status = c.status;
+  const int heads = p.Hq / c.Hkv;
+  const Work w = make_work(p, qblocks);
+  if (w.row0 >= static_cast<int64_t>(w.nq) * heads) return;  // no rows (CTA-uniform); rows without keys still get NaN
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(bar(C::BAR_FULL + s), CONV_WARPS * 32);
+      mbar_init(bar(C::BAR_EMPTY + s), 1);
+    }
+    for (int t = 0; t < NQ; ++t) {
+      mbar_init(bar(C::BAR_Q + t), BM);
+      mbar_init(bar(C::BAR_S + t), 1);
+      mbar_init(bar(C::BAR_P + t), BM);
+      mbar_init(bar(C::BAR_O + t), 1);
+    }
+    mbar_init(bar(C::BAR_DONE), 1);
+    mbar_init_fence();
+  }
+  if (warp == WARP_MMA) {
+    tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto fail = [&]() {
+    if (status) atomicOr(status, STATUS_TIMEOUT);
+  };
+
+  if (warp >= WARP_CONV) {
+    setmaxnreg_dec<REG_OTHER>();
+    if (warp < WARP_CONV + CONV_WARPS) {
+      // ---------------------------------------------------------- conversion
+      // Warp cw has keys 32 cw .. + 31 of a tile; a copy of the warp moves RPC
+      // keys, D / 16 lanes each. Items: K_0 V_0 K_1 V_1 ...
+      constexpr int PIECES = D / 16, RPC = 32 / PIECES, COPIES = 32 / RPC;
+      const int cw = warp - WARP_CONV;
+      const uint32_t step = static_cast<uint32_t>(c.Hkv) * D;
+      const int64_t ntok = static_cast<int64_t>(c.num_pages) * c.page_size;
+      const int64_t nscale = static_cast<int64_t>(c.num_pages) * c.Hkv * c.per;
+      const uint8_t* const kb = p.k_codes + w.hk * D + lane % PIECES * 16;
+      const uint8_t* const vb = p.v_codes + w.hk * D + lane % PIECES * 16;
+      uint8_t* const raw = smem + C::OFF_RAW + cw * 32 * D;
+      int tok = 0;         // the lane's key of the tile being copied
+      int64_t si = -1;     // its scales, -1: zeros
+      float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
+      // keys are looked up with K and used again for V
+      auto look_up = [&](int j) {
+        const int key = j * BN + cw * 32 + lane;
+        tok = 0;
+        si = -1;
+        if (key < w.L) {
+          const int blk = key / c.page_size, row = key - blk * c.page_size;
+          const int page = page_of(c, w.s, blk);
+          if (page >= 0 && in_bounds(status, static_cast<int64_t>(page) * c.page_size + row, ntok)) {
+            tok = page * c.page_size + row;
+            const int gi = c.group == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.group_magic));
+            si = (static_cast<int64_t>(page) * c.Hkv + w.hk) * c.per + gi;
+            if (!in_bounds(status, si, nscale)) si = -1;
+          }
+        }
+      };
+      auto copy_item = [&](int it) {
+        if (it < 2 * w.nmax) {
+          if ((it & 1) == 0) {
+            look_up(it >> 1);
+            ks_next = si >= 0 ? __ldg(p.k_scale + si) : 0.f;
+            vs_next = si >= 0 ? __ldg(p.v_scale + si) : 0.f;
+          }
+          const uint32_t at = smem_u32(raw) + (it % C::RAW) * C::RAW_BYTES;
+          const uint8_t* const base = (it & 1) ? vb : kb;
+#pragma unroll
+          for (int i = 0; i < COPIES; ++i) {
+            const int r = RPC * i + lane / PIECES;
+            const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, tok, r))) * step;
+            copy16(at + (r * PIECES + lane % PIECES) * 16, base + off);
+          }
+        }
+        copy_commit();
+      };
+      bool ok = true;
+      copy_item(0);
+      ks = ks_next;
+      vs = vs_next;
+      copy_item(1);
+      for (int it = 0; it < 2 * w.nmax && ok; ++it) {
+        const int st = it % C::STAGES, j = it >> 1;
+        // the copies of item it + 2 take the place of item it - 1's, which this
+        // thread has read; they bring the scales of tile j + 1 when it is K's turn
+        copy_item(it + 2);
+        copy_wait<2>();
+        __syncwarp();
+        if (!mbar_wait(bar(C::BAR_EMPTY + st), ((it / C::STAGES) & 1) ^ 1)) { ok = false; break; }
+        const uint8_t* const src = raw + (it % C::RAW) * C::RAW_BYTES;
+        uint8_t* const dst = smem + C::OFF_KV + st * C::TILE_BYTES;
+        if ((it & 1) == 0) {
+          // the softmax of tile j - 2 has read this slot: its P was used before
+          // the converted tile that this one replaces (V_j-2) was released
+          float* const sc = reinterpret_cast<float*>(smem + C::OFF_SCALE + (j & 1) * C::SCALE_BYTES);
+          sc[cw * 32 + lane] = ks * p.scale_log2;
+          sc[BN + cw * 32 + lane] = vs;
+          float top = vs;  // NaN does not count
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (lane == 0) sc[2 * BN + cw] = top;
+        } else {
+          ks = ks_next;
+          vs = vs_next;
+        }
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+          const int r = RPC * i + lane / PIECES, piece = lane % PIECES;
+          const uint4 x = *reinterpret_cast<const uint4*>(src + (r * PIECES + piece) * 16);
+          uint4 a, b;
+          pairs<FMT>(x.x, a.x, a.y);
+          pairs<FMT>(x.y, a.z, a.w);
+          pairs<FMT>(x.z, b.x, b.y);
+          pairs<FMT>(x.w, b.z, b.w);
+          const int row = cw * 32 + r;
+          *reinterpret_cast<uint4*>(dst + swizzled(row, 2 * piece)) = a;
+          *reinterpret_cast<uint4*>(dst + swizzled(row, 2 * piece + 1)) = b;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(C::BAR_FULL + st));
+      }
+      copy_wait<0>();
+      if (!ok && lane == 0) fail();
+    } else if (warp == WARP_MMA) {
+      // ---------------------------------------------------------- MMA issuer
+      constexpr uint32_t idesc_qk = make_idesc_f16(false, BM, BN, false);
+      constexpr uint32_t idesc_pv = make_idesc_f16(false, BM, D, true);
+      constexpr int ST = C::STAGES;
+      const int n0 = w.n[0], n1 = w.n[1], nmax = w.nmax;
+      bool ok = true;
+      for (int t = 0; t < NQ && ok; ++t)
+        if ((t ? n1 : n0) > 0 && !warp_wait(bar(C::BAR_Q + t), 0)) ok = false;
+      const uint64_t dq0 = smem_desc(sb, 16, 1024, 2u);
+      const uint64_t dk0 = smem_desc(sb + C::OFF_KV, 16, 1024, 2u);
+      const uint64_t dv0 = smem_desc(sb + C::OFF_KV, C::CHUNK_BYTES, 1024, 2u);
+      constexpr uint32_t TILE16 = C::TILE_BYTES >> 4, CHUNK16 = C::CHUNK_BYTES >> 4, VSTEP16 = (16 * 128) >> 4;
+      auto kstep = [](int k) -> uint32_t { return (k / 4) * CHUNK16 + (k % 4) * 2; };
+      auto wait_full = [&](int idx) { return warp_wait(bar(C::BAR_FULL + idx % ST), (idx / ST) & 1); };
+      auto issue_s = [&](int t, int j) {
+        const uint64_t a = dq0 + t * TILE16;
+        const uint64_t b = dk0 + ((2 * j) % ST) * TILE16;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < C::KSTEPS_QK; ++k)
+            umma_ss(tmem + t * BN, a + kstep(k), b + kstep(k), idesc_qk, k > 0 ? 1u : 0u);
+          umma_commit(bar(C::BAR_S + t));
+        }
+        __syncwarp();
+      };
+      auto issue_pv = [&](int t, int j) {
+        const uint64_t b = dv0 + ((2 * j + 1) % ST) * TILE16;
+        const uint32_t d = tmem + 256 + t * D;
+        const uint32_t a = tmem + t * BN + C::COL_P;
+        if (elect_one()) {
+          umma_ts(d, a, b, idesc_pv, j > 0 ? 1u : 0u);
+#pragma unroll
+          for (int k = 1; k < C::KSTEPS_PV; ++k) umma_ts(d, a + k * 8, b + k * VSTEP16, idesc_pv, 1u);
+          if (j == (t ? n1 : n0) - 1) umma_commit(bar(C::BAR_O + t));
+        }
+        __syncwarp();
+      };
+      for (int j = 0; j <= nmax && ok; ++j) {
+        if (j < nmax) {
+          if (!wait_full(2 * j)) { ok = false; break; }
+          tc_fence_after();
+          if (j < n0) issue_s(0, j);
+        }
+        if (j >= 1 && j - 1 < n1) {
+          if (j - 1 >= n0 && !wait_full(2 * (j - 1) + 1)) { ok = false; break; }
+          if (!warp_wait(bar(C::BAR_P + 1), (j - 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+          issue_pv(1, j - 1);
+        }
+        if (j >= 1) {
+          if (elect_one()) umma_commit(bar(C::BAR_EMPTY + (2 * (j - 1) + 1) % ST));
+          __syncwarp();
+        }
+        if (j < nmax) {
+          if (j < n1) issue_s(1, j);
+          if (elect_one()) umma_commit(bar(C::BAR_EMPTY + (2 * j) % ST));
+          __syncwarp();
+          if (j < n0) {
+            if (!wait_full(2 * j + 1) || !warp_wait(bar(C::BAR_P + 0), j & 1)) { ok = false; break; }
+            tc_fence_after();
+            issue_pv(0, j);
+          }
+        }
+      }
+      if (!ok && lane == 0) fail();
+      if (elect_one()) umma_commit(bar(C::BAR_DONE));
+      __syncwarp();
+      if (!warp_wait(bar(C::BAR_DONE), 0) && lane == 0) fail();
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    setmaxnreg_inc<REG_SOFTMAX>();
+    const int t = warp >> 2;
+    const int row = ((warp & 3) << 5) + lane;
+    const int64_t pr = w.row0 + t * BM + row;
+    const int tq = static_cast<int>(pr / heads);
+    const bool row_ok = tq < w.nq;
+    const int64_t orow = row_ok ? static_cast<int64_t>(w.q_lo + tq) * p.Hq + w.hk * heads + (pr - static_cast<int64_t>(tq) * heads) : 0;
+    const int64_t nrows = static_cast<int64_t>(p.num_queries) * p.Hq;
+    const bool row_in = row_ok && in_bounds(status, orow, nrows);
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) << 5) << 16;
+    const uint32_t tS = tmem + lane_off + t * BN;
+    const uint32_t tP = tS + C::COL_P;
+    const uint32_t tO = tmem + lane_off + 256 + t * D;
+    const int n_t = t ? w.n[1] : w.n[0];
+    const int nfull_t = t ? w.nfull[1] : w.nfull[0];
+    // the thread's row of Q, as F16
+    float back = 1.f;
+    if (n_t > 0) {
+      const uint4* const src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + orow * D);
+      uint4 x[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) x[i] = row_in ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+      if (p.bf16) {
+        uint32_t* const y = reinterpret_cast<uint32_t*>(x);
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i) top = fmaxf(top, finite_top(y[i]));
+        const float f = f16_range(top, back);
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i)
+          y[i] = pack2<false>(__uint_as_float(y[i] << 16) * f, __uint_as_float(y[i] & 0xffff0000u) * f);
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4*>(smem + t * C::TILE_BYTES + swizzled(row, i)) = x[i];
+      fence_proxy_async_smem();
+      mbar_arrive(bar(C::BAR_Q + t));
+    }
+    int pos = -1;
+    if (row_ok)
+      pos = p.positions ? (in_bounds(status, w.q_lo + tq, p.num_queries) ? __ldg(p.positions + w.q_lo + tq) : -1)
+                        : w.L - w.nq + tq;
+    const int lim = p.causal ? min(pos, w.L - 1) : (row_ok ? w.L - 1 : -1);  // last key the row sees
+    float ref = UNSEEN, l_run = 0.f;
+    bool failed = false;
+    for (int j = 0; j < n_t; ++j) {
+      const bool ok = mbar_wait(bar(C::BAR_S + t), j & 1);
+      if (__any_sync(0xffffffffu, !ok)) { failed = true; break; }
+      tc_fence_after();
+      const float4* const sk = reinterpret_cast<const float4*>(smem + C::OFF_SCALE + (j & 1) * C::SCALE_BYTES);
+      const float4* const sv = sk + BN / 4;
+      float s[128];
+      {
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, sr[i]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float4 k = sk[i];
+          const uint32_t* const x = &sr[i >> 3][(4 * i) & 31];
+          const float2 a = fmul2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(k.x, k.y));
+          const float2 b = fmul2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(k.z, k.w));
+          s[4 * i] = a.x; s[4 * i + 1] = a.y; s[4 * i + 2] = b.x; s[4 * i + 3] = b.y;
+        }
+      }
+      const bool masked = j >= nfull_t;
+      if (masked) {
+        const int key0 = j * BN;
+#pragma unroll
+        for (int i = 0; i < 128; ++i)
+          if (key0 + i > lim) s[i] = -INFINITY;
+      }
+      float c0 = fmax3(s[0], s[1], s[2]), c1 = fmax3(s[3], s[4], s[5]);
+      float c2 = fmax3(s[6], s[7], s[8]), c3 = fmax3(s[9], s[10], s[11]);
+#pragma unroll
+      for (int i = 12; i < 124; i += 8) {
+        c0 = fmax3(c0, s[i], s[i + 1]);
+        c1 = fmax3(c1, s[i + 2], s[i + 3]);
+        c2 = fmax3(c2, s[i + 4], s[i + 5]);
+        c3 = fmax3(c3, s[i + 6], s[i + 7]);
+      }
+      c0 = fmax3(c0, s[124], s[125]);
+      c1 = fmax3(c1, s[126], s[127]);
+      // the largest score, raised by the exponent of the tile's largest value scale
+      const float4 vt = sv[BN / 4];
+      const float vtop = fmaxf(fmax3(vt.x, vt.y, vt.z), vt.w);
+      const float vex = fmaxf(static_cast<float>(static_cast<int>(__float_as_uint(vtop) >> 23) - 126), -80.f);
+      const float x_tile = fmax3(c0, c1, fmaxf(c2, c3)) * back + vex;
+      const bool need = x_tile > ref + RESCALE_LOG2;
+      float alpha = 1.f;
+      if (need) {
+        alpha = fast_exp2(ref - x_tile);
+        ref = x_tile;
+        l_run *= alpha;
+      }
+      const float neg = -ref;
+      float2 sum_a = make_float2(0.f, 0.f), sum_b = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int i2 = 0; i2 < 32; i2 += 2) {
+          const int i = 64 * hh + 2 * i2;
+          const float4 v = sv[i >> 2];
+          const float2 xa = ffma2(make_float2(s[i], s[i + 1]), make_float2(back, back), make_float2(neg, neg));
+          const float2 xb = ffma2(make_float2(s[i + 2], s[i + 3]), make_float2(back, back), make_float2(neg, neg));
+          const float2 ya = make_float2(fast_exp2(xa.x), fast_exp2(xa.y));
+          const float2 yb = make_float2(fast_exp2(xb.x), fast_exp2(xb.y));
+          sum_a = fadd2(sum_a, ya);
+          sum_b = fadd2(sum_b, yb);
+          float2 za = fmul2(ya, make_float2(v.x, v.y)), zb = fmul2(yb, make_float2(v.z, v.w));
+          if (masked) {  // a masked key may have any scale
+            za.x = s[i] == -INFINITY ? 0.f : za.x;
+            za.y = s[i + 1] == -INFINITY ? 0.f : za.y;
+            zb.x = s[i + 2] == -INFINITY ? 0.f : zb.x;
+            zb.y = s[i + 3] == -INFINITY ? 0.f : zb.y;
+          }
+          pk[i2] = pack2<false>(za.x, za.y);
+          pk[i2 + 1] = pack2<false>(zb.x, zb.y);
+        }
+        tmem_st32(tP + 32 * hh, pk);
+      }
+      l_run += (sum_a.x + sum_a.y) + (sum_b.x + sum_b.y);
+      if (j > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
+          tmem_ld32(tO + 32 * i, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float2 x = fmul2(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), make_float2(alpha, alpha));
+            o[k] = __float_as_uint(x.x);
+            o[k + 1] = __float_as_uint(x.y);
+          }
+          tmem_st32(tO + 32 * i, o);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(C::BAR_P + t));
+    }
+    // ---------------------------------------------------------------- epilogue
+    const bool have = n_t > 0;
+    if (!failed && have) {
+      const bool ok = mbar_wait(bar(C::BAR_O + t), 0);
+      if (__any_sync(0xffffffffu, !ok)) failed = true;
+    }
+    if (failed) {
+      if (lane == 0) fail();
+    } else if (w.row0 + t * BM < static_cast<int64_t>(w.nq) * heads) {
+      tc_fence_after();
+      const bool live = have && l_run > 0.f;
+      const float inv = live ? 1.f / l_run : __int_as_float(0x7fc00000);
+      uint8_t* const dst = static_cast<uint8_t*>(p.out) + orow * D * 2;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t o[32];
+        if (have) {
+          tmem_ld32(tO + 32 * i, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0u;
+        }
+        if (row_in) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 x = fmul2(make_float2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), make_float2(inv, inv));
+            pk[k] = pack_out(p.bf16, x.x, x.y);
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            reinterpret_cast<uint4*>(dst + i * 64)[u] = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+        }
+      }
+      if (row_in && p.lse) p.lse[orow] = live ? (ref + log2f(l_run)) * LN2 : (l_run == 0.f ? -INFINITY : l_run);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == WARP_MMA) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+template <int D, int FMT>
+cudaError_t launch_d(const FwdParams& p, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(p.max_queries) * (p.Hq / p.c.Hkv);
+  const int64_t qblocks = (rows + NQ * BM - 1) / (NQ * BM);
+  const int64_t ctas = static_cast<int64_t>(p.c.num_seqs) * qblocks * p.c.Hkv;
+  if (ctas == 0) return cudaSuccess;
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  auto kern = tc_kernel<D, FMT>;
+  constexpr int smem = Cfg<D>::SMEM_BYTES;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(ctas), NUM_THREADS, smem, st>>>(p, static_cast<int>(qblocks));
+  return cudaGetLastError();
+}
+
+}  // namespace tc
+
+template <int FMT>
+cudaError_t launch_tc(const FwdParams& p, cudaStream_t st) {
+  return p.c.D == 128 ? tc::launch_d<128, FMT>(p, st) : tc::launch_d<64, FMT>(p, st);
+}
+
+}  // namespace kv8
+}  // namespace attn

@@ -62,5 +62,9 @@ inline DecodePlan decode_plan(int num_seqs, int Hkv, int heads, int max_queries,
 template <int FMT>
 cudaError_t launch_decode(const FwdParams& p, const DecodePlan& plan, cudaStream_t st);
 
+// Many rows, F16/BF16, D in {64, 128} (attn_kv8_tc.cuh).
+template <int FMT>
+cudaError_t launch_tc(const FwdParams& p, cudaStream_t st);
+
 }  // namespace kv8
 }  // namespace attn
