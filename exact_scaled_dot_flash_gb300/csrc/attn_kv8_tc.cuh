@@ -23,6 +23,8 @@
 // softmax and the conversion together issue for some 1500 of them.
 #pragma once
 
+#include <type_traits>
+
 #include "kv8_fwd.h"
 #include "kv8_ops.cuh"
 
@@ -34,8 +36,8 @@ constexpr int BM = 128, BN = 128, NQ = 2;
 constexpr int NUM_THREADS = 512;
 constexpr int WARP_CONV = 8, CONV_WARPS = 4, WARP_MMA = 12;
 constexpr int TMEM_COLS = 512;
-// 512 threads start with 128 registers each; 2 x 128 x 200 + 2 x 128 x 56 is the same sum
-constexpr int REG_SOFTMAX = 200, REG_OTHER = 56;
+// 512 threads start with 128 registers each; 2 x 128 x 192 + 2 x 128 x 64 is the same sum
+constexpr int REG_SOFTMAX = 192, REG_OTHER = 64;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float UNSEEN = -1e30f;
@@ -109,7 +111,8 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
   return (c >> 3) * (BN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-template <int D, int FMT>
+// RUN4: every 4 keys share their scales (group and page_size multiples of 4).
+template <int D, int FMT, bool RUN4>
 __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constant__ FwdParams p, int qblocks) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_dyn[];
@@ -155,38 +158,50 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
     if (warp < WARP_CONV + CONV_WARPS) {
       // ---------------------------------------------------------- conversion
       // Warp cw has keys 32 cw .. + 31 of a tile; a copy of the warp moves RPC
-      // keys, D / 16 lanes each. Items: K_0 V_0 K_1 V_1 ...
+      // keys, D / 16 lanes each. Items: K_0 V_0 K_1 V_1 ... The lanes of a copy
+      // are dealt out so that 8 neighbours, which a shared-memory store takes at
+      // once, have 4 pieces each of two keys that differ in bit 0: 8 places of the
+      // swizzle. The codes themselves lie in the lanes' order: a lane reads only
+      // what it copied.
       constexpr int PIECES = D / 16, RPC = 32 / PIECES, COPIES = 32 / RPC;
+      const int lpiece = (lane & 3) | (D == 128 ? (lane >> 1) & 4 : 0);
+      const int lrow = D == 128 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2;
       const int cw = warp - WARP_CONV;
       const uint32_t step = static_cast<uint32_t>(c.Hkv) * D;
       const int64_t ntok = static_cast<int64_t>(c.num_pages) * c.page_size;
       const int64_t nscale = static_cast<int64_t>(c.num_pages) * c.Hkv * c.per;
-      const uint8_t* const kb = p.k_codes + w.hk * D + lane % PIECES * 16;
-      const uint8_t* const vb = p.v_codes + w.hk * D + lane % PIECES * 16;
+      const uint8_t* const kb = p.k_codes + w.hk * D + lpiece * 16;
+      const uint8_t* const vb = p.v_codes + w.hk * D + lpiece * 16;
       uint8_t* const raw = smem + C::OFF_RAW + cw * 32 * D;
       int tok = 0;         // the lane's key of the tile being copied
       int64_t si = -1;     // its scales, -1: zeros
       float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
-      // keys are looked up with K and used again for V
-      auto look_up = [&](int j) {
-        const int key = j * BN + cw * 32 + lane;
-        tok = 0;
-        si = -1;
-        if (key < w.L) {
-          const int blk = key / c.page_size, row = key - blk * c.page_size;
-          const int page = page_of(c, w.s, blk);
-          if (page >= 0 && in_bounds(status, static_cast<int64_t>(page) * c.page_size + row, ntok)) {
-            tok = page * c.page_size + row;
-            const int gi = c.group == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.group_magic));
-            si = (static_cast<int64_t>(page) * c.Hkv + w.hk) * c.per + gi;
-            if (!in_bounds(status, si, nscale)) si = -1;
-          }
+      // The lane's key of the tile to copy next, and its page, which is read a
+      // tile ahead of its use. Keys are looked up with K and used again for V.
+      int key = cw * 32 + lane, blk = key / c.page_size, row = key - blk * c.page_size;
+      const int dblk = BN / c.page_size, drow = BN % c.page_size;
+      const int32_t* const table = c.block_table + static_cast<size_t>(w.s) * c.max_pages;
+      auto find_page = [&]() { return key < w.L && blk < c.max_pages ? __ldg(table + blk) : -1; };
+      int page = find_page();
+      auto look_up = [&]() {
+        const bool ok = page >= 0 && page < c.num_pages && in_bounds(status, static_cast<int64_t>(page) * c.page_size + row, ntok);
+        const int gi = c.group == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.group_magic));
+        tok = ok ? page * c.page_size + row : 0;
+        si = ok ? (static_cast<int64_t>(page) * c.Hkv + w.hk) * c.per + gi : -1;
+        if (si >= 0 && !in_bounds(status, si, nscale)) si = -1;
+        key += BN;
+        blk += dblk;
+        row += drow;
+        if (row >= c.page_size) {
+          row -= c.page_size;
+          ++blk;
         }
+        page = find_page();
       };
       auto copy_item = [&](int it) {
         if (it < 2 * w.nmax) {
           if ((it & 1) == 0) {
-            look_up(it >> 1);
+            look_up();
             ks_next = si >= 0 ? __ldg(p.k_scale + si) : 0.f;
             vs_next = si >= 0 ? __ldg(p.v_scale + si) : 0.f;
           }
@@ -194,9 +209,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
           const uint8_t* const base = (it & 1) ? vb : kb;
 #pragma unroll
           for (int i = 0; i < COPIES; ++i) {
-            const int r = RPC * i + lane / PIECES;
+            const int r = RPC * i + lrow;
             const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, tok, r))) * step;
-            copy16(at + (r * PIECES + lane % PIECES) * 16, base + off);
+            copy16(at + (i * 32 + lane) * 16, base + off);
           }
         }
         copy_commit();
@@ -220,8 +235,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
           // the softmax of tile j - 2 has read this slot: its P was used before
           // the converted tile that this one replaces (V_j-2) was released
           float* const sc = reinterpret_cast<float*>(smem + C::OFF_SCALE + (j & 1) * C::SCALE_BYTES);
-          sc[cw * 32 + lane] = ks * p.scale_log2;
-          sc[BN + cw * 32 + lane] = vs;
+          if constexpr (RUN4) {
+            if ((lane & 3) == 0) {
+              sc[(cw * 32 + lane) >> 2] = ks * p.scale_log2;
+              sc[BN + ((cw * 32 + lane) >> 2)] = vs;
+            }
+          } else {
+            sc[cw * 32 + lane] = ks * p.scale_log2;
+            sc[BN + cw * 32 + lane] = vs;
+          }
           float top = vs;  // NaN does not count
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -231,17 +253,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
           vs = vs_next;
         }
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) {
-          const int r = RPC * i + lane / PIECES, piece = lane % PIECES;
-          const uint4 x = *reinterpret_cast<const uint4*>(src + (r * PIECES + piece) * 16);
-          uint4 a, b;
-          pairs<FMT>(x.x, a.x, a.y);
-          pairs<FMT>(x.y, a.z, a.w);
-          pairs<FMT>(x.z, b.x, b.y);
-          pairs<FMT>(x.w, b.z, b.w);
-          const int row = cw * 32 + r;
-          *reinterpret_cast<uint4*>(dst + swizzled(row, 2 * piece)) = a;
-          *reinterpret_cast<uint4*>(dst + swizzled(row, 2 * piece + 1)) = b;
+        for (int i0 = 0; i0 < COPIES; i0 += 4) {
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = *reinterpret_cast<const uint4*>(src + ((i0 + i) * 32 + lane) * 16);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 a, b;
+            pairs<FMT>(x[i].x, a.x, a.y);
+            pairs<FMT>(x[i].y, a.z, a.w);
+            pairs<FMT>(x[i].z, b.x, b.y);
+            pairs<FMT>(x[i].w, b.z, b.w);
+            const int r = cw * 32 + RPC * (i0 + i) + lrow;
+            *reinterpret_cast<uint4*>(dst + swizzled(r, 2 * lpiece)) = a;
+            *reinterpret_cast<uint4*>(dst + swizzled(r, 2 * lpiece + 1)) = b;
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive(bar(C::BAR_FULL + st));
@@ -371,6 +398,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
       tc_fence_after();
       const float4* const sk = reinterpret_cast<const float4*>(smem + C::OFF_SCALE + (j & 1) * C::SCALE_BYTES);
       const float4* const sv = sk + BN / 4;
+      // s: products times k_scale; RUN4: the products alone
       float s[128];
       {
         uint32_t sr[4][32];
@@ -379,10 +407,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float4 k = sk[i];
           const uint32_t* const x = &sr[i >> 3][(4 * i) & 31];
-          const float2 a = fmul2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(k.x, k.y));
-          const float2 b = fmul2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(k.z, k.w));
+          float2 a = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+          float2 b = make_float2(__uint_as_float(x[2]), __uint_as_float(x[3]));
+          if constexpr (!RUN4) {
+            const float4 k = sk[i];
+            a = fmul2(a, make_float2(k.x, k.y));
+            b = fmul2(b, make_float2(k.z, k.w));
+          }
           s[4 * i] = a.x; s[4 * i + 1] = a.y; s[4 * i + 2] = b.x; s[4 * i + 3] = b.y;
         }
       }
@@ -393,17 +425,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
         for (int i = 0; i < 128; ++i)
           if (key0 + i > lim) s[i] = -INFINITY;
       }
-      float c0 = fmax3(s[0], s[1], s[2]), c1 = fmax3(s[3], s[4], s[5]);
-      float c2 = fmax3(s[6], s[7], s[8]), c3 = fmax3(s[9], s[10], s[11]);
+      float c0 = -INFINITY, c1 = c0, c2 = c0, c3 = c0;
+      if constexpr (RUN4) {  // scales are not negative: the largest product of a run gives its largest score
 #pragma unroll
-      for (int i = 12; i < 124; i += 8) {
-        c0 = fmax3(c0, s[i], s[i + 1]);
-        c1 = fmax3(c1, s[i + 2], s[i + 3]);
-        c2 = fmax3(c2, s[i + 4], s[i + 5]);
-        c3 = fmax3(c3, s[i + 6], s[i + 7]);
+        for (int i = 0; i < 8; ++i) {
+          const float4 k = sk[i];
+          auto run = [&](int r) { return fmaxf(fmax3(s[16 * i + 4 * r], s[16 * i + 4 * r + 1], s[16 * i + 4 * r + 2]), s[16 * i + 4 * r + 3]); };
+          c0 = fmaxf(c0, run(0) * k.x);
+          c1 = fmaxf(c1, run(1) * k.y);
+          c2 = fmaxf(c2, run(2) * k.z);
+          c3 = fmaxf(c3, run(3) * k.w);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 128; i += 8) {
+          c0 = fmax3(c0, s[i], s[i + 1]);
+          c1 = fmax3(c1, s[i + 2], s[i + 3]);
+          c2 = fmax3(c2, s[i + 4], s[i + 5]);
+          c3 = fmax3(c3, s[i + 6], s[i + 7]);
+        }
       }
-      c0 = fmax3(c0, s[124], s[125]);
-      c1 = fmax3(c1, s[126], s[127]);
       // the largest score, raised by the exponent of the tile's largest value scale
       const float4 vt = sv[BN / 4];
       const float vtop = fmaxf(fmax3(vt.x, vt.y, vt.z), vt.w);
@@ -418,31 +459,50 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
       }
       const float neg = -ref;
       float2 sum_a = make_float2(0.f, 0.f), sum_b = make_float2(0.f, 0.f);
+      auto probabilities = [&](auto mask) {
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t pk[32];
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t pk[32];
 #pragma unroll
-        for (int i2 = 0; i2 < 32; i2 += 2) {
-          const int i = 64 * hh + 2 * i2;
-          const float4 v = sv[i >> 2];
-          const float2 xa = ffma2(make_float2(s[i], s[i + 1]), make_float2(back, back), make_float2(neg, neg));
-          const float2 xb = ffma2(make_float2(s[i + 2], s[i + 3]), make_float2(back, back), make_float2(neg, neg));
-          const float2 ya = make_float2(fast_exp2(xa.x), fast_exp2(xa.y));
-          const float2 yb = make_float2(fast_exp2(xb.x), fast_exp2(xb.y));
-          sum_a = fadd2(sum_a, ya);
-          sum_b = fadd2(sum_b, yb);
-          float2 za = fmul2(ya, make_float2(v.x, v.y)), zb = fmul2(yb, make_float2(v.z, v.w));
-          if (masked) {  // a masked key may have any scale
-            za.x = s[i] == -INFINITY ? 0.f : za.x;
-            za.y = s[i + 1] == -INFINITY ? 0.f : za.y;
-            zb.x = s[i + 2] == -INFINITY ? 0.f : zb.x;
-            zb.y = s[i + 3] == -INFINITY ? 0.f : zb.y;
+          for (int i2 = 0; i2 < 32; i2 += 2) {
+            const int i = 64 * hh + 2 * i2;
+            float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v;
+            if constexpr (RUN4) {
+              k4 = sk[i >> 4];
+              v = sv[i >> 4];
+            } else {
+              v = sv[i >> 2];
+            }
+            auto pick = [&](const float4& f) { return (i >> 2) % 4 == 0 ? f.x : (i >> 2) % 4 == 1 ? f.y : (i >> 2) % 4 == 2 ? f.z : f.w; };
+            const float kb = RUN4 ? pick(k4) * back : back;
+            if constexpr (RUN4) v = make_float4(pick(v), pick(v), pick(v), pick(v));
+            float2 xa = ffma2(make_float2(s[i], s[i + 1]), make_float2(kb, kb), make_float2(neg, neg));
+            float2 xb = ffma2(make_float2(s[i + 2], s[i + 3]), make_float2(kb, kb), make_float2(neg, neg));
+            if constexpr (RUN4 && decltype(mask)::value) {
+              xa.x = s[i] == -INFINITY ? -INFINITY : xa.x;
+              xa.y = s[i + 1] == -INFINITY ? -INFINITY : xa.y;
+              xb.x = s[i + 2] == -INFINITY ? -INFINITY : xb.x;
+              xb.y = s[i + 3] == -INFINITY ? -INFINITY : xb.y;
+            }
+            const float2 ya = make_float2(fast_exp2(xa.x), fast_exp2(xa.y));
+            const float2 yb = make_float2(fast_exp2(xb.x), fast_exp2(xb.y));
+            sum_a = fadd2(sum_a, ya);
+            sum_b = fadd2(sum_b, yb);
+            float2 za = fmul2(ya, make_float2(v.x, v.y)), zb = fmul2(yb, make_float2(v.z, v.w));
+            if constexpr (decltype(mask)::value) {  // a masked key may have any scale
+              za.x = s[i] == -INFINITY ? 0.f : za.x;
+              za.y = s[i + 1] == -INFINITY ? 0.f : za.y;
+              zb.x = s[i + 2] == -INFINITY ? 0.f : zb.x;
+              zb.y = s[i + 3] == -INFINITY ? 0.f : zb.y;
+            }
+            pk[i2] = pack2<false>(za.x, za.y);
+            pk[i2 + 1] = pack2<false>(zb.x, zb.y);
           }
-          pk[i2] = pack2<false>(za.x, za.y);
-          pk[i2 + 1] = pack2<false>(zb.x, zb.y);
+          tmem_st32(tP + 32 * hh, pk);
         }
-        tmem_st32(tP + 32 * hh, pk);
-      }
+      };
+      if (masked) probabilities(std::true_type());
+      else probabilities(std::false_type());
       l_run += (sum_a.x + sum_a.y) + (sum_b.x + sum_b.y);
       if (j > 0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll
@@ -510,19 +570,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
   }
 }
 
-template <int D, int FMT>
-cudaError_t launch_d(const FwdParams& p, cudaStream_t st) {
+template <int D, int FMT, bool RUN4>
+cudaError_t launch_run(const FwdParams& p, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(p.max_queries) * (p.Hq / p.c.Hkv);
   const int64_t qblocks = (rows + NQ * BM - 1) / (NQ * BM);
   const int64_t ctas = static_cast<int64_t>(p.c.num_seqs) * qblocks * p.c.Hkv;
   if (ctas == 0) return cudaSuccess;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  auto kern = tc_kernel<D, FMT>;
+  auto kern = tc_kernel<D, FMT, RUN4>;
   constexpr int smem = Cfg<D>::SMEM_BYTES;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<static_cast<unsigned>(ctas), NUM_THREADS, smem, st>>>(p, static_cast<int>(qblocks));
   return cudaGetLastError();
+}
+
+template <int D, int FMT>
+cudaError_t launch_d(const FwdParams& p, cudaStream_t st) {
+  return p.c.group % 4 == 0 ? launch_run<D, FMT, true>(p, st) : launch_run<D, FMT, false>(p, st);
 }
 
 }  // namespace tc
