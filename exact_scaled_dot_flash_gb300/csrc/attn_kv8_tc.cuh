@@ -111,8 +111,9 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
   return (c >> 3) * (BN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-// RUN4: every 4 keys share their scales (group and page_size multiples of 4).
-template <int D, int FMT, bool RUN4>
+// RUN: every 1, 4 or 16 keys share their scales (group, and so page_size, a
+// multiple of it).
+template <int D, int FMT, int RUN>
 __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constant__ FwdParams p, int qblocks) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_dyn[];
@@ -235,14 +236,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
           // the softmax of tile j - 2 has read this slot: its P was used before
           // the converted tile that this one replaces (V_j-2) was released
           float* const sc = reinterpret_cast<float*>(smem + C::OFF_SCALE + (j & 1) * C::SCALE_BYTES);
-          if constexpr (RUN4) {
-            if ((lane & 3) == 0) {
-              sc[(cw * 32 + lane) >> 2] = ks * p.scale_log2;
-              sc[BN + ((cw * 32 + lane) >> 2)] = vs;
-            }
-          } else {
-            sc[cw * 32 + lane] = ks * p.scale_log2;
-            sc[BN + cw * 32 + lane] = vs;
+          if (lane % RUN == 0) {
+            sc[(cw * 32 + lane) / RUN] = ks * p.scale_log2;
+            sc[BN + (cw * 32 + lane) / RUN] = vs;
           }
           float top = vs;  // NaN does not count
 #pragma unroll
@@ -398,7 +394,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
       tc_fence_after();
       const float4* const sk = reinterpret_cast<const float4*>(smem + C::OFF_SCALE + (j & 1) * C::SCALE_BYTES);
       const float4* const sv = sk + BN / 4;
-      // s: products times k_scale; RUN4: the products alone
+      // s: products times k_scale; with runs the products alone
       float s[128];
       {
         uint32_t sr[4][32];
@@ -410,7 +406,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
           const uint32_t* const x = &sr[i >> 3][(4 * i) & 31];
           float2 a = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
           float2 b = make_float2(__uint_as_float(x[2]), __uint_as_float(x[3]));
-          if constexpr (!RUN4) {
+          if constexpr (RUN == 1) {
             const float4 k = sk[i];
             a = fmul2(a, make_float2(k.x, k.y));
             b = fmul2(b, make_float2(k.z, k.w));
@@ -420,21 +416,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
       }
       const bool masked = j >= nfull_t;
       if (masked) {
-        const int key0 = j * BN;
+        const int end = lim - j * BN;
+        asm volatile("");  // a branch, not 256 predicated instructions in every tile
 #pragma unroll
         for (int i = 0; i < 128; ++i)
-          if (key0 + i > lim) s[i] = -INFINITY;
+          if (i > end) s[i] = -INFINITY;
       }
       float c0 = -INFINITY, c1 = c0, c2 = c0, c3 = c0;
-      if constexpr (RUN4) {  // scales are not negative: the largest product of a run gives its largest score
+      if constexpr (RUN > 1) {  // scales are not negative: the largest product of a run gives its largest score
+        auto run4 = [&](int i) { return fmaxf(fmax3(s[i], s[i + 1], s[i + 2]), s[i + 3]); };
+        auto run = [&](int r) {
+          if constexpr (RUN == 4) return run4(4 * r);
+          else return fmaxf(fmax3(run4(16 * r), run4(16 * r + 4), run4(16 * r + 8)), run4(16 * r + 12));
+        };
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < BN / RUN / 4; ++i) {
           const float4 k = sk[i];
-          auto run = [&](int r) { return fmaxf(fmax3(s[16 * i + 4 * r], s[16 * i + 4 * r + 1], s[16 * i + 4 * r + 2]), s[16 * i + 4 * r + 3]); };
-          c0 = fmaxf(c0, run(0) * k.x);
-          c1 = fmaxf(c1, run(1) * k.y);
-          c2 = fmaxf(c2, run(2) * k.z);
-          c3 = fmaxf(c3, run(3) * k.w);
+          c0 = fmaxf(c0, run(4 * i) * k.x);
+          c1 = fmaxf(c1, run(4 * i + 1) * k.y);
+          c2 = fmaxf(c2, run(4 * i + 2) * k.z);
+          c3 = fmaxf(c3, run(4 * i + 3) * k.w);
         }
       } else {
 #pragma unroll
@@ -466,19 +467,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
 #pragma unroll
           for (int i2 = 0; i2 < 32; i2 += 2) {
             const int i = 64 * hh + 2 * i2;
-            float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v;
-            if constexpr (RUN4) {
-              k4 = sk[i >> 4];
-              v = sv[i >> 4];
+            float4 v;
+            float kb = back;
+            if constexpr (RUN > 1) {
+              auto pick = [&](const float4* f) {  // of the run that key i lies in
+                const float4 x = f[i / RUN / 4];
+                return i / RUN % 4 == 0 ? x.x : i / RUN % 4 == 1 ? x.y : i / RUN % 4 == 2 ? x.z : x.w;
+              };
+              kb *= pick(sk);
+              const float vr = pick(sv);
+              v = make_float4(vr, vr, vr, vr);
             } else {
               v = sv[i >> 2];
             }
-            auto pick = [&](const float4& f) { return (i >> 2) % 4 == 0 ? f.x : (i >> 2) % 4 == 1 ? f.y : (i >> 2) % 4 == 2 ? f.z : f.w; };
-            const float kb = RUN4 ? pick(k4) * back : back;
-            if constexpr (RUN4) v = make_float4(pick(v), pick(v), pick(v), pick(v));
             float2 xa = ffma2(make_float2(s[i], s[i + 1]), make_float2(kb, kb), make_float2(neg, neg));
             float2 xb = ffma2(make_float2(s[i + 2], s[i + 3]), make_float2(kb, kb), make_float2(neg, neg));
-            if constexpr (RUN4 && decltype(mask)::value) {
+            if constexpr (RUN > 1 && decltype(mask)::value) {
               xa.x = s[i] == -INFINITY ? -INFINITY : xa.x;
               xa.y = s[i + 1] == -INFINITY ? -INFINITY : xa.y;
               xb.x = s[i + 2] == -INFINITY ? -INFINITY : xb.x;
@@ -570,14 +574,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
   }
 }
 
-template <int D, int FMT, bool RUN4>
+template <int D, int FMT, int RUN>
 cudaError_t launch_run(const FwdParams& p, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(p.max_queries) * (p.Hq / p.c.Hkv);
   const int64_t qblocks = (rows + NQ * BM - 1) / (NQ * BM);
   const int64_t ctas = static_cast<int64_t>(p.c.num_seqs) * qblocks * p.c.Hkv;
   if (ctas == 0) return cudaSuccess;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  auto kern = tc_kernel<D, FMT, RUN4>;
+  auto kern = tc_kernel<D, FMT, RUN>;
   constexpr int smem = Cfg<D>::SMEM_BYTES;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -587,7 +591,10 @@ cudaError_t launch_run(const FwdParams& p, cudaStream_t st) {
 
 template <int D, int FMT>
 cudaError_t launch_d(const FwdParams& p, cudaStream_t st) {
-  return p.c.group % 4 == 0 ? launch_run<D, FMT, true>(p, st) : launch_run<D, FMT, false>(p, st);
+  // scales are read once a run: 8 or 32 vector loads fewer for a row and tile
+  return p.c.group % 16 == 0  ? launch_run<D, FMT, 16>(p, st)
+         : p.c.group % 4 == 0 ? launch_run<D, FMT, 4>(p, st)
+                              : launch_run<D, FMT, 1>(p, st);
 }
 
 }  // namespace tc
