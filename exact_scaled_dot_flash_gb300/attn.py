@@ -12,6 +12,7 @@ import contextlib
 import ctypes
 import math
 import os
+import struct
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -199,10 +200,14 @@ def device_status(device: int = 0, clear: bool = False) -> int:
 
 def _dtype_code(t):
     import torch
-    codes = {torch.float32: ATTN_F32, torch.float16: ATTN_F16, torch.bfloat16: ATTN_BF16}
-    if t.dtype not in codes:
-        raise AttnError(f"unsupported dtype {t.dtype}")
-    return codes[t.dtype]
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
+        return ATTN_BF16
+    if dtype is torch.float16:
+        return ATTN_F16
+    if dtype is torch.float32:
+        return ATTN_F32
+    raise AttnError(f"unsupported dtype {dtype}")
 
 
 def call(shape: Shape, q_ptr, k_ptr, v_ptr, mask: int, kv_lens_ptr, bias_ptr, scale: float,
@@ -715,57 +720,73 @@ def paged_mla_bwd(q, qp, latent, kpos, block_table, seq_lens, q_offsets, dout, *
 
 
 # ------------------------------------------------------------------ 8-bit paged cache
-def _on(dev):
-    """The library launches on the current device: make it the tensors' own."""
+# These calls are a few microseconds of GPU work at their smallest, so the
+# marshalling below takes the short way: raw stream handles, one query of a
+# tensor's shape and strides, descriptions packed at once.
+def _launch(dev, fn, *args):
+    """Calls the library with the tensors' device current (it launches on the current one)."""
     import torch
-    if dev.type != "cuda":
-        raise AttnError(f"tensors must be on a CUDA device, not {dev}")
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    if torch._C._cuda_getDevice() == dev.index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args)
+    if rc:
+        check(rc)
 
 
 def _stream(stream, dev, made=()):
     """Handle of ``stream`` (None: the current one). Tensors made here for a call
     on another stream than the current one are kept until that stream is done."""
     import torch
-    cur = torch.cuda.current_stream(dev)
-    if stream is None or stream.cuda_stream == cur.cuda_stream:
-        return cur.cuda_stream or None
-    for t in made:
-        if t is not None:
+    if dev.type != "cuda":
+        raise AttnError(f"tensors must be on a CUDA device, not {dev}")
+    cur = torch._C._cuda_getCurrentRawStream(dev.index)
+    if stream is None:
+        return cur or None
+    handle = stream.cuda_stream
+    if handle != cur:
+        for t in made:
             t.record_stream(stream)
-    return stream.cuda_stream or None
+    return handle or None
 
 
-def _ints(dev, **tensors):
+def _int32(name, t, shape, dev):
     import torch
-    for name, (t, shape) in tensors.items():
-        if t is not None and (t.dtype != torch.int32 or t.device != dev or t.shape != shape
-                              or not t.is_contiguous()):
-            raise AttnError(f"{name} must be a contiguous int32 {list(shape)} tensor on {dev}")
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise AttnError(f"{name} must be a contiguous int32 {list(shape)} tensor on {dev}")
+    return t.data_ptr() or None
 
 
 def _kv8_check(dev, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, offsets, offsets_name):
-    """Checks an 8-bit cache and its metadata; its C description and the number of sequences."""
+    """Checks an 8-bit cache and its metadata: its C description, the number of
+    sequences, max_pages, and the addresses in the order of the arguments."""
     import torch
-    fmt = KV8_INT8 if k_cache.dtype == torch.int8 else KV8_E4M3 if k_cache.dtype == torch.float8_e4m3fn else None
-    if fmt is None or k_cache.dim() != 4 or k_cache.device != dev or not k_cache.is_contiguous():
+    dtype, size = k_cache.dtype, k_cache.shape
+    fmt = KV8_INT8 if dtype is torch.int8 else KV8_E4M3 if dtype is torch.float8_e4m3fn else None
+    if fmt is None or len(size) != 4 or k_cache.device != dev or not k_cache.is_contiguous():
         raise AttnError(f"k_cache must be a contiguous int8 or float8_e4m3fn [pages, page_size, Hkv, D] tensor on {dev}")
-    pages, P, H, D = k_cache.shape
-    if (v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape or v_cache.device != dev
-            or not v_cache.is_contiguous()):
+    pages, P, H, D = size
+    if v_cache.dtype is not dtype or v_cache.shape != size or v_cache.device != dev or not v_cache.is_contiguous():
         raise AttnError("v_cache must be a contiguous tensor like k_cache")
-    if (k_scale.dim() != 3 or k_scale.shape[0] != pages or k_scale.shape[1] != H or k_scale.shape[2] < 1
-            or P % k_scale.shape[2]):
+    scales = k_scale.shape
+    if len(scales) != 3 or scales[0] != pages or scales[1] != H or scales[2] < 1 or P % scales[2]:
         raise AttnError("k_scale must be [pages, Hkv, page_size / group], group a divisor of page_size")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t.dtype != torch.float32 or t.shape != k_scale.shape or t.device != dev or not t.is_contiguous():
-            raise AttnError(f"{name} must be a contiguous float32 {list(k_scale.shape)} tensor on {dev}")
-    ns = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
-    if block_table.dim() != 2:
-        raise AttnError("block_table must be int32 [num_seqs, max_pages]")
-    _ints(dev, block_table=(block_table, (ns, block_table.shape[1])), seq_lens=(seq_lens, (ns,)),
-          **{offsets_name: (offsets, (ns + 1,))})
-    return Kv8Cache(pages, P, H, D, P // k_scale.shape[2], fmt), ns
+    f32 = torch.float32
+    if (k_scale.dtype is not f32 or k_scale.device != dev or not k_scale.is_contiguous() or v_scale.dtype is not f32
+            or v_scale.shape != scales or v_scale.device != dev or not v_scale.is_contiguous()):
+        raise AttnError(f"k_scale and v_scale must be contiguous float32 {list(scales)} tensors on {dev}")
+    lens, table = seq_lens.shape, block_table.shape
+    if len(lens) != 1 or len(table) != 2:
+        raise AttnError("block_table must be int32 [num_seqs, max_pages] and seq_lens int32 [num_seqs]")
+    ns = lens[0]
+    ptrs = (k_cache.data_ptr() or None, v_cache.data_ptr() or None, k_scale.data_ptr() or None,
+            v_scale.data_ptr() or None, _int32("block_table", block_table, (ns, table[1]), dev),
+            _int32("seq_lens", seq_lens, (ns,), dev), _int32(offsets_name, offsets, (ns + 1,), dev))
+    return Kv8Cache(pages, P, H, D, P // scales[2], fmt), ns, table[1], ptrs
+
+
+_STRIDES2 = ctypes.c_int64 * 2
 
 
 def kv8_write(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, tok_offsets, *, stream=None):
@@ -782,22 +803,20 @@ def kv8_write(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, t
     began keeps its scale or gets a larger one, with its codes brought to it.
     """
     dev = k.device
-    shape, ns = _kv8_check(dev, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, tok_offsets, "tok_offsets")
-    for name, t in (("k", k), ("v", v)):
-        if t.dim() != 3 or t.device != dev or t.dtype != k.dtype or t.shape != k.shape:
-            raise AttnError(f"{name} must be a [tokens, Hkv, D] tensor on {dev}, k and v alike")
-        if t.shape[2] > 1 and t.stride(2) != 1:
-            raise AttnError(f"the last dimension of {name} must be contiguous")
-    if k.shape[1] != shape.Hkv or k.shape[2] != shape.D:
-        raise AttnError("k and v must have the cache's Hkv and D")
-    i64 = ctypes.c_int64 * 2
-    with _on(dev):
-        check(load_library().attn_kv8_write(
-            shape, ns, block_table.shape[1], k.shape[0], k.data_ptr() or None, v.data_ptr() or None,
-            i64(k.stride(0), k.stride(1)), i64(v.stride(0), v.stride(1)), block_table.data_ptr() or None,
-            seq_lens.data_ptr() or None, tok_offsets.data_ptr() or None, _dtype_code(k), k_cache.data_ptr() or None,
-            v_cache.data_ptr() or None, k_scale.data_ptr() or None, v_scale.data_ptr() or None,
-            _stream(stream, dev)))
+    cache, ns, max_pages, (kc, vc, ks, vs, bt, sl, to) = _kv8_check(dev, k_cache, v_cache, k_scale, v_scale,
+                                                                   block_table, seq_lens, tok_offsets, "tok_offsets")
+    size = k.shape
+    if len(size) != 3 or size[1] != cache.Hkv or size[2] != cache.D:
+        raise AttnError("k and v must be [tokens, Hkv, D] with the cache's Hkv and D")
+    if v.device != dev or v.dtype is not k.dtype or v.shape != size:
+        raise AttnError(f"v must be a tensor like k, {k.dtype} {list(size)} on {dev}")
+    kst, vst = k.stride(), v.stride()
+    if kst[2] != 1 or vst[2] != 1:
+        raise AttnError("the last dimension of k and v must be contiguous")
+    lib = _lib or load_library()
+    st = _stream(stream, dev)
+    _launch(dev, lib.attn_kv8_write, cache, ns, max_pages, size[0], k.data_ptr() or None, v.data_ptr() or None,
+            _STRIDES2(kst[0], kst[1]), _STRIDES2(vst[0], vst[1]), bt, sl, to, _dtype_code(k), kc, vc, ks, vs, st)
 
 
 def kv8_read(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, row_offsets, num_rows: int | None = None, *,
@@ -815,35 +834,41 @@ def kv8_read(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, row_offs
     import torch
 
     dev = k_cache.device
-    shape, ns = _kv8_check(dev, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, row_offsets, "row_offsets")
-    _ints(dev, starts=(starts, (ns,)))
+    cache, ns, max_pages, (kc, vc, ks, vs, bt, sl, ro) = _kv8_check(dev, k_cache, v_cache, k_scale, v_scale,
+                                                                   block_table, seq_lens, row_offsets, "row_offsets")
     like = k_out if k_out is not None else v_out
     if num_rows is None:
         num_rows = like.shape[0] if like is not None else int(row_offsets[-1].item())
     if dtype is None:
         dtype = like.dtype if like is not None else torch.bfloat16
-    size = (num_rows, shape.Hkv, shape.D)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None and (t.shape != size or t.dtype != dtype or t.device != dev or not t.is_contiguous()):
-            raise AttnError(f"{name} must be a contiguous {dtype} {list(size)} tensor on {dev}")
-    made = []
-    if k_out is None:
-        made.append(k_out := torch.empty(size, dtype=dtype, device=dev))
-    if v_out is None:
-        made.append(v_out := torch.empty(size, dtype=dtype, device=dev))
-    with _on(dev):
-        check(load_library().attn_kv8_read(
-            shape, ns, block_table.shape[1], num_rows, k_cache.data_ptr() or None, v_cache.data_ptr() or None,
-            k_scale.data_ptr() or None, v_scale.data_ptr() or None, block_table.data_ptr() or None,
-            seq_lens.data_ptr() or None, row_offsets.data_ptr() or None, starts.data_ptr() if starts is not None else None,
-            _dtype_code(k_out), k_out.data_ptr() or None, v_out.data_ptr() or None, _stream(stream, dev, made)))
+    size = (num_rows, cache.Hkv, cache.D)
+    if like is None:  # one allocation for both
+        both = k_scale.new_empty((2, *size), dtype=dtype)
+        k_out, v_out = both.unbind(0)
+        made = (both,)
+    else:
+        made = []
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is not None and (t.shape != size or t.dtype is not dtype or t.device != dev or not t.is_contiguous()):
+                raise AttnError(f"{name} must be a contiguous {dtype} {list(size)} tensor on {dev}")
+        if k_out is None:
+            made.append(k_out := torch.empty_like(v_out))
+        if v_out is None:
+            made.append(v_out := torch.empty_like(k_out))
+    lib = _lib or load_library()
+    st = _stream(stream, dev, made)
+    _launch(dev, lib.attn_kv8_read, cache, ns, max_pages, num_rows, kc, vc, ks, vs, bt, sl, ro,
+            _int32("starts", starts, (ns,), dev) if starts is not None else None, _dtype_code(k_out),
+            k_out.data_ptr() or None, v_out.data_ptr() or None, st)
     return k_out, v_out
 
 
 def paged_kv8_workspace_bytes(shape: PagedShape) -> int:
     """Workspace bytes attn_paged_kv8_fwd needs for ``shape``."""
     n = ctypes.c_size_t(0)
-    check(load_library().attn_paged_kv8_workspace_bytes(shape, n))
+    rc = (_lib or load_library()).attn_paged_kv8_workspace_bytes(shape, n)
+    if rc:
+        check(rc)
     return n.value
 
 
@@ -860,38 +885,42 @@ def paged_kv8_fwd(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
     """
     import torch
 
-    dev = q.device
-    if q.dim() != 3 or not q.is_contiguous():
+    dev, size = q.device, q.shape
+    if len(size) != 3 or not q.is_contiguous():
         raise AttnError("q must be a contiguous [queries, Hq, D] tensor")
-    cache, ns = _kv8_check(dev, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, q_offsets, "q_offsets")
-    nq, Hq, D = q.shape
+    cache, ns, max_pages, (kc, vc, ks, vs, bt, sl, qo) = _kv8_check(dev, k_cache, v_cache, k_scale, v_scale,
+                                                                   block_table, seq_lens, q_offsets, "q_offsets")
+    nq, Hq, D = size
     if D != cache.D:
         raise AttnError("q must have the cache's D")
-    _ints(dev, positions=(positions, (nq,)))
+    pos = _int32("positions", positions, (nq,), dev) if positions is not None else None
     if max_queries is None:
         max_queries = int((q_offsets[1:] - q_offsets[:-1]).max().item()) if ns else 0
     made = []
     if out is None:
         made.append(out := torch.empty_like(q))
-    elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+    elif out.shape != size or out.dtype is not q.dtype or out.device != dev or not out.is_contiguous():
         raise AttnError("out must be a contiguous tensor like q")
-    lse = _lse_buffer(lse_out, (nq, Hq), dev) if return_lse else None
-    made.append(lse if lse_out is None else None)
-    shape = PagedShape(ns, nq, Hq, cache.Hkv, D, cache.page_size, cache.num_pages, block_table.shape[1], max_queries)
+    lse = None
+    if return_lse:
+        if lse_out is None:
+            made.append(lse := k_scale.new_empty((nq, Hq)))
+        else:
+            lse = _lse_buffer(lse_out, (nq, Hq), dev)
+    shape = PagedShape(ns, nq, Hq, cache.Hkv, D, cache.page_size, cache.num_pages, max_pages, max_queries)
     need = paged_kv8_workspace_bytes(shape)
-    if need and workspace is None:
-        made.append(workspace := torch.empty(need, dtype=torch.uint8, device=dev))
-    elif need and (workspace.device != dev or workspace.numel() * workspace.element_size() < need
-                   or not workspace.is_contiguous()):
-        raise AttnError(f"workspace must hold {need} contiguous bytes on q's device")
-    with _on(dev):
-        check(load_library().attn_paged_kv8_fwd(
-            shape, cache.group, cache.format, q.data_ptr() or None, k_cache.data_ptr() or None,
-            v_cache.data_ptr() or None, k_scale.data_ptr() or None, v_scale.data_ptr() or None,
-            block_table.data_ptr() or None, seq_lens.data_ptr() or None, q_offsets.data_ptr() or None,
-            positions.data_ptr() if positions is not None else None, 1 if causal else 0,
-            1.0 / math.sqrt(D) if scale is None else scale, _dtype_code(q), workspace.data_ptr() if need else None, need,
-            out.data_ptr() or None, lse.data_ptr() if lse is not None else None, _stream(stream, dev, made)))
+    if need:
+        if workspace is None:
+            made.append(workspace := k_scale.new_empty(((need + 3) // 4,)))
+        elif (workspace.device != dev or workspace.numel() * workspace.element_size() < need
+              or not workspace.is_contiguous()):
+            raise AttnError(f"workspace must hold {need} contiguous bytes on q's device")
+    lib = _lib or load_library()
+    st = _stream(stream, dev, made)
+    _launch(dev, lib.attn_paged_kv8_fwd, shape, cache.group, cache.format, q.data_ptr() or None, kc, vc, ks, vs, bt, sl,
+            qo, pos, 1 if causal else 0, 1.0 / math.sqrt(D) if scale is None else scale, _dtype_code(q),
+            workspace.data_ptr() if need else None, need, out.data_ptr() or None,
+            lse.data_ptr() or None if lse is not None else None, st)
     return (out, lse) if return_lse else out
 
 
@@ -930,60 +959,67 @@ def rope_frequencies(rot: int, *, base: float = 10000.0, scaling: str | None = N
     return w * keep + w / factor * (1.0 - keep), 0.1 * math.log(factor) + 1.0
 
 
+# attn_rope_shape_t: B, S, Hq, Hk, D, rot; the strides of q, k, q_out, k_out; pos_batch_stride
+_ROPE_SHAPE = struct.Struct("6i13q")
+
+
 def _rope(q, k, positions, inv_freq, layout, mscale, inverse, q_out, k_out, stream):
     import torch
 
-    dev = q.device
+    dev, dtype, size = q.device, q.dtype, q.shape
     if layout not in ("half", "interleaved"):
         raise AttnError(f"layout must be 'half' or 'interleaved', not {layout!r}")
-    dim = q.dim()
-    if dim not in (3, 4):
+    dim = len(size)
+    if dim == 3:  # packed tokens: one batch
+        B, (S, Hq, D) = 1, size
+    elif dim == 4:  # dense: the heads outside the tokens
+        B, Hq, S, D = size
+    else:
         raise AttnError("q must be [tokens, Hq, D] or [B, Hq, S, D]")
-    if k is None:
-        k_out = None
     made = []
     if q_out is None:
-        made.append(q_out := torch.empty(q.shape, dtype=q.dtype, device=dev))
-    if k is not None and k_out is None:
-        made.append(k_out := torch.empty(k.shape, dtype=k.dtype, device=dev))
-    tensors = [("q", q), ("q_out", q_out)] + ([("k", k), ("k_out", k_out)] if k is not None else [])
-    for name, t in tensors:
-        if t.dtype != q.dtype or t.device != dev or t.dim() != dim:
-            raise AttnError(f"{name} must be a {dim}-D {q.dtype} tensor on {dev}")
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
+        made.append(q_out := q.new_empty(size))
+    elif q_out.dtype is not dtype or q_out.device != dev or q_out.shape != size:
+        raise AttnError(f"q_out must be a {dtype} {list(size)} tensor on {dev}")
+
+    def strides(name, t):  # batch, token, head
+        st = t.stride()
+        if st[-1] != 1 and D > 1:
             raise AttnError(f"the last dimension of {name} must be contiguous")
-    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
-        raise AttnError("q_out and k_out must be shaped like q and k")
-    # packed [tokens, H, D] is one batch; dense [B, H, S, D] has its heads outside its tokens
-    if dim == 3:
-        B, (S, Hq, D) = 1, q.shape
-        strides = lambda t: (0, t.stride(0), t.stride(1))  # noqa: E731
-        if k is not None and (k.shape[0] != S or k.shape[2] != D):
-            raise AttnError("k must be [tokens, Hk, D] with q's tokens and D")
-        if positions.shape != (S,):
-            raise AttnError("positions must be int32 [tokens]")
+        return (0, st[0], st[1]) if dim == 3 else (st[0], st[2], st[1])
+
+    if k is None:
+        Hk, kst, kost, k_out = 0, (0, 0, 0), (0, 0, 0), None
     else:
-        B, Hq, S, D = q.shape
-        strides = lambda t: (t.stride(0), t.stride(2), t.stride(1))  # noqa: E731
-        if k is not None and (k.shape[0] != B or k.shape[2] != S or k.shape[3] != D):
-            raise AttnError("k must be [B, Hk, S, D] with q's B, S and D")
-        if positions.shape != (S,) and positions.shape != (B, S):
-            raise AttnError("positions must be int32 [S] or [B, S]")
-    if positions.dtype != torch.int32 or positions.device != dev or not positions.is_contiguous():
-        raise AttnError(f"positions must be a contiguous int32 tensor on {dev}")
-    if (inv_freq.dtype != torch.float64 or inv_freq.device != dev or inv_freq.dim() != 1
+        ksize = k.shape
+        Hk = ksize[1] if len(ksize) == dim else -1
+        if k.dtype is not dtype or k.device != dev or ksize != ((S, Hk, D) if dim == 3 else (B, Hk, S, D)):
+            raise AttnError(f"k must be a {dtype} tensor on {dev} like q but for its heads")
+        if k_out is None:
+            made.append(k_out := k.new_empty(ksize))
+        elif k_out.dtype is not dtype or k_out.device != dev or k_out.shape != ksize:
+            raise AttnError(f"k_out must be a {dtype} {list(ksize)} tensor on {dev}")
+        kst, kost = strides("k", k), strides("k_out", k_out)
+    pos = positions.shape
+    if (pos != (S,) and (dim == 3 or pos != (B, S))) or positions.dtype is not torch.int32 or positions.device != dev \
+            or not positions.is_contiguous():
+        raise AttnError(f"positions must be a contiguous int32 tensor on {dev}, "
+                        + ("[tokens]" if dim == 3 else "[S] or [B, S]"))
+    if (inv_freq.dtype is not torch.float64 or inv_freq.device != dev or inv_freq.dim() != 1
             or not inv_freq.is_contiguous()):
         raise AttnError(f"inv_freq must be a contiguous float64 [rot / 2] tensor on {dev}")
-    i64 = ctypes.c_int64 * 3
-    Hk = 0 if k is None else k.shape[1]
-    shape = RopeShape(B, S, Hq, Hk, D, 2 * inv_freq.shape[0], i64(*strides(q)), i64(*strides(k)) if Hk else i64(),
-                      i64(*strides(q_out)), i64(*strides(k_out)) if Hk else i64(), S if positions.dim() == 2 else 0)
-    with _on(dev):
-        check(load_library().attn_rope(
-            shape, q.data_ptr() or None, k.data_ptr() or None if Hk else None, positions.data_ptr() or None,
-            inv_freq.data_ptr() or None, ROPE_HALF if layout == "half" else ROPE_INTERLEAVED, inverse, mscale,
-            _dtype_code(q), q_out.data_ptr() or None, k_out.data_ptr() or None if Hk else None,
-            _stream(stream, dev, made)))
+    try:
+        shape = RopeShape.from_buffer_copy(_ROPE_SHAPE.pack(
+            B, S, Hq, Hk, D, 2 * inv_freq.shape[0], *strides("q", q), *kst, *strides("q_out", q_out), *kost,
+            S if len(pos) == 2 else 0))
+    except struct.error as e:
+        raise AttnError(f"a dimension is out of range: {e}") from None
+    lib = _lib or load_library()
+    st = _stream(stream, dev, made)
+    _launch(dev, lib.attn_rope, shape, q.data_ptr() or None, k.data_ptr() or None if Hk else None,
+            positions.data_ptr() or None, inv_freq.data_ptr() or None,
+            ROPE_HALF if layout == "half" else ROPE_INTERLEAVED, inverse, mscale, _dtype_code(q),
+            q_out.data_ptr() or None, k_out.data_ptr() or None if Hk else None, st)
     return q_out, k_out
 
 
