@@ -14,8 +14,10 @@
 // rounding of f to double leaves position * 2^-53 of a turn.
 //
 // Bytes: every element is read once and written once, and nothing else counts:
-// the angles of a token are computed once for all its heads, in shared memory.
-// A thread moves 16-byte vectors.
+// the angles of a token are computed once for all its heads, in shared memory,
+// while the first vectors are on their way. A thread moves 16-byte vectors,
+// BATCH of them (or pairs) in flight; the offsets of a CTA's tokens are computed
+// once (64-bit divisions in the row loop cost more than the copy).
 #include <math.h>
 
 #include <algorithm>
@@ -29,21 +31,24 @@ namespace rope {
 
 constexpr int THREADS = 256;
 
+constexpr int MAX_TOK = 4;  // tokens of a CTA
+constexpr int BATCH = 4;
+
 struct Side {  // queries or keys
   const void* in;
   void* out;
-  int H, copy_tail;
+  int copy_tail;
   int64_t ib, it, ih, ob, ot, oh;  // batch, token and head strides (elements)
 };
 
 struct Params {
-  int B, S, D, rot;
+  int B, S, D, rot, Hq, H;  // H: heads of queries and keys together
   int64_t pos_batch;  // 0 or S: one row of positions for all, or one each
   const int32_t* pos;
   const double* freq;
   float mscale;
   int inverse, tok;  // tok: tokens of a CTA
-  Side a, b;
+  Side side[2];
 };
 
 template <int DT> struct Elem;
@@ -66,82 +71,113 @@ struct alignas(N * sizeof(T)) Vec {
 
 // Items of a head: pairs of vectors (halves) or single vectors (interleaved),
 // then the vectors of the copied tail. N = 1: elements instead of vectors
-// (interleaved: pairs), for rows that 16-byte accesses do not fit.
-template <int DT, bool HALVES, int N>
-__device__ __forceinline__ void side(const Params& p, const Side& s, const float2* cs, int64_t tok0, int ntok) {
-  using T = typename Elem<DT>::T;
-  using V = Vec<T, N>;
-  const int half = p.rot >> 1;
-  const int turn = HALVES ? half / N : (N > 1 ? p.rot / N : half);
-  const int items = turn + (s.copy_tail ? (p.D - p.rot) / N : 0);
-  const int per = items < THREADS ? THREADS / items : 1;  // heads side by side in the CTA
-  const int h0 = items < THREADS ? threadIdx.x / items : 0;
-  if (h0 >= per) return;
-  const int rows = ntok * s.H;
-  for (int item = threadIdx.x - h0 * items; item < items; item += THREADS) {
-    for (int r = h0; r < rows; r += per) {
-      const int t = r / s.H, h = r - t * s.H;
-      const int64_t g = tok0 + t, b = g / p.S, q = g - b * p.S;
-      const T* in = static_cast<const T*>(s.in) + b * s.ib + q * s.it + h * s.ih;
-      T* out = static_cast<T*>(s.out) + b * s.ob + q * s.ot + h * s.oh;
-      const float2* c = cs + t * half;
-      if (item >= turn) {
-        const int i = p.rot + (item - turn) * N;
-        *reinterpret_cast<V*>(out + i) = *reinterpret_cast<const V*>(in + i);
-      } else if constexpr (HALVES) {
-        const int i = item * N;
-        V x = *reinterpret_cast<const V*>(in + i), y = *reinterpret_cast<const V*>(in + half + i);
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const float u = to_f(x.x[k]), v = to_f(y.x[k]);
-          const float2 w = c[i + k];
-          from_f(x.x[k], u * w.x - v * w.y);
-          from_f(y.x[k], v * w.x + u * w.y);
-        }
-        *reinterpret_cast<V*>(out + i) = x;
-        *reinterpret_cast<V*>(out + half + i) = y;
-      } else {
-        constexpr int M = N > 1 ? N : 2;
-        const int i = item * M;
-        Vec<T, M> x;
-        if constexpr (N > 1) {
-          x = *reinterpret_cast<const V*>(in + i);
-        } else {
-          x.x[0] = in[i];
-          x.x[1] = in[i + 1];
-        }
-#pragma unroll
-        for (int k = 0; k < M; k += 2) {
-          const float u = to_f(x.x[k]), v = to_f(x.x[k + 1]);
-          const float2 w = c[(i + k) >> 1];
-          from_f(x.x[k], u * w.x - v * w.y);
-          from_f(x.x[k + 1], v * w.x + u * w.y);
-        }
-        if constexpr (N > 1) {
-          *reinterpret_cast<V*>(out + i) = x;
-        } else {
-          out[i] = x.x[0];
-          out[i + 1] = x.x[1];
-        }
-      }
-    }
-  }
-}
-
+// (interleaved: pairs), for rows that 16-byte accesses do not fit. A thread keeps
+// its item and goes through the CTA's rows (token, head).
 template <int DT, bool HALVES, int N>
 __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ Params p) {
-  extern __shared__ float2 cs[];  // [tok][rot / 2] cos, sin times mscale
+  using T = typename Elem<DT>::T;
+  using V = Vec<T, N>;
+  constexpr int M = HALVES || N > 1 ? N : 2;  // elements of the first access
+  using V1 = Vec<T, M>;                       // (not one access where N is 1)
+  extern __shared__ float2 cs[];              // [tok][rot / 2] cos, sin times mscale
+  __shared__ int64_t off[2][2][MAX_TOK];      // element offset of a token: side, in / out
   const int half = p.rot >> 1;
   const int64_t total = static_cast<int64_t>(p.B) * p.S;
   const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tok;
   const int ntok = static_cast<int>(min(static_cast<int64_t>(p.tok), total - tok0));
+  if (threadIdx.x < ntok) {
+    const int64_t g = tok0 + threadIdx.x, b = g / p.S, q = g - b * p.S;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      off[i][0][threadIdx.x] = b * p.side[i].ib + q * p.side[i].it;
+      off[i][1][threadIdx.x] = b * p.side[i].ob + q * p.side[i].ot;
+    }
+  }
+  __syncthreads();
+
+  const int turn = HALVES ? half / N : (N > 1 ? p.rot / N : half);
+  const int items = turn + (p.side[0].copy_tail | p.side[1].copy_tail ? (p.D - p.rot) / N : 0);
+  const int per = items < THREADS ? THREADS / items : 1;  // rows side by side in the CTA
+  const int r0 = items < THREADS ? threadIdx.x / items : 0;
+  const int rows = r0 < per ? ntok * p.H : 0;
+  const int first = threadIdx.x - r0 * items, rstep = per * gridDim.y;
+  struct Row {
+    const T* in;
+    T* out;
+    int t;
+    bool tail_here;
+  };
+  auto row_of = [&](int r) {
+    const int t = (r >= p.H) + (r >= 2 * p.H) + (r >= 3 * p.H);
+    const int h = r - t * p.H, sd = h >= p.Hq ? 1 : 0, hh = h - sd * p.Hq;
+    const Side& s = p.side[sd];
+    return Row{static_cast<const T*>(s.in) + off[sd][0][t] + hh * s.ih, static_cast<T*>(s.out) + off[sd][1][t] + hh * s.oh,
+               t, s.copy_tail != 0};
+  };
+  V1 x[BATCH];
+  V y[BATCH];
+  auto load = [&](int item, int r) {
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      if (r + u * rstep >= rows) break;
+      const Row w = row_of(r + u * rstep);
+      if (item >= turn) {
+        if (w.tail_here) y[u] = *reinterpret_cast<const V*>(w.in + p.rot + (item - turn) * N);
+      } else if constexpr (HALVES) {
+        x[u] = *reinterpret_cast<const V1*>(w.in + item * N);
+        y[u] = *reinterpret_cast<const V*>(w.in + half + item * N);
+      } else if constexpr (N > 1) {
+        x[u] = *reinterpret_cast<const V1*>(w.in + item * N);
+      } else {
+        x[u].x[0] = w.in[2 * item];
+        x[u].x[1] = w.in[2 * item + 1];
+      }
+    }
+  };
+  auto finish = [&](int item, int r) {
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      if (r + u * rstep >= rows) break;
+      const Row w = row_of(r + u * rstep);
+      const float2* const c = cs + w.t * half;
+      if (item >= turn) {
+        if (w.tail_here) *reinterpret_cast<V*>(w.out + p.rot + (item - turn) * N) = y[u];
+      } else if constexpr (HALVES) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const float a = to_f(x[u].x[k]), b = to_f(y[u].x[k]);
+          const float2 f = c[item * N + k];
+          from_f(x[u].x[k], a * f.x - b * f.y);
+          from_f(y[u].x[k], b * f.x + a * f.y);
+        }
+        *reinterpret_cast<V1*>(w.out + item * N) = x[u];
+        *reinterpret_cast<V*>(w.out + half + item * N) = y[u];
+      } else {
+#pragma unroll
+        for (int k = 0; k < M; k += 2) {
+          const float a = to_f(x[u].x[k]), b = to_f(x[u].x[k + 1]);
+          const float2 f = c[(item * M + k) >> 1];
+          from_f(x[u].x[k], a * f.x - b * f.y);
+          from_f(x[u].x[k + 1], b * f.x + a * f.y);
+        }
+        if constexpr (N > 1) {
+          *reinterpret_cast<V1*>(w.out + item * N) = x[u];
+        } else {
+          w.out[2 * item] = x[u].x[0];
+          w.out[2 * item + 1] = x[u].x[1];
+        }
+      }
+    }
+  };
+  const int row0 = r0 + blockIdx.y * per;
+  if (first < items) load(first, row0);
   for (int i = threadIdx.x; i < half; i += THREADS) {
     constexpr double INV_2PI = 0.15915494309189533577;
     const double f = __ldg(p.freq + i) * INV_2PI;
     const uint64_t F = __double2ull_rd((f - floor(f)) * 18446744073709551616.0);
     for (int t = 0; t < ntok; ++t) {
-      const int64_t g = tok0 + t, b = g / p.S;
-      const int64_t pos = __ldg(p.pos + b * p.pos_batch + (g - b * p.S));
+      const int64_t g = tok0 + t;
+      const int64_t pos = __ldg(p.pos + (p.pos_batch ? g : (p.B == 1 ? g : g % p.S)));
       const int32_t top = static_cast<int32_t>(static_cast<uint32_t>((static_cast<uint64_t>(pos) * F) >> 32));
       float sn, cn;
       sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31
@@ -149,8 +185,12 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ P
     }
   }
   __syncthreads();
-  side<DT, HALVES, N>(p, p.a, cs, tok0, ntok);
-  if (p.b.H > 0) side<DT, HALVES, N>(p, p.b, cs, tok0, ntok);
+  for (int item = first; item < items; item += THREADS) {
+    for (int r = row0; r < rows; r += BATCH * rstep) {
+      if (item != first || r != row0) load(item, r);
+      finish(item, r);
+    }
+  }
 }
 
 template <int DT>
@@ -242,7 +282,7 @@ extern "C" int attn_rope(const attn_rope_shape_t* shape, const void* q, const vo
   }
   const int64_t tokens = static_cast<int64_t>(s.B) * s.S;
   if (tokens == 0) return ATTN_OK;
-  if (tokens > 0x7fffffffLL || static_cast<int64_t>(std::max(s.Hq, s.Hk)) * 4 > 0x7fffffffLL) return ATTN_ERR_SHAPE;
+  if (tokens > 0x7fffffffLL || (static_cast<int64_t>(s.Hq) + s.Hk) * 64 > 0x7fffffffLL) return ATTN_ERR_SHAPE;
   if (!q || !q_out || !positions || !inv_freq || (s.Hk > 0 && (!k || !k_out))) return ATTN_ERR_NULL;
   const int es = dtype == ATTN_F32 ? 4 : 2;
   const void* ptr[4] = {q, q_out, k, k_out};
@@ -288,19 +328,21 @@ extern "C" int attn_rope(const attn_rope_shape_t* shape, const void* q, const vo
   p.freq = inv_freq;
   p.mscale = mscale;
   p.inverse = inverse;
-  auto make = [&](int i) {
+  for (int i = 0; i < nside; ++i) {
     const int64_t *a = st[2 * i], *b = st[2 * i + 1];
-    return Side{ptr[2 * i], const_cast<void*>(ptr[2 * i + 1]), heads[2 * i], in_place[i] ? 0 : 1,
-                a[0], a[1], a[2], b[0], b[1], b[2]};
-  };
-  p.a = make(0);
-  if (nside == 2) p.b = make(1);
+    p.side[i] = Side{ptr[2 * i], const_cast<void*>(ptr[2 * i + 1]), in_place[i] ? 0 : 1, a[0], a[1], a[2], b[0], b[1], b[2]};
+  }
+  p.Hq = s.Hq;
+  p.H = s.Hq + (nside == 2 ? s.Hk : 0);
   const bool halves = layout == ATTN_ROPE_HALF;
   const int n = dtype == ATTN_F32 ? 4 : 8;
   vec = vec && (halves ? s.rot / 2 : s.rot) % n == 0 && (s.D - s.rot) % n == 0;
-  // a CTA takes 4 tokens when that still leaves several CTAs for each SM
-  p.tok = tokens >= 152 * 16 ? 4 : 1;
-  const dim3 grid(static_cast<unsigned>((tokens + p.tok - 1) / p.tok));
+  // A CTA takes 4 tokens when that still leaves several CTAs for each SM; with
+  // few tokens the heads of one are dealt to up to 8 CTAs.
+  p.tok = tokens >= 152 * 16 ? attn::rope::MAX_TOK : 1;
+  const int64_t want = 2 * 152 / tokens;
+  const unsigned split = static_cast<unsigned>(std::min<int64_t>({want > 1 ? want : 1, 8, (p.H + 7) / 8}));
+  const dim3 grid(static_cast<unsigned>((tokens + p.tok - 1) / p.tok), split);
   cudaError_t e;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (dtype == ATTN_F32) e = attn::rope::launch_dt<0>(p, halves, vec, grid, cs);
