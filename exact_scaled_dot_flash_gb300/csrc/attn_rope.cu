@@ -15,9 +15,14 @@
 //
 // Bytes: every element is read once and written once, and nothing else counts:
 // the angles of a token are computed once for all its heads, in shared memory,
-// while the first vectors are on their way. A thread moves 16-byte vectors,
-// BATCH of them (or pairs) in flight; the offsets of a CTA's tokens are computed
-// once (64-bit divisions in the row loop cost more than the copy).
+// while the first vectors are on their way. A thread moves 16-byte vectors. The
+// addresses of a CTA's rows are computed once, in shared memory: with every
+// thread working out its own for every 16 bytes, the instructions were the bound
+// (72 us for 8191 tokens of 40 F16 heads, D 128). For the 16-bit types, whose
+// vectors take twice the conversions, many threads with one vector each beat few
+// with several in flight (8 CTAs an SM and 1: 36.5 us, 4.6 TB/s; 4 and 4: 49 us);
+// for F32 it is the other way round (16384 tokens of 64 heads: 160 us, 6.7 TB/s,
+// with 4 vectors and 2 tokens a CTA, 171 us as the 16-bit types).
 #include <math.h>
 
 #include <algorithm>
@@ -31,8 +36,7 @@ namespace rope {
 
 constexpr int THREADS = 256;
 
-constexpr int MAX_TOK = 4;  // tokens of a CTA
-constexpr int BATCH = 4;
+constexpr int MAX_ROWS = 512;  // (token, head) rows of a CTA
 
 struct Side {  // queries or keys
   const void* in;
@@ -47,14 +51,16 @@ struct Params {
   const int32_t* pos;
   const double* freq;
   float mscale;
-  int inverse, tok;  // tok: tokens of a CTA
+  int inverse, tok, heads;  // tokens and heads of a CTA (blockIdx.y: which heads)
   Side side[2];
 };
 
+// VEC: elements of 16 bytes; BATCH: vectors a thread has in flight; CTAS: of an
+// SM; TOKENS: of a CTA, where there are many.
 template <int DT> struct Elem;
-template <> struct Elem<0> { using T = float; static constexpr int VEC = 4; };
-template <> struct Elem<1> { using T = __half; static constexpr int VEC = 8; };
-template <> struct Elem<2> { using T = __nv_bfloat16; static constexpr int VEC = 8; };
+template <> struct Elem<0> { using T = float; static constexpr int VEC = 4, BATCH = 4, CTAS = 4, TOKENS = 2; };
+template <> struct Elem<1> { using T = __half; static constexpr int VEC = 8, BATCH = 1, CTAS = 8, TOKENS = 4; };
+template <> struct Elem<2> { using T = __nv_bfloat16; static constexpr int VEC = 8, BATCH = 1, CTAS = 8, TOKENS = 4; };
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -74,24 +80,28 @@ struct alignas(N * sizeof(T)) Vec {
 // (interleaved: pairs), for rows that 16-byte accesses do not fit. A thread keeps
 // its item and goes through the CTA's rows (token, head).
 template <int DT, bool HALVES, int N>
-__global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(THREADS, Elem<DT>::CTAS) rope_kernel(const __grid_constant__ Params p) {
   using T = typename Elem<DT>::T;
   using V = Vec<T, N>;
+  constexpr int BATCH = Elem<DT>::BATCH;
   constexpr int M = HALVES || N > 1 ? N : 2;  // elements of the first access
   using V1 = Vec<T, M>;                       // (not one access where N is 1)
   extern __shared__ float2 cs[];              // [tok][rot / 2] cos, sin times mscale
-  __shared__ int64_t off[2][2][MAX_TOK];      // element offset of a token: side, in / out
+  __shared__ struct { const T* in; T* out; } row_s[MAX_ROWS];
+  __shared__ int16_t tok_s[MAX_ROWS];         // token, + 256 if the tail is copied
   const int half = p.rot >> 1;
   const int64_t total = static_cast<int64_t>(p.B) * p.S;
   const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tok;
   const int ntok = static_cast<int>(min(static_cast<int64_t>(p.tok), total - tok0));
-  if (threadIdx.x < ntok) {
-    const int64_t g = tok0 + threadIdx.x, b = g / p.S, q = g - b * p.S;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      off[i][0][threadIdx.x] = b * p.side[i].ib + q * p.side[i].it;
-      off[i][1][threadIdx.x] = b * p.side[i].ob + q * p.side[i].ot;
-    }
+  const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.H - h0);
+  const int nrow = ntok * nh;
+  for (int r = threadIdx.x; r < nrow; r += THREADS) {
+    const int t = r / nh, h = h0 + r - t * nh, sd = h >= p.Hq ? 1 : 0, hh = h - sd * p.Hq;
+    const int64_t g = tok0 + t, b = p.B == 1 ? 0 : g / p.S, q = g - b * p.S;
+    const Side& s = p.side[sd];
+    row_s[r].in = static_cast<const T*>(s.in) + b * s.ib + q * s.it + hh * s.ih;
+    row_s[r].out = static_cast<T*>(s.out) + b * s.ob + q * s.ot + hh * s.oh;
+    tok_s[r] = static_cast<int16_t>(t + (s.copy_tail ? 256 : 0));
   }
   __syncthreads();
 
@@ -99,30 +109,17 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ P
   const int items = turn + (p.side[0].copy_tail | p.side[1].copy_tail ? (p.D - p.rot) / N : 0);
   const int per = items < THREADS ? THREADS / items : 1;  // rows side by side in the CTA
   const int r0 = items < THREADS ? threadIdx.x / items : 0;
-  const int rows = r0 < per ? ntok * p.H : 0;
-  const int first = threadIdx.x - r0 * items, rstep = per * gridDim.y;
-  struct Row {
-    const T* in;
-    T* out;
-    int t;
-    bool tail_here;
-  };
-  auto row_of = [&](int r) {
-    const int t = (r >= p.H) + (r >= 2 * p.H) + (r >= 3 * p.H);
-    const int h = r - t * p.H, sd = h >= p.Hq ? 1 : 0, hh = h - sd * p.Hq;
-    const Side& s = p.side[sd];
-    return Row{static_cast<const T*>(s.in) + off[sd][0][t] + hh * s.ih, static_cast<T*>(s.out) + off[sd][1][t] + hh * s.oh,
-               t, s.copy_tail != 0};
-  };
+  const int rows = r0 < per ? nrow : 0;
+  const int first = threadIdx.x - r0 * items;
   V1 x[BATCH];
   V y[BATCH];
   auto load = [&](int item, int r) {
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
-      if (r + u * rstep >= rows) break;
-      const Row w = row_of(r + u * rstep);
+      if (r + u * per >= rows) break;
+      const auto w = row_s[r + u * per];
       if (item >= turn) {
-        if (w.tail_here) y[u] = *reinterpret_cast<const V*>(w.in + p.rot + (item - turn) * N);
+        y[u] = *reinterpret_cast<const V*>(w.in + p.rot + (item - turn) * N);
       } else if constexpr (HALVES) {
         x[u] = *reinterpret_cast<const V1*>(w.in + item * N);
         y[u] = *reinterpret_cast<const V*>(w.in + half + item * N);
@@ -137,11 +134,12 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ P
   auto finish = [&](int item, int r) {
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
-      if (r + u * rstep >= rows) break;
-      const Row w = row_of(r + u * rstep);
-      const float2* const c = cs + w.t * half;
+      if (r + u * per >= rows) break;
+      const auto w = row_s[r + u * per];
+      const int tok = tok_s[r + u * per];
+      const float2* const c = cs + (tok & 255) * half;
       if (item >= turn) {
-        if (w.tail_here) *reinterpret_cast<V*>(w.out + p.rot + (item - turn) * N) = y[u];
+        if (tok & 256) *reinterpret_cast<V*>(w.out + p.rot + (item - turn) * N) = y[u];
       } else if constexpr (HALVES) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
@@ -169,25 +167,23 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ P
       }
     }
   };
-  const int row0 = r0 + blockIdx.y * per;
-  if (first < items) load(first, row0);
-  for (int i = threadIdx.x; i < half; i += THREADS) {
+  if (first < items) load(first, r0);
+  for (int e = threadIdx.x; e < ntok * half; e += THREADS) {
     constexpr double INV_2PI = 0.15915494309189533577;
+    const int t = e / half, i = e - t * half;
+    const int64_t g = tok0 + t;
+    const int64_t pos = __ldg(p.pos + (p.pos_batch || p.B == 1 ? g : g % p.S));
     const double f = __ldg(p.freq + i) * INV_2PI;
     const uint64_t F = __double2ull_rd((f - floor(f)) * 18446744073709551616.0);
-    for (int t = 0; t < ntok; ++t) {
-      const int64_t g = tok0 + t;
-      const int64_t pos = __ldg(p.pos + (p.pos_batch ? g : (p.B == 1 ? g : g % p.S)));
-      const int32_t top = static_cast<int32_t>(static_cast<uint32_t>((static_cast<uint64_t>(pos) * F) >> 32));
-      float sn, cn;
-      sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31
-      cs[t * half + i] = make_float2(cn * p.mscale, (p.inverse ? -sn : sn) * p.mscale);
-    }
+    const int32_t top = static_cast<int32_t>(static_cast<uint32_t>((static_cast<uint64_t>(pos) * F) >> 32));
+    float sn, cn;
+    sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31
+    cs[e] = make_float2(cn * p.mscale, (p.inverse ? -sn : sn) * p.mscale);
   }
   __syncthreads();
   for (int item = first; item < items; item += THREADS) {
-    for (int r = row0; r < rows; r += BATCH * rstep) {
-      if (item != first || r != row0) load(item, r);
+    for (int r = r0; r < rows; r += BATCH * per) {
+      if (item != first || r != r0) load(item, r);
       finish(item, r);
     }
   }
@@ -337,12 +333,16 @@ extern "C" int attn_rope(const attn_rope_shape_t* shape, const void* q, const vo
   const bool halves = layout == ATTN_ROPE_HALF;
   const int n = dtype == ATTN_F32 ? 4 : 8;
   vec = vec && (halves ? s.rot / 2 : s.rot) % n == 0 && (s.D - s.rot) % n == 0;
-  // A CTA takes 4 tokens when that still leaves several CTAs for each SM; with
-  // few tokens the heads of one are dealt to up to 8 CTAs.
-  p.tok = tokens >= 152 * 16 ? attn::rope::MAX_TOK : 1;
-  const int64_t want = 2 * 152 / tokens;
-  const unsigned split = static_cast<unsigned>(std::min<int64_t>({want > 1 ? want : 1, 8, (p.H + 7) / 8}));
-  const dim3 grid(static_cast<unsigned>((tokens + p.tok - 1) / p.tok), split);
+  // A CTA takes several tokens when that still leaves several CTAs for each SM;
+  // with few tokens the heads of one are dealt to up to 8 CTAs.
+  const int several = dtype == ATTN_F32 ? attn::rope::Elem<0>::TOKENS : attn::rope::Elem<2>::TOKENS;
+  p.tok = tokens >= 152 * 16 && p.H * several <= attn::rope::MAX_ROWS ? several : 1;
+  const int64_t want = std::min<int64_t>({2 * 152 / tokens, 8, (p.H + 7) / 8});
+  const int64_t least = (static_cast<int64_t>(p.H) * p.tok + attn::rope::MAX_ROWS - 1) / attn::rope::MAX_ROWS;
+  const int split = static_cast<int>(std::max(want, least));
+  if (split > 65535) return ATTN_ERR_SHAPE;
+  p.heads = (p.H + split - 1) / split;
+  const dim3 grid(static_cast<unsigned>((tokens + p.tok - 1) / p.tok), static_cast<unsigned>((p.H + p.heads - 1) / p.heads));
   cudaError_t e;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (dtype == ATTN_F32) e = attn::rope::launch_dt<0>(p, halves, vec, grid, cs);
