@@ -21,6 +21,8 @@
 // rounded once to the output type.
 #include <math.h>
 
+#include <type_traits>
+
 #include "attn.h"
 #include "kv8.cuh"
 #include "simt.cuh"
@@ -29,6 +31,7 @@ namespace attn {
 namespace kv8 {
 
 constexpr int THREADS = 256;
+constexpr int WRITE_UNITS = 8;
 
 struct WriteParams {
   Cache c;
@@ -41,19 +44,42 @@ struct WriteParams {
 };
 
 // ------------------------------------------------------------------ element access
+// 8 elements as they lie in memory (16-bit types: 4 registers).
+template <int DT>
+struct Raw8 {
+  uint4 w[DT == 0 ? 2 : 1];
+};
+
 template <int DT, bool VEC>
-__device__ __forceinline__ void load8x(const void* base, int64_t i, float (&x)[8]) {
+__device__ __forceinline__ Raw8<DT> load_raw(const void* base, int64_t i) {
+  Raw8<DT> r;
   if constexpr (VEC) {
-    float4 a, b;
-    simt::load8<DT>(base, static_cast<size_t>(i) >> 3, a, b);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if constexpr (DT == 0) x[k] = __ldg(static_cast<const float*>(base) + i + k);
-      else if constexpr (DT == 1) x[k] = __half2float(__ldg(static_cast<const __half*>(base) + i + k));
-      else x[k] = __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(base) + i + k));
+    for (int k = 0; k < (DT == 0 ? 2 : 1); ++k)
+      r.w[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + i * (DT == 0 ? 4 : 2)) + k);
+  } else {
+    using E = std::conditional_t<DT == 0, uint32_t, uint16_t>;
+    E* const e = reinterpret_cast<E*>(r.w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = __ldg(static_cast<const E*>(base) + i + k);
+  }
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void expand(const Raw8<DT>& r, float (&x)[8]) {
+  if constexpr (DT == 0) {
+    const float* const f = reinterpret_cast<const float*>(r.w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = f[k];
+  } else {
+    const uint32_t* const w = reinterpret_cast<const uint32_t*>(r.w);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = DT == 1 ? __half22float2(*reinterpret_cast<const __half2*>(w + k))
+                               : make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+      x[2 * k] = f.x;
+      x[2 * k + 1] = f.y;
     }
   }
 }
@@ -70,13 +96,68 @@ __device__ __forceinline__ int nearest8(float x, float s, float inv) {
   return static_cast<int>(fminf(fmaxf(r, -127.f), 127.f));
 }
 
-template <int FMT>
-__device__ __forceinline__ uint32_t encode4(const float* x, float s, float inv) {
-  if constexpr (FMT == FMT_INT8) {
+// Four of them: rounded by the addition of 1.5 * 2^23, whose sum holds the
+// integer in its low byte; only where a residual reaches s / 2 are they settled
+// one by one.
+__device__ __forceinline__ uint32_t nearest8x4(const float* x, float s, float inv) {
+  constexpr float ROUND = 12582912.f;
+  float q[4], worst = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    q[k] = fmaf(x[k], inv, ROUND);
+    worst = fmaxf(worst, fabsf(fmaf(ROUND - q[k], s, x[k])));
+  }
+  if (worst >= 0.5f * s) {
     uint32_t w = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) w |= (static_cast<uint32_t>(nearest8(x[k], s, inv)) & 0xffu) << (8 * k);
     return w;
+  }
+  const uint32_t lo = __byte_perm(__float_as_uint(q[0]), __float_as_uint(q[1]), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(q[2]), __float_as_uint(q[3]), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+
+// max(|a|, |b|), a NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Running maximum of |x| over raw vectors, NaN once one was met; an infinity
+// stays. 16-bit types keep two halves of a register.
+template <int DT>
+struct AbsMax {
+  uint32_t m = 0;
+  __device__ __forceinline__ void add(const Raw8<DT>& r) {
+    const uint32_t* const w = reinterpret_cast<const uint32_t*>(r.w);
+    if constexpr (DT == 0) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = __float_as_uint(max_nan(__uint_as_float(m), __uint_as_float(w[k] & 0x7fffffffu)));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (DT == 1) asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w[k] & 0x7fff7fffu));
+        else asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[k] & 0x7fff7fffu));
+      }
+    }
+  }
+  __device__ __forceinline__ float value() const {
+    if constexpr (DT == 0) return __uint_as_float(m);
+    else if constexpr (DT == 1) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+      return max_nan(f.x, f.y);
+    } else {
+      return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
+  }
+};
+
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(const float* x, float s, float inv) {
+  if constexpr (FMT == FMT_INT8) {
+    return nearest8x4(x, s, inv);
   } else {
     uint16_t lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1] * inv), "f"(x[0] * inv));
@@ -125,22 +206,28 @@ __device__ __forceinline__ float scale_of(float amax) {
 // touch, from base(s) = off[s] / group + 2 s on. n tokens touch at most
 // floor((n + group - 2) / group) + 1 <= floor(n / group) + 2 groups, so the
 // slots of different sequences never meet, and base is monotone: the sequence
-// of a slot is found by a search that reads 32 offsets at a time.
+// of a slot is found by a search that reads 128 offsets at a time.
 __device__ __forceinline__ int seq_of_slot(const int32_t* off, int num_seqs, int group, int num_tokens, int slot,
                                            int lane) {
   int lo = 0, n = num_seqs;  // the answer is in [lo, lo + n)
   while (n > 1) {
-    const int step = (n + 31) / 32;
-    bool at = false;
-    if (lane * step < n) {
-      const int i = lo + lane * step;
-      const int o = min(max(__ldg(off + i), 0), num_tokens);
-      at = static_cast<int64_t>(o / group) + 2ll * i <= slot;
+    const int step = (n + 127) / 128;
+    int o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t at = static_cast<int64_t>(32 * k + lane) * step;
+      o[k] = at < n ? __ldg(off + lo + at) : 0;
     }
-    const unsigned m = __ballot_sync(0xffffffffu, at);
-    const int last = m ? 31 - __clz(m) : 0;
+    int last = -1;  // starts at or before the slot
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t at = static_cast<int64_t>(32 * k + lane) * step;
+      const bool in = at < n && static_cast<int64_t>(min(max(o[k], 0), num_tokens) / group) + 2 * (lo + at) <= slot;
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      if (m) last = 32 * k + 31 - __clz(m);
+    }
     const int end = lo + n;
-    lo += last * step;
+    lo += max(last, 0) * step;
     n = min(step, end - lo);
   }
   return lo;
@@ -148,17 +235,20 @@ __device__ __forceinline__ int seq_of_slot(const int32_t* off, int num_seqs, int
 
 // TPU threads (a warp, or the CTA) hold one unit: a (slot, head, k or v). The
 // elements are kept in registers between the maximum and the codes, KEEP
-// vectors of 8 a thread; a larger group reads the rest a second time.
+// vectors of 8 a thread, as they lie in memory: as fp32 they left room for half
+// the CTAs, and a CTA is a chain of dependent reads (offsets, lengths, table,
+// tokens) that only other CTAs hide. A larger group reads the rest a second time.
 template <int DT, int FMT, bool VEC, int TPU>
-__global__ void __launch_bounds__(THREADS) write_kernel(const __grid_constant__ WriteParams p) {
+__global__ void __launch_bounds__(THREADS, DT == 0 ? 2 : 4) write_kernel(const __grid_constant__ WriteParams p, int units) {
   constexpr int KEEP = 4;
   __shared__ float red[THREADS / 32];
   const Cache& c = p.c;
   const int lane = threadIdx.x & 31;
   const int tu = threadIdx.x % TPU;
-  const int unit = blockIdx.y * (THREADS / TPU) + threadIdx.x / TPU;  // head, then k / v
-  if (unit >= 2 * c.Hkv) return;  // a whole warp (TPU 32) or no thread (TPU 256) returns
-  const int kv = unit >= c.Hkv ? 1 : 0, h = unit - kv * c.Hkv;
+  // units of this thread: head, then k / v, side by side and `units` in turn
+  constexpr int SIDE = THREADS / TPU;
+  const int unit0 = blockIdx.y * SIDE * units + threadIdx.x / TPU;
+  if (unit0 >= 2 * c.Hkv) return;  // a whole warp (TPU 32) or no thread (TPU 256) returns
   const int slot = blockIdx.x;
   const int s = seq_of_slot(p.off, c.num_seqs, c.group, p.num_tokens, slot, lane);
   int lo, hi;
@@ -176,97 +266,99 @@ __global__ void __launch_bounds__(THREADS) write_kernel(const __grid_constant__ 
   const int64_t x0 = lo + (g0 + held - (static_cast<int64_t>(L) - n));  // row of the first of them
   const int vpt = c.D >> 3, sh = __ffs(vpt) - 1;  // vectors of a token
   const int nv = m * vpt;
-  const void* const x = p.x[kv];
-  const int64_t xbase = x0 * p.xt[kv] + h * p.xh[kv];
-
-  float keep[KEEP][8];
-  float amax = 0.f;
-  bool odd = false;  // a NaN or an infinity
-  auto look = [&](const float (&v)[8]) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float a = fabsf(v[k]);
-      odd = odd || !(a < INFINITY);
-      amax = fmaxf(amax, a);
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < KEEP; ++i) {
-    const int e = tu + i * TPU;
-    if (e < nv) load8x<DT, VEC>(x, xbase + (e >> sh) * p.xt[kv] + (e & (vpt - 1)) * 8, keep[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < KEEP; ++i)
-    if (tu + i * TPU < nv) look(keep[i]);
-  for (int e = tu + KEEP * TPU; e < nv; e += TPU) {
-    float v[8];
-    load8x<DT, VEC>(x, xbase + (e >> sh) * p.xt[kv] + (e & (vpt - 1)) * 8, v);
-    look(v);
-  }
-  if (odd) amax = INFINITY;  // no finite value reaches it
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if constexpr (TPU > 32) {
-    if (lane == 0) red[threadIdx.x >> 5] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < TPU / 32; ++w) amax = fmaxf(amax, red[w]);
-  }
-  const size_t si = scale_index(c, page, row0, h);
-  const int64_t nscale = static_cast<int64_t>(c.num_pages) * c.Hkv * c.per;
-  if (!in_bounds(c.status, static_cast<int64_t>(si), nscale)) return;
-  float* const sc = p.scales[kv] + si;
-  float sn = amax < INFINITY ? scale_of<FMT>(amax) : __int_as_float(0x7fc00000);
-  float so = 0.f;
-  if (held > 0) {
-    so = *sc;
-    sn = (so != so || sn != sn) ? __int_as_float(0x7fc00000) : fmaxf(so, sn);
-  }
-  if constexpr (TPU > 32) __syncthreads();  // every thread has read the old scale
-  else __syncwarp();
-  if (tu == 0) *sc = sn;
-  const size_t cbase = ((static_cast<size_t>(page) * c.page_size + row0) * c.Hkv + h) * c.D;
   const size_t cstep = static_cast<size_t>(c.Hkv) * c.D;
   const int64_t ncode8 = static_cast<int64_t>(c.num_pages) * c.page_size * c.Hkv * vpt;
-  uint8_t* const codes = p.codes[kv];
-  auto slot8 = [&](int token, int col) { return reinterpret_cast<uint2*>(codes + cbase + token * cstep + col * 8); };
-  const float inv = 1.f / sn;
-  auto put = [&](int e, const float (&v)[8]) {
-    const int t = held + (e >> sh), col = e & (vpt - 1);
-    if (!in_bounds(c.status, static_cast<int64_t>((cbase + t * cstep) >> 3) + col, ncode8)) return;
-    // a group without a scale (NaN) gets zero codes
-    *slot8(t, col) = sn == sn ? make_uint2(encode4<FMT>(v, sn, inv), encode4<FMT>(v + 4, sn, inv)) : make_uint2(0u, 0u);
+  const int64_t nscale = static_cast<int64_t>(c.num_pages) * c.Hkv * c.per;
+  auto elements = [&](int unit, int e) {  // vector e of a unit's new tokens
+    const int kv = unit >= c.Hkv ? 1 : 0, h = unit - kv * c.Hkv;
+    return load_raw<DT, VEC>(p.x[kv], (x0 + (e >> sh)) * p.xt[kv] + h * p.xh[kv] + (e & (vpt - 1)) * 8);
   };
-  if (held > 0 && sn > so) {  // the codes of earlier calls, at the larger scale
-    for (int e = tu; e < held * vpt; e += TPU) {
-      const int t = e >> sh, col = e & (vpt - 1);
-      if (!in_bounds(c.status, static_cast<int64_t>((cbase + t * cstep) >> 3) + col, ncode8)) continue;
-      uint2* const at = slot8(t, col);
-      const uint2 w = *at;
-      *at = make_uint2(recode4<FMT>(w.x, so, sn), recode4<FMT>(w.y, so, sn));
-    }
-  }
+  Raw8<DT> next[KEEP];
+  auto fetch = [&](int unit) {
 #pragma unroll
-  for (int i = 0; i < KEEP; ++i) {
-    const int e = tu + i * TPU;
-    if (e < nv) put(e, keep[i]);
-  }
-  for (int e = tu + KEEP * TPU; e < nv; e += TPU) {
-    float v[8];
-    load8x<DT, VEC>(x, xbase + (e >> sh) * p.xt[kv] + (e & (vpt - 1)) * 8, v);
-    put(e, v);
+    for (int i = 0; i < KEEP; ++i)
+      if (tu + i * TPU < nv) next[i] = elements(unit, tu + i * TPU);
+  };
+  fetch(unit0);
+  for (int u = 0; u < units; ++u) {
+    const int unit = unit0 + u * SIDE;
+    if (unit >= 2 * c.Hkv) break;
+    const int kv = unit >= c.Hkv ? 1 : 0, h = unit - kv * c.Hkv;
+    Raw8<DT> keep[KEEP];
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) keep[i] = next[i];
+    if (u + 1 < units && unit + SIDE < 2 * c.Hkv) fetch(unit + SIDE);  // on their way under this unit's work
+    AbsMax<DT> most;
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+      if (tu + i * TPU < nv) most.add(keep[i]);
+    for (int e = tu + KEEP * TPU; e < nv; e += TPU) most.add(elements(unit, e));
+    float amax = most.value();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if constexpr (TPU > 32) {
+      if (lane == 0) red[threadIdx.x >> 5] = amax;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < TPU / 32; ++w) amax = max_nan(amax, red[w]);
+    }
+    const size_t si = scale_index(c, page, row0, h);
+    if (!in_bounds(c.status, static_cast<int64_t>(si), nscale)) return;  // the same for all of the unit's threads
+    float* const sc = p.scales[kv] + si;
+    float sn = amax < INFINITY ? scale_of<FMT>(amax) : __int_as_float(0x7fc00000);
+    float so = 0.f;
+    if (held > 0) {
+      so = *sc;
+      sn = (so != so || sn != sn) ? __int_as_float(0x7fc00000) : fmaxf(so, sn);
+    }
+    if constexpr (TPU > 32) __syncthreads();  // every thread has read the old scale
+    else __syncwarp();
+    if (tu == 0) *sc = sn;
+    const size_t cbase = ((static_cast<size_t>(page) * c.page_size + row0) * c.Hkv + h) * c.D;
+    uint8_t* const codes = p.codes[kv];
+    auto slot8 = [&](int token, int col) { return reinterpret_cast<uint2*>(codes + cbase + token * cstep + col * 8); };
+    const float inv = 1.f / sn;
+    auto put = [&](int e, const Raw8<DT>& r) {
+      float v[8];
+      expand<DT>(r, v);
+      const int t = held + (e >> sh), col = e & (vpt - 1);
+      if (!in_bounds(c.status, static_cast<int64_t>((cbase + t * cstep) >> 3) + col, ncode8)) return;
+      // a group without a scale (NaN) gets zero codes
+      *slot8(t, col) = sn == sn ? make_uint2(encode4<FMT>(v, sn, inv), encode4<FMT>(v + 4, sn, inv)) : make_uint2(0u, 0u);
+    };
+    if (held > 0 && sn > so) {  // the codes of earlier calls, at the larger scale
+      for (int e = tu; e < held * vpt; e += TPU) {
+        const int t = e >> sh, col = e & (vpt - 1);
+        if (!in_bounds(c.status, static_cast<int64_t>((cbase + t * cstep) >> 3) + col, ncode8)) continue;
+        uint2* const at = slot8(t, col);
+        const uint2 w = *at;
+        *at = make_uint2(recode4<FMT>(w.x, so, sn), recode4<FMT>(w.y, so, sn));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) {
+      const int e = tu + i * TPU;
+      if (e < nv) put(e, keep[i]);
+    }
+    for (int e = tu + KEEP * TPU; e < nv; e += TPU) put(e, elements(unit, e));
   }
 }
 
 template <int DT, int FMT, bool VEC>
 cudaError_t launch_write(const WriteParams& p, cudaStream_t st) {
   const unsigned slots = static_cast<unsigned>(p.num_tokens / p.c.group + 2 * p.c.num_seqs);
-  // a warp keeps up to 1024 elements of a unit in registers, the CTA 8192
-  if (p.c.group * p.c.D <= 1024) {
-    constexpr int U = THREADS / 32;
-    write_kernel<DT, FMT, VEC, 32><<<dim3(slots, (2 * p.c.Hkv + U - 1) / U), THREADS, 0, st>>>(p);
+  // A warp keeps up to 1024 elements of a unit in registers, the CTA 8192. What
+  // counts is the tokens that a unit gets: at most a group, and about those of a
+  // sequence (64 sequences of one token, group 16: 6 us by warps, 16 us by CTAs).
+  const int64_t tokens = (static_cast<int64_t>(p.num_tokens) + p.c.num_seqs - 1) / p.c.num_seqs;
+  if (min(static_cast<int64_t>(p.c.group), tokens) * p.c.D <= 1024) {
+    constexpr int SIDE = THREADS / 32;
+    write_kernel<DT, FMT, VEC, 32><<<dim3(slots, (2 * p.c.Hkv + SIDE - 1) / SIDE), THREADS, 0, st>>>(p, 1);
   } else {
-    write_kernel<DT, FMT, VEC, THREADS><<<dim3(slots, 2 * p.c.Hkv), THREADS, 0, st>>>(p);
+    // a CTA that takes several heads in turn finds its tokens once for all of
+    // them; where that leaves enough CTAs for the SMs
+    const int units = static_cast<int64_t>(slots) * 2 * p.c.Hkv >= 152ll * 4 * WRITE_UNITS ? WRITE_UNITS : 1;
+    write_kernel<DT, FMT, VEC, THREADS><<<dim3(slots, (2 * p.c.Hkv + units - 1) / units), THREADS, 0, st>>>(p, units);
   }
   return cudaGetLastError();
 }
@@ -284,16 +376,47 @@ struct ReadParams {
 
 constexpr int READ_ROWS = 8;  // output rows of a CTA
 
-// A CTA finds its rows' places in the cache once, then moves their heads side
-// by side: 8 codes in, 8 values out a thread and step.
+// Codes of a thread and step: 16, but 4 for F32, so that the lanes' 16-byte
+// stores lie side by side (640M elements: 492 us; 576 us with 8, 788 us with 16).
+template <int DT>
+constexpr int READ_PIECE = DT == 0 ? 4 : 16;
+template <int DT>
+using ReadWord = std::conditional_t<READ_PIECE<DT> == 4, uint32_t, std::conditional_t<READ_PIECE<DT> == 8, uint2, uint4>>;
+
+template <int DT, int FMT>
+__device__ __forceinline__ void store_piece(void* out, size_t o, ReadWord<DT> w, float s) {
+  const uint32_t* const c = reinterpret_cast<const uint32_t*>(&w);
+  if constexpr (DT == 0) {
+    constexpr int N = READ_PIECE<DT> / 4;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float4 v = decode4<FMT>(c[k]);
+      reinterpret_cast<float4*>(out)[N * o + k] = make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
+    }
+  } else {
+    uint32_t r[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = decode4<FMT>(c[k]);
+      r[2 * k] = pack2<DT == 2>(v.x * s, v.y * s);
+      r[2 * k + 1] = pack2<DT == 2>(v.z * s, v.w * s);
+    }
+    reinterpret_cast<uint4*>(out)[2 * o] = make_uint4(r[0], r[1], r[2], r[3]);
+    reinterpret_cast<uint4*>(out)[2 * o + 1] = make_uint4(r[4], r[5], r[6], r[7]);
+  }
+}
+
+// A CTA finds its rows' places in the cache once; then a thread keeps its
+// piece of a row (all heads side by side) and goes through the rows, the codes
+// of k and v in flight together.
 template <int DT, int FMT>
 __global__ void __launch_bounds__(THREADS) read_kernel(const __grid_constant__ ReadParams p) {
-  __shared__ int page_s[READ_ROWS], row_s[READ_ROWS];
+  __shared__ int64_t code_s[READ_ROWS], scale_s[READ_ROWS];  // token, and its scale of head 0; -1: zeros; -2: no row
   const Cache& c = p.c;
   const int r0 = blockIdx.x * READ_ROWS;
   if (threadIdx.x < READ_ROWS) {
     const int r = r0 + threadIdx.x;
-    int page = -2, row = 0;  // -2: a row of no sequence, left alone; -1: zeros
+    int64_t code = -2, scale = 0;
     if (r < p.num_rows) {
       int lo = 0, hi = c.num_seqs;  // the last sequence that starts at or before r
       while (hi - lo > 1) {
@@ -305,47 +428,49 @@ __global__ void __launch_bounds__(THREADS) read_kernel(const __grid_constant__ R
       row_range(p.off, lo, p.num_rows, a, b);
       if (r >= a && r < b) {
         const int64_t pos = static_cast<int64_t>(p.starts ? __ldg(p.starts + lo) : 0) + (r - a);
-        page = -1;
+        code = -1;
         if (pos >= 0 && pos < seq_len(c, lo)) {
-          page = page_of(c, lo, static_cast<int>(pos / c.page_size));
-          row = static_cast<int>(pos % c.page_size);
+          const int page = page_of(c, lo, static_cast<int>(pos / c.page_size));
+          const int row = static_cast<int>(pos % c.page_size);
+          if (page >= 0) {
+            code = static_cast<int64_t>(page) * c.page_size + row;
+            scale = static_cast<int64_t>(scale_index(c, page, row, 0));
+          }
         }
       }
     }
-    page_s[threadIdx.x] = page;
-    row_s[threadIdx.x] = row;
+    code_s[threadIdx.x] = code;
+    scale_s[threadIdx.x] = scale;
   }
   __syncthreads();
-  const int vpt = c.D >> 3, sh = __ffs(vpt) - 1;
-  const int per_row = c.Hkv * vpt;
-  const int64_t ncode8 = static_cast<int64_t>(c.num_pages) * c.page_size * per_row;
+  const int per_row = c.Hkv * (c.D / READ_PIECE<DT>), sh = __ffs(c.D / READ_PIECE<DT>) - 1;  // pieces of a row
+  const int64_t ncode = static_cast<int64_t>(c.num_pages) * c.page_size * per_row;
   const int64_t nscale = static_cast<int64_t>(c.num_pages) * c.Hkv * c.per;
-  const int64_t nout8 = static_cast<int64_t>(p.num_rows) * per_row;
-  for (int e = threadIdx.x; e < READ_ROWS * per_row; e += THREADS) {
-    const int r = e / per_row, i = e - r * per_row;
-    const int page = page_s[r];
-    if (page == -2) continue;
-    const int row = row_s[r], h = i >> sh;
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-      if (page >= 0) {
-        const size_t ci = (static_cast<size_t>(page) * c.page_size + row) * per_row + i;
-        const size_t si = scale_index(c, page, row, h);
-        if (in_bounds(c.status, static_cast<int64_t>(ci), ncode8) &&
-            in_bounds(c.status, static_cast<int64_t>(si), nscale)) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.codes[kv]) + ci);
-          const float s = __ldg(p.scales[kv] + si);
-          a = decode4<FMT>(w.x);
-          b = decode4<FMT>(w.y);
-          a.x *= s; a.y *= s; a.z *= s; a.w *= s;
-          b.x *= s; b.y *= s; b.z *= s; b.w *= s;
+  const int64_t nout = static_cast<int64_t>(p.num_rows) * per_row;
+  const int side = per_row < THREADS ? THREADS / per_row : 1;  // rows side by side
+  const int first = per_row < THREADS ? threadIdx.x / per_row : 0;
+  if (first >= side) return;
+  for (int i = threadIdx.x - first * per_row; i < per_row; i += THREADS) {
+    const int64_t hs = static_cast<int64_t>(i >> sh) * c.per;
+#pragma unroll 2
+    for (int r = first; r < READ_ROWS; r += side) {
+      const int64_t code = code_s[r];
+      if (code == -2) continue;
+      ReadWord<DT> k{}, v{};
+      float a = 0.f, b = 0.f;
+      if (code >= 0) {
+        const int64_t ci = code * per_row + i, si = scale_s[r] + hs;
+        if (in_bounds(c.status, ci, ncode) && in_bounds(c.status, si, nscale)) {
+          k = __ldg(reinterpret_cast<const ReadWord<DT>*>(p.codes[0]) + ci);
+          v = __ldg(reinterpret_cast<const ReadWord<DT>*>(p.codes[1]) + ci);
+          a = __ldg(p.scales[0] + si);
+          b = __ldg(p.scales[1] + si);
         }
       }
-      const size_t o = static_cast<size_t>(r0 + r) * per_row + i;
-      if (!in_bounds(c.status, static_cast<int64_t>(o), nout8)) continue;
-      simt::store4<DT>(p.out[kv], 2 * o, a);
-      simt::store4<DT>(p.out[kv], 2 * o + 1, b);
+      const int64_t o = static_cast<int64_t>(r0 + r) * per_row + i;
+      if (!in_bounds(c.status, o, nout)) continue;
+      store_piece<DT, FMT>(p.out[0], o, k, a);
+      store_piece<DT, FMT>(p.out[1], o, v, b);
     }
   }
 }
