@@ -34,9 +34,10 @@
 // Work: the keys of all sequences, in blocks of 128 (32 a warp), are cut into
 // ranges, one for each group of Hkv CTAs (one CTA a head, side by side, since
 // their codes lie side by side). A CTA walks the sequences of its range;
-// a sequence wholly inside it is written out, a cut one as a partial (m, l, O)
-// that merge_kernel combines in order. Uneven lengths cost nothing and there
-// are no atomics.
+// a sequence wholly inside it is written out, a cut one as a partial (m, l, O).
+// The CTA that finishes a cut sequence's last part (a counter that zero_kernel
+// has cleared) combines all of them, in the order of the ranges, whichever CTA
+// that is: the result does not depend on who came last.
 #pragma once
 
 #include "kv8_fwd.h"
@@ -64,26 +65,19 @@ __device__ __forceinline__ int blocks_of(const FwdParams& p, int s) {
   return blocks_of(hi - lo, seq_len(p.c, s));
 }
 
-// First block of range r (see DecodePlan): the first `large` ranges are LARGE
-// times the length of the others.
-__device__ __forceinline__ int64_t cut(int64_t total, int r, int ranges, int large) {
-  const int64_t at = r <= large ? static_cast<int64_t>(r) * DecodePlan::LARGE
-                                : static_cast<int64_t>(large) * DecodePlan::LARGE + (r - large);
-  const int64_t all = static_cast<int64_t>(large) * DecodePlan::LARGE + (ranges - large);
-  return total * at / all;
-}
+// First block of range r.
+__device__ __forceinline__ int64_t cut(int64_t total, int r, int ranges) { return total * r / ranges; }
 
-// Blocks of all sequences; the sequence s that the first or the last block of a
-// range lies in, and that sequence's first block.
+// Blocks of all sequences; the sequence s that the first block of a range lies in,
+// and that sequence's first block.
 struct Place {
   int64_t total, at;
   int s;
 };
 
-// The whole CTA (N threads) calls it.
-template <int N>
-__device__ __forceinline__ Place locate(const FwdParams& p, int range, int ranges, int large, bool last, int64_t& u0,
-                                        int64_t& u1) {
+// The whole CTA calls it.
+__device__ __forceinline__ Place locate(const FwdParams& p, int range, int ranges, int64_t& u0, int64_t& u1) {
+  constexpr int N = THREADS;
   __shared__ int64_t warp_sum[N / 32];
   __shared__ int64_t found_at;
   __shared__ int found_s;
@@ -110,15 +104,14 @@ __device__ __forceinline__ Place locate(const FwdParams& p, int range, int range
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
-  u0 = cut(total, range, ranges, large);
-  u1 = cut(total, range + 1, ranges, large);
-  const int64_t u = last ? u1 - 1 : u0;
-  if (u >= before && u < before + mine) {
+  u0 = cut(total, range, ranges);
+  u1 = cut(total, range + 1, ranges);
+  if (u0 >= before && u0 < before + mine) {
     int s = s0;
     int64_t at = before;
     for (; s < s1; ++s) {
       const int n = blocks_of(p, s);
-      if (u < at + n) break;
+      if (u0 < at + n) break;
       at += n;
     }
     found_at = at;
@@ -172,13 +165,14 @@ struct Shared {
 // workspace holds all groups (slot_rows).
 template <int D, int FMT, int NT>
 __global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
-    decode_kernel(const __grid_constant__ FwdParams p, int ranges, int large, int slot_rows, int64_t ml_offset) {
+    decode_kernel(const __grid_constant__ FwdParams p, int ranges, int slot_rows, int64_t ml_offset, int* counters) {
   constexpr int KS = D / 16;    // 16-element steps of a head
   constexpr int KB = D / 64;    // 64-byte pieces of a key
   constexpr int VW = D / 32;    // words of V a lane holds of one key
   constexpr int ROWS = 8 * NT;
   using SH = Shared<D, NT>;
   extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ bool last_part;
   float* const so = reinterpret_cast<float*>(smem);
   float2* const sml = reinterpret_cast<float2*>(smem + SH::OFF_ML);
   float* const sqf = reinterpret_cast<float*>(smem + SH::OFF_QF);  // the rows' inverse powers of two
@@ -205,8 +199,7 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
   const int dblk = BLOCK_KEYS / c.page_size, drow = BLOCK_KEYS % c.page_size;
 
   int64_t u0, u1;
-  const Place pl = locate<THREADS>(p, range, ranges, large, false, u0, u1);
-  asm volatile("griddepcontrol.launch_dependents;");  // merge_kernel may come up; it waits for this grid's end
+  const Place pl = locate(p, range, ranges, u0, u1);
   int s = pl.s;
   int b = static_cast<int>(u0 - pl.at);
   for (int64_t u = u0; u < u1; ++s, b = 0) {
@@ -542,7 +535,7 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
         for (int k = 0; k < KS; ++k) *reinterpret_cast<float2*>(o + 2 * k) = make_float2(acc[k][i][e], acc[k][i][2 + e]);
       }
     __syncthreads();
-    const int64_t slot = 2ll * blockIdx.x + (first ? 0 : 1);
+    const int64_t slot = 2ll * blockIdx.x + (first ? 0 : 1), nslot = 2ll * ranges * c.Hkv * slot_rows;
     for (int e = threadIdx.x; e < R * (D / 4); e += THREADS) {
       const int row = e / (D / 4), d4 = e - row * (D / 4);
       float M = -INFINITY;
@@ -571,99 +564,89 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
         if (p.lse && d4 == 0) p.lse[at] = live ? (M + log2f(sum)) * LN2 : (sum == 0.f ? -INFINITY : sum);
       } else {
         const int64_t at = slot * slot_rows + row_lo + row;
-        if (!in_bounds(status, at, 2ll * ranges * c.Hkv * slot_rows)) continue;
+        if (!in_bounds(status, at, nslot)) continue;
         reinterpret_cast<float4*>(p.ws)[at * (D / 4) + d4] = o;
         if (d4 == 0) reinterpret_cast<float2*>(static_cast<uint8_t*>(p.ws) + ml_offset)[at] = make_float2(M, sum);
+      }
+    }
+    if (!whole) {
+      // the ranges rf .. rl hold the sequence's blocks
+      const int64_t begin = u - take - b, end = begin + nb;
+      const int rf = static_cast<int>(((begin + 1) * ranges + pl.total - 1) / pl.total) - 1;  // last with cut(rf) <= begin
+      const int rl = static_cast<int>((end * ranges + pl.total - 1) / pl.total) - 1;          // first with cut(rl + 1) >= end
+      const bool gaps = pl.total < ranges;  // some ranges are empty, the others have a block each
+      const int parts = gaps ? nb : rl - rf + 1;
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
+        const int64_t n = (static_cast<int64_t>(rf) * c.Hkv + h) * gridDim.y + blockIdx.y;
+        last_part = in_bounds(status, n, static_cast<int64_t>(ranges) * c.Hkv * gridDim.y) && atomicAdd(counters + n, 1) == parts - 1;
+      }
+      __syncthreads();
+      if (last_part) {
+        __threadfence();
+        const float4* const wo = static_cast<const float4*>(p.ws);
+        const float2* const wml = reinterpret_cast<const float2*>(static_cast<const uint8_t*>(p.ws) + ml_offset);
+        constexpr int G = D / 4, TEAMS = THREADS / G, BATCH = 8;  // parts read together: each read is a trip to L2
+        const int g4 = threadIdx.x % G, team = threadIdx.x / G;
+        const int share = R >= TEAMS ? 1 : TEAMS / R;  // teams of a row, added up in order
+        const int at_once = TEAMS / share;
+        const bool starts_late = begin > cut(pl.total, rf, ranges);
+        for (int base = 0; base < R; base += at_once) {
+          const int row = base + team / share, part0 = team % share;
+          const bool mine = row < R && team / share < at_once;
+          float M = -INFINITY, sum = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          auto add = [&](float2 ml, float4 x) {
+            const float n = fmaxf(M, ml.x);
+            const float f = n == -INFINITY ? 0.f : fast_exp2(M - n), e = n == -INFINITY ? 0.f : fast_exp2(ml.x - n);
+            M = n;
+            sum = sum * f + ml.y * e;
+            o = make_float4(o.x * f + x.x * e, o.y * f + x.y * e, o.z * f + x.z * e, o.w * f + x.w * e);
+          };
+          for (int r0 = rf + part0; mine && r0 <= rl; r0 += share * BATCH) {
+            float2 ml[BATCH];
+            float4 x[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+              const int r = r0 + k * share;
+              const int64_t at = (2ll * (static_cast<int64_t>(r) * c.Hkv + h) + (r == rf && starts_late ? 1 : 0)) * slot_rows + row_lo + row;
+              const bool part = r <= rl && !(gaps && cut(pl.total, r, ranges) == cut(pl.total, r + 1, ranges)) &&
+                                in_bounds(status, at, nslot);
+              ml[k] = part ? __ldcg(wml + at) : make_float2(-INFINITY, 0.f);
+              x[k] = part ? __ldcg(wo + at * G + g4) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) add(ml[k], x[k]);
+          }
+          if (share > 1) {
+            __syncthreads();
+            reinterpret_cast<float4*>(so)[team * G + g4] = o;
+            if (g4 == 0) sml[team] = make_float2(M, sum);
+            __syncthreads();
+            if (mine && part0 == 0)
+              for (int i = 1; i < share; ++i) add(sml[team + i], reinterpret_cast<const float4*>(so)[(team + i) * G + g4]);
+          }
+          if (!mine || part0 != 0) continue;
+          const bool live = sum > 0.f;
+          const float inv = live ? 1.f / sum : __int_as_float(0x7fc00000);
+          const int64_t at = row_at(row);
+          if (!in_bounds(status, at, nrows)) continue;
+          reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * D)[g4] =
+              make_uint2(pack_out(bf16, o.x * inv, o.y * inv), pack_out(bf16, o.z * inv, o.w * inv));
+          if (p.lse && g4 == 0) p.lse[at] = live ? (M + log2f(sum)) * LN2 : (sum == 0.f ? -INFINITY : sum);
+        }
       }
     }
     __syncthreads();
   }
 }
 
-// A CTA (range, head) combines the parts of the sequence that begins in the
-// range and goes on past it: its own last slot, then the first slot of the
-// ranges after it. D / 4 threads take a row; with few rows several such teams
-// share a row's parts, and their sums are added in order. Launched while the
-// decode kernel still runs; everything up to the wait needs nothing of it.
-constexpr int MERGE_THREADS = 256;
-
-template <int D>
-__global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const __grid_constant__ FwdParams p, int ranges, int large,
-                                                              int slot_rows, int64_t ml_offset) {
-  constexpr int G = D / 4, TEAMS = MERGE_THREADS / G;
-  __shared__ float4 so[TEAMS][G];
-  __shared__ float2 sml[TEAMS];
-  const Cache& c = p.c;
-  const int h = blockIdx.x % c.Hkv, range = blockIdx.x / c.Hkv;
-  int64_t u0, u1;
-  const Place pl = locate<MERGE_THREADS>(p, range, ranges, large, true, u0, u1);
-  if (u1 <= u0 || pl.at < u0) return;  // CTA-uniform, as every return below
-  int q_lo, q_hi;
-  row_range(p.q_offsets, pl.s, p.num_queries, q_lo, q_hi);
-  const int heads = p.Hq / c.Hkv;
-  const int64_t end = pl.at + blocks_of(q_hi - q_lo, seq_len(c, pl.s));
-  if (end <= u1) return;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(q_hi - q_lo) * heads, static_cast<int64_t>(slot_rows)));
-  int last = range, hi = ranges - 1;  // the range that holds block end - 1: the least with cut(last + 1) >= end
-  while (last < hi) {
-    const int mid = (last + hi) >> 1;
-    if (cut(pl.total, mid + 1, ranges, large) >= end) hi = mid;
-    else last = mid + 1;
-  }
-  const bool gaps = pl.total < (static_cast<int64_t>(large) * DecodePlan::LARGE + ranges - large);  // some ranges are empty
-  const float4* const wo = static_cast<const float4*>(p.ws);
-  const float2* const wml = reinterpret_cast<const float2*>(static_cast<const uint8_t*>(p.ws) + ml_offset);
-  const int g = threadIdx.x % G, team = threadIdx.x / G;
-  const int share = rows >= TEAMS ? 1 : TEAMS / rows;  // teams of a row
-  const int at_once = TEAMS / share;                   // rows side by side
-  const int64_t nslot = 2ll * ranges * c.Hkv * slot_rows, nrows = static_cast<int64_t>(p.num_queries) * p.Hq;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int row0 = 0; row0 < rows; row0 += at_once) {
-    const int row = row0 + team / share, part0 = team % share;
-    float M = -INFINITY, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float2 ml, float4 x) {
-      const float n = fmaxf(M, ml.x);
-      const float f = n == -INFINITY ? 0.f : fast_exp2(M - n), e = n == -INFINITY ? 0.f : fast_exp2(ml.x - n);
-      M = n;
-      sum = sum * f + ml.y * e;
-      o = make_float4(o.x * f + x.x * e, o.y * f + x.y * e, o.z * f + x.z * e, o.w * f + x.w * e);
-    };
-    if (row < rows && team / share < at_once) {
-      constexpr int BATCH = 8;  // parts read together: each read is a trip to L2
-      for (int r0 = range + part0; r0 <= last; r0 += share * BATCH) {
-        float2 ml[BATCH];
-        float4 x[BATCH];
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-          const int r = r0 + k * share;
-          const int64_t at = (2ll * (static_cast<int64_t>(r) * c.Hkv + h) + (r == range && pl.at > u0 ? 1 : 0)) * slot_rows + row;
-          const bool part = r <= last && !(gaps && cut(pl.total, r, ranges, large) == cut(pl.total, r + 1, ranges, large)) &&
-                            in_bounds(c.status, at, nslot);
-          ml[k] = part ? wml[at] : make_float2(-INFINITY, 0.f);
-          x[k] = part ? wo[at * G + g] : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) add(ml[k], x[k]);
-      }
-    }
-    if (share > 1) {
-      __syncthreads();
-      so[team][g] = o;
-      if (g == 0) sml[team] = make_float2(M, sum);
-      __syncthreads();
-      if (part0 == 0)
-        for (int i = 1; i < share; ++i) add(sml[min(team + i, TEAMS - 1)], so[min(team + i, TEAMS - 1)][g]);
-    }
-    if (row >= rows || part0 != 0 || team / share >= at_once) continue;
-    const bool live = sum > 0.f;
-    const float inv = live ? 1.f / sum : __int_as_float(0x7fc00000);
-    const int64_t at = static_cast<int64_t>(q_lo + row / heads) * p.Hq + h * heads + row % heads;
-    if (!in_bounds(c.status, at, nrows)) continue;
-    reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * D)[g] =
-        make_uint2(pack_out(p.bf16, o.x * inv, o.y * inv), pack_out(p.bf16, o.z * inv, o.w * inv));
-    if (p.lse && g == 0) p.lse[at] = live ? (M + log2f(sum)) * LN2 : (sum == 0.f ? -INFINITY : sum);
-  }
+// Clears the counters of the cut sequences.
+static __global__ void zero_kernel(int* counters, int n) {
+  asm volatile("griddepcontrol.launch_dependents;");  // the decode kernel may come up; it waits before it counts
+  for (int i = threadIdx.x; i < n; i += blockDim.x) counters[i] = 0;
 }
 
 template <int D, int FMT, int NT>
@@ -675,19 +658,23 @@ cudaError_t launch_nt(const FwdParams& p, const DecodePlan& plan, cudaStream_t s
   if (e != cudaSuccess) return e;
   const unsigned ctas = static_cast<unsigned>(plan.ranges) * p.c.Hkv;
   const int64_t ml = plan.ml_offset(p.c.Hkv, D);
-  kern<<<dim3(ctas, plan.row_groups), THREADS, smem, st>>>(p, plan.ranges, plan.large, plan.slot_rows(), ml);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || plan.ranges == 1) return e;
+  int* const counters = reinterpret_cast<int*>(static_cast<uint8_t*>(p.ws) + plan.counter_offset(p.c.Hkv, D));
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(MERGE_THREADS);
+  cfg.gridDim = dim3(ctas, plan.row_groups);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, p, plan.ranges, plan.large, plan.slot_rows(), ml);
+  if (plan.ranges > 1) {  // one range cuts nothing
+    zero_kernel<<<1, 512, 0, st>>>(counters, static_cast<int>(ctas) * plan.row_groups);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, kern, p, plan.ranges, plan.slot_rows(), ml, counters);
 }
 
 template <int D, int FMT>

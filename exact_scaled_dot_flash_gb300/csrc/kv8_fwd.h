@@ -26,13 +26,14 @@ struct FwdParams {
 // rows of a kv head (8 nt); more rows go to `row_groups` CTAs that read the same
 // codes (the second from L2).
 struct DecodePlan {
-  static constexpr int LARGE = 5;  // the first `large` ranges are this many times the others
-  int rows = 0, row_groups = 0, nt = 0, ranges = 0, large = 0;
+  int rows = 0, row_groups = 0, nt = 0, ranges = 0;
   int slot_rows() const { return row_groups * nt * 8; }
   // Partials: CTA c (range, head) owns slots 2c (its first sequence) and 2c + 1
   // (its last), each slot_rows x (D floats) and slot_rows x (m, l).
   int64_t ml_offset(int Hkv, int D) const { return 2ll * ranges * Hkv * slot_rows() * D * 4; }
-  int64_t bytes(int Hkv, int D) const { return ml_offset(Hkv, D) + 2ll * ranges * Hkv * slot_rows() * 8; }
+  // and a counter for each (range, head, row group) follows.
+  int64_t counter_offset(int Hkv, int D) const { return ml_offset(Hkv, D) + 2ll * ranges * Hkv * slot_rows() * 8; }
+  int64_t bytes(int Hkv, int D) const { return counter_offset(Hkv, D) + 4ll * ranges * Hkv * row_groups; }
 };
 
 // Calls with at most this many rows (queries x heads) of a kv head.
@@ -50,12 +51,9 @@ inline DecodePlan decode_plan(int num_seqs, int Hkv, int heads, int max_queries,
   const int64_t keys = static_cast<int64_t>(max_pages) * page_size;
   const int64_t blocks = num_seqs * (keys > 128 ? (keys + 127) / 128 : 1);
   const int64_t side = static_cast<int64_t>(Hkv) * d.row_groups;
-  int64_t large = 152 * (d.nt <= 2 ? 3 : 2) / side;
-  if (large < 1) large = 1;
-  int64_t r = large;
-  if (r > blocks) large = r = blocks;  // few blocks: one each
-  d.ranges = static_cast<int>(r);
-  d.large = static_cast<int>(large);
+  int64_t r = 152 * (d.nt <= 2 ? 3 : 2) / side;
+  if (r > blocks) r = blocks;
+  d.ranges = static_cast<int>(r > 1 ? r : 1);
   return d;
 }
 
