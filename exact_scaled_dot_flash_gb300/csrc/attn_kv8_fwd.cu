@@ -209,7 +209,15 @@ attn::kv8::DecodePlan plan_of(const attn_paged_shape_t& s) {
 extern "C" int attn_paged_kv8_workspace_bytes(const attn_paged_shape_t* shape, size_t* bytes) {
   if (!shape || !bytes) return ATTN_ERR_NULL;
   if (const int rc = check_shape(*shape)) return rc;
-  *bytes = takes_decode(*shape) ? static_cast<size_t>(plan_of(*shape).bytes(shape->Hkv, shape->D)) : 0;
+  const attn_paged_shape_t& s = *shape;
+  *bytes = 0;
+  if (takes_decode(s)) {
+    *bytes = static_cast<size_t>(plan_of(s).bytes(s.Hkv, s.D));
+  } else if (takes_tensor(s)) {
+    const int splits = attn::kv8::tc_splits(s.num_seqs, s.Hkv, attn::kv8::tc_qblocks(s.max_queries, s.Hq / s.Hkv),
+                                            s.max_pages, s.page_size);
+    if (splits > 1) *bytes = static_cast<size_t>(splits) * s.num_queries * s.Hq * (s.D * 4 + 8);
+  }
   return ATTN_OK;
 }
 

@@ -19,6 +19,9 @@
 //    that passes it by 2^8.
 // The products are F16 for BF16 queries too: a row is brought into range by a
 // power of two (see attn_kv8_decode.cuh).
+// Where the row blocks do not fill the SMs (a few short chunks over long
+// histories), their key tiles are cut into runs, one CTA each, whose unnormalised
+// outputs merge_kernel combines.
 // Bound: the tensor pipe's 2048 cycles for a tile of 256 x 128 x 128; the
 // softmax and the conversion together issue for some 1500 of them.
 #pragma once
@@ -65,18 +68,21 @@ struct Cfg {
 };
 
 struct Work {
-  int s, hk, q_lo, nq, L;
+  int s, hk, sp, q_lo, nq, L;
+  int j0;             // first key tile of the CTA's run
   int64_t row0;       // first packed row of the CTA
   int n[NQ], nmax;    // key tiles of each row tile
   int nfull[NQ];      // of which the first ones need no mask
 };
 
-__device__ __forceinline__ Work make_work(const FwdParams& p, int qblocks) {
+// Item: kv head (fastest), run, row block, sequence.
+__device__ __forceinline__ Work make_work(const FwdParams& p, int qblocks, int splits, int item) {
   Work w;
   const int heads = p.Hq / p.c.Hkv;
-  int item = static_cast<int>(blockIdx.x);
   w.hk = item % p.c.Hkv;
   item /= p.c.Hkv;
+  w.sp = item % splits;
+  item /= splits;
   // the last blocks of a sequence see the most keys and go first
   w.row0 = static_cast<int64_t>(qblocks - 1 - item % qblocks) * NQ * BM;
   w.s = item / qblocks;
@@ -103,6 +109,11 @@ __device__ __forceinline__ Work make_work(const FwdParams& p, int qblocks) {
     w.nfull[t] = least > 0 ? static_cast<int>(least / BN) : 0;
     w.nmax = max(w.nmax, w.n[t]);
   }
+  w.j0 = static_cast<int>(static_cast<int64_t>(w.nmax) * w.sp / splits);
+  const int j1 = static_cast<int>(static_cast<int64_t>(w.nmax) * (w.sp + 1) / splits);
+  w.nmax = j1 - w.j0;
+#pragma unroll
+  for (int t = 0; t < NQ; ++t) w.n[t] = max(0, min(w.n[t], j1) - w.j0);
   return w;
 }
 
@@ -114,7 +125,7 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
 // RUN: every 1, 4 or 16 keys share their scales (group, and so page_size, a
 // multiple of it).
 template <int D, int FMT, int RUN>
-__global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constant__ FwdParams p, int qblocks) {
+__global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constant__ FwdParams p, int qblocks, int splits) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -125,7 +136,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
   const Cache& c = p.c;
   int* const status = c.status;
   const int heads = p.Hq / c.Hkv;
-  const Work w = make_work(p, qblocks);
+  const Work w = make_work(p, qblocks, splits, static_cast<int>(blockIdx.x));
+  asm volatile("griddepcontrol.launch_dependents;");  // merge_kernel waits for this grid's end
   if (w.row0 >= static_cast<int64_t>(w.nq) * heads) return;  // no rows (CTA-uniform); rows without keys still get NaN
 
   if (threadIdx.x == 0) {
@@ -179,7 +191,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
       float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
       // The lane's key of the tile to copy next, and its page, which is read a
       // tile ahead of its use. Keys are looked up with K and used again for V.
-      int key = cw * 32 + lane, blk = key / c.page_size, row = key - blk * c.page_size;
+      int key = w.j0 * BN + cw * 32 + lane, blk = key / c.page_size, row = key - blk * c.page_size;
       const int dblk = BN / c.page_size, drow = BN % c.page_size;
       const int32_t* const table = c.block_table + static_cast<size_t>(w.s) * c.max_pages;
       auto find_page = [&]() { return key < w.L && blk < c.max_pages ? __ldg(table + blk) : -1; };
@@ -414,9 +426,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
           s[4 * i] = a.x; s[4 * i + 1] = a.y; s[4 * i + 2] = b.x; s[4 * i + 3] = b.y;
         }
       }
-      const bool masked = j >= nfull_t;
+      const bool masked = w.j0 + j >= nfull_t;
       if (masked) {
-        const int end = lim - j * BN;
+        const int end = lim - (w.j0 + j) * BN;
         asm volatile("");  // a branch, not 256 predicated instructions in every tile
 #pragma unroll
         for (int i = 0; i < 128; ++i)
@@ -538,7 +550,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
     } else if (w.row0 + t * BM < static_cast<int64_t>(w.nq) * heads) {
       tc_fence_after();
       const bool live = have && l_run > 0.f;
-      const float inv = live ? 1.f / l_run : __int_as_float(0x7fc00000);
+      const float inv = splits > 1 ? 1.f : live ? 1.f / l_run : __int_as_float(0x7fc00000);
+      const int64_t prow = static_cast<int64_t>(w.sp) * nrows + orow;  // of the run's partials
       uint8_t* const dst = static_cast<uint8_t*>(p.out) + orow * D * 2;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
@@ -550,7 +563,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0u;
         }
-        if (row_in) {
+        if (row_in && splits > 1) {
+          if (have && in_bounds(status, prow, splits * nrows)) {
+            float4* const part = static_cast<float4*>(p.ws) + prow * (D / 4) + i * 8;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              part[u] = make_float4(__uint_as_float(o[4 * u]), __uint_as_float(o[4 * u + 1]), __uint_as_float(o[4 * u + 2]),
+                                    __uint_as_float(o[4 * u + 3]));
+          }
+        } else if (row_in) {
           uint32_t pk[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -562,7 +583,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
             reinterpret_cast<uint4*>(dst + i * 64)[u] = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
         }
       }
-      if (row_in && p.lse) p.lse[orow] = live ? (ref + log2f(l_run)) * LN2 : (l_run == 0.f ? -INFINITY : l_run);
+      if (splits > 1) {
+        if (row_in && in_bounds(status, prow, splits * nrows))
+          reinterpret_cast<float2*>(static_cast<float4*>(p.ws) + splits * nrows * (D / 4))[prow] =
+              make_float2(l_run == 0.f ? -INFINITY : ref, l_run);
+      } else if (row_in && p.lse) p.lse[orow] = live ? (ref + log2f(l_run)) * LN2 : (l_run == 0.f ? -INFINITY : l_run);
     }
   }
   tc_fence_before();
@@ -574,19 +599,73 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
   }
 }
 
+// A warp combines the runs of one row: partials (ref, l, O) of `splits` runs.
+constexpr int MERGE_WARPS = 8;
+
+template <int D>
+__global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const __grid_constant__ FwdParams p, int qblocks, int splits) {
+  const Work w = make_work(p, qblocks, 1, static_cast<int>(blockIdx.x));
+  const int heads = p.Hq / p.c.Hkv, lane = threadIdx.x & 31;
+  const int64_t pr = w.row0 + static_cast<int64_t>(blockIdx.y) * MERGE_WARPS + (threadIdx.x >> 5);
+  if (pr >= static_cast<int64_t>(w.nq) * heads) return;
+  const int tq = static_cast<int>(pr / heads);
+  const int64_t orow = static_cast<int64_t>(w.q_lo + tq) * p.Hq + w.hk * heads + (pr - static_cast<int64_t>(tq) * heads);
+  const int64_t nrows = static_cast<int64_t>(p.num_queries) * p.Hq;
+  if (!in_bounds(p.c.status, orow, nrows)) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float4* const wo = static_cast<const float4*>(p.ws);
+  const float2* const wml = reinterpret_cast<const float2*>(wo + splits * nrows * (D / 4));
+  const float2 ml = lane < splits ? wml[lane * nrows + orow] : make_float2(-INFINITY, 0.f);
+  float M = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);  // a run without keys wrote no output
+  float sum = f == 0.f ? 0.f : f * ml.y;
+  if (ml.y != ml.y) sum = ml.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  constexpr int V = D / 32;  // floats of a lane
+  float acc[V] = {};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float fs = __shfl_sync(0xffffffffu, f, s);
+    if (fs == 0.f) continue;  // warp-uniform
+    const float* const src = reinterpret_cast<const float*>(wo) + (s * nrows + orow) * D + lane * V;
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = fmaf(fs, src[k], acc[k]);
+  }
+  const bool live = sum > 0.f;
+  const float inv = live ? 1.f / sum : __int_as_float(0x7fc00000);
+  uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + orow * D) + lane * V / 2;
+#pragma unroll
+  for (int k = 0; k < V; k += 2) dst[k / 2] = pack_out(p.bf16, acc[k] * inv, acc[k + 1] * inv);
+  if (p.lse && lane == 0) p.lse[orow] = live ? (M + log2f(sum)) * LN2 : (sum == 0.f ? -INFINITY : sum);
+}
+
 template <int D, int FMT, int RUN>
 cudaError_t launch_run(const FwdParams& p, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(p.max_queries) * (p.Hq / p.c.Hkv);
-  const int64_t qblocks = (rows + NQ * BM - 1) / (NQ * BM);
-  const int64_t ctas = static_cast<int64_t>(p.c.num_seqs) * qblocks * p.c.Hkv;
-  if (ctas == 0) return cudaSuccess;
-  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const int64_t qblocks = tc_qblocks(p.max_queries, p.Hq / p.c.Hkv);
+  const int splits = tc_splits(p.c.num_seqs, p.c.Hkv, qblocks, p.c.max_pages, p.c.page_size);
+  const int64_t blocks = static_cast<int64_t>(p.c.num_seqs) * qblocks * p.c.Hkv;
+  if (blocks == 0) return cudaSuccess;
+  if (blocks * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   auto kern = tc_kernel<D, FMT, RUN>;
   constexpr int smem = Cfg<D>::SMEM_BYTES;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(ctas), NUM_THREADS, smem, st>>>(p, static_cast<int>(qblocks));
-  return cudaGetLastError();
+  kern<<<static_cast<unsigned>(blocks * splits), NUM_THREADS, smem, st>>>(p, static_cast<int>(qblocks), splits);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || splits == 1) return e;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), NQ * BM / MERGE_WARPS);
+  cfg.blockDim = dim3(MERGE_WARPS * 32);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, p, static_cast<int>(qblocks), splits);
 }
 
 template <int D, int FMT>

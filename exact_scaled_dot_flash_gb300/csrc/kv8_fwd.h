@@ -60,7 +60,19 @@ inline DecodePlan decode_plan(int num_seqs, int Hkv, int heads, int max_queries,
 template <int FMT>
 cudaError_t launch_decode(const FwdParams& p, const DecodePlan& plan, cudaStream_t st);
 
-// Many rows, F16/BF16, D in {64, 128} (attn_kv8_tc.cuh).
+// Many rows, F16/BF16, D in {64, 128} (attn_kv8_tc.cuh): CTAs of 256 packed rows
+// of a sequence and kv head. Fewer of them than half the 152 SMs have their keys
+// cut into runs of at least 4 tiles of 128, as many as fill the SMs; the
+// workspace then holds for each run and row D floats and (m, l).
+inline int64_t tc_qblocks(int max_queries, int heads) { return (static_cast<int64_t>(max_queries) * heads + 255) / 256; }
+inline int tc_splits(int num_seqs, int Hkv, int64_t qblocks, int max_pages, int page_size) {
+  const int64_t ctas = num_seqs * qblocks * Hkv;
+  const int64_t tiles = (static_cast<int64_t>(max_pages) * page_size + 127) / 128;
+  int64_t s = ctas > 0 ? 152 / ctas : 1;
+  if (s > tiles / 4) s = tiles / 4;
+  if (s > 32) s = 32;
+  return static_cast<int>(s > 1 ? s : 1);
+}
 template <int FMT>
 cudaError_t launch_tc(const FwdParams& p, cudaStream_t st);
 

@@ -310,6 +310,9 @@ ATTENDS = [
     dict(lens=[4, 300], new=[9, 1], Hq=4, dtype="bf16", D=128),                                    # queries before token 0
     dict(lens=[2500, 9000, 40, 0, 6001], new=[1, 1, 1, 1, 1], Hq=8, dtype="bf16", P=64, G=8, D=128, fmt="e4m3"),
     dict(lens=[9000, 4100], new=[3, 3], Hq=6, dtype="f16", P=16, G=16, D=64),
+    dict(lens=[2100, 130, 1500], new=[70, 0, 90], Hq=8, dtype="bf16", P=64, G=16, D=128),          # runs of key tiles
+    dict(lens=[3000], new=[130], H=1, Hq=3, dtype="f16", P=40, G=4, D=64, fmt="e4m3"),
+    dict(lens=[1300, 0, 2000], new=[40, 20, 2], H=1, Hq=2, dtype="bf16", P=16, G=1, D=128, fmt="e4m3"),
 ]
 
 
