@@ -37,7 +37,8 @@
 // a sequence wholly inside it is written out, a cut one as a partial (m, l, O).
 // The CTA that finishes a cut sequence's last part (a counter that zero_kernel
 // has cleared) combines all of them, in the order of the ranges, whichever CTA
-// that is: the result does not depend on who came last.
+// that is: the result does not depend on who came last. Sequences of at most 512
+// keys are not cut: a CTA each (and head), no counters, no workspace.
 #pragma once
 
 #include "kv8_fwd.h"
@@ -165,7 +166,8 @@ struct Shared {
 // workspace holds all groups (slot_rows).
 template <int D, int FMT, int NT>
 __global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
-    decode_kernel(const __grid_constant__ FwdParams p, int ranges, int slot_rows, int64_t ml_offset, int* counters) {
+    decode_kernel(const __grid_constant__ FwdParams p, int ranges, int aligned, int slot_rows, int64_t ml_offset,
+                  int* counters) {
   constexpr int KS = D / 16;    // 16-element steps of a head
   constexpr int KB = D / 64;    // 64-byte pieces of a key
   constexpr int VW = D / 32;    // words of V a lane holds of one key
@@ -198,8 +200,10 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
   const bool tiles_in_page = c.page_size % TILE_KEYS == 0;
   const int dblk = BLOCK_KEYS / c.page_size, drow = BLOCK_KEYS % c.page_size;
 
-  int64_t u0, u1;
-  const Place pl = locate(p, range, ranges, u0, u1);
+  int64_t u0 = 0, u1 = 0;
+  Place pl{0, 0, range};
+  if (aligned) u1 = blocks_of(p, range);  // the range is one sequence
+  else pl = locate(p, range, ranges, u0, u1);
   int s = pl.s;
   int b = static_cast<int>(u0 - pl.at);
   for (int64_t u = u0; u < u1; ++s, b = 0) {
@@ -653,8 +657,8 @@ template <int D, int FMT, int NT>
 cudaError_t launch_nt(const FwdParams& p, const DecodePlan& plan, cudaStream_t st) {
   auto kern = decode_kernel<D, FMT, NT>;
   constexpr int smem = Shared<D, NT>::BYTES;
-  cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> configured{0};
+  cudaError_t e = allow_smem(kern, smem, p.device, configured);
   if (e != cudaSuccess) return e;
   const unsigned ctas = static_cast<unsigned>(plan.ranges) * p.c.Hkv;
   const int64_t ml = plan.ml_offset(p.c.Hkv, D);
@@ -667,14 +671,14 @@ cudaError_t launch_nt(const FwdParams& p, const DecodePlan& plan, cudaStream_t s
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  if (plan.ranges > 1) {  // one range cuts nothing
+  if (plan.cuts()) {
     zero_kernel<<<1, 512, 0, st>>>(counters, static_cast<int>(ctas) * plan.row_groups);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
   }
-  return cudaLaunchKernelEx(&cfg, kern, p, plan.ranges, plan.slot_rows(), ml, counters);
+  return cudaLaunchKernelEx(&cfg, kern, p, plan.ranges, plan.aligned, plan.slot_rows(), ml, counters);
 }
 
 template <int D, int FMT>

@@ -651,7 +651,8 @@ cudaError_t launch_run(const FwdParams& p, cudaStream_t st) {
   if (blocks * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   auto kern = tc_kernel<D, FMT, RUN>;
   constexpr int smem = Cfg<D>::SMEM_BYTES;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> configured{0};
+  cudaError_t e = allow_smem(kern, smem, p.device, configured);
   if (e != cudaSuccess) return e;
   kern<<<static_cast<unsigned>(blocks * splits), NUM_THREADS, smem, st>>>(p, static_cast<int>(qblocks), splits);
   e = cudaGetLastError();

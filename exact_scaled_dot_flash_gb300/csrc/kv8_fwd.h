@@ -1,6 +1,8 @@
 // kv8_fwd.h - parameters of the kernels behind attn_paged_kv8_fwd.
 #pragma once
 
+#include <atomic>
+
 #include "kv8.cuh"
 
 namespace attn {
@@ -26,23 +28,37 @@ struct FwdParams {
 // rows of a kv head (8 nt); more rows go to `row_groups` CTAs that read the same
 // codes (the second from L2).
 struct DecodePlan {
-  int rows = 0, row_groups = 0, nt = 0, ranges = 0;
+  int rows = 0, row_groups = 0, nt = 0, ranges = 0, aligned = 0;  // aligned: a range is a sequence
+  bool cuts() const { return !aligned && ranges > 1; }            // sequences may be cut: workspace
   int slot_rows() const { return row_groups * nt * 8; }
   // Partials: CTA c (range, head) owns slots 2c (its first sequence) and 2c + 1
   // (its last), each slot_rows x (D floats) and slot_rows x (m, l).
   int64_t ml_offset(int Hkv, int D) const { return 2ll * ranges * Hkv * slot_rows() * D * 4; }
   // and a counter for each (range, head, row group) follows.
   int64_t counter_offset(int Hkv, int D) const { return ml_offset(Hkv, D) + 2ll * ranges * Hkv * slot_rows() * 8; }
-  int64_t bytes(int Hkv, int D) const { return counter_offset(Hkv, D) + 4ll * ranges * Hkv * row_groups; }
+  int64_t bytes(int Hkv, int D) const { return cuts() ? counter_offset(Hkv, D) + 4ll * ranges * Hkv * row_groups : 0; }
 };
+
+// Opts a kernel in to `smem` bytes of shared memory, once for each device.
+template <typename K>
+cudaError_t allow_smem(K kern, int smem, int device, std::atomic<unsigned long long>& configured) {
+  const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0ull;
+  if (bit && (configured.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) configured.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
 
 // Calls with at most this many rows (queries x heads) of a kv head.
 constexpr int DECODE_ROWS = 64;
 
 // Ranges that the keys of a call are cut into, each for Hkv CTAs (and row
 // groups): as many CTAs as the 152 SMs hold at once, three each of the kernels
-// for 8 and 16 rows, two of the others; never more ranges than there can be
-// blocks of 128 keys.
+// for 8 and 16 rows, two of the others (twice as many, or a second set of small
+// ones for the SMs that are done first, cost more in partials than the balance
+// gave: 123 us instead of 114 us for 64 sequences of 1k-8k keys); never more ranges
+// than there can be blocks of 128 keys. Sequences of at most 512 keys (4 blocks)
+// are a range each: cutting them would cost a second launch and a workspace.
 inline DecodePlan decode_plan(int num_seqs, int Hkv, int heads, int max_queries, int max_pages, int page_size) {
   DecodePlan d;
   d.rows = static_cast<int>(static_cast<int64_t>(max_queries) * heads);
@@ -51,7 +67,8 @@ inline DecodePlan decode_plan(int num_seqs, int Hkv, int heads, int max_queries,
   const int64_t keys = static_cast<int64_t>(max_pages) * page_size;
   const int64_t blocks = num_seqs * (keys > 128 ? (keys + 127) / 128 : 1);
   const int64_t side = static_cast<int64_t>(Hkv) * d.row_groups;
-  int64_t r = 152 * (d.nt <= 2 ? 3 : 2) / side;
+  d.aligned = keys <= 512;
+  int64_t r = d.aligned ? num_seqs : 152 * (d.nt <= 2 ? 3 : 2) / side;
   if (r > blocks) r = blocks;
   d.ranges = static_cast<int>(r > 1 ? r : 1);
   return d;
