@@ -51,17 +51,16 @@ struct Raw8 {
 };
 
 template <int DT, bool VEC>
-__device__ __forceinline__ Raw8<DT> load_raw(const void* base, int64_t i) {
+__device__ __forceinline__ Raw8<DT> load_raw(const uint8_t* at) {
   Raw8<DT> r;
   if constexpr (VEC) {
 #pragma unroll
-    for (int k = 0; k < (DT == 0 ? 2 : 1); ++k)
-      r.w[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + i * (DT == 0 ? 4 : 2)) + k);
+    for (int k = 0; k < (DT == 0 ? 2 : 1); ++k) r.w[k] = __ldg(reinterpret_cast<const uint4*>(at) + k);
   } else {
     using E = std::conditional_t<DT == 0, uint32_t, uint16_t>;
     E* const e = reinterpret_cast<E*>(r.w);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) e[k] = __ldg(static_cast<const E*>(base) + i + k);
+    for (int k = 0; k < 8; ++k) e[k] = __ldg(reinterpret_cast<const E*>(at) + k);
   }
   return r;
 }
@@ -265,19 +264,25 @@ __global__ void __launch_bounds__(THREADS, DT == 0 ? 2 : 4) write_kernel(const _
   const int m = static_cast<int>(min(static_cast<int64_t>(c.group), L - g0)) - held;  // new tokens
   const int64_t x0 = lo + (g0 + held - (static_cast<int64_t>(L) - n));  // row of the first of them
   const int vpt = c.D >> 3, sh = __ffs(vpt) - 1;  // vectors of a token
-  const int nv = m * vpt;
-  const size_t cstep = static_cast<size_t>(c.Hkv) * c.D;
+  // The thread's vectors of a unit: column `col` of tokens t0, t0 + tinc, ... (TPU
+  // is a multiple of vpt): an addition from one to the next.
+  const int t0 = tu >> sh, col = tu & (vpt - 1), tinc = TPU >> sh;
+  const int64_t cstep = static_cast<int64_t>(c.Hkv) * c.D;
   const int64_t ncode8 = static_cast<int64_t>(c.num_pages) * c.page_size * c.Hkv * vpt;
   const int64_t nscale = static_cast<int64_t>(c.num_pages) * c.Hkv * c.per;
-  auto elements = [&](int unit, int e) {  // vector e of a unit's new tokens
+  constexpr int ES = DT == 0 ? 4 : 2;
+  auto source = [&](int unit) {  // of the thread's first vector
     const int kv = unit >= c.Hkv ? 1 : 0, h = unit - kv * c.Hkv;
-    return load_raw<DT, VEC>(p.x[kv], (x0 + (e >> sh)) * p.xt[kv] + h * p.xh[kv] + (e & (vpt - 1)) * 8);
+    return static_cast<const uint8_t*>(p.x[kv]) + ((x0 + t0) * p.xt[kv] + h * p.xh[kv] + col * 8) * ES;
   };
+  auto stride = [&](int unit) { return p.xt[unit >= c.Hkv ? 1 : 0] * (tinc * ES); };
   Raw8<DT> next[KEEP];
   auto fetch = [&](int unit) {
+    const uint8_t* at = source(unit);
+    const int64_t inc = stride(unit);
 #pragma unroll
-    for (int i = 0; i < KEEP; ++i)
-      if (tu + i * TPU < nv) next[i] = elements(unit, tu + i * TPU);
+    for (int i = 0; i < KEEP; ++i, at += inc)
+      if (t0 + i * tinc < m) next[i] = load_raw<DT, VEC>(at);
   };
   fetch(unit0);
   for (int u = 0; u < units; ++u) {
@@ -291,8 +296,12 @@ __global__ void __launch_bounds__(THREADS, DT == 0 ? 2 : 4) write_kernel(const _
     AbsMax<DT> most;
 #pragma unroll
     for (int i = 0; i < KEEP; ++i)
-      if (tu + i * TPU < nv) most.add(keep[i]);
-    for (int e = tu + KEEP * TPU; e < nv; e += TPU) most.add(elements(unit, e));
+      if (t0 + i * tinc < m) most.add(keep[i]);
+    if (t0 + KEEP * tinc < m) {  // what the registers do not keep
+      const int64_t inc = stride(unit);
+      const uint8_t* at = source(unit) + KEEP * inc;
+      for (int t = t0 + KEEP * tinc; t < m; t += tinc, at += inc) most.add(load_raw<DT, VEC>(at));
+    }
     float amax = most.value();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -315,32 +324,36 @@ __global__ void __launch_bounds__(THREADS, DT == 0 ? 2 : 4) write_kernel(const _
     else __syncwarp();
     if (tu == 0) *sc = sn;
     const size_t cbase = ((static_cast<size_t>(page) * c.page_size + row0) * c.Hkv + h) * c.D;
-    uint8_t* const codes = p.codes[kv];
-    auto slot8 = [&](int token, int col) { return reinterpret_cast<uint2*>(codes + cbase + token * cstep + col * 8); };
+    // of the group's token `held` + t0
+    uint8_t* const dst = p.codes[kv] + cbase + (held + t0) * cstep + col * 8;
+    const int64_t dinc = tinc * cstep;
     const float inv = 1.f / sn;
-    auto put = [&](int e, const Raw8<DT>& r) {
+    auto inside = [&](const uint8_t* at) { return in_bounds(c.status, (at - p.codes[kv]) >> 3, ncode8); };
+    auto put = [&](uint8_t* at, const Raw8<DT>& r) {
       float v[8];
       expand<DT>(r, v);
-      const int t = held + (e >> sh), col = e & (vpt - 1);
-      if (!in_bounds(c.status, static_cast<int64_t>((cbase + t * cstep) >> 3) + col, ncode8)) return;
+      if (!inside(at)) return;
       // a group without a scale (NaN) gets zero codes
-      *slot8(t, col) = sn == sn ? make_uint2(encode4<FMT>(v, sn, inv), encode4<FMT>(v + 4, sn, inv)) : make_uint2(0u, 0u);
+      *reinterpret_cast<uint2*>(at) =
+          sn == sn ? make_uint2(encode4<FMT>(v, sn, inv), encode4<FMT>(v + 4, sn, inv)) : make_uint2(0u, 0u);
     };
     if (held > 0 && sn > so) {  // the codes of earlier calls, at the larger scale
-      for (int e = tu; e < held * vpt; e += TPU) {
-        const int t = e >> sh, col = e & (vpt - 1);
-        if (!in_bounds(c.status, static_cast<int64_t>((cbase + t * cstep) >> 3) + col, ncode8)) continue;
-        uint2* const at = slot8(t, col);
-        const uint2 w = *at;
-        *at = make_uint2(recode4<FMT>(w.x, so, sn), recode4<FMT>(w.y, so, sn));
+      uint8_t* at = dst - held * cstep;
+      for (int t = t0; t < held; t += tinc, at += dinc) {
+        if (!inside(at)) continue;
+        const uint2 w = *reinterpret_cast<const uint2*>(at);
+        *reinterpret_cast<uint2*>(at) = make_uint2(recode4<FMT>(w.x, so, sn), recode4<FMT>(w.y, so, sn));
       }
     }
 #pragma unroll
-    for (int i = 0; i < KEEP; ++i) {
-      const int e = tu + i * TPU;
-      if (e < nv) put(e, keep[i]);
+    for (int i = 0; i < KEEP; ++i)
+      if (t0 + i * tinc < m) put(dst + i * dinc, keep[i]);
+    if (t0 + KEEP * tinc < m) {
+      const int64_t inc = stride(unit);
+      const uint8_t* at = source(unit) + KEEP * inc;
+      uint8_t* to = dst + KEEP * dinc;
+      for (int t = t0 + KEEP * tinc; t < m; t += tinc, at += inc, to += dinc) put(to, load_raw<DT, VEC>(at));
     }
-    for (int e = tu + KEEP * TPU; e < nv; e += TPU) put(e, elements(unit, e));
   }
 }
 
