@@ -116,7 +116,6 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 int attn::record_cuda_error(cudaError_t e) { return fail_cuda(e); }
 int* attn::status_word(int dev) { return status_ptr(dev); }
-attn::EncodeTiledFn attn::tensor_map_encoder() { return encode_fn(); }
 
 namespace {
 

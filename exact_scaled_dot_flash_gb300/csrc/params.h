@@ -132,8 +132,6 @@ cudaError_t launch_wait_timeout_probe(int* status, unsigned long long limit_ns,
                                       cudaStream_t stream);
 // Device address of the status word on the current device `dev`, or nullptr.
 int* status_word(int dev);
-// cuTensorMapEncodeTiled, or nullptr when the driver does not offer it.
-EncodeTiledFn tensor_map_encoder();
 // Records a failed CUDA call for attn_last_cuda_error(); returns ATTN_ERR_CUDA.
 int record_cuda_error(cudaError_t e);
 // Unique id of the calling thread's current CUDA context, 0 if there is none.
