@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
     if (row_ok)
       pos = p.positions ? (in_bounds(status, w.q_lo + tq, p.num_queries) ? __ldg(p.positions + w.q_lo + tq) : -1)
                         : w.L - w.nq + tq;
-    const int lim = p.causal ? min(pos, w.L - 1) : (row_ok ? w.L - 1 : -1);  // last key the row sees
+    // last key the row sees; a position far below 0 must not pass 2^31 in the difference to a tile's first key
+    const int lim = p.causal ? max(min(pos, w.L - 1), -1) : (row_ok ? w.L - 1 : -1);
     float ref = UNSEEN, l_run = 0.f;
     bool failed = false;
     for (int j = 0; j < n_t; ++j) {

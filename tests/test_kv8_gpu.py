@@ -529,3 +529,14 @@ def test_attention_row_counts(heads, new, H):
     # 9 .. 64 rows of a kv head, one and two groups of rows; heads that divide nothing; uneven lengths
     p = Problem(21, [300, 64, 1000], [new, 1, new - 1], dtype="f16", fmt="int8", D=64, P=16, G=4, H=H, Hq=H * heads)
     check_attention(p, attend(p, p.cache()), p.kc, p.ks, p.vc, p.vs)
+
+
+@pytest.mark.parametrize("new", [2, 90])
+@pytest.mark.parametrize("dtype,G", [("bf16", 1), ("f16", 16), ("f32", 4)])
+def test_positions_at_the_ends_of_int32(new, dtype, G):
+    # the lowest positions see no key of any tile, the highest see all
+    p = Problem(25, [400], [new], Hq=4, P=32, D=64, G=G, dtype=dtype)
+    pos = np.full(new, 350, np.int32)
+    pos[0], pos[1], pos[new // 2], pos[-1] = -2 ** 31 + 5, 2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1
+    got = attend(p, p.cache(), pos)
+    check_attention(p, got, p.kc, p.ks, p.vc, p.vs, pos)
