@@ -645,6 +645,9 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
     }
     __syncthreads();
   }
+  // a grid that cut no sequence does not end before zero_kernel either: the next
+  // one on the stream may use the workspace
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Clears the counters of the cut sequences.

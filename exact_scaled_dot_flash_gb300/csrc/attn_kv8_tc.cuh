@@ -608,12 +608,12 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const __grid_co
   const Work w = make_work(p, qblocks, 1, static_cast<int>(blockIdx.x));
   const int heads = p.Hq / p.c.Hkv, lane = threadIdx.x & 31;
   const int64_t pr = w.row0 + static_cast<int64_t>(blockIdx.y) * MERGE_WARPS + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // also without rows: this grid ends after tc_kernel's
   if (pr >= static_cast<int64_t>(w.nq) * heads) return;
   const int tq = static_cast<int>(pr / heads);
   const int64_t orow = static_cast<int64_t>(w.q_lo + tq) * p.Hq + w.hk * heads + (pr - static_cast<int64_t>(tq) * heads);
   const int64_t nrows = static_cast<int64_t>(p.num_queries) * p.Hq;
   if (!in_bounds(p.c.status, orow, nrows)) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const float4* const wo = static_cast<const float4*>(p.ws);
   const float2* const wml = reinterpret_cast<const float2*>(wo + splits * nrows * (D / 4));
   const float2 ml = lane < splits ? wml[lane * nrows + orow] : make_float2(-INFINITY, 0.f);

@@ -540,3 +540,36 @@ def test_positions_at_the_ends_of_int32(new, dtype, G):
     pos[0], pos[1], pos[new // 2], pos[-1] = -2 ** 31 + 5, 2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1
     got = attend(p, p.cache(), pos)
     check_attention(p, got, p.kc, p.ks, p.vc, p.vs, pos)
+
+
+def test_calls_that_share_a_workspace_in_turn():
+    # captured calls of one workspace, replayed back to back: sequences that are cut, one key block
+    # each (nothing to cut), few rows over runs of key tiles, and rows of no sequence
+    import torch
+    from exact_scaled_dot_flash_gb300 import attn
+    kw = dict(Hq=8, P=64, G=16, D=128)
+    ps = [Problem(26, [3000, 700], [1, 1], **kw), Problem(27, [60, 90, 2], [1, 1, 1], **kw),
+          Problem(28, [2500], [80], **kw), Problem(29, [2500, 40], [3, 1], **kw)]
+    for p in ps:  # a table with room for more than 512 keys each
+        p.table = np.pad(p.table, ((0, 0), (0, max(0, 10 - p.table.shape[1]))), constant_values=-1)
+    sets = [(p, p.cache(), p.q.cuda(), gpu(p.offs), torch.empty(p.q.shape, dtype=p.q.dtype, device="cuda"),
+             int(p.new.max())) for p in ps]
+    p, cache, q, offs, _, new = sets[0]
+    sets.append((p, cache, q, torch.zeros_like(offs), torch.empty_like(q), new))
+    work = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")
+    want = [attn.paged_kv8_fwd(q, *cache, offs, max_queries=new) for _, cache, q, offs, _, new in sets[:4]]
+    for (p, cache, q, offs, _, new), w in zip(sets, want):
+        out, lse = attn.paged_kv8_fwd(q, *cache, offs, max_queries=new, return_lse=True)
+        check_attention(p, (out, lse), p.kc, p.ks, p.vc, p.vs)
+        assert torch.equal(out, w)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for i in (0, 1, 2, 4, 3, 0, 4, 1):
+            _, cache, q, offs, out, new = sets[i]
+            attn.paged_kv8_fwd(q, *cache, offs, max_queries=new, out=out, workspace=work)
+    for _ in range(20):
+        for s in sets[:4]:
+            s[4].zero_()
+        g.replay()
+        assert all(torch.equal(s[4], w) for s, w in zip(sets, want))
