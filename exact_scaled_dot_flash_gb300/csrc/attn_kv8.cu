@@ -523,6 +523,10 @@ int check_cache(const attn_kv8_cache_t* cache, int num_seqs, int max_pages, Cach
       num_seqs < 0 || max_pages < 0 || static_cast<int64_t>(max_pages) * s.page_size > 0x7fffffffLL ||
       s.Hkv > 32767)
     return ATTN_ERR_SHAPE;
+  // extents stay far inside 64 bits
+  if (static_cast<double>(s.num_pages) * s.page_size * s.Hkv * s.D > 1e16 ||
+      static_cast<double>(num_seqs) * max_pages > 1e16)
+    return ATTN_ERR_SHAPE;
   if (!(s.D == 16 || s.D == 32 || s.D == 64 || s.D == 128)) return ATTN_ERR_HEAD_DIM;
   c.num_pages = s.num_pages;
   c.page_size = s.page_size;

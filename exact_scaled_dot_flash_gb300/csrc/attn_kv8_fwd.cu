@@ -71,7 +71,8 @@ __global__ void __launch_bounds__(THREADS) simt_kernel(const __grid_constant__ F
     acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   float m_run = -INFINITY, l_run = 0.f;
-  for (int key0 = 0; key0 < key_hi; key0 += KT) {
+  for (int64_t tile0 = 0; tile0 < key_hi; tile0 += KT) {  // 64 bits: key_hi may be 2^31 - 1
+    const int key0 = static_cast<int>(tile0);
     __syncthreads();
     for (int e = tid; e < KT * G; e += THREADS) {
       const int kr = e / G, col = e - kr * G;
@@ -183,6 +184,11 @@ int check_shape(const attn_paged_shape_t& s) {
   if (static_cast<int64_t>(s.num_seqs) * s.Hkv > 0x7fffffffLL ||
       (static_cast<int64_t>(s.max_queries) * (s.Hq / s.Hkv) + 63) / 64 > 65535 ||
       static_cast<int64_t>(s.max_pages) * s.page_size > 0x7fffffffLL)
+    return ATTN_ERR_SHAPE;
+  // extents stay far inside 64 bits
+  const double tokens = static_cast<double>(s.num_pages) * s.page_size;
+  if (tokens * s.Hkv * s.D > 1e16 || static_cast<double>(s.num_queries) * s.Hq * s.D > 1e16 ||
+      static_cast<double>(s.num_seqs) * s.max_pages > 1e16)
     return ATTN_ERR_SHAPE;
   return ATTN_OK;
 }

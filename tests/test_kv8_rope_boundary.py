@@ -248,3 +248,18 @@ def test_reference_codes():
     y = torch.from_numpy(x.astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
     assert np.array_equal(R.encode(x.astype(np.float64), "e4m3"), y)
     assert R.new_scale(448.0, "e4m3") == 1.0 and R.new_scale(449.0, "e4m3") == 2.0
+
+
+@no_gpu_only
+def test_extents_past_64_bits(lib):  # noqa: F811
+    top = (1 << 31) - 1
+    big = cache(pages=top, P=1 << 20, H=32767, D=128, G=1)
+    wide = cache(P=1, G=1)
+    for call in (write, read):
+        assert call(big) == codes["ATTN_ERR_SHAPE"]
+        assert call(wide, ns=(1 << 30) - 1, mp=top) == codes["ATTN_ERR_SHAPE"]
+    for kw in (dict(num_pages=top, page_size=1 << 20, Hkv=1 << 15, Hq=1 << 15, D=128),
+               dict(num_queries=top, Hkv=1 << 20, Hq=1 << 30, max_queries=1),
+               dict(num_seqs=(1 << 30) - 1, page_size=1, Hkv=2, max_pages=top)):
+        assert fwd(shape(**kw)) == codes["ATTN_ERR_SHAPE"], kw
+        assert lib.attn_paged_kv8_workspace_bytes(shape(**kw), ctypes.c_size_t()) == codes["ATTN_ERR_SHAPE"], kw
