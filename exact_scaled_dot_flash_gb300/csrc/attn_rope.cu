@@ -214,6 +214,7 @@ using attn::rope::Side;
 struct Span {  // what a strided tensor may touch, in bytes
   uintptr_t p;
   int64_t token, row, all;  // token stride, extent of one token's heads, extent of everything
+  int64_t batch, one;       // batch stride, extent of one batch
 };
 
 Span span_of(const void* p, int64_t B, int64_t S, int64_t H, int64_t D, const int64_t* st, int es) {
@@ -221,21 +222,29 @@ Span span_of(const void* p, int64_t B, int64_t S, int64_t H, int64_t D, const in
   s.p = reinterpret_cast<uintptr_t>(p);
   s.token = st[1] * es;
   s.row = ((H - 1) * st[2] + D) * es;
+  s.batch = st[0] * es;
+  s.one = ((S - 1) * st[1] + (H - 1) * st[2] + D) * es;
   s.all = ((B - 1) * st[0] + (S - 1) * st[1] + (H - 1) * st[2] + D) * es;
   return s;
 }
 
+// Whether pieces of na bytes every `period` from a on and of nb bytes from b on lie apart.
+bool apart_modulo(uintptr_t a, int64_t na, uintptr_t b, int64_t nb, int64_t period) {
+  if (period <= 0 || na > period || nb > period) return false;
+  const int64_t diff = static_cast<int64_t>(b) - static_cast<int64_t>(a);
+  const int64_t d = ((diff % period) + period) % period;
+  return d >= na && d + nb <= period;
+}
+
 // Whether two strided tensors may share an element. Slices of one fused
 // projection interleave without sharing any: tokens the same stride apart
-// (batches too, as multiples of it), and rows that lie apart modulo it.
+// (batches too, as multiples of it), and rows that lie apart modulo it; or
+// batches the same stride apart, and all of a batch apart modulo that (the
+// heads of one dense tensor).
 bool spans_meet(const Span& a, const Span& b, bool batches_fit) {
   if (a.p + a.all <= b.p || b.p + b.all <= a.p) return false;
-  if (batches_fit && a.token == b.token && a.token > 0 && a.row <= a.token && b.row <= a.token) {
-    const int64_t diff = static_cast<int64_t>(b.p) - static_cast<int64_t>(a.p);
-    const int64_t d = ((diff % a.token) + a.token) % a.token;
-    if (d >= a.row && d + b.row <= a.token) return false;
-  }
-  return true;
+  if (batches_fit && a.token == b.token && apart_modulo(a.p, a.row, b.p, b.row, a.token)) return false;
+  return a.batch != b.batch || !apart_modulo(a.p, a.one, b.p, b.one, a.batch);
 }
 
 // No two (batch, token, head) rows of a written tensor may share an element:
@@ -304,8 +313,8 @@ extern "C" int attn_rope(const attn_rope_shape_t* shape, const void* q, const vo
   const int64_t meta_bytes[2] = {(s.pos_batch_stride ? tokens : s.S) * 4, s.rot / 2 * 8};
   for (int i = 0; i < 2; ++i) {
     meta[i].p = reinterpret_cast<uintptr_t>(i == 0 ? static_cast<const void*>(positions) : inv_freq);
-    meta[i].token = 0;
-    meta[i].row = meta[i].all = meta_bytes[i];
+    meta[i].token = meta[i].batch = 0;
+    meta[i].row = meta[i].one = meta[i].all = meta_bytes[i];
   }
   for (int o = 1; o < 2 * nside; o += 2) {  // each output against every other tensor
     for (int i = 0; i < 2 * nside; ++i)

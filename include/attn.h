@@ -566,7 +566,8 @@ typedef struct {
  * positions: device int32 [S] or [B, S] (row stride pos_batch_stride).
  * An output may be its own input (same pointer and strides), must have no two
  * rows in the same place and may share no other element with any other
- * argument; slices of one buffer that interleave by token are told apart.
+ * argument; slices of one buffer that interleave by token or by batch are told
+ * apart.
  * Pointers aligned to their element; rows on 16-byte boundaries move as vectors.
  * Asynchronous on `stream`, one kernel. Returns ATTN_OK or a negative
  * ATTN_ERR_* code before any launch (ATTN_ERR_SCALE: mscale not finite). */

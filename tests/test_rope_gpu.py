@@ -162,3 +162,20 @@ def test_graph_and_side_stream():
     got = attn.rope(q, k, pos, f, stream=s)
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("S", [1, 21])
+def test_heads_of_one_dense_tensor_in_place(S):
+    import torch
+    from exact_scaled_dot_flash_gb300 import attn
+    r = np.random.RandomState(6)
+    buf = torch.from_numpy(r.randn(3, 4 + 2 + 2, S, 64)).to(torch.float16).cuda()
+    q, k, v = buf[:, :4], buf[:, 4:6], buf[:, 6:]
+    f, pos = attn.rope_frequencies(64)[0].cuda(), torch.from_numpy(r.randint(0, 999, (3, S)).astype(np.int32)).cuda()
+    want = attn.rope(q.contiguous(), k.contiguous(), pos, f)
+    rest = v.clone()
+    attn.rope(q, k, pos, f, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, rest)
+    for out in (buf[:, 1:5], buf[:, 3:7]):  # shares heads with q or k
+        with pytest.raises(attn.AttnError):
+            attn.rope(q, k, pos, f, q_out=out)
