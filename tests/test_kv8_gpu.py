@@ -573,3 +573,20 @@ def test_calls_that_share_a_workspace_in_turn():
             s[4].zero_()
         g.replay()
         assert all(torch.equal(s[4], w) for s, w in zip(sets, want))
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("seqs,new,Hq,H", [(1, 4, 20, 4), (2, 2, 60, 4), (20, 5, 21, 3), (30, 9, 24, 3), (45, 2, 52, 2), (9, 3, 20, 1)])
+def test_attention_by_every_way_of_cutting(seqs, new, Hq, H, wide):
+    # few and many rows over few, half and enough sequences to fill the GPU, whole and cut into runs
+    r = np.random.RandomState(30)
+    lens = r.randint(new, 1300, seqs)
+    lens[0] = 1300
+    p = Problem(30, lens, np.full(seqs, new), Hq=Hq, H=H, P=64, G=16, D=64, dtype="f16", fmt="e4m3")
+    if wide:  # room for 8192 keys
+        p.table = np.pad(p.table, ((0, 0), (0, 128 - p.table.shape[1])), constant_values=-1)
+    cache = p.cache()
+    got = attend(p, cache)
+    check_attention(p, got, p.kc, p.ks, p.vc, p.vs)
+    again = attend(p, cache)
+    assert all(a.cpu().float().numpy().tobytes() == b.cpu().float().numpy().tobytes() for a, b in zip(got, again))
