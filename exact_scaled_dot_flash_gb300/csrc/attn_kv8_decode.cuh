@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
         if (!tiles_in_page) row %= c.page_size;
         const int tok = page * c.page_size + row;
         const bool ok = page >= 0 && in_bounds(status, tok, ntok);
-        const int mine = ok ? tok : 0;  // zeros by their scale
+        const int mine = ok ? tok : -1;  // -1: zeros
         const int gi = c.group == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.group_magic));
         const int64_t si = ok ? (static_cast<int64_t>(page) * c.Hkv + h) * c.per + gi : 0;
         const int bytes = ok && in_bounds(status, si, nscale) ? 4 : 0;
@@ -349,9 +349,10 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
 #pragma unroll
         for (int j = 0; j < TILE_KEYS / RPC; ++j) {
           const int r = RPC * j + lane / PIECES;
-          const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, mine, r))) * step;
-          copy16(at + k_piece<D>(r, lane % PIECES) * 16, kb + off);
-          copy16(at + SH::TILE + v_piece<D>(r, lane % PIECES) * 16, vb + off);
+          const int key = __shfl_sync(0xffffffffu, mine, r), n = key < 0 ? 0 : 16;
+          const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(max(key, 0))) * step;
+          copy16(at + k_piece<D>(r, lane % PIECES) * 16, kb + off, n);
+          copy16(at + SH::TILE + v_piece<D>(r, lane % PIECES) * 16, vb + off, n);
         }
       }
       copy_commit();

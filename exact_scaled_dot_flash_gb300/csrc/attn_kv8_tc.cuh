@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
       const uint8_t* const kb = p.k_codes + w.hk * D + lpiece * 16;
       const uint8_t* const vb = p.v_codes + w.hk * D + lpiece * 16;
       uint8_t* const raw = smem + C::OFF_RAW + cw * 32 * D;
-      int tok = 0;         // the lane's key of the tile being copied
+      int tok = -1;        // the lane's key of the tile being copied, -1: zeros
       int64_t si = -1;     // its scales, -1: zeros
       float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
       // The lane's key of the tile to copy next, and its page, which is read a
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
       auto look_up = [&]() {
         const bool ok = page >= 0 && page < c.num_pages && in_bounds(status, static_cast<int64_t>(page) * c.page_size + row, ntok);
         const int gi = c.group == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.group_magic));
-        tok = ok ? page * c.page_size + row : 0;
+        tok = ok ? page * c.page_size + row : -1;
         si = ok ? (static_cast<int64_t>(page) * c.Hkv + w.hk) * c.per + gi : -1;
         if (si >= 0 && !in_bounds(status, si, nscale)) si = -1;
         key += BN;
@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
 #pragma unroll
           for (int i = 0; i < COPIES; ++i) {
             const int r = RPC * i + lrow;
-            const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, tok, r))) * step;
-            copy16(at + (i * 32 + lane) * 16, base + off);
+            const int key = __shfl_sync(0xffffffffu, tok, r);
+            copy16(at + (i * 32 + lane) * 16, base + static_cast<uint64_t>(static_cast<uint32_t>(max(key, 0))) * step,
+                   key < 0 ? 0 : 16);
           }
         }
         copy_commit();

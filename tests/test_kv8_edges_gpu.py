@@ -1,0 +1,86 @@
+"""The 8-bit paged cache on the GPU where bytes, scales and scores are not those that this library's
+writer makes of ordinary values: e4m3 codes 0x7f and 0xff, keys that are not there, value scales far
+apart, scales of another program. Against the restatement in 64 bits (kv8_ref.py).
+
+``close`` counts only what a row sees. With u half a step of the type of q, A = sum_j p_j |v_j|,
+b = max_j scale sum_d |q_d| |k_jd|, w = max_j p_j v_scale_j and c the largest code among the n keys
+that the row sees:
+  u |o|                    the output's rounding,
+  2^-11 A                  p_j v_scale_j as F16 (F16 and BF16 only),
+  2^-24 n w c              one below 2^-14 of w is subnormal in F16: off by up to 2^-24 of w,
+  2^-24 (16 b + 128) A     fp32: scores, exp2 and sums,
+  2^-126 n max|v|          the range of fp32: exp2 gives 0 below 2^-126,
+  2^-24                    F16 outputs below its normal range."""
+import numpy as np
+import pytest
+
+from tests import kv8_ref as R
+from tests.gpu_util import to_f64
+from tests.test_kv8_gpu import U, Problem, _clean_status, attend, gpu, tdt  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def close(p, got, positions=None, causal=True, scale=None, rows=None):
+    out, lse = to_f64(got[0]), got[1].cpu().numpy().astype(np.float64)
+    scale = 1 / np.sqrt(p.D) if scale is None else scale
+    k, v = R.read_all(p.kc, p.ks, p.fmt), R.read_all(p.vc, p.vs, p.fmt)
+    code = np.abs(R.values(p.vc, p.fmt))
+    u = U[p.dtype]
+    q = p.q.double().numpy()
+    for s, L in enumerate(p.lens):
+        j = np.arange(L)
+        page, row = p.table[s, j // p.P], j % p.P
+        ok = (page >= 0) & (page < p.pages)
+        at = np.where(ok, page, 0)
+        kk, vv = (np.where(ok[:, None, None], x[at, row], 0.0) for x in (k, v))
+        cc = np.where(ok[:, None], code[at, row].max(-1), 0.0)                      # [L, H]
+        vs = np.where(ok[:, None], p.vs[at, :, row // p.G].astype(np.float64), 0.0)  # [L, H]
+        for i in range(int(p.offs[s]), int(p.offs[s + 1])):
+            if rows is not None and not rows[i]:
+                continue
+            pos = int(positions[i]) if positions is not None else L - int(p.offs[s + 1]) + i
+            n = min(L, pos + 1) if causal else L
+            for h in range(p.Hq):
+                hk = h // (p.Hq // p.H)
+                t = kk[:n, hk] @ q[i, h] * scale
+                e = np.exp(t - t.max())
+                pr = e / e.sum()
+                o, A = pr @ vv[:n, hk], pr @ np.abs(vv[:n, hk])
+                b = (np.abs(kk[:n, hk]) @ np.abs(q[i, h])).max() * scale
+                tol = u * np.abs(o) + 2.0 ** -24 * (16 * b + 128) * A + 2.0 ** -126 * n * np.abs(vv[:n, hk]).max()
+                if p.dtype != "f32":
+                    tol = tol + 2.0 ** -11 * A + 2.0 ** -24 * n * (pr * vs[:n, hk]).max() * cc[:n, hk].max()
+                if p.dtype == "f16":
+                    tol = tol + 2.0 ** -24
+                err = np.abs(out[i, h] - o)
+                assert (err <= tol).all(), (f"sequence {s} row {i} head {h}: {np.max(err / np.maximum(tol, 1e-300)):.3g} "
+                                            f"of the tolerance, {out[i, h, :3]} for {o[:3]}")
+                ref = t.max() + np.log(e.sum())
+                assert abs(lse[i, h] - ref) <= 2.0 ** -24 * (16 * b + 128 + 4 * abs(ref)), f"lse of row {i} head {h}"
+
+
+NAN_BYTES = np.array([0x7f, 0xff], np.uint8)
+
+
+def nobody_has_page_0(p):
+    free = np.setdiff1d(np.arange(p.pages), p.table[p.table >= 0])
+    if 0 not in free:
+        p.table[p.table == 0] = free[0]
+
+
+@pytest.mark.parametrize("dtype,fmt,D", [("bf16", "e4m3", 128), ("f16", "e4m3", 64), ("f16", "int8", 128), ("f32", "e4m3", 64)])
+@pytest.mark.parametrize("new", [1, 5, 90])
+def test_keys_that_are_not_there_read_nothing(dtype, fmt, D, new):
+    # behind the last token of a tile, and on pages outside the cache: zeros, whatever the bytes that
+    # the cache begins with (its page 0 belongs to no sequence and was never written)
+    p = Problem(40, [99, 150, 333], [new] * 3, dtype=dtype, fmt=fmt, D=D, Hq=8, P=32, G=4)
+    nobody_has_page_0(p)
+    p.table[1, 1], p.table[2, 3] = -1, p.pages
+    r = np.random.RandomState(41)
+    for c in (p.kc, p.vc):
+        c[0] = r.choice(NAN_BYTES, c[0].shape)
+    p.ks[0], p.vs[0] = np.nan, np.nan
+    got = attend(p, p.cache())
+    assert np.isfinite(to_f64(got[0])).all()
+    close(p, got)
