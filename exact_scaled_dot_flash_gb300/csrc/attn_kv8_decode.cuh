@@ -28,7 +28,8 @@
 //    falls below 2^-24 there is 2^-40 of the row's largest element), and the
 //    probabilities get 11 bits instead of 8. Codes convert exactly: int8 by
 //    placing the byte, offset by 128, under the exponent of 1024 and
-//    subtracting; e4m3 by the conversion instruction;
+//    subtracting; e4m3 by the conversion instruction (its two NaN codes: a
+//    warp that meets a NaN takes its keys again);
 //  - k_scale enters the score in fp32, v_scale the probability before it is
 //    rounded. A row has one reference exponent for both: with y = 2^(x - ref),
 //    l = sum y and P' = y v_scale, and ref moves up when a P' passes 2^8 (one vote
@@ -45,6 +46,8 @@
 // that is: the result does not depend on who came last. Sequences of at most 512
 // keys are not cut: a CTA each (and head), no counters, no workspace.
 #pragma once
+
+#include <type_traits>
 
 #include "kv8_fwd.h"
 #include "kv8_ops.cuh"
@@ -314,217 +317,239 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 3 : 2)
     // Of a row: y = 2^(x - ref) for a score x (log2 units), l the lane's part of
     // the sum of y, acc the sum of P' = y v_scale times the codes.
     float ref[NT][2], l[NT][2], acc[KS][NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      ref[i][0] = ref[i][1] = UNSEEN;
-      l[i][0] = l[i][1] = 0.f;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) acc[k][i][0] = acc[k][i][1] = acc[k][i][2] = acc[k][i][3] = 0.f;
-    }
-    // Lane (g, t): keys ka and ka + 2 of each 16 of a tile in S^T, 4 t .. 4 t + 3 in V^T
-    const int ka = 4 * (g >> 1) + (g & 1);
-    const int last_key = min(most + 1, (b + take) * BLOCK_KEYS);
-    int key0 = b * BLOCK_KEYS + warp * TILE_KEYS;
-    // The tile to copy next; a lane has one of its keys. The page is looked up
-    // one tile ahead of the copy.
-    int ckey = key0, blk = key0 / c.page_size, row0 = key0 - blk * c.page_size;
-    auto find_page = [&]() {
-      if (ckey + lane >= L) return -1;
-      return page_of(c, s, tiles_in_page ? blk : blk + (row0 + lane) / c.page_size);
-    };
-    int page = find_page();
-    auto copy_tile = [&](int stage) {
-      if (ckey < last_key) {
-        int row = row0 + lane;
-        if (!tiles_in_page) row %= c.page_size;
-        const int tok = page * c.page_size + row;
-        const bool ok = page >= 0 && in_bounds(status, tok, ntok);
-        const int mine = ok ? tok : -1;  // -1: zeros
-        const int gi = c.group == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.group_magic));
-        const int64_t si = ok ? (static_cast<int64_t>(page) * c.Hkv + h) * c.per + gi : 0;
-        const int bytes = ok && in_bounds(status, si, nscale) ? 4 : 0;
-        const uint32_t at = ring_at + stage * SH::STAGE;
-        copy4(at + 2 * SH::TILE + lane * 4, p.k_scale + (bytes ? si : 0), bytes);
-        copy4(at + 2 * SH::TILE + 4 * TILE_KEYS + lane * 4, p.v_scale + (bytes ? si : 0), bytes);
-#pragma unroll
-        for (int j = 0; j < TILE_KEYS / RPC; ++j) {
-          const int r = RPC * j + lane / PIECES;
-          const int key = __shfl_sync(0xffffffffu, mine, r), n = key < 0 ? 0 : 16;
-          const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(max(key, 0))) * step;
-          copy16(at + k_piece<D>(r, lane % PIECES) * 16, kb + off, n);
-          copy16(at + SH::TILE + v_piece<D>(r, lane % PIECES) * 16, vb + off, n);
-        }
-      }
-      copy_commit();
-      ckey += BLOCK_KEYS;
-      blk += dblk;
-      row0 += drow;
-      if (row0 >= c.page_size) {
-        row0 -= c.page_size;
-        ++blk;
-      }
-      page = find_page();
-    };
-#pragma unroll
-    for (int i = 0; i < SH::STAGES - 1; ++i) copy_tile(i);
-    int stage = 0;
-    for (; key0 < last_key; key0 += BLOCK_KEYS) {
-      copy_wait<SH::STAGES - 2>();
-      __syncwarp();  // the tile's copies of every lane; and every lane is done with the tile before
-      copy_tile(stage == 0 ? SH::STAGES - 1 : stage - 1);
-      const uint8_t* const at = ring + stage * SH::STAGE;
-      stage = stage == SH::STAGES - 1 ? 0 : stage + 1;
-      const float* const scales = reinterpret_cast<const float*>(at + 2 * SH::TILE);
-      float sc[2][NT][4], vs[2][2];
-      const bool masked = key0 + TILE_KEYS - 1 > least;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {  // 16 keys
-        uint32_t kr[2][KB * 4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int i = 0; i < KB; ++i) {
-            const uint4 x = reinterpret_cast<const uint4*>(at)[k_piece<D>(16 * u + ka + 2 * e, 4 * i + t)];
-            kr[e][4 * i] = x.x; kr[e][4 * i + 1] = x.y; kr[e][4 * i + 2] = x.z; kr[e][4 * i + 3] = x.w;
-          }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) sc[u][i][0] = sc[u][i][1] = sc[u][i][2] = sc[u][i][3] = 0.f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t a0, a1, a2, a3;
-          pairs<FMT>(kr[0][k], a0, a2);
-          pairs<FMT>(kr[1][k], a1, a3);
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            if constexpr (NT == 1) {
-              mma16816(sc[u][i], a0, a1, a2, a3, qf[k][0], qf[k][1]);
-            } else {
-              const uint2 w = sq[(i * KS + k) * 32 + lane];
-              mma16816(sc[u][i], a0, a1, a2, a3, w.x, w.y);
-            }
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float f = scales[16 * u + ka + 2 * e] * p.scale_log2;
-          vs[u][e] = scales[TILE_KEYS + 16 * u + ka + 2 * e];
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            sc[u][i][2 * e] *= f;
-            sc[u][i][2 * e + 1] *= f;
-          }
-        }
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (key0 + 16 * u + ka + (e & 2) > lim[i][e & 1]) sc[u][i][e] = -INFINITY;
-        }
-      }
-      // y and P' against the rows' references
-      float z[2][NT][4], d[NT][2];
-      auto against = [&](int i) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) d[i][e] = 0.f;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float y = fast_exp2(fmaf(sc[u][i][e], back[i][e & 1], -ref[i][e & 1]));
-            d[i][e & 1] += y;
-            z[u][i][e] = y * vs[u][e >> 1];
-          }
-      };
-      float big = 0.f;
+    auto stream = [&](auto every) {
+      constexpr bool EVERY = decltype(every)::value;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        against(i);
+        ref[i][0] = ref[i][1] = UNSEEN;
+        l[i][0] = l[i][1] = 0.f;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          big = fmax3(big, z[u][i][0], z[u][i][1]);
-          big = fmax3(big, z[u][i][2], z[u][i][3]);
-        }
-        // y itself past 2^88: value scales so small that P' does not show it
-        constexpr float DOWN = 8.271806125530277e-25f;  // 2^-80
-        big = fmax3(big, d[i][0] * DOWN, d[i][1] * DOWN);
+        for (int k = 0; k < KS; ++k) acc[k][i][0] = acc[k][i][1] = acc[k][i][2] = acc[k][i][3] = 0.f;
       }
-      if (__any_sync(0xffffffffu, big > 256.f)) {
+      // Lane (g, t): keys ka and ka + 2 of each 16 of a tile in S^T, 4 t .. 4 t + 3 in V^T
+      const int ka = 4 * (g >> 1) + (g & 1);
+      const int last_key = min(most + 1, (b + take) * BLOCK_KEYS);
+      int key0 = b * BLOCK_KEYS + warp * TILE_KEYS;
+      // The tile to copy next; a lane has one of its keys. The page is looked up
+      // one tile ahead of the copy.
+      int ckey = key0, blk = key0 / c.page_size, row0 = key0 - blk * c.page_size;
+      auto find_page = [&]() {
+        if (ckey + lane >= L) return -1;
+        return page_of(c, s, tiles_in_page ? blk : blk + (row0 + lane) / c.page_size);
+      };
+      int page = find_page();
+      auto copy_tile = [&](int stage) {
+        if (ckey < last_key) {
+          int row = row0 + lane;
+          if (!tiles_in_page) row %= c.page_size;
+          const int tok = page * c.page_size + row;
+          const bool ok = page >= 0 && in_bounds(status, tok, ntok);
+          const int mine = ok ? tok : -1;  // -1: zeros
+          const int gi = c.group == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.group_magic));
+          const int64_t si = ok ? (static_cast<int64_t>(page) * c.Hkv + h) * c.per + gi : 0;
+          const int bytes = ok && in_bounds(status, si, nscale) ? 4 : 0;
+          const uint32_t at = ring_at + stage * SH::STAGE;
+          copy4(at + 2 * SH::TILE + lane * 4, p.k_scale + (bytes ? si : 0), bytes);
+          copy4(at + 2 * SH::TILE + 4 * TILE_KEYS + lane * 4, p.v_scale + (bytes ? si : 0), bytes);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
+          for (int j = 0; j < TILE_KEYS / RPC; ++j) {
+            const int r = RPC * j + lane / PIECES;
+            const int key = __shfl_sync(0xffffffffu, mine, r), n = key < 0 ? 0 : 16;
+            const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(max(key, 0))) * step;
+            copy16(at + k_piece<D>(r, lane % PIECES) * 16, kb + off, n);
+            copy16(at + SH::TILE + v_piece<D>(r, lane % PIECES) * 16, vb + off, n);
+          }
+        }
+        copy_commit();
+        ckey += BLOCK_KEYS;
+        blk += dblk;
+        row0 += drow;
+        if (row0 >= c.page_size) {
+          row0 -= c.page_size;
+          ++blk;
+        }
+        page = find_page();
+      };
+#pragma unroll
+      for (int i = 0; i < SH::STAGES - 1; ++i) copy_tile(i);
+      int stage = 0;
+      for (; key0 < last_key; key0 += BLOCK_KEYS) {
+        copy_wait<SH::STAGES - 2>();
+        __syncwarp();  // the tile's copies of every lane; and every lane is done with the tile before
+        copy_tile(stage == 0 ? SH::STAGES - 1 : stage - 1);
+        const uint8_t* const at = ring + stage * SH::STAGE;
+        stage = stage == SH::STAGES - 1 ? 0 : stage + 1;
+        const float* const scales = reinterpret_cast<const float*>(at + 2 * SH::TILE);
+        float sc[2][NT][4], vs[2][2];
+        const bool masked = key0 + TILE_KEYS - 1 > least;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {  // 16 keys
+          uint32_t kr[2][KB * 4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < KB; ++i) {
+              const uint4 x = reinterpret_cast<const uint4*>(at)[k_piece<D>(16 * u + ka + 2 * e, 4 * i + t)];
+              kr[e][4 * i] = x.x; kr[e][4 * i + 1] = x.y; kr[e][4 * i + 2] = x.z; kr[e][4 * i + 3] = x.w;
+            }
+#pragma unroll
+          for (int i = 0; i < NT; ++i) sc[u][i][0] = sc[u][i][1] = sc[u][i][2] = sc[u][i][3] = 0.f;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            uint32_t a0, a1, a2, a3;
+            pairs<FMT, EVERY>(kr[0][k], a0, a2);
+            pairs<FMT, EVERY>(kr[1][k], a1, a3);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              if constexpr (NT == 1) {
+                mma16816(sc[u][i], a0, a1, a2, a3, qf[k][0], qf[k][1]);
+              } else {
+                const uint2 w = sq[(i * KS + k) * 32 + lane];
+                mma16816(sc[u][i], a0, a1, a2, a3, w.x, w.y);
+              }
+            }
+          }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = fmaxf(fmaxf(sc[0][i][e], sc[0][i][2 + e]), fmaxf(sc[1][i][e], sc[1][i][2 + e]));
+            const float f = scales[16 * u + ka + 2 * e] * p.scale_log2;
+            vs[u][e] = scales[TILE_KEYS + 16 * u + ka + 2 * e];
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-            const bool none = x == -INFINITY;
-            x = none ? 0.f : x * back[i][e];
-            float w = 0.f;  // the largest p v_scale of the tile, p relative to x
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int a = 0; a < 2; ++a)
-                w = fmaxf(w, fast_exp2(fmaf(sc[u][i][2 * a + e], back[i][e], -x)) * vs[u][a]);
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
-            // w < 2^ex
-            const int ex = static_cast<int>(__float_as_uint(w) >> 23) - 126;
-            const float n = none ? ref[i][e] : fmaxf(ref[i][e], x + fmaxf(static_cast<float>(ex), -Y_RANGE));
-            const float f = fast_exp2(ref[i][e] - n);
-            ref[i][e] = n;
-            l[i][e] *= f;
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              acc[k][i][e] *= f;
-              acc[k][i][2 + e] *= f;
+            for (int i = 0; i < NT; ++i) {
+              sc[u][i][2 * e] *= f;
+              sc[u][i][2 * e + 1] *= f;
             }
           }
-          against(i);
-        }
-      }
-      uint32_t pf[2][NT][2];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        l[i][0] += d[i][0];
-        l[i][1] += d[i][1];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (masked) {  // a masked key may have any scale
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[u][i][e] = sc[u][i][e] == -INFINITY ? 0.f : z[u][i][e];
-          }
-          pf[u][i][0] = transpose8x8(pack2<false>(z[u][i][0], z[u][i][1]));
-          pf[u][i][1] = transpose8x8(pack2<false>(z[u][i][2], z[u][i][3]));
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t vr[4][VW];
-        const uint8_t* const va = at + SH::TILE;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (D == 128) {
-            const uint4 x = reinterpret_cast<const uint4*>(va)[v_piece<D>(16 * u + 4 * t + i, g)];
-            vr[i][0] = x.x; vr[i][1] = x.y; vr[i][2] = x.z; vr[i][3] = x.w;
-          } else {
-            const uint2 x = reinterpret_cast<const uint2*>(va)[v_piece<D>(16 * u + 4 * t + i, g >> 1) * 2 + (g & 1)];
-            vr[i][0] = x.x; vr[i][1] = x.y;
-          }
-        }
-#pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          // keys 0, 1 and 2, 3 of the lane interleaved: two steps' operands
-          uint32_t a[2][4];
-          pairs<FMT>(__byte_perm(vr[0][w], vr[1][w], 0x5140), a[0][0], a[0][1]);
-          pairs<FMT>(__byte_perm(vr[2][w], vr[3][w], 0x5140), a[0][2], a[0][3]);
-          pairs<FMT>(__byte_perm(vr[0][w], vr[1][w], 0x7362), a[1][0], a[1][1]);
-          pairs<FMT>(__byte_perm(vr[2][w], vr[3][w], 0x7362), a[1][2], a[1][3]);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
+          if (masked) {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
-              mma16816(acc[2 * w + k][i], a[k][0], a[k][1], a[k][2], a[k][3], pf[u][i][0], pf[u][i][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (key0 + 16 * u + ka + (e & 2) > lim[i][e & 1]) sc[u][i][e] = -INFINITY;
+          }
         }
+        // y and P' against the rows' references
+        float z[2][NT][4], d[NT][2];
+        auto against = [&](int i) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) d[i][e] = 0.f;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float y = fast_exp2(fmaf(sc[u][i][e], back[i][e & 1], -ref[i][e & 1]));
+              d[i][e & 1] += y;
+              z[u][i][e] = y * vs[u][e >> 1];
+            }
+        };
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          against(i);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            big = fmax3(big, z[u][i][0], z[u][i][1]);
+            big = fmax3(big, z[u][i][2], z[u][i][3]);
+          }
+          // y itself past 2^88: value scales so small that P' does not show it
+          constexpr float DOWN = 8.271806125530277e-25f;  // 2^-80
+          big = fmax3(big, d[i][0] * DOWN, d[i][1] * DOWN);
+        }
+        if (__any_sync(0xffffffffu, big > 256.f)) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaxf(fmaxf(sc[0][i][e], sc[0][i][2 + e]), fmaxf(sc[1][i][e], sc[1][i][2 + e]));
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+              const bool none = x == -INFINITY;
+              x = none ? 0.f : x * back[i][e];
+              float w = 0.f;  // the largest p v_scale of the tile, p relative to x
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+                  w = fmaxf(w, fast_exp2(fmaf(sc[u][i][2 * a + e], back[i][e], -x)) * vs[u][a]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
+              // w < 2^ex
+              const int ex = static_cast<int>(__float_as_uint(w) >> 23) - 126;
+              const float n = none ? ref[i][e] : fmaxf(ref[i][e], x + fmaxf(static_cast<float>(ex), -Y_RANGE));
+              const float f = fast_exp2(ref[i][e] - n);
+              ref[i][e] = n;
+              l[i][e] *= f;
+#pragma unroll
+              for (int k = 0; k < KS; ++k) {
+                acc[k][i][e] *= f;
+                acc[k][i][2 + e] *= f;
+              }
+            }
+            against(i);
+          }
+        }
+        uint32_t pf[2][NT][2];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          l[i][0] += d[i][0];
+          l[i][1] += d[i][1];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (masked) {  // a masked key may have any scale
+#pragma unroll
+              for (int e = 0; e < 4; ++e) z[u][i][e] = sc[u][i][e] == -INFINITY ? 0.f : z[u][i][e];
+            }
+            pf[u][i][0] = transpose8x8(pack2<false>(z[u][i][0], z[u][i][1]));
+            pf[u][i][1] = transpose8x8(pack2<false>(z[u][i][2], z[u][i][3]));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t vr[4][VW];
+          const uint8_t* const va = at + SH::TILE;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (D == 128) {
+              const uint4 x = reinterpret_cast<const uint4*>(va)[v_piece<D>(16 * u + 4 * t + i, g)];
+              vr[i][0] = x.x; vr[i][1] = x.y; vr[i][2] = x.z; vr[i][3] = x.w;
+            } else {
+              const uint2 x = reinterpret_cast<const uint2*>(va)[v_piece<D>(16 * u + 4 * t + i, g >> 1) * 2 + (g & 1)];
+              vr[i][0] = x.x; vr[i][1] = x.y;
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            // keys 0, 1 and 2, 3 of the lane interleaved: two steps' operands
+            uint32_t a[2][4];
+            pairs<FMT, EVERY>(__byte_perm(vr[0][w], vr[1][w], 0x5140), a[0][0], a[0][1]);
+            pairs<FMT, EVERY>(__byte_perm(vr[2][w], vr[3][w], 0x5140), a[0][2], a[0][3]);
+            pairs<FMT, EVERY>(__byte_perm(vr[0][w], vr[1][w], 0x7362), a[1][0], a[1][1]);
+            pairs<FMT, EVERY>(__byte_perm(vr[2][w], vr[3][w], 0x7362), a[1][2], a[1][3]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+                mma16816(acc[2 * w + k][i], a[k][0], a[k][1], a[k][2], a[k][3], pf[u][i][0], pf[u][i][1]);
+          }
+        }
+      }
+    };
+    stream(std::false_type());
+    if constexpr (FMT == FMT_E4M3) {
+      // A NaN in a sum may come of a code 0x7f or 0xff, of a key that some row of the
+      // warp sees or of a masked one's value: the warp's keys once more, with every
+      // code as what it stands for. (A NaN of the query or of a scale stays one.)
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        nan |= l[i][0] != l[i][0] || l[i][1] != l[i][1];
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) nan |= acc[k][i][e] != acc[k][i][e];
+      }
+      if (__any_sync(0xffffffffu, nan)) {
+        __syncwarp();  // every lane is done with the ring
+        stream(std::true_type());
       }
     }
     copy_wait<0>();

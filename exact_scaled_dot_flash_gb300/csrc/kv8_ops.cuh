@@ -7,14 +7,27 @@
 namespace attn {
 namespace kv8 {
 
-// The 4 codes of a word as two F16 pairs: bytes 0, 1 and bytes 2, 3.
-template <int FMT>
+// The 4 codes of a word as two F16 pairs: bytes 0, 1 and bytes 2, 3. The
+// conversion instruction makes NaN of the e4m3 codes 0x7f and 0xff, which stand
+// for +-480: the kernels look for a NaN among what they made of a tile, and
+// convert it again with EVERY. EVERY places the code's 7 bits in the top of F16's
+// exponent and mantissa, the value times 2^(7 - 15), subnormals included, and
+// multiplies by 2^8, exactly: 5 instructions for a pair instead of 1.
+template <int FMT, bool EVERY = false>
 __device__ __forceinline__ void pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (FMT == FMT_INT8) {
     const uint32_t u = w ^ 0x80808080u;  // c + 128
     const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);  // 1024 + (c + 128)
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+  } else if constexpr (EVERY) {
+    auto one = [](uint32_t p) {  // a code in the high byte of each half
+      uint32_t r;
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"((p & 0x80008000u) | ((p & 0x7f007f00u) >> 1)), "r"(0x5c005c00u));
+      return r;
+    };
+    lo = one(__byte_perm(w, 0u, 0x1404));
+    hi = one(__byte_perm(w, 0u, 0x3424));
   } else {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"

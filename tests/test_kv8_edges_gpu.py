@@ -16,7 +16,7 @@ import pytest
 
 from tests import kv8_ref as R
 from tests.gpu_util import to_f64
-from tests.test_kv8_gpu import U, Problem, _clean_status, attend, gpu, tdt  # noqa: F401
+from tests.test_kv8_gpu import U, Problem, _clean_status, attend, gpu, same_cache, tdt, write  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +84,53 @@ def test_keys_that_are_not_there_read_nothing(dtype, fmt, D, new):
     got = attend(p, p.cache())
     assert np.isfinite(to_f64(got[0])).all()
     close(p, got)
+
+
+@pytest.mark.parametrize("dtype,D,G", [("bf16", 128, 16), ("f16", 64, 1), ("f16", 128, 4), ("f32", 64, 8)])
+@pytest.mark.parametrize("new", [1, 5, 90])
+def test_codes_7f_and_ff_are_480(dtype, D, G, new):
+    # the two e4m3 codes that the writer never makes: +-480 to every reader, and nothing to a row
+    # whose mask hides them
+    from exact_scaled_dot_flash_gb300 import attn
+    p = Problem(42, [99, 150, 333], [new] * 3, dtype=dtype, fmt="e4m3", D=D, Hq=8, P=32, G=G)
+    r = np.random.RandomState(43)
+    for c in (p.kc, p.vc):
+        c[...] = np.where(r.rand(*c.shape) < 0.02, r.choice(NAN_BYTES, c.shape), c)
+        c[p.table[1, 4], 20:22, :, 3] = 0xff  # tokens 148, 149 of sequence 1: only its last rows see them
+    cache = p.cache()
+    offs = gpu(np.concatenate([[0], np.cumsum(p.lens)]).astype(np.int32))
+    rows = attn.kv8_read(*cache, offs, dtype=tdt(dtype))
+    for got, c, s in zip(rows, (p.kc, p.vc), (p.ks, p.vs)):
+        ref = R.read_rows(c, s, p.table, p.lens, offs.cpu().numpy(), int(p.lens.sum()), "e4m3")
+        assert (np.abs(to_f64(got) - ref) <= (U[dtype] + 2.0 ** -24) * np.abs(ref) + 2.0 ** -25).all()
+    got = attend(p, cache)
+    assert np.isfinite(to_f64(got[0])).all()
+    close(p, got)
+    # only in places that no row but the last one sees
+    q = Problem(44, [99, 150, 333], [new] * 3, dtype=dtype, fmt="e4m3", D=D, Hq=8, P=32, G=G)
+    q.vc[q.table[1, 4], 21] = 0xff
+    q.kc[q.table[2, 10], 12] = 0x7f
+    close(q, attend(q, q.cache()))
+
+
+@pytest.mark.parametrize("new", [1, 90])
+def test_nan_scales_beside_codes_7f_and_ff(new):
+    # NaN groups stay NaN, the rest stays finite
+    p = Problem(45, [99, 150], [new, new], dtype="bf16", fmt="e4m3", D=128, Hq=8, P=32, G=4)
+    r = np.random.RandomState(46)
+    p.vc[...] = np.where(r.rand(*p.vc.shape) < 0.02, r.choice(NAN_BYTES, p.vc.shape), p.vc)
+    p.vs[p.table[0, 0], 0, 0] = np.nan
+    out = to_f64(attend(p, p.cache())[0])
+    assert np.isnan(out[:new, :4]).all() and np.isfinite(out[:new, 4:]).all() and np.isfinite(out[new:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_groups_that_grow_over_codes_7f_and_ff(dtype):
+    # tokens of an earlier call that hold the two codes are brought to a larger scale from +-480
+    p = Problem(47, [40, 21, 70], [3, 2, 5], dtype=dtype, fmt="e4m3", G=16, loud=400.0)
+    r = np.random.RandomState(48)
+    for c in (p.kc, p.vc):
+        c[...] = np.where(r.rand(*c.shape) < 0.2, r.choice(NAN_BYTES, c.shape), c)
+    cache, want = p.cache(), p.written()
+    write(p, cache)
+    same_cache(p, cache, want)
