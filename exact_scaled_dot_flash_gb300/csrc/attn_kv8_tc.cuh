@@ -15,8 +15,12 @@
 //    that each tile's softmax runs under the other's products;
 //  - warps 0-7 own a row a thread: x = S ks scale in fp32, y = 2^(x - ref),
 //    P = y vs rounded to F16 back into tensor memory, l += y. ref holds the
-//    row's largest score and the tile's largest value scale, and moves only when
-//    that passes it by 2^8.
+//    row's largest x + log2 vs, and moves only when that passes it by 2^8: the
+//    row's largest P is 1 or more, whichever keys have the largest scores and
+//    whichever the largest scales, and what F16 loses of those below 2^-14 is
+//    small beside it. With a scale for each key, the largest score and the tile's
+//    largest scale bound that sum where the tile's scales lie within a factor of
+//    64 (such chunks, D 128, e4m3: 284 us, 316 with the sum for every key).
 // The products are F16 for BF16 queries too: a row is brought into range by a
 // power of two (see attn_kv8_decode.cuh).
 // Where the row blocks do not fill the SMs (a few short chunks over long
@@ -42,11 +46,17 @@ constexpr int BM = 128, BN = 128, NQ = 2;
 constexpr int NUM_THREADS = 512;
 constexpr int WARP_CONV = 8, CONV_WARPS = 4, WARP_MMA = 12;
 constexpr int TMEM_COLS = 512;
-// 512 threads start with 128 registers each; 2 x 128 x 184 + 2 x 128 x 72 is the same sum
-// (192 and 64: 252 us instead of 248 on the chunks above, the conversion of e4m3 spills)
-constexpr int REG_SOFTMAX = 184, REG_OTHER = 72;
+// 512 threads start with 128 registers each: 2 x 128 x (REG_SOFTMAX + REG_OTHER) is
+// the same sum. At D 128 the conversion of e4m3 would spill with 64 (252 us instead of
+// 248 on the chunks above).
+template <int D> constexpr int REG_SOFTMAX = D == 128 ? 184 : 192;
+template <int D> constexpr int REG_OTHER = 256 - REG_SOFTMAX<D>;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float RESCALE_LOG2 = 8.0f;
+constexpr float SPREAD = 64.f;
+constexpr float SLACK_LOG2 = 7.f;   // a bound that takes the largest scale, below 2^vex, for one that is SPREAD times as small
+constexpr float Y_RANGE = 80.f;     // y <= 2^(80 + 8 + 7): its sum over 2^31 keys is within fp32
+constexpr float VS_LEAST = 8.271806125530277e-25f;  // 2^-Y_RANGE: smaller value scales count as this
 constexpr float UNSEEN = -1e30f;
 
 template <int D>
@@ -57,7 +67,7 @@ struct Cfg {
   static constexpr int STAGES = 3;                     // converted tiles: K_j, V_j, K_j+1
   static constexpr int RAW = 3;                        // tiles of codes on their way
   static constexpr int RAW_BYTES = BN * D;
-  static constexpr int SCALE_BYTES = 2 * BN * 4 + 16;  // ks, vs, the warps' largest vs
+  static constexpr int SCALE_BYTES = 3 * BN * 4 + 32;  // ks, vs, log2 vs; the warps' largest and least vs
   static constexpr int OFF_KV = NQ * TILE_BYTES;
   static constexpr int OFF_RAW = OFF_KV + STAGES * TILE_BYTES;
   static constexpr int OFF_SCALE = OFF_RAW + RAW * RAW_BYTES;
@@ -171,7 +181,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
   };
 
   if (warp >= WARP_CONV) {
-    setmaxnreg_dec<REG_OTHER>();
+    setmaxnreg_dec<REG_OTHER<D>>();
     if (warp < WARP_CONV + CONV_WARPS) {
       // ---------------------------------------------------------- conversion
       // Warp cw has keys 32 cw .. + 31 of a tile; a copy of the warp moves RPC
@@ -256,11 +266,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
           if (lane % RUN == 0) {
             sc[(cw * 32 + lane) / RUN] = ks * p.scale_log2;
             sc[BN + (cw * 32 + lane) / RUN] = vs;
+            sc[2 * BN + (cw * 32 + lane) / RUN] = fmaxf(__log2f(vs), -Y_RANGE);  // a NaN counts as the least
           }
-          float top = vs;  // NaN does not count
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (lane == 0) sc[2 * BN + cw] = top;
+          if constexpr (RUN == 1) {
+            // the bits of floats that are not negative are in their order; NaN does not
+            // count, and keys behind the sequence's end are not among the least
+            constexpr uint32_t MOST = 0x7f7fffffu;
+            const uint32_t bits = __float_as_uint(vs);
+            const bool there = (w.j0 + j) * BN + cw * 32 + lane < w.L;
+            const uint32_t top = __reduce_max_sync(0xffffffffu, bits <= MOST ? bits : 0u);
+            const uint32_t low = __reduce_min_sync(0xffffffffu, bits <= MOST && there ? bits : MOST);
+            if (lane == 0) {
+              sc[3 * BN + cw] = __uint_as_float(top);
+              sc[3 * BN + CONV_WARPS + cw] = __uint_as_float(low);
+            }
+          }
         } else {
           ks = ks_next;
           vs = vs_next;
@@ -379,7 +399,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
-    setmaxnreg_inc<REG_SOFTMAX>();
+    setmaxnreg_inc<REG_SOFTMAX<D>>();
     const int t = warp >> 2;
     const int row = ((warp & 3) << 5) + lane;
     const int64_t pr = w.row0 + t * BM + row;
@@ -429,7 +449,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
       if (__any_sync(0xffffffffu, !ok)) { failed = true; break; }
       tc_fence_after();
       const float4* const sk = reinterpret_cast<const float4*>(smem + C::OFF_SCALE + (j & 1) * C::SCALE_BYTES);
-      const float4* const sv = sk + BN / 4;
+      const float4 *const sv = sk + BN / 4, *const sl = sv + BN / 4;
       // s: products times k_scale; with runs the products alone
       float s[128];
       {
@@ -468,25 +488,40 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < BN / RUN / 4; ++i) {
           const float4 k = sk[i];
-          c0 = fmaxf(c0, run(4 * i) * k.x);
-          c1 = fmaxf(c1, run(4 * i + 1) * k.y);
-          c2 = fmaxf(c2, run(4 * i + 2) * k.z);
-          c3 = fmaxf(c3, run(4 * i + 3) * k.w);
+          const float4 e = sl[i];
+          c0 = fmaxf(c0, fmaf(run(4 * i) * k.x, back, e.x));
+          c1 = fmaxf(c1, fmaf(run(4 * i + 1) * k.y, back, e.y));
+          c2 = fmaxf(c2, fmaf(run(4 * i + 2) * k.z, back, e.z));
+          c3 = fmaxf(c3, fmaf(run(4 * i + 3) * k.w, back, e.w));
         }
       } else {
+        const float4 vt = sl[BN / 4], vl = sl[BN / 4 + 1];
+        const float vtop = fmaxf(fmax3(vt.x, vt.y, vt.z), vt.w), vlow = fminf(fminf(vl.x, vl.y), fminf(vl.z, vl.w));
+        if (vtop > fmaxf(vlow, VS_LEAST) * SPREAD) {  // the same for the CTA's threads
+          asm volatile("");
+          const float2 b2 = make_float2(back, back);
 #pragma unroll
-        for (int i = 0; i < 128; i += 8) {
-          c0 = fmax3(c0, s[i], s[i + 1]);
-          c1 = fmax3(c1, s[i + 2], s[i + 3]);
-          c2 = fmax3(c2, s[i + 4], s[i + 5]);
-          c3 = fmax3(c3, s[i + 6], s[i + 7]);
+          for (int i = 0; i < 128; i += 4) {
+            const float4 e = sl[i / 4];
+            const float2 xa = ffma2(make_float2(s[i], s[i + 1]), b2, make_float2(e.x, e.y));
+            const float2 xb = ffma2(make_float2(s[i + 2], s[i + 3]), b2, make_float2(e.z, e.w));
+            c0 = fmax3(c0, xa.x, xa.y);
+            c1 = fmax3(c1, xb.x, xb.y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 128; i += 8) {
+            c0 = fmax3(c0, s[i], s[i + 1]);
+            c1 = fmax3(c1, s[i + 2], s[i + 3]);
+            c2 = fmax3(c2, s[i + 4], s[i + 5]);
+            c3 = fmax3(c3, s[i + 6], s[i + 7]);
+          }
+          const float vex = static_cast<float>(static_cast<int>(__float_as_uint(vtop) >> 23) - 126);  // vtop < 2^vex
+          c0 = fmax3(c0, c1, fmaxf(c2, c3)) * back + fmaxf(vex, -Y_RANGE);
+          c1 = c2 = c3 = -INFINITY;
         }
       }
-      // the largest score, raised by the exponent of the tile's largest value scale
-      const float4 vt = sv[BN / 4];
-      const float vtop = fmaxf(fmax3(vt.x, vt.y, vt.z), vt.w);
-      const float vex = fmaxf(static_cast<float>(static_cast<int>(__float_as_uint(vtop) >> 23) - 126), -80.f);
-      const float x_tile = fmax3(c0, c1, fmaxf(c2, c3)) * back + vex;
+      const float x_tile = fmax3(c0, c1, fmaxf(c2, c3)) - (RUN == 1 ? SLACK_LOG2 : 0.f);
       const bool need = x_tile > ref + RESCALE_LOG2;
       float alpha = 1.f;
       if (need) {

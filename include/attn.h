@@ -508,10 +508,12 @@ ATTN_API int attn_kv8_read(const attn_kv8_cache_t* cache, int num_seqs, int max_
  * written); group and format are those of the cache, k_scale and v_scale its
  * scales. Codes enter the products unrounded (every code is exact in F16 and
  * BF16); scores, softmax statistics and outputs are summed in fp32. The
- * F16/BF16 kernels round p_j * v_scale_j to F16, the largest of a row brought
- * near 1 (terms below 2^-14 of it are off by up to 2^-25 of it), and a BF16 query
- * to F16 by a power of two for its row (elements below 2^-29 of its largest by up
- * to 2^-40 of it).
+ * F16/BF16 kernels round p_j * v_scale_j to F16, the largest that a row sees
+ * brought to 1/2 or more: terms below 2^-14 of it are off by up to 2^-24 of it (of
+ * 2^-80, where it is less than that). Value scales above 2^100 cost the
+ * probabilities below 2^-26 of the largest. A BF16 query is brought to F16 by a
+ * power of two for its row (elements below 2^-29 of its largest are off by up to
+ * 2^-40 of it).
  *
  * workspace: attn_paged_kv8_workspace_bytes(shape) bytes (0 for some shapes),
  * 16-byte aligned, caller-owned, disjoint from every other buffer, its contents

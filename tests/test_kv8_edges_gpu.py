@@ -134,3 +134,51 @@ def test_groups_that_grow_over_codes_7f_and_ff(dtype):
     cache, want = p.cache(), p.written()
     write(p, cache)
     same_cache(p, cache, want)
+
+
+def loud_key(p, s, j, code=16):
+    """Key j of sequence s scores far above the others: its codes point along the (positive) queries."""
+    p.kc[p.table[s, j // p.P], j % p.P] = code if p.fmt == "int8" else 0x58  # 16
+
+
+@pytest.mark.parametrize("dtype,fmt,D,G", [("f16", "int8", 128, 1), ("bf16", "e4m3", 64, 4), ("f16", "e4m3", 128, 16),
+                                           ("bf16", "int8", 128, 16), ("f32", "int8", 64, 4)])
+@pytest.mark.parametrize("new", [1, 40, 90])
+@pytest.mark.parametrize("down", [5, 8, 14, 24, 60, None])
+def test_the_top_key_has_a_small_value_scale(dtype, fmt, D, G, new, down):
+    # the key that takes nearly all of a row's probability holds values 2^-down of the others' (None:
+    # zeros), so that the others' small probabilities count
+    import torch
+    p = Problem(50, [1500, 400], [new, new], dtype=dtype, fmt=fmt, D=D, G=G, P=32, Hq=4, H=1)
+    p.q = p.q.abs()
+    p.ks[...] = 0.01 if fmt == "int8" else 2.0 ** -8
+    p.vs[...] = 2.0 ** -6
+    for s, page in ((0, p.table[0, 0]), (1, p.table[1, 0])):
+        p.kc[page, :G] = 0
+        loud_key(p, s, 0)
+        # the others' scores lie within some 2 of 0; the top one lies at 12 + log2(1500)
+        t = 16 * p.q[p.offs[s]:p.offs[s + 1]].double().sum(-1).mean().item() / np.sqrt(D)
+        p.ks[page, :, 0] = 19 * np.log(2.0) / t
+        p.vs[page, :, 0] = 2.0 ** (-6 - down) if down else 0.0
+    close(p, attend(p, p.cache()))
+
+
+@pytest.mark.parametrize("dtype,fmt,D,G", [("f16", "int8", 128, 1), ("bf16", "e4m3", 64, 4), ("bf16", "e4m3", 128, 16),
+                                           ("f32", "int8", 64, 4)])
+@pytest.mark.parametrize("new", [2, 90, 200])
+@pytest.mark.parametrize("up", [14, 25, 40, 100])
+@pytest.mark.parametrize("mask", ["causal", "positions"])
+def test_hidden_keys_of_large_value_scales(dtype, fmt, D, G, new, up, mask):
+    # the values of the last group are 2^up of the others'; only the rows behind its first token see it
+    p = Problem(51, [320, 416], [new, new], dtype=dtype, fmt=fmt, D=D, G=G, P=32, Hq=4, H=1)
+    p.vs[...] = 2.0 ** -14
+    for s, L in enumerate(p.lens):
+        p.vs[p.table[s, (L - 1) // p.P], :, -1] = 2.0 ** (up - 14)
+    seen = np.concatenate([np.arange(L - n, L) for L, n in zip(p.lens, p.new)]).astype(np.int32)
+    last = np.concatenate([np.full(n, L - G) for L, n in zip(p.lens, p.new)])
+    if mask == "positions":
+        seen = np.concatenate([np.random.RandomState(52).permutation(a) for a in np.split(seen, [new])]).astype(np.int32)
+    got = attend(p, p.cache(), seen if mask == "positions" else None)
+    # in F16 the rows that see it may pass the type's range: they are not compared
+    rows = seen < last if dtype == "f16" and up > 14 else None
+    close(p, got, seen, rows=rows)
