@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_kernel(const __grid_constan
         copy_item(it + 2);
         copy_wait<2>();
         __syncwarp();
-        if (!mbar_wait(bar(C::BAR_EMPTY + st), ((it / C::STAGES) & 1) ^ 1)) { ok = false; break; }
+        if (!warp_wait(bar(C::BAR_EMPTY + st), ((it / C::STAGES) & 1) ^ 1)) { ok = false; break; }  // the whole warp
         const uint8_t* const src = raw + (it % C::RAW) * C::RAW_BYTES;
         uint8_t* const dst = smem + C::OFF_KV + st * C::TILE_BYTES;
         if ((it & 1) == 0) {
