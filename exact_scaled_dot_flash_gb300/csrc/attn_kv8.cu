@@ -12,7 +12,8 @@
 // of x / S, ties to the even code, exactly: an fp32 quotient can be rounded
 // onto a tie, so the int8 code is settled by its residual x - r S, which fp32
 // holds exactly (see nearest8), and the e4m3 scale, a power of two, divides
-// exactly (a float format gains nothing from a finer scale). A NaN or infinity
+// exactly (a float format gains nothing from a finer scale; one that another
+// program left in a part-filled group divides with its remainder). A NaN or infinity
 // among the new tokens makes the group's scale NaN: the group then reads as
 // NaN until a call writes its first token again.
 // Bytes: the new tokens are read once and one byte written for each element. 32
@@ -156,20 +157,49 @@ struct AbsMax {
   }
 };
 
+// The 4 e4m3 codes nearest to q.
+__device__ __forceinline__ uint32_t e4m3x4(const float* q) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(q[1]), "f"(q[0]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(q[3]), "f"(q[2]));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+__device__ __forceinline__ bool power_of_two(float s) { return (__float_as_uint(s) & 0x7fffffu) == 0; }
+
+// q, off the exact value by d's sign and less than its own last place: cut towards
+// zero, with the lowest bit set for what was cut away, so that the conversion to
+// fewer bits is the only rounding.
+__device__ __forceinline__ float cut_odd(float q, float d) {
+  const uint32_t b = __float_as_uint(q);
+  return d == 0.f || q == 0.f ? q : __uint_as_float((b - ((d < 0.f) != (q < 0.f) ? 1u : 0u)) | 1u);
+}
+
+// The e4m3 codes nearest to x / s for any s, ties to even. The remainder x - q s is
+// exact wherever q could be a border of two codes (q has 5 bits then).
+__device__ __forceinline__ uint32_t e4m3x4_over(const float* x, float s) {
+  float q[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    q[k] = __fdiv_rn(x[k], s);
+    q[k] = cut_odd(q[k], fmaf(-q[k], s, x[k]));
+  }
+  return e4m3x4(q);
+}
+
 template <int FMT>
 __device__ __forceinline__ uint32_t encode4(const float* x, float s, float inv) {
   if constexpr (FMT == FMT_INT8) {
     return nearest8x4(x, s, inv);
   } else {
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1] * inv), "f"(x[0] * inv));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3] * inv), "f"(x[2] * inv));
-    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+    const float q[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
+    return e4m3x4(q);
   }
 }
 
-// Codes of c * s_old / s for s > s_old. The fp32 product is within 2^-15 of the
-// quotient (|c| <= 128); only one that lies that near a tie is settled in fp64.
+// Codes of c * s_old / s for s > s_old. int8: the fp32 product is within 2^-15 of
+// the quotient (|c| <= 128); only one that lies that near a tie is settled in
+// fp64. e4m3: s > s_old is a power of two (the writer's), the ratio exact.
 template <int FMT>
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float s_old, float s) {
   const float4 v = decode4<FMT>(w);
@@ -187,7 +217,13 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float s_old, float s) {
     }
     return o;
   } else {
-    return encode4<FMT>(c, s, ratio);
+    float q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float p = c[k] * ratio;
+      q[k] = cut_odd(p, fmaf(c[k], ratio, -p));
+    }
+    return e4m3x4(q);
   }
 }
 
@@ -288,6 +324,7 @@ __global__ void __launch_bounds__(THREADS, DT == 0 ? 2 : 4) write_kernel(const _
       if (t0 + i * tinc < m) next[i] = load_raw<DT, VEC>(at);
   };
   fetch(unit0);
+  uint32_t odd = 0;  // units whose scale is no power of two (e4m3)
   for (int u = 0; u < units; ++u) {
     const int unit = unit0 + u * SIDE;
     if (unit >= 2 * c.Hkv) break;
@@ -340,14 +377,6 @@ __global__ void __launch_bounds__(THREADS, DT == 0 ? 2 : 4) write_kernel(const _
       *reinterpret_cast<uint2*>(at) =
           sn == sn ? make_uint2(encode4<FMT>(v, sn, inv), encode4<FMT>(v + 4, sn, inv)) : make_uint2(0u, 0u);
     };
-    if (held > 0 && sn > so) {  // the codes of earlier calls, at the larger scale
-      uint8_t* at = dst - held * cstep;
-      for (int t = t0; t < held; t += tinc, at += dinc) {
-        if (!inside(at)) continue;
-        const uint2 w = *reinterpret_cast<const uint2*>(at);
-        *reinterpret_cast<uint2*>(at) = make_uint2(recode4<FMT>(w.x, so, sn), recode4<FMT>(w.y, so, sn));
-      }
-    }
 #pragma unroll
     for (int i = 0; i < KEEP; ++i)
       if (t0 + i * tinc < m) put(dst + i * dinc, keep[i]);
@@ -356,6 +385,34 @@ __global__ void __launch_bounds__(THREADS, DT == 0 ? 2 : 4) write_kernel(const _
       const uint8_t* at = source(unit) + KEEP * inc;
       uint8_t* to = dst + KEEP * dinc;
       for (int t = t0 + KEEP * tinc; t < m; t += tinc, at += inc, to += dinc) put(to, load_raw<DT, VEC>(at));
+    }
+    if (held > 0 && sn > so) {  // the codes of earlier calls, at the larger scale
+      uint8_t* at = dst - held * cstep;
+      for (int t = t0; t < held; t += tinc, at += dinc) {
+        if (!inside(at)) continue;
+        const uint2 w = *reinterpret_cast<const uint2*>(at);
+        *reinterpret_cast<uint2*>(at) = make_uint2(recode4<FMT>(w.x, so, sn), recode4<FMT>(w.y, so, sn));
+      }
+    }
+    if (FMT == FMT_E4M3 && sn == sn && !power_of_two(sn)) odd |= 1u << u;
+  }
+  if (FMT == FMT_E4M3 && odd) {  // the same for all of a unit's threads; only where held > 0
+    // part-filled groups whose scale is another program's: the new tokens once more
+    if constexpr (TPU > 32) __syncthreads();  // the scales are written
+    else __syncwarp();
+    for (; odd; odd &= odd - 1) {
+      const int unit = unit0 + (__ffs(odd) - 1) * SIDE;
+      const int kv = unit >= c.Hkv ? 1 : 0, h = unit - kv * c.Hkv;
+      const float sn = p.scales[kv][scale_index(c, page, row0, h)];
+      const uint8_t* at = source(unit);
+      uint8_t* to = p.codes[kv] + ((static_cast<size_t>(page) * c.page_size + row0) * c.Hkv + h) * c.D +
+                    (held + t0) * cstep + col * 8;
+      for (int t = t0; t < m; t += tinc, at += stride(unit), to += tinc * cstep) {
+        float v[8];
+        expand<DT>(load_raw<DT, VEC>(at), v);
+        if (in_bounds(c.status, (to - p.codes[kv]) >> 3, ncode8))
+          *reinterpret_cast<uint2*>(to) = make_uint2(e4m3x4_over(v, sn), e4m3x4_over(v + 4, sn));
+      }
     }
   }
 }

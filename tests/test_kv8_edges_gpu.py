@@ -182,3 +182,29 @@ def test_hidden_keys_of_large_value_scales(dtype, fmt, D, G, new, up, mask):
     # in F16 the rows that see it may pass the type's range: they are not compared
     rows = seen < last if dtype == "f16" and up > 14 else None
     close(p, got, seen, rows=rows)
+
+
+@pytest.mark.parametrize("loud", [1.0, 300.0])
+def test_appending_at_a_scale_that_is_no_power_of_two(loud):
+    # e4m3 groups that another program began: their scale divides, and their codes move to a larger
+    # one, to the nearest code, ties to even, however near a quotient is to the border of two codes
+    import torch
+    p = Problem(53, [40, 21, 70, 13], [3, 2, 5, 1], dtype="f32", fmt="e4m3", G=16, H=3, loud=loud)
+    r = np.random.RandomState(54)
+    for s in (p.ks, p.vs):
+        s *= r.uniform(1.0, 2.0, s.shape).astype(np.float32)
+    border = (R.E4M3[:126] + R.E4M3[1:127]) / 2
+    for x, sc in ((p.k, p.ks), (p.v, p.vs)):
+        for s, (L, n) in enumerate(zip(p.lens, p.new)):
+            for t in range(n):
+                j = L - n + t
+                S = sc[p.table[s, j // p.P], :, j % p.P // p.G].astype(np.float64)[:, None]  # [H, 1]
+                y = (r.choice(border[20:110], (p.H, p.D)) * S * r.choice([-1, 1], (p.H, p.D))).astype(np.float32)
+                y = np.nextafter(y, np.float32(np.inf) * r.randint(-1, 2, y.shape).astype(np.float32)) if t % 2 else y
+                y[:, :4] = [0.0, -0.0, 1e-42, -3e-45]  # quotients that leave fp32's range
+                x[p.offs[s] + t] = torch.from_numpy(y * np.float32(loud))
+    cache, want = p.cache(), p.written()
+    write(p, cache)
+    same_cache(p, cache, want)
+    write(p, cache)
+    same_cache(p, cache, want, "second call: ")
