@@ -200,7 +200,7 @@ def test_appending_at_a_scale_that_is_no_power_of_two(loud):
                 j = L - n + t
                 S = sc[p.table[s, j // p.P], :, j % p.P // p.G].astype(np.float64)[:, None]  # [H, 1]
                 y = (r.choice(border[20:110], (p.H, p.D)) * S * r.choice([-1, 1], (p.H, p.D))).astype(np.float32)
-                y = np.nextafter(y, np.float32(np.inf) * r.randint(-1, 2, y.shape).astype(np.float32)) if t % 2 else y
+                y = np.nextafter(y, r.choice(np.array([-np.inf, 0, np.inf], np.float32), y.shape)) if t % 2 else y
                 y[:, :4] = [0.0, -0.0, 1e-42, -3e-45]  # quotients that leave fp32's range
                 x[p.offs[s] + t] = torch.from_numpy(y * np.float32(loud))
     cache, want = p.cache(), p.written()
