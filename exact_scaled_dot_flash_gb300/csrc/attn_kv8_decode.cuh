@@ -62,7 +62,7 @@ constexpr int TILE_KEYS = 32;
 constexpr int BLOCK_KEYS = TILE_KEYS * WARPS;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float Y_RANGE = 80.f;     // y <= 2^80: below it a row of tiny value scales still fills F16
-constexpr float UNSEEN = -1e30f;    // reference of a row without keys: its first one passes every range
+constexpr float UNSEEN = -3e38f;    // reference of a row without keys: its first one passes every range
 
 __device__ __forceinline__ int blocks_of(int nq, int L) {
   return nq > 0 ? max(1, (L + BLOCK_KEYS - 1) / BLOCK_KEYS) : 0;  // without keys: one, for the NaN rows

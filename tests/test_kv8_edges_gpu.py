@@ -208,3 +208,24 @@ def test_appending_at_a_scale_that_is_no_power_of_two(loud):
     same_cache(p, cache, want)
     write(p, cache)
     same_cache(p, cache, want, "second call: ")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("new", [1, 90])
+def test_scores_far_below_zero(dtype, new):
+    # every score is about -10^31, one of them half of the others: that key takes all
+    import torch
+    p = Problem(55, [200, 131], [new, new], dtype=dtype, fmt="int8", D=64, Hq=4, H=1, G=1)
+    p.q = -torch.ones_like(p.q) * 512
+    p.kc[...] = 64
+    p.ks[...] = 2.0 ** 87
+    best = [7, 3]
+    for s, j in enumerate(best):
+        p.ks[p.table[s, j // p.P], :, j % p.P] = 2.0 ** 86
+    out, lse = attend(p, p.cache())
+    v = R.read_all(p.vc, p.vs, "int8")
+    for s, j in enumerate(best):
+        ref = v[p.table[s, j // p.P], j % p.P]  # [1, D]
+        assert (np.abs(to_f64(out[p.offs[s]:p.offs[s + 1]]) - ref) <= 2 * U[dtype] * np.abs(ref) + 2.0 ** -20).all()
+        want = -512 * 64 * 64 * 2.0 ** 86 / 8
+        assert (np.abs(lse[p.offs[s]:p.offs[s + 1]].cpu().numpy() / want - 1) <= 2.0 ** -20).all()
