@@ -678,7 +678,9 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const __grid_co
   float M = ml.x;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);  // a run without keys wrote no output
+  const bool has_keys = ml.x != -INFINITY;  // a run without keys wrote no output
+  const unsigned runs = __ballot_sync(0xffffffffu, has_keys);
+  const float f = has_keys ? fast_exp2(ml.x - M) : 0.f;
   float sum = f == 0.f ? 0.f : f * ml.y;
   if (ml.y != ml.y) sum = ml.y;
 #pragma unroll
@@ -688,7 +690,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const __grid_co
 #pragma unroll 4
   for (int s = 0; s < splits; ++s) {
     const float fs = __shfl_sync(0xffffffffu, f, s);
-    if (fs == 0.f) continue;  // warp-uniform
+    if (!(runs >> s & 1)) continue;  // warp-uniform; a weight of 0 is added too: 0 * NaN
     const float* const src = reinterpret_cast<const float*>(wo) + (s * nrows + orow) * D + lane * V;
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = fmaf(fs, src[k], acc[k]);

@@ -229,3 +229,20 @@ def test_scores_far_below_zero(dtype, new):
         assert (np.abs(to_f64(out[p.offs[s]:p.offs[s + 1]]) - ref) <= 2 * U[dtype] * np.abs(ref) + 2.0 ** -20).all()
         want = -512 * 64 * 64 * 2.0 ** 86 / 8
         assert (np.abs(lse[p.offs[s]:p.offs[s + 1]].cpu().numpy() / want - 1) <= 2.0 ** -20).all()
+
+
+def test_a_nan_group_far_below_the_top_score():
+    # 0 * NaN: a group without values makes its rows NaN however small its probability, also where the
+    # key tiles are cut into runs and another run holds the scores that count
+    import torch
+    p = Problem(56, [3000], [80], dtype="bf16", fmt="int8", D=128, Hq=2, H=1, G=16, P=32)
+    p.q = p.q.abs()
+    p.kc[...] = 20
+    p.ks[...] = 2.0 ** -20
+    t = 20 * p.q.double().sum(-1).min().item() / np.sqrt(128) * 1.44
+    for page in p.table[0, 80:]:
+        p.ks[page] = 400 / t  # their scores lie 400 and more above, in powers of two
+    clean = to_f64(attend(p, p.cache(), causal=False)[0])
+    assert np.isfinite(clean).all()
+    p.vs[p.table[0, 1], 0, 0] = np.nan
+    assert np.isnan(to_f64(attend(p, p.cache(), causal=False)[0])).all()
