@@ -246,3 +246,25 @@ def test_a_nan_group_far_below_the_top_score():
     assert np.isfinite(clean).all()
     p.vs[p.table[0, 1], 0, 0] = np.nan
     assert np.isnan(to_f64(attend(p, p.cache(), causal=False)[0])).all()
+
+
+@pytest.mark.parametrize("dtype,D,G", [("bf16", 128, 16), ("f16", 64, 1)])
+@pytest.mark.parametrize("new,H,Hq", [(1, 2, 8), (3, 2, 10), (12, 1, 4), (70, 1, 2)])
+def test_codes_7f_and_ff_in_cut_sequences(dtype, D, G, new, H, Hq):
+    # the two codes and absent pages where the keys of a sequence are shared out over the GPU
+    p = Problem(57, [2600, 40, 1313], [new] * 3, dtype=dtype, fmt="e4m3", D=D, Hq=Hq, H=H, P=32, G=G)
+    nobody_has_page_0(p)
+    r = np.random.RandomState(58)
+    for c in (p.kc, p.vc):
+        for s, page in ((0, 3), (0, 40), (0, 80), (2, 7)):  # a few pages of them, the others none
+            at = p.table[s, page]
+            c[at] = np.where(r.rand(*c[at].shape) < 0.3, r.choice(NAN_BYTES, c[at].shape), c[at])
+        c[0] = 0xff
+    p.table[0, 10], p.table[2, 20] = -1, p.pages + 3
+    got = attend(p, p.cache())
+    # of 70 rows of the sequence of 40 tokens the first 30 lie before its first token: no keys, NaN
+    rows = np.concatenate([np.arange(L - n, L) >= 0 for L, n in zip(p.lens, p.new)])
+    assert np.isfinite(to_f64(got[0])[rows]).all() and np.isnan(to_f64(got[0])[~rows]).all()
+    close(p, got, rows=rows)
+    again = attend(p, p.cache())
+    assert all(a.cpu().float().numpy().tobytes() == b.cpu().float().numpy().tobytes() for a, b in zip(got, again))
