@@ -28,6 +28,7 @@
 #include <type_traits>
 
 #include "attn.h"
+#include "host_checks.h"
 #include "kv8.cuh"
 #include "simt.cuh"
 
@@ -431,7 +432,7 @@ cudaError_t launch_write(const WriteParams& p, cudaStream_t st) {
     // a CTA that takes several heads in turn finds its tokens once for all of
     // them; where that leaves two CTAs an SM (32 prompts and reading them back:
     // 94 us, 114 one by one; 8: 32 and 36; 4, too few: 21 and 19; 1: 15 and 9)
-    const int units = static_cast<int64_t>(slots) * 2 * p.c.Hkv >= 152ll * 2 * WRITE_UNITS ? WRITE_UNITS : 1;
+    const int units = static_cast<int64_t>(slots) * 2 * p.c.Hkv >= 2ll * SMS * WRITE_UNITS ? WRITE_UNITS : 1;
     write_kernel<DT, FMT, VEC, THREADS><<<dim3(slots, (2 * p.c.Hkv + units - 1) / units), THREADS, 0, st>>>(p, units);
   }
   return cudaGetLastError();
@@ -455,19 +456,15 @@ constexpr int READ_ROWS = 8;  // output rows of a CTA
 template <int DT>
 constexpr int READ_PIECE = DT == 0 ? 4 : 16;
 template <int DT>
-using ReadWord = std::conditional_t<READ_PIECE<DT> == 4, uint32_t, std::conditional_t<READ_PIECE<DT> == 8, uint2, uint4>>;
+using ReadWord = std::conditional_t<READ_PIECE<DT> == 4, uint32_t, uint4>;
 
 template <int DT, int FMT>
 __device__ __forceinline__ void store_piece(void* out, size_t o, ReadWord<DT> w, float s) {
-  const uint32_t* const c = reinterpret_cast<const uint32_t*>(&w);
   if constexpr (DT == 0) {
-    constexpr int N = READ_PIECE<DT> / 4;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const float4 v = decode4<FMT>(c[k]);
-      reinterpret_cast<float4*>(out)[N * o + k] = make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
-    }
+    const float4 v = decode4<FMT>(w);
+    reinterpret_cast<float4*>(out)[o] = make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
   } else {
+    const uint32_t* const c = reinterpret_cast<const uint32_t*>(&w);
     uint32_t r[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -560,20 +557,10 @@ cudaError_t launch_read(const ReadParams& p, cudaStream_t st) {
 
 namespace {
 
+using attn::aligned;
+using attn::Buf;
+using attn::meet;
 using attn::kv8::Cache;
-
-struct Buf {
-  const void* p;
-  int64_t n;
-};
-
-bool meet(const Buf& a, const Buf& b) {
-  if (!a.p || !b.p || a.n <= 0 || b.n <= 0) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x < y + static_cast<uintptr_t>(b.n) && y < x + static_cast<uintptr_t>(a.n);
-}
-
-bool aligned(const void* p, int to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 
 // Shape checks shared by the cache's entries; fills `c` but for its pointers.
 int check_cache(const attn_kv8_cache_t* cache, int num_seqs, int max_pages, Cache& c) {

@@ -13,6 +13,7 @@
 #include <initializer_list>
 
 #include "attn.h"
+#include "host_checks.h"
 #include "kv8_fwd.h"
 #include "simt.cuh"
 
@@ -163,18 +164,9 @@ cudaError_t launch_simt(const FwdParams& p, cudaStream_t st) {
 
 namespace {
 
-struct Buf {
-  const void* p;
-  int64_t n;
-};
-
-bool meet(const Buf& a, const Buf& b) {
-  if (!a.p || !b.p || a.n <= 0 || b.n <= 0) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x < y + static_cast<uintptr_t>(b.n) && y < x + static_cast<uintptr_t>(a.n);
-}
-
-bool aligned(const void* p, int to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+using attn::aligned;
+using attn::Buf;
+using attn::meet;
 
 int check_shape(const attn_paged_shape_t& s) {
   if (s.num_seqs < 0 || s.num_queries < 0 || s.Hq <= 0 || s.Hkv <= 0 || s.D <= 0 || s.page_size <= 0 ||

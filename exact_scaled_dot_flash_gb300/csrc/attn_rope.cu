@@ -28,6 +28,7 @@
 #include <algorithm>
 
 #include "attn.h"
+#include "host_checks.h"
 #include "params.h"
 #include "ptx.cuh"
 
@@ -346,8 +347,8 @@ extern "C" int attn_rope(const attn_rope_shape_t* shape, const void* q, const vo
   // with few tokens the heads of one are dealt to up to 8 CTAs (64 tokens of 40
   // heads: 2.9 us by two each, 3.4 by one).
   const int several = dtype == ATTN_F32 ? attn::rope::Elem<0>::TOKENS : attn::rope::Elem<2>::TOKENS;
-  p.tok = tokens >= 152 * 16 && p.H * several <= attn::rope::MAX_ROWS ? several : 1;
-  const int64_t want = std::min<int64_t>({2 * 152 / tokens, 8, (p.H + 7) / 8});
+  p.tok = tokens >= attn::SMS * 16 && p.H * several <= attn::rope::MAX_ROWS ? several : 1;
+  const int64_t want = std::min<int64_t>({2 * attn::SMS / tokens, 8, (p.H + 7) / 8});
   const int64_t least = (static_cast<int64_t>(p.H) * p.tok + attn::rope::MAX_ROWS - 1) / attn::rope::MAX_ROWS;
   const int split = static_cast<int>(std::max(want, least));
   if (split > 65535) return ATTN_ERR_SHAPE;

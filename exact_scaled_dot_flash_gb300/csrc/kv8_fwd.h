@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "host_checks.h"
 #include "kv8.cuh"
 
 namespace attn {
@@ -72,7 +73,7 @@ inline DecodePlan decode_plan(int num_seqs, int Hkv, int heads, int max_queries,
   const int64_t blocks = num_seqs * (keys > 128 ? (keys + 127) / 128 : 1);
   const int64_t side = static_cast<int64_t>(Hkv) * d.row_groups;
   d.aligned = keys <= 512;
-  int64_t r = d.aligned ? num_seqs : 152 * (d.nt <= 2 ? 3 : 2) / side;
+  int64_t r = d.aligned ? num_seqs : SMS * (d.nt <= 2 ? 3 : 2) / side;
   if (!d.aligned) {
     const double n = static_cast<double>(blocks) / num_seqs;
     const double m = sqrt(n * ((group_rows + 3) / 4) / 8);
@@ -98,7 +99,7 @@ inline int64_t tc_qblocks(int max_queries, int heads) { return (static_cast<int6
 inline int tc_splits(int num_seqs, int Hkv, int64_t qblocks, int max_pages, int page_size) {
   const int64_t ctas = num_seqs * qblocks * Hkv;
   const int64_t tiles = (static_cast<int64_t>(max_pages) * page_size + 127) / 128;
-  int64_t s = ctas <= 0 ? 1 : ctas > 50 && ctas <= 114 && tiles >= 64 ? 304 / ctas : 152 / ctas;
+  int64_t s = ctas <= 0 ? 1 : ctas > 50 && ctas <= 114 && tiles >= 64 ? 2 * SMS / ctas : SMS / ctas;
   if (s > tiles / 4) s = tiles / 4;
   if (s > 32) s = 32;
   return static_cast<int>(s > 1 ? s : 1);
@@ -116,7 +117,7 @@ inline bool decode_takes(int num_seqs, int Hkv, int heads, int max_queries, int 
   if (rows <= 16) return true;
   if (decode_plan(num_seqs, Hkv, heads, max_queries, max_pages, page_size).few_keys) return false;
   return rows <= 48 || (tc_splits(num_seqs, Hkv, 1, max_pages, page_size) == 1 &&
-                        static_cast<int64_t>(num_seqs) * Hkv < 152);
+                        static_cast<int64_t>(num_seqs) * Hkv < SMS);
 }
 template <int FMT>
 cudaError_t launch_tc(const FwdParams& p, cudaStream_t st);
