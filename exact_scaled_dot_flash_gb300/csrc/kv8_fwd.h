@@ -93,12 +93,16 @@ cudaError_t launch_decode(const FwdParams& p, const DecodePlan& plan, cudaStream
 // are cut into runs of at least 4 tiles of 128, as many as fill the SMs (48 CTAs
 // over up to 3.5k keys: 41 us, 67 whole); over 8k keys and more, 51 to 114 CTAs are
 // cut to fill them twice (up to 16k keys, 100 rows of 20 sequences, 80 CTAs: 138 us,
-// 228 whole; 104 CTAs: 174, 229; but 112 CTAs over up to 3.5k keys: 77, 68). The
-// workspace then holds for each run and row D floats and (m, l).
+// 228 whole; 104 CTAs: 174, 229; but 112 CTAs over up to 3.5k keys: 77, 68). From 115
+// CTAs on it depends on how far the lengths lie apart, which the host does not know:
+// 120 CTAs, 3k-16k keys: 170 us, 227 whole; all of 16k: 246, 234. Nor are these borders
+// sharp: 80 CTAs over 2k-7.9k keys take 74 us cut, 113 whole, as they are run.
+// The workspace then holds for each run and row D floats and (m, l).
+inline int64_t key_tiles(int max_pages, int page_size) { return (static_cast<int64_t>(max_pages) * page_size + 127) / 128; }
 inline int64_t tc_qblocks(int max_queries, int heads) { return (static_cast<int64_t>(max_queries) * heads + 255) / 256; }
 inline int tc_splits(int num_seqs, int Hkv, int64_t qblocks, int max_pages, int page_size) {
   const int64_t ctas = num_seqs * qblocks * Hkv;
-  const int64_t tiles = (static_cast<int64_t>(max_pages) * page_size + 127) / 128;
+  const int64_t tiles = key_tiles(max_pages, page_size);
   int64_t s = ctas <= 0 ? 1 : ctas > 50 && ctas <= 114 && tiles >= 64 ? 2 * SMS / ctas : SMS / ctas;
   if (s > tiles / 4) s = tiles / 4;
   if (s > 32) s = 32;
@@ -108,16 +112,21 @@ inline int tc_splits(int num_seqs, int Hkv, int64_t qblocks, int max_pages, int 
 // Which of the two takes a call. More than 64 rows: the kernel for many. 17 to 64
 // rows of so few keys that the other one's CTAs would not fill the SMs: it too (30
 // rows, one sequence of some 6k keys, 4 kv heads: 28 against 50 us; 12 sequences: 87
-// against 75). 49 to 64 rows: where its CTAs, whole or cut, fill the SMs (50 rows
-// of 12 sequences: 87 against 107 us, of 20: 132 against 145, of 40: 227 against
-// 260; of 30, whose 120 CTAs are not cut: 229 against 198 us).
+// against 75). 49 to 64 rows: where its CTAs, cut or not, fill the SMs, or have few
+// keys, since its time is that of its longest CTA and the other one's that of all
+// keys. 4k-16k keys, CTAs whole, 50 to 64 rows: up to 120 CTAs the few-row kernel is
+// the faster one (2k-7.9k keys, 80 CTAs: 88 against 113 us; 3k-16k keys, 120: 170, 227),
+// from there on they cross (2k-7.9k, 148: 131 against 115; 3k-16k, 148: 203, 229). Fewer
+// keys, any number of CTAs: the many-row one (4 to 960 CTAs, up to 500 keys: 1.0 to 1.35
+// times as fast, up to 2k keys 1.3 to 1.7 times; 80 to 148 CTAs up to 3.5k keys: 59 to 61
+// against 57 to 80 us).
 inline bool decode_takes(int num_seqs, int Hkv, int heads, int max_queries, int max_pages, int page_size) {
   const int64_t rows = static_cast<int64_t>(max_queries) * heads;
   if (rows > 64) return false;
   if (rows <= 16) return true;
   if (decode_plan(num_seqs, Hkv, heads, max_queries, max_pages, page_size).few_keys) return false;
-  return rows <= 48 || (tc_splits(num_seqs, Hkv, 1, max_pages, page_size) == 1 &&
-                        static_cast<int64_t>(num_seqs) * Hkv < SMS);
+  return rows <= 48 || (tc_splits(num_seqs, Hkv, 1, max_pages, page_size) == 1 && key_tiles(max_pages, page_size) >= 32 &&
+                        static_cast<int64_t>(num_seqs) * Hkv <= 120);
 }
 template <int FMT>
 cudaError_t launch_tc(const FwdParams& p, cudaStream_t st);
