@@ -2,10 +2,10 @@
 // rows (queries x heads of a kv head, at most 32 a CTA and 64 a call): decode
 // steps and drafted tokens (F16/BF16, D in {64, 128}).
 //
-// Measured: 64 sequences of 1k-8k keys, 32 / 8 heads, D 128, e4m3: 110 us, 5.8 TB/s
-// of codes (87% of the copy bandwidth); one row of 130k keys, int8: 60 us, 4.5 TB/s;
-// 35 rows of 12 sequences: 81 us, 1.7 TB/s (two row groups convert the codes twice;
-// the instructions are the bound from 16 rows on).
+// Measured: 64 sequences of 1k-8k keys, 32 / 8 heads, D 128, e4m3: 112 us, 5.75 TB/s
+// (85% of the copy bandwidth); one row of 130k keys, int8: 61 us, 4.4 TB/s; 35 rows
+// of 12 sequences: 82 us, 1.7 TB/s (two row groups convert the codes twice; the
+// instructions are the bound from 16 rows on; 25 to 32 rows at D 128 spill).
 //
 // Bound: the bytes of the codes, read once for all the rows of a kv head. At
 // the copy bandwidth an SM is fed 21 bytes a cycle, and each byte has to become

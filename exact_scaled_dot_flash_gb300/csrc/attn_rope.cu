@@ -8,10 +8,11 @@
 // Angles: of a far position only the fraction of a turn matters, and fp32
 // loses it (position 10^6 leaves an error of 0.06 rad). inv_freq / 2 pi is
 // taken once as a 64-bit fraction of a turn, F = frac(f) 2^64; position * F
-// modulo 2^64 is then the exact fraction of the product, for every int32
+// modulo 2^64 is then the exact fraction of the product with F, for every int32
 // position, and its upper 32 bits as a signed number are the angle in half
-// turns, in [-1, 1), which sincospi takes without any range reduction. The
-// rounding of f to double leaves position * 2^-53 of a turn.
+// turns, in [-1, 1), which sincospi takes without any range reduction. f itself
+// is off by 2^-52 of it (the product in double and its constant): an angle by
+// position * inv_freq * 2^-52, 5e-7 at the last position and inv_freq 1.
 //
 // Bytes: every element is read once and written once, and nothing else counts:
 // the angles of a token are computed once for all its heads, in shared memory,
@@ -20,7 +21,8 @@
 // thread working out its own for every 16 bytes, the instructions were the bound
 // (72 us for 8191 tokens of 40 F16 heads, D 128). For the 16-bit types, whose
 // vectors take twice the conversions, many threads with one vector each beat few
-// with several in flight (8 CTAs an SM and 1: 36.5 us, 4.6 TB/s; 4 and 4: 49 us);
+// with several in flight (F16, 8 CTAs an SM and 1: 36.5 us, 4.6 TB/s; 4 and 4: 49
+// us; the 32 registers of a thread hold an F16 item, of a BF16 one 40-72 bytes spill);
 // for F32 it is the other way round (16384 tokens of 64 heads: 160 us, 6.7 TB/s,
 // with 4 vectors and 2 tokens a CTA, 171 us as the 16-bit types).
 #include <math.h>

@@ -533,7 +533,8 @@ ATTN_API int attn_paged_kv8_fwd(const attn_paged_shape_t* shape, int group, int 
                                 void* stream);
 
 /* attn_paged_kv8_workspace_bytes - workspace attn_paged_kv8_fwd needs for
- * `shape` (every dtype, group and format). Returns ATTN_OK, ATTN_ERR_NULL,
+ * `shape` (every dtype, group and format; F32 calls bring it too, though their
+ * kernel does not use it). Returns ATTN_OK, ATTN_ERR_NULL,
  * ATTN_ERR_SHAPE or ATTN_ERR_HEAD_DIM. */
 ATTN_API int attn_paged_kv8_workspace_bytes(const attn_paged_shape_t* shape, size_t* bytes);
 
@@ -562,9 +563,10 @@ typedef struct {
  * inverse = 1 turns by -a: the transposed map, which takes the gradient of the
  * outputs to the gradient of the inputs (and, at mscale 1, undoes the turn).
  * inv_freq: device double [rot/2], finite, so scaling for long contexts is a
- * choice of frequencies and mscale. The fraction of a turn is computed in
- * 64 bits: no loss at any int32 position. Products and sums in fp32, rounded
- * once to `dtype`.
+ * choice of frequencies and mscale. The fraction of a turn is computed in 64
+ * bits: an angle is off by at most |p| * inv_freq * 2^-52 (5e-7 at the last int32
+ * position and inv_freq 1) before the fp32 sine and cosine. Products and sums in
+ * fp32, rounded once to `dtype`.
  * positions: device int32 [S] or [B, S] (row stride pos_batch_stride).
  * An output may be its own input (same pointer and strides), must have no two
  * rows in the same place and may share no other element with any other
