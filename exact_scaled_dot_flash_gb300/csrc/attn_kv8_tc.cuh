@@ -57,7 +57,7 @@ constexpr float SPREAD = 64.f;
 constexpr float SLACK_LOG2 = 7.f;   // a bound that takes the largest scale, below 2^vex, for one that is SPREAD times as small
 constexpr float Y_RANGE = 80.f;     // y <= 2^(80 + 8 + 7): its sum over 2^31 keys is within fp32
 constexpr float VS_LEAST = 8.271806125530277e-25f;  // 2^-Y_RANGE: smaller value scales count as this
-constexpr float UNSEEN = -3e38f;    // reference of a row without keys: below every finite score, and finite
+constexpr float UNSEEN = -3e38f;    // reference of a row without keys: at the end of fp32's range, and finite
 
 template <int D>
 struct Cfg {

@@ -5,6 +5,7 @@ import ctypes
 import pytest
 
 from exact_scaled_dot_flash_gb300 import attn as A
+from tests.test_boundary import lib  # noqa: F401
 
 
 def workspace(num_seqs, heads, max_queries, keys, Hkv=4, page=64, D=128):
@@ -16,7 +17,7 @@ def workspace(num_seqs, heads, max_queries, keys, Hkv=4, page=64, D=128):
 
 
 @pytest.mark.parametrize("seqs", [20, 24, 30, 36, 37])
-def test_50_rows_of_sequences_that_are_not_cut(seqs):
+def test_50_rows_of_sequences_that_are_not_cut(lib, seqs):  # noqa: F811
     # 80 to 148 CTAs of 256 rows: over at most 3.5k keys those of the kernel for many rows, whole; over
     # 7.9k keys the other kernel, where they are few
     assert workspace(seqs, 10, 5, 3520) == 0
@@ -24,6 +25,6 @@ def test_50_rows_of_sequences_that_are_not_cut(seqs):
     assert (workspace(seqs, 10, 5, 7936) > 0) == (seqs <= 30)
 
 
-def test_few_rows_share_out_the_keys():
+def test_few_rows_share_out_the_keys(lib):  # noqa: F811
     assert workspace(30, 1, 1, 3520) > 0 and workspace(30, 8, 5, 3520) > 0
     assert workspace(30, 8, 1, 512) == 0
