@@ -63,6 +63,11 @@ class RopeShape(ctypes.Structure):
                 [("pos_batch_stride", ctypes.c_int64)])
 
 
+class Pages(ctypes.Structure):
+    """attn_pages_t."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_seqs", "max_pages", "page_size", "num_pages")]
+
+
 def library_path() -> str:
     return os.path.join(_HERE, _LIBNAME)
 
@@ -159,6 +164,29 @@ def _open(path):
     lib.attn_rope.argtypes = [ctypes.POINTER(RopeShape), vp, vp, vp, vp, ctypes.c_int, ctypes.c_int, ctypes.c_float,
                               ctypes.c_int, vp, vp, vp]
     lib.attn_rope.restype = ctypes.c_int
+    lib.attn_rope_axes.argtypes = [ctypes.POINTER(RopeShape), vp, vp, vp, ctypes.c_int64, ctypes.c_int, vp, vp,
+                                   ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_int, vp, vp, vp]
+    lib.attn_rope_axes.restype = ctypes.c_int
+    pvp, pool = ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(Pages)
+    lib.attn_pages_copy.argtypes = [ctypes.c_int, pvp, pi64, ctypes.c_int, vp, vp, ctypes.c_int, vp]
+    lib.attn_pages_copy.restype = ctypes.c_int
+    lib.attn_pages_fork.argtypes = [pool, vp, vp, vp, vp, vp, ctypes.c_int, vp]
+    lib.attn_pages_fork.restype = ctypes.c_int
+    lib.attn_pages_free.argtypes = [pool, vp, vp, vp, vp, ctypes.c_int, vp]
+    lib.attn_pages_free.restype = ctypes.c_int
+    lib.attn_pages_reserve.argtypes = [pool, vp, vp, vp, vp, pvp, pi64, ctypes.c_int, vp, vp, ctypes.c_size_t, vp]
+    lib.attn_pages_reserve.restype = ctypes.c_int
+    lib.attn_pages_compact.argtypes = [pool, vp, vp, pvp, pi64, ctypes.c_int, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.attn_pages_compact.restype = ctypes.c_int
+    lib.attn_pages_workspace_bytes.argtypes = [pool, ctypes.POINTER(ctypes.c_size_t)]
+    lib.attn_pages_workspace_bytes.restype = ctypes.c_int
+    lib.attn_paged_prefix_fwd.argtypes = [ctypes.POINTER(PagedShape), ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp, vp,
+                                          vp, vp, vp, ctypes.c_int, ctypes.c_float, ctypes.c_int, vp, ctypes.c_size_t,
+                                          vp, vp, vp]
+    lib.attn_paged_prefix_fwd.restype = ctypes.c_int
+    lib.attn_paged_prefix_workspace_bytes.argtypes = [ctypes.POINTER(PagedShape), ctypes.c_int, ctypes.c_int,
+                                                      ctypes.POINTER(ctypes.c_size_t)]
+    lib.attn_paged_prefix_workspace_bytes.restype = ctypes.c_int
     lib.attn_fwd_host.argtypes = [ctypes.POINTER(Shape), vp, vp, vp, ctypes.c_int, vp, vp, ctypes.c_float,
                                   ctypes.c_int, vp, ctypes.c_size_t, vp, vp]
     lib.attn_fwd_host.restype = ctypes.c_int
@@ -924,6 +952,232 @@ def paged_kv8_fwd(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
     return (out, lse) if return_lse else out
 
 
+# ------------------------------------------------------------------ pages of a cache
+def _pool(block_table, seq_lens, refs, page_size):
+    """Checks a pool's arrays (seq_lens None: the call does not take it): its C description and its device."""
+    dev = refs.device
+    size = block_table.shape
+    if len(size) != 2 or refs.dim() != 1:
+        raise AttnError("block_table must be int32 [num_seqs, max_pages] and refs int32 [num_pages]")
+    _int32("block_table", block_table, size, dev)
+    _int32("refs", refs, refs.shape, dev)
+    if seq_lens is not None:
+        _int32("seq_lens", seq_lens, size[:1], dev)
+    return Pages(size[0], size[1], page_size, refs.shape[0]), dev
+
+
+def _buffers(caches, num_pages, dev):
+    """The buffers of a call: addresses and bytes of a page of each."""
+    ptrs, sizes = [], []
+    for t in caches:
+        if t.device != dev or t.dim() < 1 or t.shape[0] != num_pages or not t.is_contiguous():
+            raise AttnError(f"caches must be contiguous [num_pages = {num_pages}, ...] tensors on {dev}")
+        ptrs.append(t.data_ptr() or None)
+        sizes.append(t.nbytes // num_pages if num_pages else 1)
+    n = len(ptrs)
+    return (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), n
+
+
+def _rows(name, t, dev):
+    if t.dim() != 1:
+        raise AttnError(f"{name} must be a one-dimensional int32 tensor on {dev}")
+    return _int32(name, t, t.shape, dev)
+
+
+def pages_copy(caches, src, dst, *, stream=None):
+    """Page src[i] of every cache to page dst[i] (attn_pages_copy).
+
+    caches: a sequence of contiguous CUDA tensors [num_pages, ...] of any types (keys
+    and values of each layer, codes and scales). src, dst int32 [n] on the same
+    device; a pair that names a page outside the pool is passed over, and no
+    destination may be named by another pair.
+    """
+    caches = tuple(caches)
+    if not caches:
+        return
+    dev, pages = caches[0].device, caches[0].shape[0] if caches[0].dim() else 0
+    bufs = _buffers(caches, pages, dev)
+    if src.shape != dst.shape:
+        raise AttnError("src and dst must have the same length")
+    lib = _lib or load_library()
+    st = _stream(stream, dev)
+    _launch(dev, lib.attn_pages_copy, pages, *bufs, _rows("src", src, dev), _rows("dst", dst, dev), src.shape[0], st)
+
+
+def pages_fork(block_table, seq_lens, refs, parents, children, *, page_size: int, stream=None):
+    """Row children[i] of the table becomes a copy of row parents[i] (attn_pages_fork), in place.
+
+    block_table int32 [num_seqs, max_pages] (-1: no page), seq_lens int32
+    [num_seqs], refs int32 [num_pages] (entries of the table that name each page; 0:
+    free); parents, children int32 [n]. The child shares the parent's pages; what it
+    held before is given back. No cache data moves: :func:`pages_reserve` copies a
+    shared page before one of its sequences writes to it. The children must differ from one another and
+    from the parents.
+    """
+    pool, dev = _pool(block_table, seq_lens, refs, page_size)
+    if parents.shape != children.shape:
+        raise AttnError("parents and children must have the same length")
+    lib = _lib or load_library()
+    st = _stream(stream, dev)
+    _launch(dev, lib.attn_pages_fork, pool, block_table.data_ptr() or None, seq_lens.data_ptr() or None,
+            refs.data_ptr() or None, _rows("parents", parents, dev), _rows("children", children, dev), parents.shape[0], st)
+
+
+def pages_free(block_table, seq_lens, refs, seqs, *, stream=None):
+    """Sequences ``seqs`` (int32 [n]) give back their pages (attn_pages_free), in place:
+    their rows become -1, their lengths 0. The pool's arrays as for :func:`pages_fork`."""
+    pool, dev = _pool(block_table, seq_lens, refs, 1)
+    lib = _lib or load_library()
+    st = _stream(stream, dev)
+    _launch(dev, lib.attn_pages_free, pool, block_table.data_ptr() or None, seq_lens.data_ptr() or None,
+            refs.data_ptr() or None, _rows("seqs", seqs, dev), seqs.shape[0], st)
+
+
+def pages_workspace_bytes(pool: Pages) -> int:
+    """Workspace bytes attn_pages_reserve and attn_pages_compact need for ``pool``."""
+    n = ctypes.c_size_t(0)
+    rc = (_lib or load_library()).attn_pages_workspace_bytes(pool, n)
+    if rc:
+        check(rc)
+    return n.value
+
+
+def _pool_space(refs, pool, workspace, made):
+    need = pages_workspace_bytes(pool)
+    if workspace is None:
+        made.append(workspace := refs.new_empty((need + 3) // 4))
+    elif (workspace.device != refs.device or workspace.numel() * workspace.element_size() < need
+          or not workspace.is_contiguous()):
+        raise AttnError(f"workspace must hold {need} contiguous bytes on the pool's device")
+    return workspace.data_ptr(), need
+
+
+def pages_reserve(block_table, seq_lens, refs, new_tokens, caches=(), *, page_size: int, result=None, workspace=None,
+                  stream=None):
+    """Room for new_tokens[s] tokens behind the seq_lens[s] of every sequence (attn_pages_reserve), in place.
+
+    The blocks that they go to get the lowest free pages where they have none, and
+    where their page is shared, with its data copied in every one of ``caches``
+    ([num_pages, ...] tensors) if the block holds tokens (copy on write). new_tokens
+    int32 [num_seqs]; the pool's arrays as for :func:`pages_fork`. seq_lens stays:
+    the write that follows counts the tokens. Returns ``result``, int32 [2] on the
+    device: pages taken, pages lacking (then nothing was changed).
+    """
+    pool, dev = _pool(block_table, seq_lens, refs, page_size)
+    bufs = _buffers(caches, pool.num_pages, dev)
+    made = []
+    if result is None:
+        made.append(result := refs.new_empty(2))
+    ws, need = _pool_space(refs, pool, workspace, made)
+    lib = _lib or load_library()
+    st = _stream(stream, dev, made)
+    _launch(dev, lib.attn_pages_reserve, pool, block_table.data_ptr() or None, seq_lens.data_ptr() or None,
+            refs.data_ptr() or None, _int32("new_tokens", new_tokens, seq_lens.shape, dev), *bufs,
+            _int32("result", result, (2,), dev), ws, need, st)
+    return result
+
+
+def pages_compact(block_table, refs, caches, *, page_map=None, used=None, workspace=None, stream=None):
+    """Moves the pages in use to the low end of the pool (attn_pages_compact), in place:
+    the i-th free page below U receives the i-th page in use from U on, U the number
+    of pages in use, in every one of ``caches``; block_table and refs follow. Returns
+    (page_map, used): int32 [num_pages], where each page now is (-1: it was free),
+    and int32 [1], U, on the device."""
+    pool, dev = _pool(block_table, None, refs, 1)
+    bufs = _buffers(caches, pool.num_pages, dev)
+    made = []
+    if page_map is None:
+        made.append(page_map := refs.new_empty(pool.num_pages))
+    if used is None:
+        made.append(used := refs.new_empty(1))
+    ws, need = _pool_space(refs, pool, workspace, made)
+    lib = _lib or load_library()
+    st = _stream(stream, dev, made)
+    _launch(dev, lib.attn_pages_compact, pool, block_table.data_ptr() or None, refs.data_ptr() or None, *bufs,
+            _int32("page_map", page_map, refs.shape, dev), _int32("used", used, (1,), dev), ws, need, st)
+    return page_map, used
+
+
+# ------------------------------------------------------------------ a shared prefix
+def paged_prefix_workspace_bytes(shape: PagedShape, num_groups: int, max_group_queries: int) -> int:
+    """Workspace bytes attn_paged_prefix_fwd needs."""
+    n = ctypes.c_size_t(0)
+    rc = (_lib or load_library()).attn_paged_prefix_workspace_bytes(shape, num_groups, max_group_queries, n)
+    if rc:
+        check(rc)
+    return n.value
+
+
+def paged_prefix_fwd(q, k_cache, v_cache, block_table, seq_lens, q_offsets, group_offsets, prefix_lens, *,
+                     positions=None, causal: bool = True, scale: float | None = None, max_queries: int | None = None,
+                     max_group_queries: int | None = None, return_lse: bool = False, out=None, stream=None,
+                     workspace=None, lse_out=None):
+    """:func:`paged_fwd` for groups of sequences that begin with the same tokens (attn_paged_prefix_fwd).
+
+    Sequences group_offsets[g] .. group_offsets[g+1]-1 (int32 [groups + 1]) share
+    their first prefix_lens[g] tokens (int32 [groups]): the rows of the table name
+    the same pages for them (:func:`pages_fork`), or copies. Their keys and values are
+    read once for the whole group. The other arguments and the results are those
+    of :func:`paged_fwd`; ``max_group_queries`` bounds the queries of one group
+    (computed, with a host sync, when None), and ``workspace`` (a CUDA uint8 tensor of
+    :func:`paged_prefix_workspace_bytes`) is allocated here when not given.
+    :func:`paged_bwd` takes the results.
+    """
+    import torch
+
+    dev, size, dtype = q.device, q.shape, q.dtype
+    if len(size) != 3 or not q.is_contiguous():
+        raise AttnError("q must be a contiguous [queries, Hq, D] tensor")
+    nq, Hq, D = size
+    csize = k_cache.shape
+    if len(csize) != 4 or csize[3] != D or v_cache.shape != csize:
+        raise AttnError("k_cache and v_cache must be [pages, page_size, Hkv, D] with q's D")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.device != dev or t.dtype is not dtype or not t.is_contiguous():
+            raise AttnError(f"{name} must be a contiguous {dtype} tensor on {dev}")
+    pages, P, Hkv, _ = csize
+    table, lens, goff = block_table.shape, seq_lens.shape, group_offsets.shape
+    if len(lens) != 1 or len(table) != 2 or len(goff) != 1 or goff[0] < 1:
+        raise AttnError("block_table must be int32 [num_seqs, max_pages], seq_lens int32 [num_seqs] and group_offsets "
+                        "int32 [groups + 1]")
+    ns, ng = lens[0], goff[0] - 1
+    bt, sl = _int32("block_table", block_table, (ns, table[1]), dev), _int32("seq_lens", seq_lens, lens, dev)
+    qo, go = _int32("q_offsets", q_offsets, (ns + 1,), dev), _int32("group_offsets", group_offsets, goff, dev)
+    pl = _int32("prefix_lens", prefix_lens, (ng,), dev)
+    pos = _int32("positions", positions, (nq,), dev) if positions is not None else None
+    if max_queries is None:
+        max_queries = int((q_offsets[1:] - q_offsets[:-1]).max().item()) if ns else 0
+    if max_group_queries is None:
+        at = q_offsets[group_offsets.clamp(0, ns).long()]
+        max_group_queries = max(int((at[1:] - at[:-1]).max().item()), 0) if ng else 0
+    made = []
+    if out is None:
+        made.append(out := torch.empty_like(q))
+    elif out.shape != size or out.dtype is not dtype or out.device != dev or not out.is_contiguous():
+        raise AttnError("out must be a contiguous tensor like q")
+    lse = None
+    if return_lse:
+        if lse_out is None:
+            made.append(lse := q.new_empty((nq, Hq), dtype=torch.float32))
+        else:
+            lse = _lse_buffer(lse_out, (nq, Hq), dev)
+    shape = PagedShape(ns, nq, Hq, Hkv, D, P, pages, table[1], max_queries)
+    need = paged_prefix_workspace_bytes(shape, ng, max_group_queries)
+    if need:
+        if workspace is None:
+            made.append(workspace := q.new_empty(need, dtype=torch.uint8))
+        elif (workspace.device != dev or workspace.numel() * workspace.element_size() < need
+              or not workspace.is_contiguous()):
+            raise AttnError(f"workspace must hold {need} contiguous bytes on q's device")
+    lib = _lib or load_library()
+    st = _stream(stream, dev, made)
+    _launch(dev, lib.attn_paged_prefix_fwd, shape, ng, max_group_queries, q.data_ptr() or None, k_cache.data_ptr() or None,
+            v_cache.data_ptr() or None, bt, sl, qo, pos, go, pl, 1 if causal else 0,
+            1.0 / math.sqrt(D) if scale is None else scale, _dtype_code(q), workspace.data_ptr() if need else None, need,
+            out.data_ptr() or None, lse.data_ptr() or None if lse is not None else None, st)
+    return (out, lse) if return_lse else out
+
+
 # ------------------------------------------------------------------ rotary positions
 def rope_frequencies(rot: int, *, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
                      original_positions: int = 4096, fast_turns: float = 32.0, slow_turns: float = 1.0):
@@ -963,7 +1217,23 @@ def rope_frequencies(rot: int, *, base: float = 10000.0, scaling: str | None = N
 _ROPE_SHAPE = struct.Struct("6i13q")
 
 
-def _rope(q, k, positions, inv_freq, layout, mscale, inverse, q_out, k_out, stream):
+def rope_axes(sections, *, cycle: bool = False):
+    """Axis of each pair for :func:`rope`: int32 host tensor [sum(sections)].
+
+    ``sections[a]`` pairs turn by axis a: in runs (the first ``sections[0]`` pairs
+    by axis 0, and so on), or with ``cycle`` in turn, axis by axis, for as long as
+    each has pairs left.
+    """
+    import torch
+
+    sections = [int(n) for n in sections]
+    if not sections or min(sections) < 0 or len(sections) > 256:
+        raise AttnError("sections must be 1 to 256 numbers of pairs")
+    pairs = [(i if cycle else 0, a) for a, n in enumerate(sections) for i in range(n)]
+    return torch.tensor([a for _, a in sorted(pairs)] if cycle else [a for _, a in pairs], dtype=torch.int32)
+
+
+def _rope(q, k, positions, inv_freq, layout, mscale, inverse, axes, q_out, k_out, stream):
     import torch
 
     dev, dtype, size = q.device, q.dtype, q.shape
@@ -1001,9 +1271,13 @@ def _rope(q, k, positions, inv_freq, layout, mscale, inverse, q_out, k_out, stre
             raise AttnError(f"k_out must be a {dtype} {list(ksize)} tensor on {dev}")
         kst, kost = strides("k", k), strides("k_out", k_out)
     pos = positions.shape
+    if axes is not None:  # an array of positions for each axis
+        if len(pos) < 2:
+            raise AttnError("positions must have a dimension of axes before the tokens'")
+        num_axes, pos = pos[0], pos[1:]
     if (pos != (S,) and (dim == 3 or pos != (B, S))) or positions.dtype is not torch.int32 or positions.device != dev \
             or not positions.is_contiguous():
-        raise AttnError(f"positions must be a contiguous int32 tensor on {dev}, "
+        raise AttnError(f"positions must be a contiguous int32 tensor on {dev}, " + ("" if axes is None else "[axes] of ")
                         + ("[tokens]" if dim == 3 else "[S] or [B, S]"))
     if (inv_freq.dtype is not torch.float64 or inv_freq.device != dev or inv_freq.dim() != 1
             or not inv_freq.is_contiguous()):
@@ -1016,6 +1290,13 @@ def _rope(q, k, positions, inv_freq, layout, mscale, inverse, q_out, k_out, stre
         raise AttnError(f"a dimension is out of range: {e}") from None
     lib = _lib or load_library()
     st = _stream(stream, dev, made)
+    if axes is not None:
+        _launch(dev, lib.attn_rope_axes, shape, q.data_ptr() or None, k.data_ptr() or None if Hk else None,
+                positions.data_ptr() or None, B * S if len(pos) == 2 else S, num_axes,
+                _int32("axes", axes, inv_freq.shape, dev), inv_freq.data_ptr() or None,
+                ROPE_HALF if layout == "half" else ROPE_INTERLEAVED, inverse, mscale, _dtype_code(q),
+                q_out.data_ptr() or None, k_out.data_ptr() or None if Hk else None, st)
+        return q_out, k_out
     _launch(dev, lib.attn_rope, shape, q.data_ptr() or None, k.data_ptr() or None if Hk else None,
             positions.data_ptr() or None, inv_freq.data_ptr() or None,
             ROPE_HALF if layout == "half" else ROPE_INTERLEAVED, inverse, mscale, _dtype_code(q),
@@ -1023,9 +1304,9 @@ def _rope(q, k, positions, inv_freq, layout, mscale, inverse, q_out, k_out, stre
     return q_out, k_out
 
 
-def rope(q, k, positions, inv_freq, *, layout: str = "half", mscale: float = 1.0, q_out=None, k_out=None,
+def rope(q, k, positions, inv_freq, *, layout: str = "half", mscale: float = 1.0, axes=None, q_out=None, k_out=None,
          stream=None):
-    """Rotary positions of queries and keys (attn_rope).
+    """Rotary positions of queries and keys (attn_rope, attn_rope_axes).
 
     q [tokens, Hq, D] and k [tokens, Hk, D] (packed, as :func:`paged_fwd` and
     :func:`kv8_write` take them) or [B, Hq, S, D] and [B, Hk, S, D] (dense, as
@@ -1033,15 +1314,18 @@ def rope(q, k, positions, inv_freq, *, layout: str = "half", mscale: float = 1.0
     float32, float16 or bfloat16. positions int32 [tokens], [S] or [B, S];
     inv_freq float64 [rot / 2] on the same device (:func:`rope_frequencies`),
     which turns the first rot elements of each head. ``layout``: "half" pairs
-    element i with i + rot / 2, "interleaved" 2i with 2i + 1. ``q_out``/``k_out``
-    receive the results when given; they may be q and k themselves. Returns
-    (q_out, k_out).
+    element i with i + rot / 2, "interleaved" 2i with 2i + 1. ``axes`` int32 [rot / 2]
+    on the same device (:func:`rope_axes`): the axis of each pair, for tokens with a
+    position on each of several axes (time, height, width); positions then has a
+    dimension of axes in front, [axes, tokens], [axes, S] or [axes, B, S].
+    ``q_out``/``k_out`` receive the results when given; they may be q and k
+    themselves. Returns (q_out, k_out).
     """
-    return _rope(q, k, positions, inv_freq, layout, mscale, 0, q_out, k_out, stream)
+    return _rope(q, k, positions, inv_freq, layout, mscale, 0, axes, q_out, k_out, stream)
 
 
-def rope_bwd(dq, dk, positions, inv_freq, *, layout: str = "half", mscale: float = 1.0, q_out=None, k_out=None,
-             stream=None):
+def rope_bwd(dq, dk, positions, inv_freq, *, layout: str = "half", mscale: float = 1.0, axes=None, q_out=None,
+             k_out=None, stream=None):
     """Gradients of :func:`rope` with respect to q and k, from those of its outputs
     (the turn by the opposite angle, same mscale); arguments as for :func:`rope`."""
-    return _rope(dq, dk, positions, inv_freq, layout, mscale, 1, q_out, k_out, stream)
+    return _rope(dq, dk, positions, inv_freq, layout, mscale, 1, axes, q_out, k_out, stream)

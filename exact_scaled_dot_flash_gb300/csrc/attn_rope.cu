@@ -51,6 +51,9 @@ struct Side {  // queries or keys
 struct Params {
   int B, S, D, rot, Hq, H;  // H: heads of queries and keys together
   int64_t pos_batch;  // 0 or S: one row of positions for all, or one each
+  int64_t pos_axis;   // from axis to axis
+  int axes;
+  const int32_t* axis;  // [rot / 2] axis of each pair; nullptr: one position for all
   const int32_t* pos;
   const double* freq;
   float mscale;
@@ -82,7 +85,7 @@ struct alignas(N * sizeof(T)) Vec {
 // then the vectors of the copied tail. N = 1: elements instead of vectors
 // (interleaved: pairs), for rows that 16-byte accesses do not fit. A thread keeps
 // its item and goes through the CTA's rows (token, head).
-template <int DT, bool HALVES, int N>
+template <int DT, bool HALVES, int N, bool AXES>
 __global__ void __launch_bounds__(THREADS, Elem<DT>::CTAS) rope_kernel(const __grid_constant__ Params p) {
   using T = typename Elem<DT>::T;
   using V = Vec<T, N>;
@@ -175,7 +178,14 @@ __global__ void __launch_bounds__(THREADS, Elem<DT>::CTAS) rope_kernel(const __g
     constexpr double INV_2PI = 0.15915494309189533577;
     const int t = e / half, i = e - t * half;
     const int64_t g = tok0 + t;
-    const int64_t pos = __ldg(p.pos + (p.pos_batch || p.B == 1 ? g : g % p.S));
+    const int64_t at = p.pos_batch || p.B == 1 ? g : g % p.S;
+    int64_t pos;
+    if constexpr (AXES) {
+      const int a = __ldg(p.axis + i);
+      pos = a >= 0 && a < p.axes ? __ldg(p.pos + a * p.pos_axis + at) : 0;
+    } else {
+      pos = __ldg(p.pos + at);
+    }
     const double f = __ldg(p.freq + i) * INV_2PI;
     const uint64_t F = __double2ull_rd((f - floor(f)) * 18446744073709551616.0);
     const int32_t top = static_cast<int32_t>(static_cast<uint32_t>((static_cast<uint64_t>(pos) * F) >> 32));
@@ -192,16 +202,16 @@ __global__ void __launch_bounds__(THREADS, Elem<DT>::CTAS) rope_kernel(const __g
   }
 }
 
-template <int DT>
+template <int DT, bool AXES>
 cudaError_t launch_dt(const Params& p, bool halves, bool vec, dim3 grid, cudaStream_t st) {
   constexpr int N = Elem<DT>::VEC;
   const size_t smem = static_cast<size_t>(p.tok) * (p.rot / 2) * sizeof(float2);
   if (halves) {
-    if (vec) rope_kernel<DT, true, N><<<grid, THREADS, smem, st>>>(p);
-    else rope_kernel<DT, true, 1><<<grid, THREADS, smem, st>>>(p);
+    if (vec) rope_kernel<DT, true, N, AXES><<<grid, THREADS, smem, st>>>(p);
+    else rope_kernel<DT, true, 1, AXES><<<grid, THREADS, smem, st>>>(p);
   } else {
-    if (vec) rope_kernel<DT, false, N><<<grid, THREADS, smem, st>>>(p);
-    else rope_kernel<DT, false, 1><<<grid, THREADS, smem, st>>>(p);
+    if (vec) rope_kernel<DT, false, N, AXES><<<grid, THREADS, smem, st>>>(p);
+    else rope_kernel<DT, false, 1, AXES><<<grid, THREADS, smem, st>>>(p);
   }
   return cudaGetLastError();
 }
@@ -266,9 +276,10 @@ bool rows_apart(int64_t B, int64_t S, int64_t H, int64_t D, const int64_t* st) {
 
 }  // namespace
 
-extern "C" int attn_rope(const attn_rope_shape_t* shape, const void* q, const void* k, const int32_t* positions,
-                         const double* inv_freq, int layout, int inverse, float mscale, attn_dtype_t dtype,
-                         void* q_out, void* k_out, void* stream) {
+// Both entry points; axis: nullptr for attn_rope (num_axes 1).
+static int rope_call(const attn_rope_shape_t* shape, const void* q, const void* k, const int32_t* positions,
+                     int64_t pos_axis_stride, int num_axes, const int32_t* axis, const double* inv_freq, int layout,
+                     int inverse, float mscale, attn_dtype_t dtype, void* q_out, void* k_out, void* stream) {
   if (!shape) return ATTN_ERR_NULL;
   const attn_rope_shape_t s = *shape;
   if (dtype != ATTN_F32 && dtype != ATTN_F16 && dtype != ATTN_BF16) return ATTN_ERR_DTYPE;
@@ -305,25 +316,30 @@ extern "C" int attn_rope(const attn_rope_shape_t* shape, const void* q, const vo
     const int n[3] = {s.B, s.S, heads[i]};
     for (int j = 0; j < 3; ++j) vec = vec && (n[j] == 1 || (st[i][j] * es) % 16 == 0);
   }
-  if ((reinterpret_cast<uintptr_t>(positions) & 3u) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u))
+  if ((reinterpret_cast<uintptr_t>(positions) & 3u) || (reinterpret_cast<uintptr_t>(axis) & 3u) ||
+      (reinterpret_cast<uintptr_t>(inv_freq) & 7u))
     return ATTN_ERR_ALIGN;
   bool in_place[2] = {false, false};
   for (int i = 0; i < nside; ++i) {
     in_place[i] = ptr[2 * i] == ptr[2 * i + 1];
     for (int j = 0; j < 3; ++j) in_place[i] = in_place[i] && st[2 * i][j] == st[2 * i + 1][j];
   }
-  Span meta[2];
-  const int64_t meta_bytes[2] = {(s.pos_batch_stride ? tokens : s.S) * 4, s.rot / 2 * 8};
-  for (int i = 0; i < 2; ++i) {
-    meta[i].p = reinterpret_cast<uintptr_t>(i == 0 ? static_cast<const void*>(positions) : inv_freq);
-    meta[i].token = meta[i].batch = 0;
-    meta[i].row = meta[i].one = meta[i].all = meta_bytes[i];
-  }
+  auto span_of_bytes = [](const void* at, int64_t bytes) {
+    Span m;
+    m.p = reinterpret_cast<uintptr_t>(at);
+    m.token = m.batch = 0;
+    m.row = m.one = m.all = bytes;
+    return m;
+  };
+  const int64_t pos_bytes = (s.pos_batch_stride ? tokens : s.S) * 4;
   for (int o = 1; o < 2 * nside; o += 2) {  // each output against every other tensor
     for (int i = 0; i < 2 * nside; ++i)
       if (i != o && !(i == o - 1 && in_place[o / 2]) && spans_meet(sp[o], sp[i], fit)) return ATTN_ERR_OVERLAP;
-    for (const Span& m : meta)
-      if (spans_meet(sp[o], m, false)) return ATTN_ERR_OVERLAP;
+    if (spans_meet(sp[o], span_of_bytes(inv_freq, s.rot / 2 * 8), false) ||
+        (axis && spans_meet(sp[o], span_of_bytes(axis, s.rot / 2 * 4), false)))
+      return ATTN_ERR_OVERLAP;
+    for (int a = 0; a < num_axes; ++a)
+      if (spans_meet(sp[o], span_of_bytes(positions + a * pos_axis_stride, pos_bytes), false)) return ATTN_ERR_OVERLAP;
   }
 
   Params p{};
@@ -333,6 +349,9 @@ extern "C" int attn_rope(const attn_rope_shape_t* shape, const void* q, const vo
   p.rot = s.rot;
   p.pos_batch = s.pos_batch_stride;
   p.pos = positions;
+  p.pos_axis = pos_axis_stride;
+  p.axes = num_axes;
+  p.axis = axis;
   p.freq = inv_freq;
   p.mscale = mscale;
   p.inverse = inverse;
@@ -358,8 +377,26 @@ extern "C" int attn_rope(const attn_rope_shape_t* shape, const void* q, const vo
   const dim3 grid(static_cast<unsigned>((tokens + p.tok - 1) / p.tok), static_cast<unsigned>((p.H + p.heads - 1) / p.heads));
   cudaError_t e;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (dtype == ATTN_F32) e = attn::rope::launch_dt<0>(p, halves, vec, grid, cs);
-  else if (dtype == ATTN_F16) e = attn::rope::launch_dt<1>(p, halves, vec, grid, cs);
-  else e = attn::rope::launch_dt<2>(p, halves, vec, grid, cs);
+#define ATTN_ROPE(DT) (axis ? attn::rope::launch_dt<DT, true>(p, halves, vec, grid, cs) : attn::rope::launch_dt<DT, false>(p, halves, vec, grid, cs))
+  e = dtype == ATTN_F32 ? ATTN_ROPE(0) : dtype == ATTN_F16 ? ATTN_ROPE(1) : ATTN_ROPE(2);
+#undef ATTN_ROPE
   return e == cudaSuccess ? ATTN_OK : attn::record_cuda_error(e);
+}
+
+extern "C" int attn_rope(const attn_rope_shape_t* shape, const void* q, const void* k, const int32_t* positions,
+                         const double* inv_freq, int layout, int inverse, float mscale, attn_dtype_t dtype,
+                         void* q_out, void* k_out, void* stream) {
+  return rope_call(shape, q, k, positions, 0, 1, nullptr, inv_freq, layout, inverse, mscale, dtype, q_out, k_out, stream);
+}
+
+extern "C" int attn_rope_axes(const attn_rope_shape_t* shape, const void* q, const void* k, const int32_t* positions,
+                              int64_t pos_axis_stride, int num_axes, const int32_t* axis, const double* inv_freq,
+                              int layout, int inverse, float mscale, attn_dtype_t dtype, void* q_out, void* k_out,
+                              void* stream) {
+  if (num_axes < 1 || num_axes > ATTN_ROPE_MAX_AXES || pos_axis_stride < 0 ||
+      static_cast<double>(pos_axis_stride) * num_axes > 1e17)
+    return ATTN_ERR_SHAPE;
+  if (!axis) return ATTN_ERR_NULL;
+  return rope_call(shape, q, k, positions, pos_axis_stride, num_axes, axis, inv_freq, layout, inverse, mscale, dtype,
+                   q_out, k_out, stream);
 }

@@ -5,8 +5,10 @@
  * attn_fwd_host), its backward (attn_bwd), attention and MLA over a paged
  * cache (attn_paged_fwd, attn_paged_mla) and their backward (attn_paged_bwd,
  * attn_paged_mla_bwd), a paged cache of 8-bit codes (attn_kv8_write,
- * attn_kv8_read, attn_paged_kv8_fwd) and rotary positions (attn_rope). Each
- * entry below states its own definition and source.
+ * attn_kv8_read, attn_paged_kv8_fwd), the pages of a cache (attn_pages_*),
+ * attention of sequences that share a prefix (attn_paged_prefix_fwd) and rotary
+ * positions (attn_rope, attn_rope_axes). Each entry below states its own
+ * definition and source.
  *
  * The operation, per batch b, query head hq and query row i:
  *
@@ -538,11 +540,154 @@ ATTN_API int attn_paged_kv8_fwd(const attn_paged_shape_t* shape, int group, int 
  * ATTN_ERR_SHAPE or ATTN_ERR_HEAD_DIM. */
 ATTN_API int attn_paged_kv8_workspace_bytes(const attn_paged_shape_t* shape, size_t* bytes);
 
+/* ------------------------------------------------------------ pages of a cache
+ * (The ruDNN user guide, section 9, names a copy-on-write cache update, append;
+ * these calls are this library's form of it.)
+ *
+ * Which pages the sequences of a paged cache hold, kept on the device:
+ *   block_table [num_seqs, max_pages] int32   page of key block b of sequence s; an
+ *               entry outside [0, num_pages) (-1) names none
+ *   seq_lens [num_seqs] int32                  tokens of each sequence
+ *   refs [num_pages] int32                     entries of the table that name the page;
+ *               0: the page is free
+ * A pool begins with a table of -1, lengths and refs of 0. The calls below keep refs
+ * equal to the number of entries, whatever row numbers they are given (a row
+ * outside [0, num_seqs) is passed over). They work for every cache whose buffers
+ * are [num_pages, ...]: keys and values of any type and of every layer, 8-bit codes
+ * and their scales, latent rows.
+ *
+ * Buffers of a call: `bufs` (host array of num_bufs device pointers) and
+ * `page_bytes` (host array: bytes of one page of each), at most
+ * ATTN_PAGES_MAX_BUFFERS. Page p of buffer i is the page_bytes[i] bytes from bufs[i] +
+ * p * page_bytes[i] on. Pages whose address and size are multiples of 16 bytes move
+ * as 16-byte vectors, others by single words or bytes.
+ *
+ * Every call is asynchronous on `stream`, synchronises nothing and returns ATTN_OK or
+ * a negative ATTN_ERR_* code before any launch. The int32 arrays are device
+ * pointers, 4-byte aligned; arrays that a call writes are disjoint from its other
+ * arguments. Calls on one pool run one after another. */
+typedef struct {
+  int32_t num_seqs, max_pages, page_size, num_pages;
+} attn_pages_t;
+
+#define ATTN_PAGES_MAX_BUFFERS 1024
+
+/* attn_pages_copy - page src[i] of every buffer to page dst[i], i in [0, n).
+ * src, dst: device int32 [n]. A pair with either page outside [0, num_pages) or with
+ * src = dst is passed over. A page may be the source of several pairs; what a page
+ * holds that is the destination of two pairs, or of one and the source of another, is
+ * unspecified afterwards. One kernel for every 64 buffers. */
+ATTN_API int attn_pages_copy(int num_pages, void* const* bufs, const int64_t* page_bytes, int num_bufs,
+                             const int32_t* src, const int32_t* dst, int n, void* stream);
+
+/* attn_pages_fork - rows that go on from other rows: for each i in [0, n) sequence
+ * children[i] becomes a copy of sequence parents[i]. Its row names the parent's pages
+ * of the blocks that hold tokens (b * page_size < seq_lens[parent]) and none beyond;
+ * it takes the parent's length; the pages that its row named before are given back.
+ * No cache data moves: attn_pages_reserve copies a shared page when one of its
+ * sequences is about to write to it. parents, children: device int32 [n]; a parent
+ * may have several children; the children differ from one another and none of them
+ * is a parent in the same call (a pair of a row with itself is passed over). Where
+ * that is not kept the rows end as a mixture; refs still counts their entries. One
+ * kernel. */
+ATTN_API int attn_pages_fork(const attn_pages_t* pool, int32_t* block_table, int32_t* seq_lens, int32_t* refs,
+                             const int32_t* parents, const int32_t* children, int n, void* stream);
+
+/* attn_pages_free - sequences end: every entry of the rows seqs[0 .. n-1] (device
+ * int32) is given back (refs - 1) and becomes -1, their lengths 0. The same row twice
+ * counts once. One kernel. */
+ATTN_API int attn_pages_free(const attn_pages_t* pool, int32_t* block_table, int32_t* seq_lens, int32_t* refs,
+                             const int32_t* seqs, int n, void* stream);
+
+/* attn_pages_reserve - room for new tokens: sequence s is about to receive
+ * new_tokens[s] tokens (device int32 [num_seqs]; 0 or less: none) behind its
+ * seq_lens[s] (which the call leaves as they are; both together at most max_pages *
+ * page_size, what is more is cut off). Blocks from seq_lens[s] / page_size to the one of the
+ * last new token are then the sequence's own: taken in the order of (s, b), a block
+ *   - without a page gets the lowest-numbered free one;
+ *   - whose page other entries name too (refs > 1 at that moment) gets the
+ *     lowest-numbered free one instead, its old page loses one reference, and, where
+ *     the block already holds tokens (b * page_size < seq_lens[s]), the page is
+ *     copied, in every buffer;
+ *   - else keeps its page.
+ * result: device int32 [2]: the pages taken, and the pages that are lacking. Where
+ * the pool has too few free pages, nothing is changed and result is 0 and their
+ * number: free a sequence and call again.
+ * workspace: attn_pages_workspace_bytes(pool) bytes, 16-byte aligned, caller-owned, its
+ * contents of no meaning before or after. 1 + ceil(num_bufs / 64) kernels. */
+ATTN_API int attn_pages_reserve(const attn_pages_t* pool, int32_t* block_table, const int32_t* seq_lens,
+                                int32_t* refs, const int32_t* new_tokens,
+                                void* const* bufs, const int64_t* page_bytes, int num_bufs, int32_t* result,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* attn_pages_compact - moves the pages in use to the low end of the pool: with U pages
+ * in use (refs > 0), the i-th free page below U receives the i-th page in use from U
+ * on, in every buffer; refs and the table follow. Pages from U on keep their bytes
+ * and are free.
+ * page_map: device int32 [num_pages], where each page now is (its own number if it
+ * stayed, -1 for a page that was free). used: device int32 [1], U. workspace as for
+ * attn_pages_reserve. 1 + max(1, ceil(num_bufs / 64)) kernels. */
+ATTN_API int attn_pages_compact(const attn_pages_t* pool, int32_t* block_table, int32_t* refs,
+                                void* const* bufs, const int64_t* page_bytes, int num_bufs,
+                                int32_t* page_map, int32_t* used,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* attn_pages_workspace_bytes - workspace of attn_pages_reserve and
+ * attn_pages_compact: 3 num_pages + 3 num_seqs + 8 ints, each array rounded up to 16
+ * bytes. Returns ATTN_OK, ATTN_ERR_NULL or ATTN_ERR_SHAPE. */
+ATTN_API int attn_pages_workspace_bytes(const attn_pages_t* pool, size_t* bytes);
+
+/* ------------------------------------------------------------ a shared prefix
+ * attn_paged_prefix_fwd - attn_paged_fwd for a batch in which groups of sequences
+ * begin with the same tokens (a system prompt, a document with many questions, the
+ * answers to one request): the keys and values that a group shares are read once
+ * for all of its queries. (The pages have no counterpart.)
+ *
+ * Group g is the sequences group_offsets[g] .. group_offsets[g+1]-1 (device int32
+ * [num_groups + 1], clamped to [0, num_seqs], not decreasing), and their first
+ * prefix_lens[g] tokens (device int32 [num_groups]) are the same: each row of the
+ * table names pages that hold them, the same pages or copies (a prefix may end inside
+ * a page), and the call reads them through the row of any member. A sequence of no
+ * group, or one with fewer tokens than the prefix, is right too. Everything else is as for
+ * attn_paged_fwd: the shape, packed queries, positions (NULL: the newest), the causal
+ * mask, rows that see no key (NaN, lse -inf), pages outside the cache (zero keys
+ * and values), query rows of no sequence (not written), lse. attn_paged_bwd takes the
+ * results: it sums the gradients of a page over all that read it.
+ *
+ * With the prefix's part and the sequence's own part of a row's softmax,
+ *   M = max(m_a, m_b),  l = 2^(m_a - M) l_a + 2^(m_b - M) l_b,
+ *   out = (2^(m_a - M) O_a + 2^(m_b - M) O_b) / l;
+ * parts are summed in fp32 and joined in a fixed order: repeated calls give identical
+ * bits. F16/BF16 kernels round the probabilities to the input type before they meet
+ * the values, as attn_paged_fwd's do.
+ *
+ * max_group_queries: an upper bound on the queries of one group (as max_queries for
+ * one sequence: it sizes the grid; rows beyond a bound that is too small get
+ * unspecified values). D in {16, 32, 64, 128}, every dtype, any page size.
+ * workspace: attn_paged_prefix_workspace_bytes bytes, 16-byte aligned, caller-owned,
+ * disjoint from every other buffer, its contents of no meaning before or after; calls
+ * in flight at once need one each. */
+ATTN_API int attn_paged_prefix_fwd(const attn_paged_shape_t* shape, int num_groups, int max_group_queries,
+                                   const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_table, const int32_t* seq_lens,
+                                   const int32_t* q_offsets, const int32_t* positions,
+                                   const int32_t* group_offsets, const int32_t* prefix_lens,
+                                   int causal, float scale, attn_dtype_t dtype,
+                                   void* workspace, size_t workspace_bytes,
+                                   void* out, float* lse,
+                                   void* stream);
+
+/* attn_paged_prefix_workspace_bytes - workspace attn_paged_prefix_fwd needs (every
+ * dtype). Returns ATTN_OK, ATTN_ERR_NULL, ATTN_ERR_SHAPE or ATTN_ERR_HEAD_DIM. */
+ATTN_API int attn_paged_prefix_workspace_bytes(const attn_paged_shape_t* shape, int num_groups,
+                                               int max_group_queries, size_t* bytes);
+
 /* ------------------------------------------------------------ rotary positions
  * Layouts of the pairs in the first `rot` elements of a head: pair i is
  * elements i and i + rot/2 (HALF), or 2i and 2i + 1 (INTERLEAVED). */
 enum { ATTN_ROPE_HALF = 0, ATTN_ROPE_INTERLEAVED = 1 };
 #define ATTN_ROPE_MAX_D 512
+#define ATTN_ROPE_MAX_AXES 256
 
 /* q [B, S, Hq, D] and k [B, S, Hk, D] by strides: elements from batch to batch,
  * token to token and head to head, 0 or more each; a head's D elements lie side
@@ -580,6 +725,22 @@ ATTN_API int attn_rope(const attn_rope_shape_t* shape, const void* q, const void
                        int layout, int inverse, float mscale, attn_dtype_t dtype,
                        void* q_out, void* k_out,
                        void* stream);
+
+/* attn_rope_axes - attn_rope for tokens that lie on a grid (time, height and width of
+ * a video, rows and columns of an image): pair i of a token turns by
+ *   a = positions[axis[i]][token] * inv_freq[i].
+ * axis: device int32 [rot/2], 4-byte aligned, the axis of each pair; a pair whose axis lies
+ * outside [0, num_axes) is not turned (a = 0; mscale applies). positions: num_axes
+ * (1 .. ATTN_ROPE_MAX_AXES) arrays as attn_rope takes them, pos_axis_stride elements
+ * apart (0 or more; the arrays may overlap one another). Text tokens have the same position on
+ * every axis and turn as in attn_rope. Everything else is as for attn_rope,
+ * inverse = 1 the gradient. */
+ATTN_API int attn_rope_axes(const attn_rope_shape_t* shape, const void* q, const void* k,
+                            const int32_t* positions, int64_t pos_axis_stride, int num_axes,
+                            const int32_t* axis, const double* inv_freq,
+                            int layout, int inverse, float mscale, attn_dtype_t dtype,
+                            void* q_out, void* k_out,
+                            void* stream);
 
 /* Size of the device scratch array built into the library for
  * attn_fwd_split_noalloc (32 MiB per GPU that loads the library). */
