@@ -193,7 +193,6 @@ namespace {
 using attn::aligned;
 using attn::Buf;
 using attn::meet;
-using attn::prefix::Plan;
 
 int check_shape(const attn_paged_shape_t& s, int num_groups, int max_group_queries) {
   if (s.num_seqs < 0 || s.num_queries < 0 || s.Hq <= 0 || s.Hkv <= 0 || s.D <= 0 || s.page_size <= 0 ||
@@ -215,21 +214,43 @@ int check_shape(const attn_paged_shape_t& s, int num_groups, int max_group_queri
   return ATTN_OK;
 }
 
-// Parts of a row: as many as fill the SMs when one group has all the queries.
+// How a call runs and lays out its workspace.
+struct Plan {
+  int most_parts = 1;                 // parts of a row's prefix
+  int prefix_nt = 0, suffix_nt = 0;   // few-row kernels: 8-row groups of a CTA
+  int ranges = 0;                     // of the suffix stage
+  int64_t ml_offset = 0, o_offset = 0, cut_ml_offset = 0, cut_o_offset = 0, counter_offset = 0, bytes = 0;
+};
+
 Plan plan_of(const attn_paged_shape_t& s, int num_groups, int max_group_queries) {
+  using namespace attn::prefix;
   Plan d;
-  if (num_groups == 0 || s.num_queries == 0 || max_group_queries == 0) return d;
-  const int64_t rows = static_cast<int64_t>(s.num_queries) * s.Hq;
-  const int64_t units = s.Hkv * ((static_cast<int64_t>(std::min(max_group_queries, s.num_queries)) * (s.Hq / s.Hkv) + 63) / 64);
-  const int64_t tiles = (static_cast<int64_t>(s.max_pages) * s.page_size + 127) / 128;
-  const int64_t parts = std::min<int64_t>({attn::prefix::MAX_PARTS, (attn::SMS + units - 1) / units, std::max<int64_t>(tiles, 1)});
-  d.most_parts = static_cast<int>(parts);
+  const int64_t heads = s.Hq / s.Hkv, rows = static_cast<int64_t>(s.num_queries) * s.Hq;
+  const int64_t group_rows = std::min(max_group_queries, s.num_queries) * heads;
+  d.prefix_nt = rows::nt_of(group_rows);
+  d.suffix_nt = rows::nt_of(s.max_queries * heads);
+  // A row's prefix is cut into as many parts as its group's CTAs can be, and not into more than 64 MB
+  // of workspace; the parts that a call uses are settled on the device.
+  const int64_t ctas = static_cast<int64_t>(attn::SMS) * rows::ctas_of_sm(s.D, d.prefix_nt);
+  const int64_t units = s.Hkv * (num_groups == 1 ? std::max<int64_t>(1, (group_rows + 255) / 256) : 1);
+  const int64_t room = (64ll << 20) / std::max<int64_t>(1, rows * (4 * s.D + 8));
+  d.most_parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({MAX_PARTS, (ctas + units - 1) / units, room})));
+  const int suffix_ctas = attn::SMS * rows::ctas_of_sm(s.D, d.suffix_nt);
+  d.ranges = std::max(1, suffix_ctas / s.Hkv);
   auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
+  const int64_t parts = num_groups > 0 && max_group_queries > 0 ? d.most_parts : 0;
+  const int64_t slots = 2ll * d.ranges * s.Hkv * 8 * d.suffix_nt;
   d.ml_offset = up(num_groups * 4ll);
   d.o_offset = up(d.ml_offset + parts * rows * 8);
-  d.bytes = d.o_offset + parts * rows * s.D * 4;
+  d.cut_ml_offset = d.o_offset + parts * rows * s.D * 4;
+  d.cut_o_offset = up(d.cut_ml_offset + slots * 8);
+  d.counter_offset = d.cut_o_offset + slots * s.D * 4;
+  d.bytes = d.counter_offset + up(4ll * d.ranges * s.Hkv);
   return d;
 }
+
+// Shapes of the 16-bit kernels.
+bool takes_rows(const attn_paged_shape_t& s) { return (s.D == 64 || s.D == 128) && s.num_pages > 0; }
 
 }  // namespace
 
@@ -316,6 +337,21 @@ extern "C" int attn_paged_prefix_fwd(const attn_paged_shape_t* shape, int num_gr
   p.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan.ml_offset);
   p.o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.o_offset);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype != ATTN_F32 && takes_rows(s)) {
+    uint8_t* const ws = static_cast<uint8_t*>(workspace);
+    const attn::prefix::rows::Cuts cuts{reinterpret_cast<float*>(ws + plan.cut_o_offset),
+                                        reinterpret_cast<float2*>(ws + plan.cut_ml_offset),
+                                        reinterpret_cast<int*>(ws + plan.counter_offset)};
+    const bool bf16 = dtype == ATTN_BF16;
+    const int counters = plan.ranges * s.Hkv;
+    using namespace attn::prefix::rows;
+    e = bf16 ? launch_prefix<true>(p, plan.prefix_nt, cuts.counters, counters, st)
+             : launch_prefix<false>(p, plan.prefix_nt, cuts.counters, counters, st);
+    if (e == cudaSuccess)
+      e = bf16 ? launch_suffix<true>(p, plan.suffix_nt, cuts, plan.ranges, st)
+               : launch_suffix<false>(p, plan.suffix_nt, cuts, plan.ranges, st);
+    return e == cudaSuccess ? ATTN_OK : attn::record_cuda_error(e);
+  }
   e = dtype == ATTN_F32 ? attn::prefix::launch_dt<0>(p, st)
       : dtype == ATTN_F16 ? attn::prefix::launch_dt<1>(p, st) : attn::prefix::launch_dt<2>(p, st);
   return e == cudaSuccess ? ATTN_OK : attn::record_cuda_error(e);

@@ -1,0 +1,10 @@
+// attn_prefix_rows_suffix_f16.cu - the few-row suffix stage for F16 (prefix_rows.cuh).
+#include "prefix_rows.cuh"
+
+namespace attn {
+namespace prefix {
+namespace rows {
+template cudaError_t launch_suffix<false>(const Params&, int, const Cuts&, int, cudaStream_t);
+}  // namespace rows
+}  // namespace prefix
+}  // namespace attn

@@ -12,6 +12,8 @@
 //           joins its own part with those of the prefix and writes out and lse.
 #pragma once
 
+#include <atomic>
+
 #include "host_checks.h"
 #include "params.h"
 #include "ptx.cuh"
@@ -109,11 +111,45 @@ __device__ __forceinline__ int reader_of(const Params& p, int a, int b, int pre)
   return static_cast<int>(~static_cast<uint32_t>(best));
 }
 
-// How the rows' parts are laid out in the workspace, on the host.
-struct Plan {
-  int most_parts = 0;
-  int64_t ml_offset = 0, o_offset = 0, bytes = 0;
+// Opts a kernel in to `smem` bytes of shared memory, once for each device.
+template <typename K>
+cudaError_t allow_smem(K kern, int smem, int device, std::atomic<unsigned long long>& configured) {
+  const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0ull;
+  if (bit && (configured.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) configured.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
+
+// ------------------------------------------------------------------ few rows (prefix_rows.cuh)
+namespace rows {
+
+constexpr int WARPS = 4;
+constexpr int THREADS = WARPS * 32;
+constexpr int BLOCK = 16 * WARPS;  // keys of a block: 16 a warp
+constexpr int LEAST_BLOCKS = 4;    // of a range
+
+// CTAs of an SM: what the shared memory holds, and enough registers for the outputs.
+__host__ __device__ constexpr int ctas_of_sm(int D, int nt) { return D == 128 ? 2 : nt <= 2 ? 4 : 3; }
+
+// Groups of 8 rows that a CTA takes.
+inline int nt_of(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }
+
+// Workspace of the sequences that are cut: CTA c (range, head) owns slots 2c (its first unit) and
+// 2c + 1 (its last), each 8 nt x D floats and 8 nt (m, l); a counter for each CTA.
+struct Cuts {
+  float* o;
+  float2* ml;
+  int* counters;
 };
+
+// counters: cleared by the prefix stage, which is always launched before the suffix stage.
+template <bool BF16>
+cudaError_t launch_prefix(const Params& p, int nt, int* counters, int num_counters, cudaStream_t st);
+template <bool BF16>
+cudaError_t launch_suffix(const Params& p, int nt, const Cuts& cuts, int ranges, cudaStream_t st);
+
+}  // namespace rows
 
 }  // namespace prefix
 }  // namespace attn

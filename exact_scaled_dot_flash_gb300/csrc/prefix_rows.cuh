@@ -1,0 +1,750 @@
+// prefix_rows.cuh - both stages of attn_paged_prefix_fwd (prefix.cuh) for few rows, at most 32
+// a CTA: decode steps and drafted tokens behind a prefix, and the prefixes of small
+// groups (F16/BF16, D in {64, 128}, any page size).
+//
+// Bound: the bytes of the keys and values, read once for all the rows of a kv head.
+// A warp streams its own 16-key tiles through three buffers of cp.async copies in shared
+// memory, without a barrier between warps:
+//  - S^T = K Q^T (keys x rows), then O^T = V^T P^T, by mma.sync with the cache as the A
+//    operand, so that 8 columns hold the rows instead of 16 or 128; K by ldmatrix, V by its
+//    transposing form, P^T from S^T by one movmatrix for 8 keys x 8 rows;
+//  - a row has a reference exponent: y = 2^(x - ref), and ref moves up only when a y passes
+//    2^15 (one vote a tile instead of a reduction), to bring the largest y to 2^8. F16
+//    probabilities then keep their full precision down to 2^-22 of the largest.
+//
+// Suffix stage: the keys of all sequences, in blocks of 64 (16 a warp), are cut into ranges
+// of equal length, one for each group of Hkv CTAs (one a head, side by side). A CTA walks the
+// sequences of its range; a sequence wholly inside it is joined with its prefix's parts
+// and written out, a cut one leaves parts, and the CTA that finishes the last of them (a
+// counter that the prefix stage has cleared) joins all in the order of the ranges.
+// Prefix stage: a group's keys are cut into parts of one length for all groups, the
+// shortest that the grid's CTAs can take at once; a CTA takes a part for 32 rows and a head.
+#pragma once
+
+#include "prefix.cuh"
+
+namespace attn {
+namespace prefix {
+namespace rows {
+
+constexpr int TILE = 16;                  // keys of a warp's tile
+constexpr int STAGES = 3;
+constexpr float UNSEEN = -3e38f;          // reference of a row without keys: its first one passes every range
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D, int NT>
+struct Shared {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int TILE_BYTES = TILE * D * 2;             // K or V
+  static constexpr int RING = WARPS * STAGES * 2 * TILE_BYTES;
+  static constexpr int ROW = D + 4;
+  static constexpr int O = WARPS * ROWS * ROW * 4;            // the warps' outputs, in the ring's place
+  static constexpr int OFF_ML = RING > O ? RING : O;
+  static constexpr int OFF_LIM = OFF_ML + WARPS * ROWS * 8;
+  static constexpr int OFF_Q = OFF_LIM + ROWS * 4;            // query operands, in the lanes' order
+  static constexpr int BYTES = OFF_Q + NT * (D / 16) * 32 * 8;
+};
+
+// A CTA's piece of a unit: rows (queries from q_lo on, `nq` of them, times heads; row_lo the
+// first of R rows), keys [from, to), read through row `table` of the table.
+struct Piece {
+  int q_lo, row_lo, R, h, table, from, to;
+};
+
+// The parts of the softmax of the piece's rows: streams the keys and leaves the warps'
+// parts in shared memory (so, sml). The whole CTA calls it. lims: keys each row sees.
+template <int D, bool BF16, int NT>
+__device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t* smem) {
+  constexpr int KS = D / 16;       // 16-element steps of a head
+  constexpr int ROWS = 8 * NT;
+  using SH = Shared<D, NT>;
+  float* const so = reinterpret_cast<float*>(smem);
+  float2* const sml = reinterpret_cast<float2*>(smem + SH::OFF_ML);
+  const int* const lims = reinterpret_cast<const int*>(smem + SH::OFF_LIM);
+  uint2* const sq = reinterpret_cast<uint2*>(smem + SH::OFF_Q);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int heads = p.Hq / p.Hkv;
+  int* const status = p.status;
+  const int64_t nrows = static_cast<int64_t>(p.num_queries) * p.Hq;
+
+  // query operands: of 8 rows by warp: lane (g, t) holds elements 16 k + 2 t, + 1 and + 8, + 9 of row g
+  for (int i = warp; i < NT; i += WARPS) {
+    const int row = 8 * i + g;
+    const uint32_t* src = nullptr;
+    if (row < w.R) {
+      const int q = (w.row_lo + row) / heads;
+      const int64_t at = static_cast<int64_t>(w.q_lo + q) * p.Hq + w.h * heads + (w.row_lo + row - q * heads);
+      if (in_bounds(status, at, nrows)) src = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) + at * D);
+    }
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+      sq[(i * KS + k) * 32 + lane] = src ? make_uint2(__ldg(src + 8 * k + t), __ldg(src + 8 * k + 4 + t)) : make_uint2(0u, 0u);
+  }
+  __syncthreads();
+  uint2 qf[NT == 1 ? KS : 1];
+  if constexpr (NT == 1) {
+#pragma unroll
+    for (int k = 0; k < KS; ++k) qf[k] = sq[k * 32 + lane];
+  }
+  int lim[NT][2];  // keys that the lane's rows (8 i + 2 t, + 1) see
+  int least = w.to, most = 0;
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = 8 * i + 2 * t + e;
+      lim[i][e] = min(lims[row], w.to);
+      if (row < w.R) {
+        least = min(least, lim[i][e]);
+        most = max(most, lim[i][e]);
+      }
+    }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  }
+
+  float ref[NT][2], l[NT][2], acc[KS][NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    ref[i][0] = ref[i][1] = UNSEEN;
+    l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) acc[k][i][0] = acc[k][i][1] = acc[k][i][2] = acc[k][i][3] = 0.f;
+  }
+  constexpr int PIECES = D / 8;          // 16-byte pieces of a key
+  constexpr int RPC = 32 / PIECES;       // keys that one copy of the warp covers
+  const uint32_t ring = smem_u32(smem) + warp * STAGES * 2 * SH::TILE_BYTES;
+  const int64_t ntok = static_cast<int64_t>(p.num_pages) * p.page_size;
+  const int64_t step = static_cast<int64_t>(p.Hkv) * D * 2;  // bytes from token to token
+  const uint8_t* const kb = static_cast<const uint8_t*>(p.k) + (w.h * D + lane % PIECES * 8) * 2;
+  const uint8_t* const vb = static_cast<const uint8_t*>(p.v) + (w.h * D + lane % PIECES * 8) * 2;
+  // The lane's key of the tile to copy next: its block and the row in it.
+  int ckey = w.from + warp * TILE + (lane & (TILE - 1));
+  const int tile0 = w.from + warp * TILE;
+  int cfirst = tile0;
+  int blk = ckey / p.page_size, row = ckey - blk * p.page_size;
+  const int dblk = BLOCK / p.page_size, drow = BLOCK - dblk * p.page_size;
+  auto find_page = [&]() { return ckey < most ? page_of(p, w.table, blk) : -1; };
+  int page = find_page();
+  auto copy_tile = [&](int stage) {
+    if (cfirst < most) {
+      const int64_t tok = static_cast<int64_t>(page) * p.page_size + row;
+      const int64_t mine = page >= 0 && in_bounds(status, tok, ntok) ? tok : -1;  // -1: zeros
+      const uint32_t at = ring + stage * 2 * SH::TILE_BYTES;
+#pragma unroll
+      for (int j = 0; j < TILE / RPC; ++j) {
+        const int r = RPC * j + lane / PIECES, c = lane % PIECES;
+        const int64_t key = __shfl_sync(0xffffffffu, mine, r);
+        const int n = key < 0 ? 0 : 16;
+        const int64_t off = (key < 0 ? 0 : key) * step;
+        const uint32_t to = at + (r * PIECES + (c ^ (r & 7))) * 16;
+        copy16(to, kb + off, n);
+        copy16(to + SH::TILE_BYTES, vb + off, n);
+      }
+    }
+    copy_commit();
+    cfirst += BLOCK;
+    ckey += BLOCK;
+    blk += dblk;
+    row += drow;
+    if (row >= p.page_size) {
+      row -= p.page_size;
+      ++blk;
+    }
+    page = find_page();
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) copy_tile(i);
+  int stage = 0;
+  // ldmatrix addresses: K rows (lane & 15), piece 2 k + lane / 16; V rows (lane & 7) + 8 (lane / 16), piece 2 k + lane / 8 % 2
+  const int kr = lane & 15, vr = (lane & 7) + ((lane >> 4) << 3);
+  for (int key0 = tile0; key0 < most; key0 += BLOCK) {
+    copy_wait<STAGES - 2>();
+    __syncwarp();  // the tile's copies of every lane; and every lane is done with the tile before
+    copy_tile(stage == 0 ? STAGES - 1 : stage - 1);
+    const uint32_t ka = ring + stage * 2 * SH::TILE_BYTES, va = ka + SH::TILE_BYTES;
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
+    float sc[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      uint32_t a[4];
+      ldsm4(a, ka + (kr * PIECES + ((2 * k + (lane >> 4)) ^ (kr & 7))) * 16);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        if constexpr (NT == 1) {
+          mma16816<BF16>(sc[i], a, qf[k].x, qf[k].y);
+        } else {
+          const uint2 b = sq[(i * KS + k) * 32 + lane];
+          mma16816<BF16>(sc[i], a, b.x, b.y);
+        }
+      }
+    }
+    const bool masked = key0 + TILE > least;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sc[i][e] *= p.scale_log2;
+        if (masked && key0 + g + (e & 2) * 4 >= lim[i][e & 1]) sc[i][e] = -INFINITY;
+      }
+    float y[NT][4], big = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[i][e] = fast_exp2(sc[i][e] - ref[i][e & 1]);
+      big = fmax3(big, y[i][0], y[i][1]);
+      big = fmax3(big, y[i][2], y[i][3]);
+    }
+    if (__any_sync(0xffffffffu, big > 32768.f)) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(sc[i][e], sc[i][2 + e]);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+          const float n = x == -INFINITY ? ref[i][e] : fmaxf(ref[i][e], x - 8.f);
+          const float f = fast_exp2(ref[i][e] - n);
+          ref[i][e] = n;
+          l[i][e] *= f;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            acc[k][i][e] *= f;
+            acc[k][i][2 + e] *= f;
+          }
+          y[i][e] = fast_exp2(sc[i][e] - n);
+          y[i][2 + e] = fast_exp2(sc[i][2 + e] - n);
+        }
+    }
+    uint32_t pf[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      l[i][0] += y[i][0] + y[i][2];
+      l[i][1] += y[i][1] + y[i][3];
+      pf[i][0] = transpose8x8(pack2<BF16>(y[i][0], y[i][1]));
+      pf[i][1] = transpose8x8(pack2<BF16>(y[i][2], y[i][3]));
+    }
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      uint32_t a[4];
+      ldsm4_t(a, va + (vr * PIECES + ((2 * k + ((lane >> 3) & 1)) ^ (vr & 7))) * 16);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) mma16816<BF16>(acc[k][i], a, pf[i][0], pf[i][1]);
+    }
+  }
+  copy_wait<0>();
+  __syncthreads();  // the ring's place takes the warps' parts
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], o);
+      const int r = 8 * i + 2 * t + e;
+      // a warp without keys has no reference
+      if (g == 0) sml[warp * ROWS + r] = make_float2(l[i][e] == 0.f ? -INFINITY : ref[i][e], l[i][e]);
+      float* const o = so + (warp * ROWS + r) * SH::ROW + g;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        o[16 * k] = acc[k][i][e];
+        o[16 * k + 8] = acc[k][i][2 + e];
+      }
+    }
+  __syncthreads();
+}
+
+// A row's running part: 4 elements of O, relative to 2^M.
+struct Part {
+  float M = -INFINITY, sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(float2 ml, float4 x) {
+    const float n = fmaxf(M, ml.x);
+    const float f = n == -INFINITY ? 0.f : fast_exp2(M - n), e = n == -INFINITY ? 0.f : fast_exp2(ml.x - n);
+    M = n;
+    sum = sum * f + ml.y * e;
+    o = make_float4(o.x * f + x.x * e, o.y * f + x.y * e, o.z * f + x.z * e, o.w * f + x.w * e);
+  }
+};
+
+// Of row r of the piece, elements 4 d4 ..: the warps' parts together.
+template <int D, int NT>
+__device__ __forceinline__ Part of_warps(const uint8_t* smem, int r, int d4) {
+  constexpr int ROWS = 8 * NT;
+  using SH = Shared<D, NT>;
+  const float* const so = reinterpret_cast<const float*>(smem);
+  const float2* const sml = reinterpret_cast<const float2*>(smem + SH::OFF_ML);
+  Part a;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w)
+    a.add(sml[w * ROWS + r], *reinterpret_cast<const float4*>(so + (w * ROWS + r) * SH::ROW + 4 * d4));
+  return a;
+}
+
+// Adds the prefix's parts of a row (n of them), BATCH read together: each read is a trip to L2.
+template <int D>
+__device__ __forceinline__ void add_prefix(const Params& p, Part& a, int64_t row, int d4, int n) {
+  constexpr int BATCH = 4;
+  const int64_t rows = static_cast<int64_t>(p.num_queries) * p.Hq;
+  for (int z0 = 0; z0 < n; z0 += BATCH) {
+    float2 ml[BATCH];
+    float4 x[BATCH];
+#pragma unroll
+    for (int z = 0; z < BATCH; ++z) {
+      const int64_t at = (z0 + z) * rows + row;
+      const bool is = z0 + z < n && in_bounds(p.status, at, p.most_parts * rows);
+      ml[z] = is ? __ldcg(p.ml + at) : make_float2(-INFINITY, 0.f);
+      x[z] = is ? __ldcg(reinterpret_cast<const float4*>(p.o) + at * (D / 4) + d4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int z = 0; z < BATCH; ++z) a.add(ml[z], x[z]);
+  }
+}
+
+template <int D, bool BF16>
+__device__ __forceinline__ void write_out(const Params& p, const Part& a, int64_t row, int d4) {
+  if (!in_bounds(p.status, row, static_cast<int64_t>(p.num_queries) * p.Hq)) return;
+  const bool live = a.sum > 0.f;
+  const float inv = live ? 1.f / a.sum : __int_as_float(0x7fc00000);
+  reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D)[d4] =
+      make_uint2(pack2<BF16>(a.o.x * inv, a.o.y * inv), pack2<BF16>(a.o.z * inv, a.o.w * inv));
+  if (p.lse && d4 == 0) p.lse[row] = live ? (a.M + log2f(a.sum)) * LN2 : (a.sum == 0.f ? -INFINITY : a.sum);
+}
+
+// ------------------------------------------------------------------ prefix stage
+// Blocks of keys (of `block`) and of rows (of `rows`) of a group.
+__device__ __forceinline__ void group_work(const Params& p, int g, int block, int rows, int& key_blocks, int& row_blocks) {
+  int a, b;
+  group_range(p, g, a, b);
+  const int nq = a < b ? max(query_at(p, b) - query_at(p, a), 0) : 0;
+  row_blocks = static_cast<int>((static_cast<int64_t>(nq) * (p.Hq / p.Hkv) + rows - 1) / rows);
+  key_blocks = (prefix_len(p, g) + block - 1) / block;
+  if (key_blocks == 0 || row_blocks == 0) key_blocks = row_blocks = 0;
+}
+
+struct Item {
+  int g, part, parts, rb, h, chunk;  // g < 0: none
+  int64_t total;                     // items of all
+};
+
+// Item number `item` of the prefix stage for a grid of `ctas`. A warp calls it.
+__device__ __forceinline__ Item item_of(const Params& p, int64_t item, int ctas, int block, int rows) {
+  const int lane = threadIdx.x & 31;
+  auto warp_sum = [](int64_t x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+  };
+  // the lane's group stays in registers where there are no more than lanes
+  int kb0 = 0, rb0 = 0, longest = 0;
+  if (lane < p.num_groups) group_work(p, lane, block, rows, kb0, rb0);
+  for (int g = lane; g < p.num_groups; g += 32) {
+    int kb = kb0, rb = rb0;
+    if (g >= 32) group_work(p, g, block, rows, kb, rb);
+    longest = max(longest, kb);
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  // the shortest part with which the items fit the grid (and a row's parts the workspace)
+  int lo = max(1, (longest + p.most_parts - 1) / p.most_parts), hi = max(longest, 1);
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    int64_t n = 0;
+    for (int g = lane; g < p.num_groups; g += 32) {
+      int kb = kb0, rb = rb0;
+      if (g >= 32) group_work(p, g, block, rows, kb, rb);
+      n += static_cast<int64_t>((kb + mid - 1) / mid) * rb;
+    }
+    if (warp_sum(n) * p.Hkv <= ctas) hi = mid;
+    else lo = mid + 1;
+  }
+  int64_t all = 0;
+  for (int g = lane; g < p.num_groups; g += 32) {
+    int kb = kb0, rb = rb0;
+    if (g >= 32) group_work(p, g, block, rows, kb, rb);
+    all += static_cast<int64_t>((kb + lo - 1) / lo) * rb;
+  }
+  Item it{-1, 0, 0, 0, 0, lo, warp_sum(all) * p.Hkv};
+  int64_t before = 0;
+  for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
+    const int g = g0 + lane;
+    int kb = kb0, rb = rb0;
+    if (g0 > 0) {
+      kb = rb = 0;
+      if (g < p.num_groups) group_work(p, g, block, rows, kb, rb);
+    }
+    const int parts = (kb + lo - 1) / lo;
+    const int64_t mine = static_cast<int64_t>(parts) * rb * p.Hkv;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + incl > item);
+    if (past) {
+      const int who = __ffs(past) - 1;
+      it.g = g0 + who;
+      it.parts = __shfl_sync(0xffffffffu, parts, who);
+      const int rbs = __shfl_sync(0xffffffffu, rb, who);
+      int64_t r = item - before - __shfl_sync(0xffffffffu, incl - mine, who);
+      it.h = static_cast<int>(r % p.Hkv);
+      r /= p.Hkv;
+      it.rb = static_cast<int>(r % rbs);
+      it.part = static_cast<int>(r / rbs);
+      return it;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return it;
+}
+
+// Each row's limit of a group's rows (row_lo on), into shared memory.
+__device__ __forceinline__ void group_limits(const Params& p, int a, int b, int q_lo, int row_lo, int R, int rows, int* lims) {
+  const int heads = p.Hq / p.Hkv;
+  for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+    int x = 0;
+    if (r < R) {
+      const int i = q_lo + (row_lo + r) / heads;
+      x = limit_of(p, last_at_most(p.q_offsets, a, b, i), i);
+    }
+    lims[r] = x;
+  }
+}
+
+template <int D, bool BF16, int NT>
+__global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT)) prefix_kernel(const __grid_constant__ Params p, int* counters, int num_counters) {
+  asm volatile("griddepcontrol.launch_dependents;");  // the suffix stage may come up: it waits before it reads
+  constexpr int ROWS = 8 * NT;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Item shared_item;
+  using SH = Shared<D, NT>;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i < num_counters; i += static_cast<int64_t>(gridDim.x) * THREADS)
+    counters[i] = 0;
+  for (int64_t n = blockIdx.x;; n += gridDim.x) {
+    if (threadIdx.x < 32) {
+      const Item x = item_of(p, n, gridDim.x, BLOCK, ROWS);
+      if (threadIdx.x == 0) shared_item = x;
+    }
+    __syncthreads();
+    const Item it = shared_item;
+    if (it.g < 0) return;
+    int a, b;
+    group_range(p, it.g, a, b);
+    const int pre = prefix_len(p, it.g), heads = p.Hq / p.Hkv;
+    Piece w;
+    w.q_lo = query_at(p, a);
+    w.row_lo = it.rb * ROWS;
+    const int64_t left = static_cast<int64_t>(query_at(p, b) - w.q_lo) * heads - w.row_lo;
+    w.R = static_cast<int>(min(left, static_cast<int64_t>(ROWS)));
+    w.h = it.h;
+    w.from = it.part * it.chunk * BLOCK;
+    w.to = min(pre, w.from + it.chunk * BLOCK);
+    group_limits(p, a, b, w.q_lo, w.row_lo, w.R, ROWS, reinterpret_cast<int*>(smem + SH::OFF_LIM));
+    w.table = reader_of(p, a, b, pre);
+    if (it.part == 0 && it.rb == 0 && it.h == 0 && threadIdx.x == 0) p.parts[it.g] = it.parts;
+    stream<D, BF16, NT>(p, w, smem);
+    const int64_t rows = static_cast<int64_t>(p.num_queries) * p.Hq;
+    for (int e = threadIdx.x; e < w.R * (D / 4); e += THREADS) {
+      const int r = e / (D / 4), d4 = e - r * (D / 4);
+      const Part x = of_warps<D, NT>(smem, r, d4);
+      const int q = (w.row_lo + r) / heads;
+      const int64_t at = it.part * rows + static_cast<int64_t>(w.q_lo + q) * p.Hq + w.h * heads + (w.row_lo + r - q * heads);
+      if (!in_bounds(p.status, at, p.most_parts * rows)) continue;
+      reinterpret_cast<float4*>(p.o)[at * (D / 4) + d4] = x.o;
+      if (d4 == 0) p.ml[at] = make_float2(x.M, x.sum);
+    }
+    if (n + gridDim.x >= it.total) return;
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ suffix stage
+// Keys of sequence s that are its own: [start, L); `pre`: tokens its group shares.
+struct Own {
+  int group, pre, start, L;
+};
+
+__device__ __forceinline__ Own own_of(const Params& p, int s) {
+  Own o;
+  o.L = seq_len(p, s);
+  o.group = group_of(p, s);
+  o.pre = o.group >= 0 ? prefix_len(p, o.group) : 0;
+  o.start = min(o.pre, o.L);
+  return o;
+}
+
+__device__ __forceinline__ int key_blocks(int n) { return max(1, (n + BLOCK - 1) / BLOCK); }  // without keys: one
+
+__device__ __forceinline__ int row_blocks(const Params& p, int nq, int rows) {
+  return static_cast<int>((static_cast<int64_t>(nq) * (p.Hq / p.Hkv) + rows - 1) / rows);
+}
+
+// First block of range r.
+__device__ __forceinline__ int64_t cut(int64_t total, int r, int ranges) { return total * r / ranges; }
+
+// Blocks in the order (sequence, row block, key block). The whole CTA calls it.
+struct Place {
+  int64_t total, at;  // blocks of all; first block of the unit that range begins in
+  int s, rb, ranges;
+};
+
+template <int ROWS>
+__device__ __forceinline__ Place locate(const Params& p, int range, int ranges, int least, int64_t& u0, int64_t& u1) {
+  __shared__ int64_t warp_sum[THREADS / 32];
+  __shared__ int64_t found_at;
+  __shared__ int found_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.num_seqs + THREADS - 1) / THREADS;
+  const int s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
+  auto blocks = [&](int s) -> int64_t {
+    const int nq = query_at(p, s + 1) - query_at(p, s);
+    if (nq <= 0) return 0;
+    const Own o = own_of(p, s);
+    return static_cast<int64_t>(key_blocks(o.L - o.start)) * row_blocks(p, nq, ROWS);
+  };
+  int64_t mine = 0;
+  for (int s = s0; s < s1; ++s) mine += blocks(s);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  if (tid == 0) {
+    found_at = 0;
+    found_s = 0;
+  }
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  Place pl;
+  pl.total = total;
+  // no more ranges than leave `least` blocks to each
+  pl.ranges = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(ranges), total / least)));
+  u0 = range < pl.ranges ? cut(total, range, pl.ranges) : total;
+  u1 = range < pl.ranges ? cut(total, range + 1, pl.ranges) : total;
+  if (u0 >= before && u0 < before + mine) {
+    int s = s0;
+    int64_t at = before;
+    for (; s < s1; ++s) {
+      const int64_t n = blocks(s);
+      if (u0 < at + n) break;
+      at += n;
+    }
+    found_at = at;
+    found_s = s;
+  }
+  __syncthreads();
+  pl.s = found_s;
+  pl.at = found_at;
+  return pl;
+}
+
+template <int D, bool BF16, int NT>
+__global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT))
+    suffix_kernel(const __grid_constant__ Params p, const Cuts cuts, int ranges, int least) {
+  constexpr int ROWS = 8 * NT, G = D / 4;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ bool last_part;
+  using SH = Shared<D, NT>;
+  const int h = blockIdx.x % p.Hkv, range = blockIdx.x / p.Hkv;
+  const int heads = p.Hq / p.Hkv;
+  bool waited = false;  // for the prefix stage: its parts and the counters
+  auto wait = [&]() {
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    waited = true;
+  };
+  int64_t u0, u1;
+  const Place pl = locate<ROWS>(p, range, ranges, least, u0, u1);
+  int64_t begin = pl.at;  // first block of the sequence
+  for (int64_t u = u0, s = pl.s; u < u1; ++s) {
+    const int q_lo = query_at(p, s), nq = query_at(p, s + 1) - q_lo;
+    if (nq <= 0) continue;
+    const Own own = own_of(p, s);
+    const int nb = key_blocks(own.L - own.start), rbs = row_blocks(p, nq, ROWS);
+    for (int rb = static_cast<int>((u - begin) / nb); rb < rbs && u < u1; ++rb) {
+      const int64_t first = begin + static_cast<int64_t>(rb) * nb;  // of the unit
+      const int b = static_cast<int>(u - first);
+      const int take = static_cast<int>(min(static_cast<int64_t>(nb - b), u1 - u));
+      const bool starts = u == u0, whole = take == nb;
+      u += take;
+      Piece w;
+      w.q_lo = q_lo;
+      w.row_lo = rb * ROWS;
+      w.R = static_cast<int>(min(static_cast<int64_t>(nq) * heads - w.row_lo, static_cast<int64_t>(ROWS)));
+      w.h = h;
+      w.table = static_cast<int>(s);
+      w.from = own.start + b * BLOCK;
+      w.to = min(own.L, w.from + take * BLOCK);
+      auto row_at = [&](int r) {
+        const int q = (w.row_lo + r) / heads;
+        return static_cast<int64_t>(q_lo + q) * p.Hq + h * heads + (w.row_lo + r - q * heads);
+      };
+      int* const lims = reinterpret_cast<int*>(smem + SH::OFF_LIM);
+      for (int r = threadIdx.x; r < ROWS; r += THREADS)
+        lims[r] = r < w.R ? limit_of(p, static_cast<int>(s), q_lo + (w.row_lo + r) / heads) : 0;
+      stream<D, BF16, NT>(p, w, smem);
+      const int64_t slot = 2ll * blockIdx.x + (starts ? 0 : 1), nslot = 2ll * ranges * p.Hkv * ROWS;
+      if (whole) {
+        wait();
+        const int parts = own.pre > 0 ? min(__ldcg(p.parts + own.group), p.most_parts) : 0;
+        for (int e = threadIdx.x; e < w.R * G; e += THREADS) {
+          const int r = e / G, d4 = e - r * G;
+          Part x = of_warps<D, NT>(smem, r, d4);
+          add_prefix<D>(p, x, row_at(r), d4, parts);
+          write_out<D, BF16>(p, x, row_at(r), d4);
+        }
+      } else {
+        for (int e = threadIdx.x; e < w.R * G; e += THREADS) {
+          const int r = e / G, d4 = e - r * G;
+          const Part x = of_warps<D, NT>(smem, r, d4);
+          const int64_t at = slot * ROWS + r;
+          if (!in_bounds(p.status, at, nslot)) continue;
+          reinterpret_cast<float4*>(cuts.o)[at * G + d4] = x.o;
+          if (d4 == 0) cuts.ml[at] = make_float2(x.M, x.sum);
+        }
+        // the ranges rf .. rl hold the unit's blocks
+        const int64_t end = first + nb;
+        const int rf = static_cast<int>(((first + 1) * pl.ranges + pl.total - 1) / pl.total) - 1;  // last with cut(rf) <= first
+        const int rl = static_cast<int>((end * pl.ranges + pl.total - 1) / pl.total) - 1;          // first with cut(rl + 1) >= end
+        __threadfence();
+        wait();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          const int64_t n = static_cast<int64_t>(rf) * p.Hkv + h;  // a range begins one cut unit at most
+          last_part = in_bounds(p.status, n, static_cast<int64_t>(ranges) * p.Hkv) && atomicAdd(cuts.counters + n, 1) == rl - rf;
+        }
+        __syncthreads();
+        if (last_part) {
+          __threadfence();
+          const bool starts_late = first > cut(pl.total, rf, pl.ranges);
+          const int parts = own.pre > 0 ? min(__ldcg(p.parts + own.group), p.most_parts) : 0;
+          for (int e = threadIdx.x; e < w.R * G; e += THREADS) {
+            const int r = e / G, d4 = e - r * G;
+            Part x;
+            constexpr int BATCH = 4;
+            for (int r0 = rf; r0 <= rl; r0 += BATCH) {
+              float2 ml[BATCH];
+              float4 y[BATCH];
+#pragma unroll
+              for (int k = 0; k < BATCH; ++k) {
+                const int64_t at = (2ll * (static_cast<int64_t>(r0 + k) * p.Hkv + h) + (r0 + k == rf && starts_late ? 1 : 0)) * ROWS + r;
+                const bool is = r0 + k <= rl && in_bounds(p.status, at, nslot);
+                ml[k] = is ? __ldcg(cuts.ml + at) : make_float2(-INFINITY, 0.f);
+                y[k] = is ? __ldcg(reinterpret_cast<const float4*>(cuts.o) + at * G + d4) : make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+#pragma unroll
+              for (int k = 0; k < BATCH; ++k) x.add(ml[k], y[k]);
+            }
+            add_prefix<D>(p, x, row_at(r), d4, parts);
+            write_out<D, BF16>(p, x, row_at(r), d4);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    begin += static_cast<int64_t>(nb) * rbs;
+  }
+  wait();  // no CTA ends before the prefix stage: the next call on the stream may use the workspace
+}
+
+// ------------------------------------------------------------------ launches
+template <int D, bool BF16, int NT>
+cudaError_t launch_prefix_nt(const Params& p, int* counters, int num_counters, cudaStream_t st) {
+  auto kern = prefix_kernel<D, BF16, NT>;
+  constexpr int smem = Shared<D, NT>::BYTES;
+  static std::atomic<unsigned long long> configured{0};
+  const cudaError_t e = allow_smem(kern, smem, p.device, configured);
+  if (e != cudaSuccess) return e;
+  kern<<<SMS * ctas_of_sm(D, NT), THREADS, smem, st>>>(p, counters, num_counters);
+  return cudaGetLastError();
+}
+
+template <int D, bool BF16, int NT>
+cudaError_t launch_suffix_nt(const Params& p, const Cuts& cuts, int ranges, cudaStream_t st) {
+  auto kern = suffix_kernel<D, BF16, NT>;
+  constexpr int smem = Shared<D, NT>::BYTES;
+  static std::atomic<unsigned long long> configured{0};
+  const cudaError_t e = allow_smem(kern, smem, p.device, configured);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ranges) * p.Hkv);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p, cuts, ranges, LEAST_BLOCKS);
+}
+
+#define ATTN_NT(F, NT, ...)                                        \
+  (p.D == 128 ? (NT == 1   ? F<128, BF16, 1>(__VA_ARGS__)          \
+                 : NT == 2 ? F<128, BF16, 2>(__VA_ARGS__)          \
+                 : NT == 3 ? F<128, BF16, 3>(__VA_ARGS__)          \
+                           : F<128, BF16, 4>(__VA_ARGS__))         \
+              : (NT == 1   ? F<64, BF16, 1>(__VA_ARGS__)           \
+                 : NT == 2 ? F<64, BF16, 2>(__VA_ARGS__)           \
+                 : NT == 3 ? F<64, BF16, 3>(__VA_ARGS__)           \
+                           : F<64, BF16, 4>(__VA_ARGS__)))
+
+template <bool BF16>
+cudaError_t launch_prefix(const Params& p, int nt, int* counters, int num_counters, cudaStream_t st) {
+  return ATTN_NT(launch_prefix_nt, nt, p, counters, num_counters, st);
+}
+
+template <bool BF16>
+cudaError_t launch_suffix(const Params& p, int nt, const Cuts& cuts, int ranges, cudaStream_t st) {
+  return ATTN_NT(launch_suffix_nt, nt, p, cuts, ranges, st);
+}
+#undef ATTN_NT
+
+}  // namespace rows
+}  // namespace prefix
+}  // namespace attn
