@@ -60,6 +60,8 @@ attn::EncodeTiledFn encode_fn() {
 
 }  // namespace
 
+attn::EncodeTiledFn attn::encode_tiled() { return encode_fn(); }
+
 // Unique id of the calling thread's current CUDA context (0 when there is
 // none yet, or the driver cannot tell).
 unsigned long long attn::current_context_id() {

@@ -214,10 +214,17 @@ int check_shape(const attn_paged_shape_t& s, int num_groups, int max_group_queri
   return ATTN_OK;
 }
 
+// Shapes of the 16-bit kernels for few rows, and of those for many.
+bool takes_rows(const attn_paged_shape_t& s) { return (s.D == 64 || s.D == 128) && s.num_pages > 0; }
+bool takes_tc(const attn_paged_shape_t& s) {
+  return takes_rows(s) && s.page_size % 8 == 0 && (128 % s.page_size == 0 || s.page_size % 128 == 0);
+}
+
 // How a call runs and lays out its workspace.
 struct Plan {
   int most_parts = 1;                 // parts of a row's prefix
-  int prefix_nt = 0, suffix_nt = 0;   // few-row kernels: 8-row groups of a CTA
+  bool prefix_tc = false, suffix_tc = false;  // the kernel for many rows
+  int prefix_nt = 0, suffix_nt = 0;   // that for few: 8-row groups of a CTA
   int ranges = 0;                     // of the suffix stage
   int64_t ml_offset = 0, o_offset = 0, cut_ml_offset = 0, cut_o_offset = 0, counter_offset = 0, bytes = 0;
 };
@@ -227,11 +234,14 @@ Plan plan_of(const attn_paged_shape_t& s, int num_groups, int max_group_queries)
   Plan d;
   const int64_t heads = s.Hq / s.Hkv, rows = static_cast<int64_t>(s.num_queries) * s.Hq;
   const int64_t group_rows = std::min(max_group_queries, s.num_queries) * heads;
+  const int64_t seq_rows = s.max_queries * heads;
+  d.prefix_tc = group_rows > 32 && takes_tc(s) && s.Hkv * ((s.num_queries * heads + 255) / 256 + num_groups) <= 0x7fffffffLL;
+  d.suffix_tc = seq_rows > 32 && takes_tc(s) && s.num_seqs * s.Hkv * ((seq_rows + 255) / 256) <= 0x7fffffffLL;
   d.prefix_nt = rows::nt_of(group_rows);
-  d.suffix_nt = rows::nt_of(s.max_queries * heads);
+  d.suffix_nt = rows::nt_of(seq_rows);
   // A row's prefix is cut into as many parts as its group's CTAs can be, and not into more than 64 MB
   // of workspace; the parts that a call uses are settled on the device.
-  const int64_t ctas = static_cast<int64_t>(attn::SMS) * rows::ctas_of_sm(s.D, d.prefix_nt);
+  const int64_t ctas = static_cast<int64_t>(attn::SMS) * (d.prefix_tc ? 1 : rows::ctas_of_sm(s.D, d.prefix_nt));
   const int64_t units = s.Hkv * (num_groups == 1 ? std::max<int64_t>(1, (group_rows + 255) / 256) : 1);
   const int64_t room = (64ll << 20) / std::max<int64_t>(1, rows * (4 * s.D + 8));
   d.most_parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({MAX_PARTS, (ctas + units - 1) / units, room})));
@@ -248,9 +258,6 @@ Plan plan_of(const attn_paged_shape_t& s, int num_groups, int max_group_queries)
   d.bytes = d.counter_offset + up(4ll * d.ranges * s.Hkv);
   return d;
 }
-
-// Shapes of the 16-bit kernels.
-bool takes_rows(const attn_paged_shape_t& s) { return (s.D == 64 || s.D == 128) && s.num_pages > 0; }
 
 }  // namespace
 
@@ -345,9 +352,21 @@ extern "C" int attn_paged_prefix_fwd(const attn_paged_shape_t* shape, int num_gr
     const bool bf16 = dtype == ATTN_BF16;
     const int counters = plan.ranges * s.Hkv;
     using namespace attn::prefix::rows;
-    e = bf16 ? launch_prefix<true>(p, plan.prefix_nt, cuts.counters, counters, st)
-             : launch_prefix<false>(p, plan.prefix_nt, cuts.counters, counters, st);
-    if (e == cudaSuccess)
+    attn::EncodeTiledFn enc = nullptr;
+    if (plan.prefix_tc || plan.suffix_tc) {
+      enc = attn::encode_tiled();
+      if (!enc) return attn::record_cuda_error(cudaErrorNotSupported);
+    }
+    using attn::prefix::tc::launch;
+    if (plan.prefix_tc)
+      e = bf16 ? launch<true, true>(enc, p, cuts.counters, counters, st) : launch<false, true>(enc, p, cuts.counters, counters, st);
+    else
+      e = bf16 ? launch_prefix<true>(p, plan.prefix_nt, cuts.counters, counters, st)
+               : launch_prefix<false>(p, plan.prefix_nt, cuts.counters, counters, st);
+    if (e != cudaSuccess) return attn::record_cuda_error(e);
+    if (plan.suffix_tc)
+      e = bf16 ? launch<true, false>(enc, p, nullptr, 0, st) : launch<false, false>(enc, p, nullptr, 0, st);
+    else
       e = bf16 ? launch_suffix<true>(p, plan.suffix_nt, cuts, plan.ranges, st)
                : launch_suffix<false>(p, plan.suffix_nt, cuts, plan.ranges, st);
     return e == cudaSuccess ? ATTN_OK : attn::record_cuda_error(e);

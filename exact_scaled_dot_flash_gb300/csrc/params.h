@@ -38,6 +38,9 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// The encoder, or nullptr where the driver has none.
+EncodeTiledFn encode_tiled();
+
 namespace tc {
 // How the additive bias reaches the softmax: none; read by each thread from
 // global memory; or staged by TMA through a shared-memory ring (D <= 64).

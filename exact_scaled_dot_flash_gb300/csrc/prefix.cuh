@@ -151,5 +151,14 @@ cudaError_t launch_suffix(const Params& p, int nt, const Cuts& cuts, int ranges,
 
 }  // namespace rows
 
+// ------------------------------------------------------------------ many rows (prefix_tc.cuh)
+namespace tc {
+
+// One stage; counters as above (prefix stage).
+template <bool BF16, bool PREFIX>
+cudaError_t launch(EncodeTiledFn enc, const Params& p, int* counters, int num_counters, cudaStream_t st);
+
+}  // namespace tc
+
 }  // namespace prefix
 }  // namespace attn
