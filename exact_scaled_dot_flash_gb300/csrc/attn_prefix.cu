@@ -24,6 +24,9 @@ constexpr int ROWS = 64;
 constexpr int THREADS = 256;
 constexpr int KT = 32;
 
+// Parts of a prefix of `pre` keys, 128 keys or more each.
+__device__ __forceinline__ int parts_of_simt(const Params& p, int pre) { return min(p.most_parts, (pre + 127) / 128); }
+
 template <int D, int DT, bool PREFIX>
 __global__ void __launch_bounds__(THREADS) simt_kernel(const __grid_constant__ Params p) {
   constexpr int G = D / 4;
@@ -38,11 +41,13 @@ __global__ void __launch_bounds__(THREADS) simt_kernel(const __grid_constant__ P
   if constexpr (PREFIX) group_range(p, unit, a, b);
   else group = group_of(p, unit);
   const int pre = group >= 0 ? prefix_len(p, group) : 0;
+  const int parts = pre > 0 ? parts_of_simt(p, pre) : 0;
   if constexpr (PREFIX) {
-    if (blockIdx.y == 0 && blockIdx.z == 0 && hk == 0 && tid == 0) p.parts[unit] = p.most_parts;
+    if (static_cast<int>(blockIdx.z) >= parts) return;
   }
   if (a >= b) return;
-  const int q_lo = query_at(p, a), nq = max(query_at(p, b) - q_lo, 0);
+  int q_lo;
+  const int nq = queries_of(p, a, b, PREFIX ? p.max_group_queries : p.max_queries, q_lo);
   const int64_t r = static_cast<int64_t>(blockIdx.y) * ROWS + rl;
   if (static_cast<int64_t>(blockIdx.y) * ROWS >= static_cast<int64_t>(nq) * heads) return;  // CTA-uniform
   const int tq = static_cast<int>(r / heads), h = hk * heads + static_cast<int>(r - static_cast<int64_t>(tq) * heads);
@@ -55,8 +60,8 @@ __global__ void __launch_bounds__(THREADS) simt_kernel(const __grid_constant__ P
   if constexpr (PREFIX) {
     row = reader_of(p, a, b, pre);
     const int64_t tiles = (pre + KT - 1) / KT;
-    from = static_cast<int>(tiles * blockIdx.z / gridDim.z) * KT;
-    to = min(pre, static_cast<int>(tiles * (blockIdx.z + 1) / gridDim.z) * KT);
+    from = static_cast<int>(tiles * blockIdx.z / parts) * KT;
+    to = min(pre, static_cast<int>(tiles * (blockIdx.z + 1) / parts) * KT);
     lim = min(lim, to);
   } else {
     row = s;
@@ -135,20 +140,32 @@ __global__ void __launch_bounds__(THREADS) simt_kernel(const __grid_constant__ P
     if (part == 0) p.ml[at] = make_float2(m_run, l_run);
   } else {
     if (!row_ok || !in_bounds(st, lrow, rows)) return;
-    const int parts = pre > 0 ? min(p.parts[group], p.most_parts) : 0;
-    for (int z = 0; z < parts; ++z) {
-      const int64_t at = z * rows + lrow;
-      const float2 ml = p.ml[at];
-      const float m = fmaxf(m_run, ml.x);
-      if (m == -INFINITY) continue;
-      const float f = fast_exp2(m_run - m), e = fast_exp2(ml.x - m);
-      m_run = m;
-      l_run = l_run * f + ml.y * e;
+    constexpr int BATCH = 4;  // parts read together: each read is a trip to L2
+    for (int z0 = 0; z0 < parts; z0 += BATCH) {
+      float2 ml[BATCH];
+      float4 y[BATCH][GPT];
 #pragma unroll
-      for (int i = 0; i < GPT; ++i) {
-        float4 x = acc[i];
-        x.x *= f; x.y *= f; x.z *= f; x.w *= f;
-        acc[i] = axpy4(e, reinterpret_cast<const float4*>(p.o)[at * G + part + 4 * i], x);
+      for (int z = 0; z < BATCH; ++z) {
+        const int64_t at = (z0 + z) * rows + lrow;
+        const bool is = z0 + z < parts && in_bounds(st, at, p.most_parts * rows);
+        ml[z] = is ? __ldcg(p.ml + at) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int i = 0; i < GPT; ++i)
+          y[z][i] = is ? __ldcg(reinterpret_cast<const float4*>(p.o) + at * G + part + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int z = 0; z < BATCH; ++z) {
+        const float m = fmaxf(m_run, ml[z].x);
+        if (m == -INFINITY) continue;
+        const float f = fast_exp2(m_run - m), e = fast_exp2(ml[z].x - m);
+        m_run = m;
+        l_run = l_run * f + ml[z].y * e;
+#pragma unroll
+        for (int i = 0; i < GPT; ++i) {
+          float4 x = acc[i];
+          x.x *= f; x.y *= f; x.z *= f; x.w *= f;
+          acc[i] = axpy4(e, y[z][i], x);
+        }
       }
     }
     const bool live = l_run > 0.f;
@@ -239,23 +256,23 @@ Plan plan_of(const attn_paged_shape_t& s, int num_groups, int max_group_queries)
   d.suffix_tc = seq_rows > 32 && takes_tc(s) && s.num_seqs * s.Hkv * ((seq_rows + 255) / 256) <= 0x7fffffffLL;
   d.prefix_nt = rows::nt_of(group_rows);
   d.suffix_nt = rows::nt_of(seq_rows);
-  // A row's prefix is cut into as many parts as its group's CTAs can be, and not into more than 64 MB
-  // of workspace; the parts that a call uses are settled on the device.
+  // Room for as many parts of a row's prefix as its group's CTAs can leave (two each where they split
+  // their keys), within 64 MB where that is enough for MIN_PARTS; a call uses what the device settles on.
   const int64_t ctas = static_cast<int64_t>(attn::SMS) * (d.prefix_tc ? 1 : rows::ctas_of_sm(s.D, d.prefix_nt));
   const int64_t units = s.Hkv * (num_groups == 1 ? std::max<int64_t>(1, (group_rows + 255) / 256) : 1);
   const int64_t room = (64ll << 20) / std::max<int64_t>(1, rows * (4 * s.D + 8));
-  d.most_parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({MAX_PARTS, (ctas + units - 1) / units, room})));
+  d.most_parts = static_cast<int>(std::max<int64_t>(MIN_PARTS, std::min<int64_t>({MAX_PARTS, 2 * (ctas + units - 1) / units, room})));
   const int suffix_ctas = attn::SMS * rows::ctas_of_sm(s.D, d.suffix_nt);
   d.ranges = std::max(1, suffix_ctas / s.Hkv);
-  auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
+  auto up = [](int64_t n) { return (n + 31) / 32 * 32; };  // the parts move in 32 bytes
   const int64_t parts = num_groups > 0 && max_group_queries > 0 ? d.most_parts : 0;
   const int64_t slots = 2ll * d.ranges * s.Hkv * 8 * d.suffix_nt;
-  d.ml_offset = up(num_groups * 4ll);
+  d.ml_offset = up(sizeof(Head) + num_groups * sizeof(Rec));
   d.o_offset = up(d.ml_offset + parts * rows * 8);
   d.cut_ml_offset = d.o_offset + parts * rows * s.D * 4;
   d.cut_o_offset = up(d.cut_ml_offset + slots * 8);
   d.counter_offset = d.cut_o_offset + slots * s.D * 4;
-  d.bytes = d.counter_offset + up(4ll * d.ranges * s.Hkv);
+  d.bytes = d.counter_offset + up(4ll * d.ranges * s.Hkv) + 16;  // it begins at the next 32 bytes
   return d;
 }
 
@@ -340,12 +357,13 @@ extern "C" int attn_paged_prefix_fwd(const attn_paged_shape_t* shape, int num_gr
   p.lse = lse;
   p.status = attn::status_word(dev);
   p.most_parts = plan.most_parts;
-  p.parts = static_cast<int32_t*>(workspace);
-  p.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan.ml_offset);
-  p.o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.o_offset);
+  uint8_t* const ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 31) / 32 * 32);
+  p.head = reinterpret_cast<attn::prefix::Head*>(ws);
+  p.rec = reinterpret_cast<attn::prefix::Rec*>(p.head + 1);
+  p.ml = reinterpret_cast<float2*>(ws + plan.ml_offset);
+  p.o = reinterpret_cast<float*>(ws + plan.o_offset);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype != ATTN_F32 && takes_rows(s)) {
-    uint8_t* const ws = static_cast<uint8_t*>(workspace);
     const attn::prefix::rows::Cuts cuts{reinterpret_cast<float*>(ws + plan.cut_o_offset),
                                         reinterpret_cast<float2*>(ws + plan.cut_ml_offset),
                                         reinterpret_cast<int*>(ws + plan.counter_offset)};

@@ -5,9 +5,13 @@
 // A row (query, head) sees the keys j < lim of its sequence. Group g's first `pre`
 // keys are the same for all its members, so a call has two stages:
 //   prefix: a unit is a group, its rows all the queries of its members (packed, so they
-//           lie side by side), its keys [0, pre). A row leaves `parts` parts (m, l, O) in
-//           the workspace, one for each run of keys that its unit was cut into:
+//           lie side by side), its keys [0, pre). A row leaves parts (m, l, O) in the
+//           workspace, one for each run of keys that its unit was cut into:
 //           O = sum_j 2^(x_j - m) v_j, l = sum_j 2^(x_j - m), x in log2 units.
+//           The 16-bit kernels share out the work in equal ranges: the blocks (a run of
+//           keys for a block of rows and a head) of all groups, in one order, are cut into
+//           as many ranges as there are CTAs, so a row's parts are the ranges that its
+//           unit's blocks lie in (Head, Rec, parts_of).
 //   suffix: a unit is a sequence, its keys [pre, L) (all of them outside a group). It
 //           joins its own part with those of the prefix and writes out and lse.
 #pragma once
@@ -22,7 +26,20 @@ namespace attn {
 namespace prefix {
 
 constexpr float LN2 = 0.6931471805599453f;
-constexpr int MAX_PARTS = 32;
+constexpr int MAX_PARTS = 32, MIN_PARTS = 4;  // room for the parts of a row
+
+// How the prefix stage was shared out, in the workspace: block total and ranges of the call; of each
+// group its first block, the blocks of one (row block, head), the row blocks, whether the last
+// one has at most half the rows (its blocks then hold twice the keys, and a range leaves two
+// parts), and the first query.
+struct Head {
+  int64_t total;
+  int32_t ranges, row_block;
+};
+struct Rec {
+  int64_t first;
+  int32_t nb, rbs, half, q_lo;
+};
 
 struct Params {
   int num_seqs, num_queries, num_groups, Hq, Hkv, D, page_size, num_pages, max_pages;
@@ -36,7 +53,8 @@ struct Params {
   int* status;
   // workspace
   int most_parts;   // slots of a row
-  int32_t* parts;   // [num_groups] parts of each row of the group
+  Head* head;
+  Rec* rec;         // [num_groups]
   float2* ml;       // [most_parts, num_queries * Hq]
   float* o;         // [most_parts, num_queries * Hq, D]
 };
@@ -111,6 +129,145 @@ __device__ __forceinline__ int reader_of(const Params& p, int a, int b, int pre)
   return static_cast<int>(~static_cast<uint32_t>(best));
 }
 
+__device__ __forceinline__ int64_t cut(int64_t total, int r, int ranges) { return total * r / ranges; }  // first block of range r
+
+// The range that block x lies in (ranges <= total).
+__device__ __forceinline__ int range_of(int64_t x, int64_t total, int ranges) {
+  return static_cast<int>(((x + 1) * ranges + total - 1) / total) - 1;
+}
+
+// Queries of the sequences [a, b), from q_lo on, at most `most`.
+__device__ __forceinline__ int queries_of(const Params& p, int a, int b, int most, int& q_lo) {
+  q_lo = query_at(p, a);
+  return a < b ? min(max(query_at(p, b) - q_lo, 0), most) : 0;
+}
+
+// What a group brings to the prefix stage: `first` is filled in by the caller.
+__device__ __forceinline__ Rec rec_of(const Params& p, int g, int key_block, int row_block, bool halves) {
+  int a, b;
+  group_range(p, g, a, b);
+  Rec r;
+  r.first = 0;
+  const int64_t rows = static_cast<int64_t>(queries_of(p, a, b, p.max_group_queries, r.q_lo)) * (p.Hq / p.Hkv);
+  r.nb = (prefix_len(p, g) + key_block - 1) / key_block;
+  r.rbs = r.nb > 0 ? static_cast<int>((rows + row_block - 1) / row_block) : 0;
+  r.half = halves && r.rbs > 0 && rows - static_cast<int64_t>(r.rbs - 1) * row_block <= row_block / 2;
+  return r;
+}
+
+__device__ __forceinline__ int64_t full_blocks(const Params& p, const Rec& r) { return static_cast<int64_t>(r.rbs - r.half) * p.Hkv * r.nb; }
+
+__device__ __forceinline__ int64_t blocks_of(const Params& p, const Rec& r) {
+  return full_blocks(p, r) + (r.half ? static_cast<int64_t>(p.Hkv) * ((r.nb + 1) / 2) : 0);
+}
+
+// Shares out the prefix stage: the ranges, this CTA's blocks [u0, u1), and the group that u0 lies in with its
+// first block. Every thread of the CTA calls it; CTA 0 leaves Head and Rec in the workspace.
+struct Share {
+  int64_t total, u0, u1, first;
+  int ranges, g;
+};
+
+template <int THREADS>
+__device__ __forceinline__ Share share_out(const Params& p, int ctas, int key_block, int row_block, bool halves) {
+  __shared__ int64_t warp_sum[THREADS / 32];
+  __shared__ int most_full, most_half, found_g;
+  __shared__ int64_t found_first;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.num_groups + THREADS - 1) / THREADS;
+  const int g0 = min(tid * per, p.num_groups), g1 = min(g0 + per, p.num_groups);
+  if (tid == 0) most_full = most_half = found_g = 0, found_first = 0;
+  __syncthreads();
+  int64_t mine = 0;
+  int full = 0, half = 0;
+  Rec r0{};
+  for (int g = g0; g < g1; ++g) {
+    const Rec r = rec_of(p, g, key_block, row_block, halves);
+    if (g == g0) r0 = r;
+    mine += blocks_of(p, r);
+    if (r.rbs > r.half) full = max(full, r.nb);
+    if (r.half) half = max(half, (r.nb + 1) / 2);
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  full = __reduce_max_sync(0xffffffffu, full);
+  half = __reduce_max_sync(0xffffffffu, half);
+  if (lane == 0 && full) atomicMax(&most_full, full);
+  if (lane == 0 && half) atomicMax(&most_half, half);
+  __syncthreads();
+  Share s;
+  int64_t before = incl - mine;
+  s.total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    s.total += warp_sum[w];
+  }
+  // as many ranges as CTAs, if they leave a row no more parts than its room: n blocks lie in
+  // at most n ranges / total + 1 ranges
+  int64_t ranges = min(static_cast<int64_t>(ctas), s.total);
+  if (most_full) ranges = min(ranges, s.total * (p.most_parts - 1) / most_full);
+  if (most_half) ranges = min(ranges, s.total * (p.most_parts / 2 - 1) / most_half);
+  s.ranges = static_cast<int>(max(ranges, static_cast<int64_t>(1)));
+  const bool mine_too = static_cast<int>(blockIdx.x) < s.ranges;
+  s.u0 = mine_too ? cut(s.total, blockIdx.x, s.ranges) : s.total;
+  s.u1 = mine_too ? cut(s.total, blockIdx.x + 1, s.ranges) : s.total;
+  if (blockIdx.x == 0 || (s.u0 >= before && s.u0 < before + mine)) {
+    int64_t at = before;
+    for (int g = g0; g < g1; ++g) {
+      Rec r = g == g0 ? r0 : rec_of(p, g, key_block, row_block, halves);
+      const int64_t n = blocks_of(p, r);
+      if (s.u0 >= at && s.u0 < at + n) {
+        found_g = g;
+        found_first = at;
+      }
+      r.first = at;
+      if (blockIdx.x == 0) p.rec[g] = r;
+      at += n;
+    }
+  }
+  if (blockIdx.x == 0 && tid == 0) *p.head = Head{s.total, s.ranges, row_block};
+  __syncthreads();
+  s.g = found_g;
+  s.first = found_first;
+  return s;
+}
+
+// Parts of the prefix that row (query, head h * heads + hr) of group g has.
+__device__ __forceinline__ int parts_of(const Params& p, int g, int query, int hr, int h) {
+  const int64_t total = __ldcg(reinterpret_cast<const long long*>(&p.head->total));
+  const int ranges = __ldcg(&p.head->ranges), row_block = __ldcg(&p.head->row_block);
+  const Rec* const at = p.rec + g;
+  const int64_t first = __ldcg(reinterpret_cast<const long long*>(&at->first));
+  const int nb = __ldcg(&at->nb), rbs = __ldcg(&at->rbs), half = __ldcg(&at->half), q_lo = __ldcg(&at->q_lo);
+  const int64_t row = static_cast<int64_t>(query - q_lo) * (p.Hq / p.Hkv) + hr;
+  const int rb = static_cast<int>(row / row_block);
+  if (row < 0 || rb >= rbs || total <= 0) return 0;
+  const bool two = half && rb == rbs - 1;
+  const int n = two ? (nb + 1) / 2 : nb;
+  const int64_t start = first + static_cast<int64_t>(rb) * p.Hkv * nb + static_cast<int64_t>(h) * n;
+  const int pieces = range_of(start + n - 1, total, ranges) - range_of(start, total, ranges) + 1;
+  return min(two ? 2 * pieces : pieces, p.most_parts);
+}
+
+// 8 floats of the workspace: 32 bytes, one sector.
+__device__ __forceinline__ void load8cg(float (&r)[8], const float* at) {
+  asm volatile("ld.global.cg.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+               : "l"(at)
+               : "memory");
+}
+__device__ __forceinline__ void store8(float* at, const float (&r)[8]) {
+  asm volatile("st.global.v8.f32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]),
+               "f"(r[5]), "f"(r[6]), "f"(r[7]), "l"(at)
+               : "memory");
+}
+
 // Opts a kernel in to `smem` bytes of shared memory, once for each device.
 template <typename K>
 cudaError_t allow_smem(K kern, int smem, int device, std::atomic<unsigned long long>& configured) {
@@ -127,10 +284,10 @@ namespace rows {
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
 constexpr int BLOCK = 16 * WARPS;  // keys of a block: 16 a warp
-constexpr int LEAST_BLOCKS = 4;    // of a range
+constexpr int LEAST_BLOCKS = 4;    // of a range of the suffix stage, where units are cut
 
 // CTAs of an SM: what the shared memory holds, and enough registers for the outputs.
-__host__ __device__ constexpr int ctas_of_sm(int D, int nt) { return D == 128 ? 2 : nt <= 2 ? 4 : 3; }
+__host__ __device__ constexpr int ctas_of_sm(int D, int nt) { return D == 128 ? (nt <= 2 ? 3 : 2) : nt <= 2 ? 4 : 3; }
 
 // Groups of 8 rows that a CTA takes.
 inline int nt_of(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }

@@ -3,7 +3,7 @@
 // groups (F16/BF16, D in {64, 128}, any page size).
 //
 // Bound: the bytes of the keys and values, read once for all the rows of a kv head.
-// A warp streams its own 16-key tiles through three buffers of cp.async copies in shared
+// A warp streams its own 16-key tiles through two or three buffers of cp.async copies in shared
 // memory, without a barrier between warps:
 //  - S^T = K Q^T (keys x rows), then O^T = V^T P^T, by mma.sync with the cache as the A
 //    operand, so that 8 columns hold the rows instead of 16 or 128; K by ldmatrix, V by its
@@ -17,8 +17,7 @@
 // sequences of its range; a sequence wholly inside it is joined with its prefix's parts
 // and written out, a cut one leaves parts, and the CTA that finishes the last of them (a
 // counter that the prefix stage has cleared) joins all in the order of the ranges.
-// Prefix stage: a group's keys are cut into parts of one length for all groups, the
-// shortest that the grid's CTAs can take at once; a CTA takes a part for 32 rows and a head.
+// Prefix stage: blocks of 64 keys for 8 NT rows and a head, shared out as prefix.cuh says.
 #pragma once
 
 #include "prefix.cuh"
@@ -28,7 +27,6 @@ namespace prefix {
 namespace rows {
 
 constexpr int TILE = 16;                  // keys of a warp's tile
-constexpr int STAGES = 3;
 constexpr float UNSEEN = -3e38f;          // reference of a row without keys: its first one passes every range
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
@@ -71,13 +69,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 template <int D, int NT>
 struct Shared {
   static constexpr int ROWS = 8 * NT;
+  static constexpr int STAGES = ctas_of_sm(D, NT) == 3 && D == 128 ? 2 : 3;
   static constexpr int TILE_BYTES = TILE * D * 2;             // K or V
   static constexpr int RING = WARPS * STAGES * 2 * TILE_BYTES;
   static constexpr int ROW = D + 4;
   static constexpr int O = WARPS * ROWS * ROW * 4;            // the warps' outputs, in the ring's place
   static constexpr int OFF_ML = RING > O ? RING : O;
   static constexpr int OFF_LIM = OFF_ML + WARPS * ROWS * 8;
-  static constexpr int OFF_Q = OFF_LIM + ROWS * 4;            // query operands, in the lanes' order
+  static constexpr int OFF_PARTS = OFF_LIM + ROWS * 4;        // parts of each row's prefix
+  static constexpr int OFF_Q = OFF_PARTS + ROWS * 4;          // query operands, in the lanes' order
   static constexpr int BYTES = OFF_Q + NT * (D / 16) * 32 * 8;
 };
 
@@ -94,6 +94,7 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
   constexpr int KS = D / 16;       // 16-element steps of a head
   constexpr int ROWS = 8 * NT;
   using SH = Shared<D, NT>;
+  constexpr int STAGES = SH::STAGES;
   float* const so = reinterpret_cast<float*>(smem);
   float2* const sml = reinterpret_cast<float2*>(smem + SH::OFF_ML);
   const int* const lims = reinterpret_cast<const int*>(smem + SH::OFF_LIM);
@@ -323,7 +324,7 @@ __device__ __forceinline__ Part of_warps(const uint8_t* smem, int r, int d4) {
 // Adds the prefix's parts of a row (n of them), BATCH read together: each read is a trip to L2.
 template <int D>
 __device__ __forceinline__ void add_prefix(const Params& p, Part& a, int64_t row, int d4, int n) {
-  constexpr int BATCH = 4;
+  constexpr int BATCH = 8;
   const int64_t rows = static_cast<int64_t>(p.num_queries) * p.Hq;
   for (int z0 = 0; z0 < n; z0 += BATCH) {
     float2 ml[BATCH];
@@ -351,92 +352,6 @@ __device__ __forceinline__ void write_out(const Params& p, const Part& a, int64_
 }
 
 // ------------------------------------------------------------------ prefix stage
-// Blocks of keys (of `block`) and of rows (of `rows`) of a group.
-__device__ __forceinline__ void group_work(const Params& p, int g, int block, int rows, int& key_blocks, int& row_blocks) {
-  int a, b;
-  group_range(p, g, a, b);
-  const int nq = a < b ? max(query_at(p, b) - query_at(p, a), 0) : 0;
-  row_blocks = static_cast<int>((static_cast<int64_t>(nq) * (p.Hq / p.Hkv) + rows - 1) / rows);
-  key_blocks = (prefix_len(p, g) + block - 1) / block;
-  if (key_blocks == 0 || row_blocks == 0) key_blocks = row_blocks = 0;
-}
-
-struct Item {
-  int g, part, parts, rb, h, chunk;  // g < 0: none
-  int64_t total;                     // items of all
-};
-
-// Item number `item` of the prefix stage for a grid of `ctas`. A warp calls it.
-__device__ __forceinline__ Item item_of(const Params& p, int64_t item, int ctas, int block, int rows) {
-  const int lane = threadIdx.x & 31;
-  auto warp_sum = [](int64_t x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-  };
-  // the lane's group stays in registers where there are no more than lanes
-  int kb0 = 0, rb0 = 0, longest = 0;
-  if (lane < p.num_groups) group_work(p, lane, block, rows, kb0, rb0);
-  for (int g = lane; g < p.num_groups; g += 32) {
-    int kb = kb0, rb = rb0;
-    if (g >= 32) group_work(p, g, block, rows, kb, rb);
-    longest = max(longest, kb);
-  }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  // the shortest part with which the items fit the grid (and a row's parts the workspace)
-  int lo = max(1, (longest + p.most_parts - 1) / p.most_parts), hi = max(longest, 1);
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    int64_t n = 0;
-    for (int g = lane; g < p.num_groups; g += 32) {
-      int kb = kb0, rb = rb0;
-      if (g >= 32) group_work(p, g, block, rows, kb, rb);
-      n += static_cast<int64_t>((kb + mid - 1) / mid) * rb;
-    }
-    if (warp_sum(n) * p.Hkv <= ctas) hi = mid;
-    else lo = mid + 1;
-  }
-  int64_t all = 0;
-  for (int g = lane; g < p.num_groups; g += 32) {
-    int kb = kb0, rb = rb0;
-    if (g >= 32) group_work(p, g, block, rows, kb, rb);
-    all += static_cast<int64_t>((kb + lo - 1) / lo) * rb;
-  }
-  Item it{-1, 0, 0, 0, 0, lo, warp_sum(all) * p.Hkv};
-  int64_t before = 0;
-  for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
-    const int g = g0 + lane;
-    int kb = kb0, rb = rb0;
-    if (g0 > 0) {
-      kb = rb = 0;
-      if (g < p.num_groups) group_work(p, g, block, rows, kb, rb);
-    }
-    const int parts = (kb + lo - 1) / lo;
-    const int64_t mine = static_cast<int64_t>(parts) * rb * p.Hkv;
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, before + incl > item);
-    if (past) {
-      const int who = __ffs(past) - 1;
-      it.g = g0 + who;
-      it.parts = __shfl_sync(0xffffffffu, parts, who);
-      const int rbs = __shfl_sync(0xffffffffu, rb, who);
-      int64_t r = item - before - __shfl_sync(0xffffffffu, incl - mine, who);
-      it.h = static_cast<int>(r % p.Hkv);
-      r /= p.Hkv;
-      it.rb = static_cast<int>(r % rbs);
-      it.part = static_cast<int>(r / rbs);
-      return it;
-    }
-    before += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  return it;
-}
-
 // Each row's limit of a group's rows (row_lo on), into shared memory.
 __device__ __forceinline__ void group_limits(const Params& p, int a, int b, int q_lo, int row_lo, int R, int rows, int* lims) {
   const int heads = p.Hq / p.Hkv;
@@ -455,45 +370,52 @@ __global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT)) prefix_kernel(cons
   asm volatile("griddepcontrol.launch_dependents;");  // the suffix stage may come up: it waits before it reads
   constexpr int ROWS = 8 * NT;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ Item shared_item;
   using SH = Shared<D, NT>;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i < num_counters; i += static_cast<int64_t>(gridDim.x) * THREADS)
     counters[i] = 0;
-  for (int64_t n = blockIdx.x;; n += gridDim.x) {
-    if (threadIdx.x < 32) {
-      const Item x = item_of(p, n, gridDim.x, BLOCK, ROWS);
-      if (threadIdx.x == 0) shared_item = x;
+  const Share sh = share_out<THREADS>(p, gridDim.x, BLOCK, ROWS, false);
+  const int heads = p.Hq / p.Hkv;
+  int64_t u = sh.u0, first = sh.first;
+  for (int g = sh.g; u < sh.u1; ++g) {
+    const Rec rec = rec_of(p, g, BLOCK, ROWS, false);
+    const int64_t n = blocks_of(p, rec);
+    if (u >= first + n) {
+      first += n;
+      continue;
     }
-    __syncthreads();
-    const Item it = shared_item;
-    if (it.g < 0) return;
     int a, b;
-    group_range(p, it.g, a, b);
-    const int pre = prefix_len(p, it.g), heads = p.Hq / p.Hkv;
-    Piece w;
-    w.q_lo = query_at(p, a);
-    w.row_lo = it.rb * ROWS;
-    const int64_t left = static_cast<int64_t>(query_at(p, b) - w.q_lo) * heads - w.row_lo;
-    w.R = static_cast<int>(min(left, static_cast<int64_t>(ROWS)));
-    w.h = it.h;
-    w.from = it.part * it.chunk * BLOCK;
-    w.to = min(pre, w.from + it.chunk * BLOCK);
-    group_limits(p, a, b, w.q_lo, w.row_lo, w.R, ROWS, reinterpret_cast<int*>(smem + SH::OFF_LIM));
-    w.table = reader_of(p, a, b, pre);
-    if (it.part == 0 && it.rb == 0 && it.h == 0 && threadIdx.x == 0) p.parts[it.g] = it.parts;
-    stream<D, BF16, NT>(p, w, smem);
-    const int64_t rows = static_cast<int64_t>(p.num_queries) * p.Hq;
-    for (int e = threadIdx.x; e < w.R * (D / 4); e += THREADS) {
-      const int r = e / (D / 4), d4 = e - r * (D / 4);
-      const Part x = of_warps<D, NT>(smem, r, d4);
-      const int q = (w.row_lo + r) / heads;
-      const int64_t at = it.part * rows + static_cast<int64_t>(w.q_lo + q) * p.Hq + w.h * heads + (w.row_lo + r - q * heads);
-      if (!in_bounds(p.status, at, p.most_parts * rows)) continue;
-      reinterpret_cast<float4*>(p.o)[at * (D / 4) + d4] = x.o;
-      if (d4 == 0) p.ml[at] = make_float2(x.M, x.sum);
+    group_range(p, g, a, b);
+    const int pre = prefix_len(p, g), table = reader_of(p, a, b, pre);
+    int q_lo;
+    const int64_t rows = static_cast<int64_t>(queries_of(p, a, b, p.max_group_queries, q_lo)) * heads;
+    while (u < sh.u1 && u < first + n) {
+      const int unit = static_cast<int>((u - first) / rec.nb), k0 = static_cast<int>(u - first - static_cast<int64_t>(unit) * rec.nb);
+      const int take = static_cast<int>(min(static_cast<int64_t>(rec.nb - k0), sh.u1 - u));
+      const int part = static_cast<int>(blockIdx.x) - range_of(u - k0, sh.total, sh.ranges);
+      u += take;
+      Piece w;
+      w.q_lo = q_lo;
+      w.row_lo = unit / p.Hkv * ROWS;
+      w.R = static_cast<int>(min(rows - w.row_lo, static_cast<int64_t>(ROWS)));
+      w.h = unit % p.Hkv;
+      w.table = table;
+      w.from = k0 * BLOCK;
+      w.to = min(pre, w.from + take * BLOCK);
+      group_limits(p, a, b, q_lo, w.row_lo, w.R, ROWS, reinterpret_cast<int*>(smem + SH::OFF_LIM));
+      stream<D, BF16, NT>(p, w, smem);
+      const int64_t nrows = static_cast<int64_t>(p.num_queries) * p.Hq;
+      for (int e = threadIdx.x; e < w.R * (D / 4); e += THREADS) {
+        const int r = e / (D / 4), d4 = e - r * (D / 4);
+        const Part x = of_warps<D, NT>(smem, r, d4);
+        const int q = (w.row_lo + r) / heads;
+        const int64_t at = part * nrows + static_cast<int64_t>(w.q_lo + q) * p.Hq + w.h * heads + (w.row_lo + r - q * heads);
+        if (!in_bounds(p.status, at, p.most_parts * nrows)) continue;
+        reinterpret_cast<float4*>(p.o)[at * (D / 4) + d4] = x.o;
+        if (d4 == 0) p.ml[at] = make_float2(x.M, x.sum);
+      }
+      __syncthreads();
     }
-    if (n + gridDim.x >= it.total) return;
-    __syncthreads();
+    first += n;
   }
 }
 
@@ -518,9 +440,6 @@ __device__ __forceinline__ int row_blocks(const Params& p, int nq, int rows) {
   return static_cast<int>((static_cast<int64_t>(nq) * (p.Hq / p.Hkv) + rows - 1) / rows);
 }
 
-// First block of range r.
-__device__ __forceinline__ int64_t cut(int64_t total, int r, int ranges) { return total * r / ranges; }
-
 // Blocks in the order (sequence, row block, key block). The whole CTA calls it.
 struct Place {
   int64_t total, at;  // blocks of all; first block of the unit that range begins in
@@ -531,18 +450,24 @@ template <int ROWS>
 __device__ __forceinline__ Place locate(const Params& p, int range, int ranges, int least, int64_t& u0, int64_t& u1) {
   __shared__ int64_t warp_sum[THREADS / 32];
   __shared__ int64_t found_at;
-  __shared__ int found_s;
+  __shared__ int found_s, units;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.num_seqs + THREADS - 1) / THREADS;
   const int s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
-  auto blocks = [&](int s) -> int64_t {
-    const int nq = query_at(p, s + 1) - query_at(p, s);
+  auto blocks = [&](int s, int& rbs) -> int64_t {
+    int q_lo;
+    const int nq = queries_of(p, s, s + 1, p.max_queries, q_lo);
+    rbs = row_blocks(p, nq, ROWS);
     if (nq <= 0) return 0;
     const Own o = own_of(p, s);
-    return static_cast<int64_t>(key_blocks(o.L - o.start)) * row_blocks(p, nq, ROWS);
+    return static_cast<int64_t>(key_blocks(o.L - o.start)) * rbs;
   };
   int64_t mine = 0;
-  for (int s = s0; s < s1; ++s) mine += blocks(s);
+  int my_units = 0, rbs;
+  for (int s = s0; s < s1; ++s) {
+    mine += blocks(s, rbs);
+    my_units += rbs;
+  }
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -550,10 +475,10 @@ __device__ __forceinline__ Place locate(const Params& p, int range, int ranges, 
     if (lane >= o) incl += x;
   }
   if (lane == 31) warp_sum[warp] = incl;
-  if (tid == 0) {
-    found_at = 0;
-    found_s = 0;
-  }
+  if (tid == 0) found_at = found_s = units = 0;
+  __syncthreads();
+  my_units = __reduce_add_sync(0xffffffffu, my_units);
+  if (lane == 0) atomicAdd(&units, my_units);
   __syncthreads();
   int64_t before = incl - mine, total = 0;
 #pragma unroll
@@ -563,15 +488,16 @@ __device__ __forceinline__ Place locate(const Params& p, int range, int ranges, 
   }
   Place pl;
   pl.total = total;
-  // no more ranges than leave `least` blocks to each
-  pl.ranges = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(ranges), total / least)));
+  // one for each unit, and no more than leave `least` blocks to each where units are cut
+  const int64_t most = max(static_cast<int64_t>(units), total / least);
+  pl.ranges = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(ranges), most)));
   u0 = range < pl.ranges ? cut(total, range, pl.ranges) : total;
   u1 = range < pl.ranges ? cut(total, range + 1, pl.ranges) : total;
   if (u0 >= before && u0 < before + mine) {
     int s = s0;
     int64_t at = before;
     for (; s < s1; ++s) {
-      const int64_t n = blocks(s);
+      const int64_t n = blocks(s, rbs);
       if (u0 < at + n) break;
       at += n;
     }
@@ -601,10 +527,16 @@ __global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT))
   int64_t u0, u1;
   const Place pl = locate<ROWS>(p, range, ranges, least, u0, u1);
   int64_t begin = pl.at;  // first block of the sequence
-  for (int64_t u = u0, s = pl.s; u < u1; ++s) {
-    const int q_lo = query_at(p, s), nq = query_at(p, s + 1) - q_lo;
+  Own own{};
+  int q_lo = 0, nq = 0, s = pl.s;
+  auto look = [&](int i) {  // sequence i
+    nq = queries_of(p, i, i + 1, p.max_queries, q_lo);
+    own = own_of(p, i);
+  };
+  if (u0 < u1) look(s);
+  for (int64_t u = u0; u < u1; ++s) {
+    if (s != pl.s) look(s);
     if (nq <= 0) continue;
-    const Own own = own_of(p, s);
     const int nb = key_blocks(own.L - own.start), rbs = row_blocks(p, nq, ROWS);
     for (int rb = static_cast<int>((u - begin) / nb); rb < rbs && u < u1; ++rb) {
       const int64_t first = begin + static_cast<int64_t>(rb) * nb;  // of the unit
@@ -617,7 +549,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT))
       w.row_lo = rb * ROWS;
       w.R = static_cast<int>(min(static_cast<int64_t>(nq) * heads - w.row_lo, static_cast<int64_t>(ROWS)));
       w.h = h;
-      w.table = static_cast<int>(s);
+      w.table = s;
       w.from = own.start + b * BLOCK;
       w.to = min(own.L, w.from + take * BLOCK);
       auto row_at = [&](int r) {
@@ -626,16 +558,28 @@ __global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT))
       };
       int* const lims = reinterpret_cast<int*>(smem + SH::OFF_LIM);
       for (int r = threadIdx.x; r < ROWS; r += THREADS)
-        lims[r] = r < w.R ? limit_of(p, static_cast<int>(s), q_lo + (w.row_lo + r) / heads) : 0;
+        lims[r] = r < w.R ? limit_of(p, s, q_lo + (w.row_lo + r) / heads) : 0;
+      int* const parts = reinterpret_cast<int*>(smem + SH::OFF_PARTS);
+      auto count_parts = [&]() {  // of each row; by the last warp, that the limits leave idle
+        const int r = static_cast<int>(threadIdx.x) - (THREADS - 32);
+        if (r < 0 || r >= w.R) return;
+        const int q = (w.row_lo + r) / heads;
+        parts[r] = own.pre > 0 ? parts_of(p, own.group, q_lo + q, w.row_lo + r - q * heads, h) : 0;
+      };
+      const bool counted = waited;  // before the keys where the prefix stage is known to be complete
+      if (counted) count_parts();
       stream<D, BF16, NT>(p, w, smem);
+      wait();
+      if (!counted) {
+        count_parts();
+        __syncthreads();
+      }
       const int64_t slot = 2ll * blockIdx.x + (starts ? 0 : 1), nslot = 2ll * ranges * p.Hkv * ROWS;
       if (whole) {
-        wait();
-        const int parts = own.pre > 0 ? min(__ldcg(p.parts + own.group), p.most_parts) : 0;
         for (int e = threadIdx.x; e < w.R * G; e += THREADS) {
           const int r = e / G, d4 = e - r * G;
           Part x = of_warps<D, NT>(smem, r, d4);
-          add_prefix<D>(p, x, row_at(r), d4, parts);
+          add_prefix<D>(p, x, row_at(r), d4, parts[r]);
           write_out<D, BF16>(p, x, row_at(r), d4);
         }
       } else {
@@ -649,10 +593,8 @@ __global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT))
         }
         // the ranges rf .. rl hold the unit's blocks
         const int64_t end = first + nb;
-        const int rf = static_cast<int>(((first + 1) * pl.ranges + pl.total - 1) / pl.total) - 1;  // last with cut(rf) <= first
-        const int rl = static_cast<int>((end * pl.ranges + pl.total - 1) / pl.total) - 1;          // first with cut(rl + 1) >= end
+        const int rf = range_of(first, pl.total, pl.ranges), rl = range_of(end - 1, pl.total, pl.ranges);
         __threadfence();
-        wait();
         __syncthreads();
         if (threadIdx.x == 0) {
           const int64_t n = static_cast<int64_t>(rf) * p.Hkv + h;  // a range begins one cut unit at most
@@ -662,7 +604,6 @@ __global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT))
         if (last_part) {
           __threadfence();
           const bool starts_late = first > cut(pl.total, rf, pl.ranges);
-          const int parts = own.pre > 0 ? min(__ldcg(p.parts + own.group), p.most_parts) : 0;
           for (int e = threadIdx.x; e < w.R * G; e += THREADS) {
             const int r = e / G, d4 = e - r * G;
             Part x;
@@ -680,7 +621,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT))
 #pragma unroll
               for (int k = 0; k < BATCH; ++k) x.add(ml[k], y[k]);
             }
-            add_prefix<D>(p, x, row_at(r), d4, parts);
+            add_prefix<D>(p, x, row_at(r), d4, parts[r]);
             write_out<D, BF16>(p, x, row_at(r), d4);
           }
         }

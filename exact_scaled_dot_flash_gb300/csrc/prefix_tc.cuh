@@ -3,8 +3,8 @@
 // multiple of 128): the prefix of a group with more than 32 rows (queries x heads of a kv
 // head), and the own keys of sequences with many new tokens.
 //
-// The pipeline is the dense forward's (attn_tc.cuh: 384 threads, two tiles of 128 rows that share
-// every K/V tile, S and P in tensor memory, MMA order S_0 PV_1 S_1 PV_0, lazy rescale), with
+// The pipeline is the dense forward's (attn_tc.cuh: two tiles of 128 rows, S and P in tensor
+// memory, MMA order S_0 PV_1 S_1 PV_0, lazy rescale), with
 //  - rows packed as row = query * heads + head, whatever the number of heads: each softmax
 //    thread copies its own row of q into the swizzled tile (a TMA box would want heads
 //    to divide 128);
@@ -12,9 +12,13 @@
 //    [pages, page_size, Hkv, D] of the cache;
 //  - values past the last key set to zero in shared memory before their product: a page's
 //    unwritten rows may hold NaN, which a probability of 0 does not remove;
-//  - prefix stage: a CTA takes one part of the keys (Item) for 256 rows and leaves (m, l, O);
-//    suffix stage: a CTA takes all own keys of a sequence for 256 rows and joins them
-//    with the prefix's parts.
+//  - one CTA an SM that goes through several pieces of work without a break: a warp works out
+//    the next piece from the metadata while the others compute, and the copies of its
+//    first tiles fly during the epilogue of the piece before.
+// Prefix stage: pieces of equal ranges of all groups' blocks (prefix.cuh), 128 keys for 256
+// rows. Where a unit has 128 rows or fewer (the last rows of a group), the two row tiles take the
+// same rows and every other key tile, and leave a part each: a block is 256 keys.
+// Suffix stage: a piece is all own keys of a sequence for 256 rows, joined with the prefix's parts.
 #pragma once
 
 #include <algorithm>
@@ -30,7 +34,7 @@ constexpr int BN = 128;
 constexpr int NQ = 2;
 constexpr int ROWS = BM * NQ;
 constexpr int NUM_THREADS = 384;
-constexpr int WARP_TMA = 8, WARP_MMA = 9;
+constexpr int WARP_TMA = 8, WARP_MMA = 9, WARP_PLAN = 10;
 constexpr int TMEM_COLS = 512;
 constexpr int REG_SOFTMAX = 200;
 constexpr int REG_OTHER = 96;
@@ -41,7 +45,7 @@ struct Cfg {
   static constexpr int NCHUNK = D / 64;
   static constexpr int CHUNK_BYTES = BN * 128;
   static constexpr int TILE_BYTES = NCHUNK * CHUNK_BYTES;
-  static constexpr int STAGES = D == 128 ? 4 : 8;
+  static constexpr int STAGES = D == 128 ? 5 : 8;
   static constexpr uint32_t LAYOUT = 2u;  // 128-byte swizzle
   static constexpr int SBO = 1024;
   static constexpr int KSTEPS_QK = D / 16;
@@ -51,99 +55,163 @@ struct Cfg {
   static constexpr int OFF_BAR = OFF_KV + STAGES * TILE_BYTES;
   static constexpr int BAR_FULL = 0, BAR_EMPTY = STAGES, BAR_Q = 2 * STAGES, BAR_S = BAR_Q + NQ;
   static constexpr int BAR_P = BAR_S + NQ, BAR_O = BAR_P + NQ, BAR_DONE = BAR_O + NQ;
-  static constexpr int OFF_MISC = OFF_BAR + (BAR_DONE + 1) * 8;
-  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static constexpr int BAR_WORK = BAR_DONE + 1, BAR_FREE = BAR_WORK + 2;  // the pieces' ring
+  static constexpr int OFF_MISC = OFF_BAR + (BAR_FREE + 2) * 8;
+  static constexpr int OFF_WORK = (OFF_MISC + 16 + 15) / 16 * 16;
+  static constexpr int SMEM_BYTES = OFF_WORK + 2 * 64 + 1024;
 };
 
+// A piece of work: rows row0 .. of a unit (queries from q_lo on, nq of them, times heads), keys
+// [lo, to), of which the key tiles j0 .. j0 + n - 1 of a row tile are this piece's.
 struct Work {
-  int s0, s1;         // the unit's sequences [s0, s1)
-  int table;          // row of the table that names the pages
-  int q_lo, nq, h;
-  int64_t row0;       // first packed row
-  int lo, to;         // keys [lo, to), of which tiles j0 .. j0 + n - 1
-  int j0, n[NQ], nmax;
-  int group, part, parts;
+  int s0, s1;          // the unit's sequences
+  int table;           // row of the table that names the pages
+  int q_lo, nq, h, row0;
+  int lo, to, j0;
+  int n[NQ];           // key tiles of each row tile; split: both have the same rows, and tiles j0, j0 + 2 ..
+  int split, part, group;
+  int state;           // 0: no more work, 1: rows may see fewer keys than [lo, to), 2: every row sees all
 };
+static_assert(sizeof(Work) == 64);
+
+// The pieces of a CTA, one after another. A warp calls it, all lanes with the same results.
+template <bool PREFIX>
+struct Planner {
+  int64_t u, u1, first;  // prefix: blocks, first one of group g
+  int g;
+  int64_t item, items;   // suffix
+  int qblocks;
+  Share sh;
+  bool fresh;
+  Rec rec;
+  int a, b, pre, table, to, q_lo, nq;
+  bool open;
+
+  __device__ __forceinline__ void load_group(const Params& p) {
+    rec = rec_of(p, g, BN, ROWS, true);
+    group_range(p, g, a, b);
+    nq = queries_of(p, a, b, p.max_group_queries, q_lo);
+    pre = prefix_len(p, g);
+    // the member whose row covers the most of the prefix, and whether a row sees less of it
+    unsigned long long best = 0;
+    int least = 0x7fffffff;
+    for (int s = a + static_cast<int>(threadIdx.x & 31); s < b; s += 32) {
+      const int L = seq_len(p, s), n = query_at(p, s + 1) - query_at(p, s);
+      const unsigned long long x = (static_cast<unsigned long long>(min(L, pre)) << 32) | static_cast<uint32_t>(~s);
+      best = x > best ? x : best;
+      if (n > 0) least = min(least, p.causal ? L - n + 1 : L);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const unsigned long long x = __shfl_xor_sync(0xffffffffu, best, o);
+      best = x > best ? x : best;
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    table = static_cast<int>(~static_cast<uint32_t>(best));
+    to = static_cast<int>(best >> 32);
+    open = least >= to && !(p.causal && p.positions);
+  }
+
+  __device__ __forceinline__ bool next(const Params& p, Work& w) {
+    const int heads = p.Hq / p.Hkv;
+    if constexpr (PREFIX) {
+      if (u >= u1) return false;
+      while (fresh || u >= first + blocks_of(p, rec)) {
+        if (!fresh) {
+          first += blocks_of(p, rec);
+          ++g;
+        }
+        fresh = false;
+        rec = rec_of(p, g, BN, ROWS, true);
+        if (u < first + blocks_of(p, rec)) load_group(p);
+      }
+      const int64_t off = u - first, full = full_blocks(p, rec);
+      w.split = off >= full;
+      const int n = w.split ? (rec.nb + 1) / 2 : rec.nb;
+      const int64_t in = w.split ? off - full : off;
+      const int unit = static_cast<int>(in / n), k0 = static_cast<int>(in - static_cast<int64_t>(unit) * n);
+      const int take = static_cast<int>(min(static_cast<int64_t>(n - k0), u1 - u));
+      const int piece = static_cast<int>(blockIdx.x) - range_of(u - k0, sh.total, sh.ranges);
+      u += take;
+      w.s0 = a;
+      w.s1 = b;
+      w.table = table;
+      w.q_lo = q_lo;
+      w.nq = nq;
+      w.h = unit % p.Hkv;
+      w.row0 = (w.split ? rec.rbs - 1 : unit / p.Hkv) * ROWS;
+      w.lo = 0;
+      w.to = to;
+      w.group = g;
+      const int tiles = (to + BN - 1) / BN;  // with keys; a reader shorter than the prefix has fewer than nb
+      if (w.split) {
+        w.part = 2 * piece;
+        w.j0 = 2 * k0;
+        const int k = max(min(2 * (k0 + take), tiles) - w.j0, 0);
+        w.n[0] = (k + 1) / 2;
+        w.n[1] = k / 2;
+      } else {
+        w.part = piece;
+        w.j0 = k0;
+        w.n[0] = max(min(k0 + take, tiles) - k0, 0);
+        w.n[1] = w.row0 + BM < nq * heads ? w.n[0] : 0;
+      }
+      w.state = open ? 2 : 1;
+      return true;
+    } else {
+      for (; item < items; item += gridDim.x) {
+        int64_t r = item;
+        w.h = static_cast<int>(r % p.Hkv);
+        r /= p.Hkv;
+        w.row0 = static_cast<int>(qblocks - 1 - r % qblocks) * ROWS;  // the last blocks see the most keys and go first
+        w.s0 = w.table = static_cast<int>(r / qblocks);
+        w.s1 = w.s0 + 1;
+        w.nq = queries_of(p, w.s0, w.s1, p.max_queries, w.q_lo);
+        if (w.row0 >= static_cast<int64_t>(w.nq) * heads) continue;
+        const rows::Own own = rows::own_of(p, w.s0);
+        w.group = own.pre > 0 ? own.group : -1;
+        w.lo = own.start;
+        w.to = own.L;
+        w.j0 = own.start / BN;
+        w.split = w.part = 0;
+        const int all = query_at(p, w.s1) - w.q_lo;
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) {
+          const int r0 = w.row0 + t * BM;
+          w.n[t] = 0;
+          if (r0 >= static_cast<int64_t>(w.nq) * heads) continue;
+          int end = w.to;  // keys that the tile's rows see
+          if (p.causal && !p.positions) end = min(end, w.to - all + min(w.nq - 1, (r0 + BM - 1) / heads) + 1);
+          w.n[t] = end > w.lo ? (end + BN - 1) / BN - w.j0 : 0;
+        }
+        w.state = 1;
+        item += gridDim.x;
+        return true;
+      }
+      return false;
+    }
+  }
+};
+
+// A value that is the same in all lanes of a warp, from a reduction, whose result is uniform.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
 
 template <int D, bool BF16, bool PREFIX>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-              const __grid_constant__ Params p, int ctas, int qblocks, int* counters, int num_counters) {
+              const __grid_constant__ Params p, int qblocks, int64_t items, int* counters, int num_counters) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_dyn[];
-  __shared__ rows::Item shared_item;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_u32(smem);
   auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  Work* const works = reinterpret_cast<Work*>(smem + C::OFF_WORK);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int heads = p.Hq / p.Hkv;
   if constexpr (PREFIX) {
     asm volatile("griddepcontrol.launch_dependents;");  // the suffix stage may come up: it waits before it reads
     for (int i = blockIdx.x * NUM_THREADS + threadIdx.x; i < num_counters; i += gridDim.x * NUM_THREADS) counters[i] = 0;
   }
-
-  // -------------------------------------------------------------- the CTA's work
-  Work w;
-  if constexpr (PREFIX) {
-    if (warp == 0) {
-      const rows::Item x = rows::item_of(p, blockIdx.x, ctas, BN, ROWS);
-      if (lane == 0) shared_item = x;
-    }
-    __syncthreads();
-    const rows::Item it = shared_item;
-    if (it.g < 0) return;
-    group_range(p, it.g, w.s0, w.s1);
-    const int pre = prefix_len(p, it.g);
-    w.table = reader_of(p, w.s0, w.s1, pre);
-    w.h = it.h;
-    w.row0 = static_cast<int64_t>(it.rb) * ROWS;
-    w.group = it.g;
-    w.part = it.part;
-    w.parts = it.parts;
-    w.lo = 0;
-    w.to = min(pre, seq_len(p, w.table));
-    w.j0 = it.part * it.chunk;
-    if (it.part == 0 && it.rb == 0 && it.h == 0 && threadIdx.x == 0) p.parts[it.g] = it.parts;
-  } else {
-    int item = blockIdx.x;
-    w.h = item % p.Hkv;
-    item /= p.Hkv;
-    w.row0 = static_cast<int64_t>(qblocks - 1 - item % qblocks) * ROWS;  // the last blocks see the most keys and go first
-    w.table = w.s0 = item / qblocks;
-    w.s1 = w.s0 + 1;
-    const rows::Own own = rows::own_of(p, w.s0);
-    w.group = own.pre > 0 ? own.group : -1;
-    w.lo = own.start;
-    w.to = own.L;
-    w.j0 = own.start / BN;
-    w.part = w.parts = 0;
-  }
-  w.q_lo = query_at(p, w.s0);
-  w.nq = max(query_at(p, w.s1) - w.q_lo, 0);
-  const int64_t unit_rows = static_cast<int64_t>(w.nq) * heads;
-  if (w.row0 >= unit_rows) {  // CTA-uniform
-    // the suffix stage does not end before the prefix's: the next call on the stream may use the workspace
-    if constexpr (!PREFIX) asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
-  w.nmax = 0;
-#pragma unroll
-  for (int t = 0; t < NQ; ++t) {
-    const int64_t r0 = w.row0 + t * BM;
-    w.n[t] = 0;
-    if (r0 >= unit_rows) continue;
-    int end = w.to;  // keys that the tile's rows see
-    if constexpr (PREFIX) {
-      end = static_cast<int>(min(static_cast<int64_t>(end), (static_cast<int64_t>(w.j0) + shared_item.chunk) * BN));
-    } else if (p.causal && !p.positions) {
-      const int64_t last_q = min(static_cast<int64_t>(w.nq) - 1, (r0 + BM - 1) / heads);
-      end = static_cast<int>(min(static_cast<int64_t>(end), static_cast<int64_t>(w.to) - w.nq + last_q + 1));
-    }
-    w.n[t] = end > w.lo && end > w.j0 * BN ? (end + BN - 1) / BN - w.j0 : 0;
-    w.nmax = max(w.nmax, w.n[t]);
-  }
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(bar(C::BAR_FULL + s), 1);
@@ -156,11 +224,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(bar(C::BAR_O + t), 1);
     }
     mbar_init(bar(C::BAR_DONE), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::BAR_WORK + i), 1);
+      mbar_init(bar(C::BAR_FREE + i), 10);  // the copying and the issuing warp, 8 softmax warps
+    }
     mbar_init_fence();
   }
   if (warp == WARP_MMA) {
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish();
+  }
+  Planner<PREFIX> plan;
+  if constexpr (PREFIX) {
+    plan.sh = share_out<NUM_THREADS>(p, SMS, BN, ROWS, true);
+    plan.u = plan.sh.u0;
+    plan.u1 = plan.sh.u1;
+    plan.first = plan.sh.first;
+    plan.g = plan.sh.g;
+    plan.fresh = true;
+  } else {
+    plan.item = blockIdx.x;
+    plan.items = items;
+    plan.qblocks = qblocks;
   }
   tc_fence_before();
   __syncthreads();
@@ -169,40 +254,86 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto fail = [&]() {
     if (p.status) atomicOr(p.status, STATUS_TIMEOUT);
   };
+  // Piece i for a warp that takes part in it (all lanes); false: none, or a wait gave up.
+  auto get_work = [&](int i, Work& w) {
+    if (!warp_wait(bar(C::BAR_WORK + (i & 1)), (i >> 1) & 1)) {
+      if (lane == 0) fail();
+      return false;
+    }
+    w = works[i & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::BAR_FREE + (i & 1)));
+    return w.state != 0;
+  };
 
   if (warp >= 8) {
     setmaxnreg_dec<REG_OTHER>();
-    if (warp == WARP_TMA && lane == 0) {
-      // ------------------------------------------------------------ producer
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
+    if (warp == WARP_PLAN) {
+      // ------------------------------------------------------------ the pieces, ahead of the others
+      for (int i = 0;; ++i) {
+        Work w{};
+        const bool more = plan.next(p, w);
+        bool free = false;  // looked at now and then: the others need the issue slots
+        for (int k = 0; k < 4000000 && !(free = mbar_test_nb(bar(C::BAR_FREE + (i & 1)), ((i >> 1) & 1) ^ 1)); ++k) __nanosleep(500);
+        if (!__all_sync(0xffffffffu, free)) {
+          if (lane == 0) fail();
+          break;
+        }
+        if (!more) w.state = 0;
+        if (lane == 0) {
+          works[i & 1] = w;
+          mbar_arrive(bar(C::BAR_WORK + (i & 1)));
+        }
+        __syncwarp();
+        if (!more) break;
+      }
+    } else if (warp == WARP_TMA) {
+      // ------------------------------------------------------------ producer: a lane for each box of a tile
       const int box_rows = p.page_size < BN ? p.page_size : BN;
       const int boxes = BN / box_rows;
       int it = 0;
       bool ok = true;
-      for (int jj = 0; jj < w.nmax && ok; ++jj) {
-        const int j = w.j0 + jj;  // key tile
-        for (int kv = 0; kv < 2; ++kv, ++it) {
-          const int st = it % C::STAGES;
-          if (!mbar_wait(bar(C::BAR_EMPTY + st), ((it / C::STAGES) & 1) ^ 1)) { ok = false; break; }
-          mbar_arrive_expect_tx(bar(C::BAR_FULL + st), C::TILE_BYTES);
-          const CUtensorMap* m = kv == 0 ? &tm_k : &tm_v;
-          for (int i = 0; i < boxes; ++i) {
-            const int key = j * BN + i * box_rows;
-            const int page = key < w.to ? page_of(p, w.table, key / p.page_size) : -1;  // -1: zero-filled box
-            // checked build: the box lands inside its chunk of the ring slot (a
-            // skipped copy leaves the slot's barrier to time out)
-            if (!range_in_bounds(p.status, i * box_rows, box_rows, BN)) continue;
-            for (int c = 0; c < C::NCHUNK; ++c)
-              tma_load_4d(sb + C::OFF_KV + st * C::TILE_BYTES + c * C::CHUNK_BYTES + i * box_rows * 128, m,
-                          bar(C::BAR_FULL + st), c * 64, w.h, key % p.page_size, page);
+      Work w{};
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+      }
+      auto load = [&](const CUtensorMap* m, int j) {  // key tile j into the next slot
+        // the page is looked up before the wait: it costs a trip to L2
+        const int key = j * BN + lane * box_rows, blk = key / p.page_size, in_page = key - blk * p.page_size;
+        const int page = lane < boxes && key < w.to ? page_of(p, w.table, blk) : -1;  // -1: zero-filled box
+        const int st = it % C::STAGES;
+        if (!warp_wait(bar(C::BAR_EMPTY + st), ((it / C::STAGES) & 1) ^ 1)) return false;
+        ++it;
+        if (lane == 0) mbar_arrive_expect_tx(bar(C::BAR_FULL + st), C::TILE_BYTES);
+        __syncwarp();
+        // checked build: the box lands inside its chunk of the ring slot (a
+        // skipped copy leaves the slot's barrier to time out)
+        if (lane < boxes && range_in_bounds(p.status, lane * box_rows, box_rows, BN)) {
+          for (int c = 0; c < C::NCHUNK; ++c)
+            tma_load_4d(sb + C::OFF_KV + st * C::TILE_BYTES + c * C::CHUNK_BYTES + lane * box_rows * 128, m,
+                        bar(C::BAR_FULL + st), c * 64, w.h, in_page, page);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int i = 0; ok && get_work(i, w); ++i) {
+        if (w.split) {  // in the order of the MMAs
+          for (int j = 0; j <= w.n[0] && ok; ++j) {
+            if (j < w.n[0]) ok = load(&tm_k, w.j0 + 2 * j);
+            if (ok && j >= 1 && j - 1 < w.n[1]) ok = load(&tm_v, w.j0 + 2 * j - 1);
+            if (ok && j < w.n[1]) ok = load(&tm_k, w.j0 + 2 * j + 1);
+            if (ok && j < w.n[0]) ok = load(&tm_v, w.j0 + 2 * j);
           }
+        } else {
+          const int nmax = max(w.n[0], w.n[1]);
+          for (int j = 0; j < nmax && ok; ++j) ok = load(&tm_k, w.j0 + j) && load(&tm_v, w.j0 + j);
         }
       }
-      if (!ok) fail();
+      if (!ok && lane == 0) fail();
       for (int st = 0; st < C::STAGES && st < it; ++st) {
         const int fills = (it - st + C::STAGES - 1) / C::STAGES;
-        if (!mbar_wait(bar(C::BAR_FULL + st), (fills - 1) & 1)) fail();
+        if (!warp_wait(bar(C::BAR_FULL + st), (fills - 1) & 1) && lane == 0) fail();
       }
     } else if (warp == WARP_MMA) {
       // ------------------------------------------------------------ MMA issuer
@@ -210,10 +341,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       constexpr uint32_t idesc_qk = make_idesc_f16(BF16, BM, BN, false);
       constexpr uint32_t idesc_pv = make_idesc_f16(BF16, BM, D, true);
       constexpr int ST = C::STAGES;
-      const int n0 = w.n[0], n1 = w.n[1], nmax = w.nmax;
-      bool ok = true;
-      for (int t = 0; t < NQ && ok; ++t)
-        if ((t ? n1 : n0) > 0 && !warp_wait(bar(C::BAR_Q + t), 0)) ok = false;
       const uint64_t dq0 = smem_desc(sb, 16, C::SBO, C::LAYOUT);
       const uint64_t dk0 = smem_desc(sb + C::OFF_KV, 16, C::SBO, C::LAYOUT);
       const uint64_t dv0 = smem_desc(sb + C::OFF_KV, C::CHUNK_BYTES, C::SBO, C::LAYOUT);
@@ -221,23 +348,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       constexpr uint32_t CHUNK16 = C::CHUNK_BYTES >> 4;
       constexpr uint32_t VSTEP16 = (16 * 128) >> 4;
       auto kstep = [](int k) -> uint32_t { return (k / 4) * CHUNK16 + (k % 4) * 2; };
-      bool fix = nmax > 0 && static_cast<int64_t>(w.j0 + nmax) * BN > w.to;  // the last tile goes past the keys
-      auto wait_full = [&](int idx) {
-        if (!warp_wait(bar(C::BAR_FULL + idx % ST), (idx / ST) & 1)) return false;
-        if (fix && idx == 2 * nmax - 1) {  // values past the last key: whole rows, the swizzle stays inside them
-          fix = false;
-          uint8_t* const v = smem + C::OFF_KV + idx % ST * C::TILE_BYTES;
-          for (int e = max(w.to - (w.j0 + nmax - 1) * BN, 0) * 8 + lane; e < BN * 8; e += 32)
+      int it0 = 0;            // ring slots of the pieces before
+      int done[NQ] = {0, 0};  // key tiles of each row tile in the pieces before
+      int used[NQ] = {0, 0};  // pieces with such
+      bool ok = true;
+      Work w{};
+      auto wait_full = [&](int idx) { return warp_wait(bar(C::BAR_FULL + idx % ST), (idx / ST) & 1); };
+      // Values past the last key (tile j of the unit, in ring slot idx): whole rows, the swizzle stays inside them.
+      auto fix_values = [&](int j, int idx) {
+        if ((j + 1) * BN <= w.to) return;
+        uint8_t* const v = smem + C::OFF_KV + idx % ST * C::TILE_BYTES;
+        for (int e = max(w.to - j * BN, 0) * 8 + lane; e < BN * 8; e += 32)
 #pragma unroll
-            for (int c = 0; c < C::NCHUNK; ++c) *reinterpret_cast<uint4*>(v + c * C::CHUNK_BYTES + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        return true;
+          for (int c = 0; c < C::NCHUNK; ++c) *reinterpret_cast<uint4*>(v + c * C::CHUNK_BYTES + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
       };
-      auto issue_s = [&](int t, int j) {
+      auto issue_s = [&](int t, int idx) {
         const uint64_t a = dq0 + t * TILE16;
-        const uint64_t b = dk0 + ((2 * j) % ST) * TILE16;
+        const uint64_t b = dk0 + (idx % ST) * TILE16;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < C::KSTEPS_QK; ++k)
@@ -246,44 +375,100 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         __syncwarp();
       };
-      auto issue_pv = [&](int t, int j) {
-        const uint64_t b = dv0 + ((2 * j + 1) % ST) * TILE16;
+      auto issue_pv = [&](int t, int j, int idx, bool last) {
+        const uint64_t b = dv0 + (idx % ST) * TILE16;
         const uint32_t d = tmem + 256 + t * D;
         const uint32_t a = tmem + t * BN + C::COL_P;
         if (elect_one()) {
           umma_ts(d, a, b, idesc_pv, j > 0 ? 1u : 0u);
 #pragma unroll
           for (int k = 1; k < C::KSTEPS_PV; ++k) umma_ts(d, a + k * 8, b + k * VSTEP16, idesc_pv, 1u);
-          if (j == (t ? n1 : n0) - 1) umma_commit(bar(C::BAR_O + t));
+          if (last) umma_commit(bar(C::BAR_O + t));
         }
         __syncwarp();
       };
-      for (int j = 0; j <= nmax && ok; ++j) {  // every wait is bounded
-        if (j < nmax) {
-          if (!wait_full(2 * j)) { ok = false; break; }
-          tc_fence_after();
-          if (j < n0) issue_s(0, j);
-        }
-        if (j >= 1 && j - 1 < n1) {
-          if (j - 1 >= n0 && !wait_full(2 * (j - 1) + 1)) { ok = false; break; }
-          if (!warp_wait(bar(C::BAR_P + 1), (j - 1) & 1)) { ok = false; break; }
-          tc_fence_after();
-          issue_pv(1, j - 1);
-        }
-        if (j >= 1) {
-          if (elect_one()) umma_commit(bar(C::BAR_EMPTY + (2 * (j - 1) + 1) % ST));
-          __syncwarp();
-        }
-        if (j < nmax) {
-          if (j < n1) issue_s(1, j);
-          if (elect_one()) umma_commit(bar(C::BAR_EMPTY + (2 * j) % ST));
-          __syncwarp();
-          if (j < n0) {
-            if (!wait_full(2 * j + 1) || !warp_wait(bar(C::BAR_P + 0), j & 1)) { ok = false; break; }
-            tc_fence_after();
-            issue_pv(0, j);
+      auto release = [&](int idx) {
+        if (elect_one()) umma_commit(bar(C::BAR_EMPTY + idx % ST));
+        __syncwarp();
+      };
+      auto wait_p = [&](int t, int j) { return warp_wait(bar(C::BAR_P + t), (done[t] + j) & 1); };
+      for (int i = 0; ok && get_work(i, w); ++i) {
+        // the loops below run in uniform registers, as the MMAs take their operands
+        const int n0 = uniform(w.n[0]), n1 = uniform(w.n[1]), nmax = max(n0, n1);
+        const bool split = uniform(w.split) != 0;
+        for (int t = 0; t < NQ && ok; ++t)
+          if ((t ? n1 : n0) > 0) {
+            ok = warp_wait(bar(C::BAR_Q + t), used[t] & 1);
+            ++used[t];
           }
+        // every wait is bounded
+        if (split) {
+          int idx = it0;
+          for (int j = 0; j <= n0 && ok; ++j) {
+            if (j < n0) {
+              if (!(ok = wait_full(idx))) break;
+              tc_fence_after();
+              issue_s(0, idx);
+              release(idx++);
+            }
+            if (j >= 1 && j - 1 < n1) {
+              if (!(ok = wait_full(idx))) break;
+              fix_values(w.j0 + 2 * j - 1, idx);
+              if (!(ok = wait_p(1, j - 1))) break;
+              tc_fence_after();
+              issue_pv(1, j - 1, idx, j == n1);
+              release(idx++);
+            }
+            if (j < n1) {
+              if (!(ok = wait_full(idx))) break;
+              tc_fence_after();
+              issue_s(1, idx);
+              release(idx++);
+            }
+            if (j < n0) {
+              if (!(ok = wait_full(idx))) break;
+              fix_values(w.j0 + 2 * j, idx);
+              if (!(ok = wait_p(0, j))) break;
+              tc_fence_after();
+              issue_pv(0, j, idx, j == n0 - 1);
+              release(idx++);
+            }
+          }
+          it0 = idx;
+        } else {
+          for (int j = 0; j <= nmax && ok; ++j) {
+            const int idx = it0 + 2 * j;
+            if (j < nmax) {
+              if (!(ok = wait_full(idx))) break;
+              tc_fence_after();
+              if (j < n0) issue_s(0, idx);
+            }
+            if (j >= 1 && j - 1 < n1) {
+              if (j - 1 >= n0) {
+                if (!(ok = wait_full(idx - 1))) break;
+                fix_values(w.j0 + j - 1, idx - 1);
+              }
+              if (!(ok = wait_p(1, j - 1))) break;
+              tc_fence_after();
+              issue_pv(1, j - 1, idx - 1, j == n1);
+            }
+            if (j >= 1) release(idx - 1);
+            if (j < nmax) {
+              if (j < n1) issue_s(1, idx);
+              release(idx);
+              if (j < n0) {
+                if (!(ok = wait_full(idx + 1))) break;
+                fix_values(w.j0 + j, idx + 1);
+                if (!(ok = wait_p(0, j))) break;
+                tc_fence_after();
+                issue_pv(0, j, idx + 1, j == n0 - 1);
+              }
+            }
+          }
+          it0 += 2 * nmax;
         }
+        done[0] += n0;
+        done[1] += n1;
       }
       if (!ok && lane == 0) fail();
       if (elect_one()) umma_commit(bar(C::BAR_DONE));
@@ -296,161 +481,177 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     setmaxnreg_inc<REG_SOFTMAX>();
     const int t = warp >> 2;
     const int row = ((warp & 3) << 5) + lane;
-    const int64_t pr = w.row0 + t * BM + row;  // packed row: query * heads + head
-    const int tq = static_cast<int>(pr / heads);
-    const bool row_ok = tq < w.nq;
-    const int64_t orow = row_ok ? static_cast<int64_t>(w.q_lo + tq) * p.Hq + w.h * heads + (pr - static_cast<int64_t>(tq) * heads) : 0;
     const int64_t nrows = static_cast<int64_t>(p.num_queries) * p.Hq;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) << 5) << 16;
     const uint32_t tS = tmem + lane_off + t * BN;
     const uint32_t tP = tS + C::COL_P;
     const uint32_t tO = tmem + lane_off + 256 + t * D;
-    const int n_t = t ? w.n[1] : w.n[0];
     const float sc = p.scale_log2;
-    if (n_t > 0) {  // the thread's row of q, into the swizzled tile
-      const bool in = row_ok && in_bounds(p.status, orow, nrows);
-      const uint4* const src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + orow * D);
-      uint8_t* const dst = smem + t * C::TILE_BYTES + row * 128;
+    const int heads = p.Hq / p.Hkv;
+    int done = 0, used = 0;  // key tiles and pieces before
+    bool failed = false, waited = false;
+    for (int i = 0; !failed; ++i) {
+      Work w{};
+      if (!get_work(i, w)) break;
+      const int pr = w.row0 + (w.split ? 0 : t * BM) + row;  // packed row: query * heads + head
+      const int tq = pr / heads;
+      const bool row_ok = tq < w.nq;
+      const int64_t orow = row_ok ? static_cast<int64_t>(w.q_lo + tq) * p.Hq + w.h * heads + (pr - tq * heads) : 0;
+      const bool row_in = row_ok && in_bounds(p.status, orow, nrows);
+      const int n_t = w.n[t], step = w.split ? 2 : 1, jt = w.j0 + (w.split ? t : 0);
+      if (n_t > 0) {  // the thread's row of q, into the swizzled tile
+        const uint4* const src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + orow * D);
+        uint8_t* const dst = smem + t * C::TILE_BYTES + row * 128;
 #pragma unroll
-      for (int c = 0; c < C::NCHUNK; ++c) {
-        uint4 x[8];
+        for (int c = 0; c < C::NCHUNK; ++c) {
+          uint4 x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = in ? __ldg(src + c * 8 + i) : make_uint4(0u, 0u, 0u, 0u);
+          for (int k = 0; k < 8; ++k) x[k] = row_in ? __ldg(src + c * 8 + k) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(dst + c * C::CHUNK_BYTES + ((i ^ (row & 7)) << 4)) = x[i];
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(bar(C::BAR_Q + t));
-    }
-    int lim = 0;  // keys that the row sees
-    if (row_ok) {
-      const int i = w.q_lo + tq;
-      lim = min(w.to, limit_of(p, PREFIX ? last_at_most(p.q_offsets, w.s0, w.s1, i) : w.s0, i));
-    }
-    const int least = __reduce_min_sync(0xffffffffu, row_ok ? lim : w.to);
-    float m_run = -INFINITY, l_run = 0.f;
-    bool failed = false;
-    for (int j = 0; j < n_t; ++j) {
-      const bool ok = mbar_wait(bar(C::BAR_S + t), j & 1);
-      if (__any_sync(0xffffffffu, !ok)) { failed = true; break; }
-      tc_fence_after();
-      float s[128];
-      {
-        uint32_t sr[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, sr[c]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(sr[i >> 5][i & 31]);
-      }
-      const int key0 = (w.j0 + j) * BN;
-      if (key0 + BN > least || key0 < w.lo) {
-#pragma unroll
-        for (int i = 0; i < 128; ++i) {
-          const int key = key0 + i;
-          if (key >= lim || key < w.lo) s[i] = -INFINITY;
+          for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(dst + c * C::CHUNK_BYTES + ((k ^ (row & 7)) << 4)) = x[k];
         }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(bar(C::BAR_Q + t));
       }
-      float c0 = fmax3(s[0], s[1], s[2]), c1 = fmax3(s[3], s[4], s[5]);
-      float c2 = fmax3(s[6], s[7], s[8]), c3 = fmax3(s[9], s[10], s[11]);
-#pragma unroll
-      for (int i = 12; i < 124; i += 8) {
-        c0 = fmax3(c0, s[i], s[i + 1]);
-        c1 = fmax3(c1, s[i + 2], s[i + 3]);
-        c2 = fmax3(c2, s[i + 4], s[i + 5]);
-        c3 = fmax3(c3, s[i + 6], s[i + 7]);
+      int lim = 0;  // keys that the row sees
+      if (w.state == 2) {
+        lim = w.to;
+      } else if (row_ok) {
+        const int q = w.q_lo + tq;
+        lim = min(w.to, limit_of(p, PREFIX ? last_at_most(p.q_offsets, w.s0, w.s1, q) : w.s0, q));
       }
-      c0 = fmax3(c0, s[124], s[125]);
-      c1 = fmax3(c1, s[126], s[127]);
-      const float m_tile = fmax3(c0, c1, fmaxf(c2, c3)) * sc;
-      const bool need = m_tile > m_run + RESCALE_LOG2;
-      float alpha = 1.f;
-      if (need) {
-        alpha = fast_exp2(m_run - m_tile);
-        m_run = m_tile;
-        l_run *= alpha;
-      }
-      const float neg_m = (m_run == -INFINITY) ? 0.f : -m_run;
-      float2 sum_a = make_float2(0.f, 0.f), sum_b = make_float2(0.f, 0.f);
+      const int least = __reduce_min_sync(0xffffffffu, row_ok ? lim : w.to);
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < n_t; ++j) {
+        const bool ok = mbar_wait(bar(C::BAR_S + t), (done + j) & 1);
+        if (__any_sync(0xffffffffu, !ok)) { failed = true; break; }
+        tc_fence_after();
+        float s[128];
+        {
+          uint32_t sr[4][32];
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const int i = 64 * hh + 2 * c;
-          const float2 xa = ffma2(make_float2(s[i], s[i + 1]), make_float2(sc, sc), make_float2(neg_m, neg_m));
-          const float2 xb = ffma2(make_float2(s[i + 2], s[i + 3]), make_float2(sc, sc), make_float2(neg_m, neg_m));
-          const float2 pa = make_float2(fast_exp2(xa.x), fast_exp2(xa.y));
-          const float2 pb = make_float2(fast_exp2(xb.x), fast_exp2(xb.y));
-          sum_a = fadd2(sum_a, pa);
-          sum_b = fadd2(sum_b, pb);
-          pk[c] = pack2<BF16>(pa.x, pa.y);
-          pk[c + 1] = pack2<BF16>(pb.x, pb.y);
-        }
-        tmem_st32(tP + 32 * hh, pk);
-      }
-      l_run += (sum_a.x + sum_a.y) + (sum_b.x + sum_b.y);
-      if (j > 0 && __any_sync(0xffffffffu, need)) {
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + 32 * c, o);
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, sr[c]);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 x = fmul2(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), make_float2(alpha, alpha));
-            o[i] = __float_as_uint(x.x);
-            o[i + 1] = __float_as_uint(x.y);
-          }
-          tmem_st32(tO + 32 * c, o);
+          for (int k = 0; k < 128; ++k) s[k] = __uint_as_float(sr[k >> 5][k & 31]);
         }
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar(C::BAR_P + t));
-    }
-    // ---------------------------------------------------------------- epilogue
-    const bool have = n_t > 0;
-    if (!failed && have) {
-      const bool ok = mbar_wait(bar(C::BAR_O + t), 0);
-      if (__any_sync(0xffffffffu, !ok)) failed = true;
-    }
-    if (failed) {
-      if (lane == 0) fail();
-    } else if (w.row0 + t * BM < unit_rows) {
-      tc_fence_after();
-      const bool row_in = row_ok && in_bounds(p.status, orow, nrows);
-      if constexpr (PREFIX) {
-        const int64_t at = w.part * nrows + orow;
-        const bool ok = row_in && in_bounds(p.status, at, p.most_parts * nrows);
-        float4* const dst = reinterpret_cast<float4*>(p.o) + at * (D / 4);
-        if (have) {
+        const int key0 = (jt + j * step) * BN;
+        if (key0 + BN > least || key0 < w.lo) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k) {
+            const int key = key0 + k;
+            if (key >= lim || key < w.lo) s[k] = -INFINITY;
+          }
+        }
+        float c0 = fmax3(s[0], s[1], s[2]), c1 = fmax3(s[3], s[4], s[5]);
+        float c2 = fmax3(s[6], s[7], s[8]), c3 = fmax3(s[9], s[10], s[11]);
+#pragma unroll
+        for (int k = 12; k < 124; k += 8) {
+          c0 = fmax3(c0, s[k], s[k + 1]);
+          c1 = fmax3(c1, s[k + 2], s[k + 3]);
+          c2 = fmax3(c2, s[k + 4], s[k + 5]);
+          c3 = fmax3(c3, s[k + 6], s[k + 7]);
+        }
+        c0 = fmax3(c0, s[124], s[125]);
+        c1 = fmax3(c1, s[126], s[127]);
+        const float m_tile = fmax3(c0, c1, fmaxf(c2, c3)) * sc;
+        const bool need = m_tile > m_run + RESCALE_LOG2;
+        float alpha = 1.f;
+        if (need) {
+          alpha = fast_exp2(m_run - m_tile);
+          m_run = m_tile;
+          l_run *= alpha;
+        }
+        const float neg_m = (m_run == -INFINITY) ? 0.f : -m_run;
+        float2 sum_a = make_float2(0.f, 0.f), sum_b = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const int k = 64 * hh + 2 * c;
+            const float2 xa = ffma2(make_float2(s[k], s[k + 1]), make_float2(sc, sc), make_float2(neg_m, neg_m));
+            const float2 xb = ffma2(make_float2(s[k + 2], s[k + 3]), make_float2(sc, sc), make_float2(neg_m, neg_m));
+            const float2 pa = make_float2(fast_exp2(xa.x), fast_exp2(xa.y));
+            const float2 pb = make_float2(fast_exp2(xb.x), fast_exp2(xb.y));
+            sum_a = fadd2(sum_a, pa);
+            sum_b = fadd2(sum_b, pb);
+            pk[c] = pack2<BF16>(pa.x, pa.y);
+            pk[c + 1] = pack2<BF16>(pb.x, pb.y);
+          }
+          tmem_st32(tP + 32 * hh, pk);
+        }
+        l_run += (sum_a.x + sum_a.y) + (sum_b.x + sum_b.y);
+        if (j > 0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(tO + 32 * c, o);
             tmem_wait_ld();
-            if (ok) {
 #pragma unroll
-              for (int u = 0; u < 8; ++u)
-                dst[c * 8 + u] = make_float4(__uint_as_float(o[4 * u]), __uint_as_float(o[4 * u + 1]),
-                                             __uint_as_float(o[4 * u + 2]), __uint_as_float(o[4 * u + 3]));
+            for (int k = 0; k < 32; k += 2) {
+              const float2 x = fmul2(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), make_float2(alpha, alpha));
+              o[k] = __float_as_uint(x.x);
+              o[k + 1] = __float_as_uint(x.y);
+            }
+            tmem_st32(tO + 32 * c, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(C::BAR_P + t));
+      }
+      done += n_t;
+      // -------------------------------------------------------------- epilogue
+      const bool have = n_t > 0;
+      if (!failed && have) {
+        const bool ok = mbar_wait(bar(C::BAR_O + t), used & 1);
+        ++used;
+        if (__any_sync(0xffffffffu, !ok)) failed = true;
+      }
+      if (failed) {
+        if (lane == 0) fail();
+        break;
+      }
+      if (!w.split && w.row0 + t * BM >= w.nq * heads) continue;  // no rows of this tile
+      tc_fence_after();
+      if constexpr (PREFIX) {
+        const int64_t at = (w.part + (w.split ? t : 0)) * nrows + orow;
+        const bool ok = row_in && in_bounds(p.status, at, p.most_parts * nrows);
+        float* const dst = p.o + at * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (have) {
+            tmem_ld32(tO + 32 * c, o);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
+          }
+          if (ok) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              float x[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[8 * u + k]);
+              store8(dst + c * 32 + 8 * u, x);
             }
           }
-        } else if (ok) {
-          for (int u = 0; u < D / 4; ++u) dst[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         if (ok) p.ml[at] = make_float2(have ? m_run : -INFINITY, l_run);
       } else {
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // the prefix's parts
-        const int parts = w.group >= 0 ? min(__ldcg(p.parts + w.group), p.most_parts) : 0;
+        if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the prefix's parts
+        waited = true;
+        const int parts = w.group >= 0 && row_in ? parts_of(p, w.group, w.q_lo + tq, pr - tq * heads, w.h) : 0;
         float M = have ? m_run : -INFINITY;
-        for (int z = 0; z < parts; ++z)
-          if (row_in) M = fmaxf(M, __ldcg(p.ml + z * nrows + orow).x);
-        const float own = M == -INFINITY ? 0.f : fast_exp2(m_run - M);
+        for (int z = 0; z < parts; ++z) M = fmaxf(M, __ldcg(p.ml + z * nrows + orow).x);
+        const bool any = M != -INFINITY;
+        const float own = any ? fast_exp2(m_run - M) : 0.f;
         float sum = l_run * own;
         for (int z = 0; z < parts; ++z)
-          if (row_in && M != -INFINITY) {
+          if (any) {
             const float2 ml = __ldcg(p.ml + z * nrows + orow);
             sum = fmaf(ml.y, fast_exp2(ml.x - M), sum);
           }
@@ -465,28 +666,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tmem_wait_ld();
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0u;
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
           }
           if (row_in) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * own);
-            for (int z = 0; z < parts && M != -INFINITY; ++z) {
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * own);
+            for (int z = 0; z < parts && any; ++z) {
               const int64_t at = z * nrows + orow;
               const float f = fast_exp2(__ldcg(p.ml + at).x - M);
-              const float4* const src = reinterpret_cast<const float4*>(p.o) + at * (D / 4) + c * 8;
 #pragma unroll
-              for (int u = 0; u < 8; ++u) {
-                const float4 x = __ldcg(src + u);
-                o[4 * u] = __float_as_uint(fmaf(f, x.x, __uint_as_float(o[4 * u])));
-                o[4 * u + 1] = __float_as_uint(fmaf(f, x.y, __uint_as_float(o[4 * u + 1])));
-                o[4 * u + 2] = __float_as_uint(fmaf(f, x.z, __uint_as_float(o[4 * u + 2])));
-                o[4 * u + 3] = __float_as_uint(fmaf(f, x.w, __uint_as_float(o[4 * u + 3])));
+              for (int u = 0; u < 4; ++u) {
+                float x[8];
+                load8cg(x, p.o + at * D + c * 32 + 8 * u);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[8 * u + k] = __float_as_uint(fmaf(f, x[k], __uint_as_float(o[8 * u + k])));
               }
             }
             uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              pk[i] = pack2<BF16>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+            for (int k = 0; k < 16; ++k)
+              pk[k] = pack2<BF16>(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
               reinterpret_cast<uint4*>(dst + c * 64)[u] = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
@@ -494,6 +693,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         if (row_in && p.lse) p.lse[orow] = live ? (M + log2f(sum)) * LN2 : (sum == 0.f ? -INFINITY : sum);
       }
+    }
+    // the suffix stage does not end before the prefix's: the next call on the stream may use the workspace
+    if constexpr (!PREFIX) {
+      if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
     }
   }
   tc_fence_before();
@@ -527,11 +730,9 @@ cudaError_t launch_d(EncodeTiledFn enc, const Params& p, int* counters, int num_
   if (e != cudaSuccess) return e;
   const int64_t heads = p.Hq / p.Hkv;
   const int64_t qblocks = (p.max_queries * heads + ROWS - 1) / ROWS;
-  // prefix stage: one item a CTA; cut or not, there are no more than this
-  const int64_t ctas = PREFIX ? std::max<int64_t>(SMS, p.Hkv * ((p.num_queries * heads + ROWS - 1) / ROWS + p.num_groups))
-                              : p.num_seqs * qblocks * p.Hkv;
+  const int64_t items = p.num_seqs * qblocks * p.Hkv;
+  const int64_t ctas = PREFIX ? SMS : std::min<int64_t>(items, SMS);
   if (ctas == 0) return cudaSuccess;
-  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -542,7 +743,7 @@ cudaError_t launch_d(EncodeTiledFn enc, const Params& p, int* counters, int num_
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = PREFIX ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, tk, tv, p, SMS, static_cast<int>(qblocks), counters, num_counters);
+  return cudaLaunchKernelEx(&cfg, kern, tk, tv, p, static_cast<int>(qblocks), items, counters, num_counters);
 }
 
 template <bool BF16, bool PREFIX>
