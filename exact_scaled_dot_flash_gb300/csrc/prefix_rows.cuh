@@ -3,8 +3,8 @@
 // groups (F16/BF16, D in {64, 128}, any page size).
 //
 // Bound: the bytes of the keys and values, read once for all the rows of a kv head.
-// A warp streams its own 16-key tiles through two or three buffers of cp.async copies in shared
-// memory, without a barrier between warps:
+// A warp streams its own 16-key tiles through buffers of cp.async copies in shared memory,
+// without a barrier between warps:
 //  - S^T = K Q^T (keys x rows), then O^T = V^T P^T, by mma.sync with the cache as the A
 //    operand, so that 8 columns hold the rows instead of 16 or 128; K by ldmatrix, V by its
 //    transposing form, P^T from S^T by one movmatrix for 8 keys x 8 rows;
@@ -165,23 +165,25 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
   const int dblk = BLOCK / p.page_size, drow = BLOCK - dblk * p.page_size;
   auto find_page = [&]() { return ckey < most ? page_of(p, w.table, blk) : -1; };
   int page = find_page();
-  auto copy_tile = [&](int stage) {
+  int64_t mine = -1;  // its row of the cache; -1: zeros
+  auto copy_half = [&](uint32_t at, const uint8_t* from) {  // K or V of the tile at cfirst
     if (cfirst < most) {
-      const int64_t tok = static_cast<int64_t>(page) * p.page_size + row;
-      const int64_t mine = page >= 0 && in_bounds(status, tok, ntok) ? tok : -1;  // -1: zeros
-      const uint32_t at = ring + stage * 2 * SH::TILE_BYTES;
 #pragma unroll
       for (int j = 0; j < TILE / RPC; ++j) {
         const int r = RPC * j + lane / PIECES, c = lane % PIECES;
         const int64_t key = __shfl_sync(0xffffffffu, mine, r);
-        const int n = key < 0 ? 0 : 16;
-        const int64_t off = (key < 0 ? 0 : key) * step;
-        const uint32_t to = at + (r * PIECES + (c ^ (r & 7))) * 16;
-        copy16(to, kb + off, n);
-        copy16(to + SH::TILE_BYTES, vb + off, n);
+        copy16(at + (r * PIECES + (c ^ (r & 7))) * 16, from + (key < 0 ? 0 : key) * step, key < 0 ? 0 : 16);
       }
     }
     copy_commit();
+  };
+  auto copy_keys = [&](int stage) {
+    const int64_t tok = static_cast<int64_t>(page) * p.page_size + row;
+    mine = page >= 0 && in_bounds(status, tok, ntok) ? tok : -1;
+    copy_half(ring + stage * 2 * SH::TILE_BYTES, kb);
+  };
+  auto copy_values = [&](int stage) {  // of the same tile; then on to the next one, whose page is looked up ahead
+    copy_half(ring + stage * 2 * SH::TILE_BYTES + SH::TILE_BYTES, vb);
     cfirst += BLOCK;
     ckey += BLOCK;
     blk += dblk;
@@ -192,17 +194,19 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
     }
     page = find_page();
   };
+  // K and V of a tile are copies of their own: the place of K is free, and filled again, while V waits
 #pragma unroll
-  for (int i = 0; i < STAGES - 1; ++i) copy_tile(i);
+  for (int i = 0; i < STAGES; ++i) {
+    copy_keys(i);
+    copy_values(i);
+  }
   int stage = 0;
   // ldmatrix addresses: K rows (lane & 15), piece 2 k + lane / 16; V rows (lane & 7) + 8 (lane / 16), piece 2 k + lane / 8 % 2
   const int kr = lane & 15, vr = (lane & 7) + ((lane >> 4) << 3);
   for (int key0 = tile0; key0 < most; key0 += BLOCK) {
-    copy_wait<STAGES - 2>();
-    __syncwarp();  // the tile's copies of every lane; and every lane is done with the tile before
-    copy_tile(stage == 0 ? STAGES - 1 : stage - 1);
+    copy_wait<2 * STAGES - 1>();
+    __syncwarp();  // the tile's keys by every lane
     const uint32_t ka = ring + stage * 2 * SH::TILE_BYTES, va = ka + SH::TILE_BYTES;
-    stage = stage == STAGES - 1 ? 0 : stage + 1;
     float sc[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
@@ -220,6 +224,8 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
         }
       }
     }
+    __syncwarp();  // every lane has read them
+    copy_keys(stage);
     const bool masked = key0 + TILE > least;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -265,6 +271,8 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
       pf[i][0] = transpose8x8(pack2<BF16>(y[i][0], y[i][1]));
       pf[i][1] = transpose8x8(pack2<BF16>(y[i][2], y[i][3]));
     }
+    copy_wait<2 * STAGES - 1>();
+    __syncwarp();  // its values
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       uint32_t a[4];
@@ -272,6 +280,9 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
 #pragma unroll
       for (int i = 0; i < NT; ++i) mma16816<BF16>(acc[k][i], a, pf[i][0], pf[i][1]);
     }
+    __syncwarp();
+    copy_values(stage);
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
   }
   copy_wait<0>();
   __syncthreads();  // the ring's place takes the warps' parts

@@ -502,14 +502,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (n_t > 0) {  // the thread's row of q, into the swizzled tile
         const uint4* const src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + orow * D);
         uint8_t* const dst = smem + t * C::TILE_BYTES + row * 128;
+        uint4 x[C::NCHUNK * 8];
 #pragma unroll
-        for (int c = 0; c < C::NCHUNK; ++c) {
-          uint4 x[8];
+        for (int k = 0; k < C::NCHUNK * 8; ++k) x[k] = row_in ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = row_in ? __ldg(src + c * 8 + k) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(dst + c * C::CHUNK_BYTES + ((k ^ (row & 7)) << 4)) = x[k];
-        }
+        for (int k = 0; k < C::NCHUNK * 8; ++k)
+          *reinterpret_cast<uint4*>(dst + k / 8 * C::CHUNK_BYTES + (((k % 8) ^ (row & 7)) << 4)) = x[k];
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(bar(C::BAR_Q + t));
