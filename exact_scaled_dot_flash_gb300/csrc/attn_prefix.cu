@@ -243,7 +243,8 @@ struct Plan {
   bool prefix_tc = false, suffix_tc = false;  // the kernel for many rows
   int prefix_nt = 0, suffix_nt = 0;   // that for few: 8-row groups of a CTA
   int ranges = 0;                     // of the suffix stage
-  int64_t ml_offset = 0, o_offset = 0, cut_ml_offset = 0, cut_o_offset = 0, counter_offset = 0, bytes = 0;
+  int64_t ml_offset = 0, o_offset = 0, bytes = 0;
+  int64_t head_offset = 0, first_offset = 0, own_ml_offset = 0, own_o_offset = 0, cut_ml_offset = 0, cut_o_offset = 0;
 };
 
 Plan plan_of(const attn_paged_shape_t& s, int num_groups, int max_group_queries) {
@@ -269,10 +270,17 @@ Plan plan_of(const attn_paged_shape_t& s, int num_groups, int max_group_queries)
   const int64_t slots = 2ll * d.ranges * s.Hkv * 8 * d.suffix_nt;
   d.ml_offset = up(sizeof(Head) + num_groups * sizeof(Rec));
   d.o_offset = up(d.ml_offset + parts * rows * 8);
-  d.cut_ml_offset = d.o_offset + parts * rows * s.D * 4;
-  d.cut_o_offset = up(d.cut_ml_offset + slots * 8);
-  d.counter_offset = d.cut_o_offset + slots * s.D * 4;
-  d.bytes = d.counter_offset + up(4ll * d.ranges * s.Hkv) + 16;  // it begins at the next 32 bytes
+  d.bytes = up(d.o_offset + parts * rows * s.D * 4);
+  if (takes_rows(s) && !d.suffix_tc) {
+    d.head_offset = d.bytes;
+    d.first_offset = d.head_offset + sizeof(Head);
+    d.own_ml_offset = up(d.first_offset + s.num_seqs * 8ll);
+    d.own_o_offset = up(d.own_ml_offset + rows * 8);
+    d.cut_ml_offset = d.own_o_offset + rows * s.D * 4;
+    d.cut_o_offset = up(d.cut_ml_offset + slots * 8);
+    d.bytes = d.cut_o_offset + slots * s.D * 4;
+  }
+  d.bytes += 16;  // it begins at the next 32 bytes
   return d;
 }
 
@@ -364,29 +372,36 @@ extern "C" int attn_paged_prefix_fwd(const attn_paged_shape_t* shape, int num_gr
   p.o = reinterpret_cast<float*>(ws + plan.o_offset);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype != ATTN_F32 && takes_rows(s)) {
-    const attn::prefix::rows::Cuts cuts{reinterpret_cast<float*>(ws + plan.cut_o_offset),
-                                        reinterpret_cast<float2*>(ws + plan.cut_ml_offset),
-                                        reinterpret_cast<int*>(ws + plan.counter_offset)};
+    if (!plan.suffix_tc) {
+      p.suffix_rows = 8 * plan.suffix_nt;
+      p.suffix_ranges = plan.ranges;
+      p.suffix_head = reinterpret_cast<attn::prefix::Head*>(ws + plan.head_offset);
+      p.suffix_first = reinterpret_cast<int64_t*>(ws + plan.first_offset);
+      p.own_ml = reinterpret_cast<float2*>(ws + plan.own_ml_offset);
+      p.own_o = reinterpret_cast<float*>(ws + plan.own_o_offset);
+      p.cut_ml = reinterpret_cast<float2*>(ws + plan.cut_ml_offset);
+      p.cut_o = reinterpret_cast<float*>(ws + plan.cut_o_offset);
+    }
     const bool bf16 = dtype == ATTN_BF16;
-    const int counters = plan.ranges * s.Hkv;
     using namespace attn::prefix::rows;
+    using attn::prefix::tc::launch;
     attn::EncodeTiledFn enc = nullptr;
     if (plan.prefix_tc || plan.suffix_tc) {
       enc = attn::encode_tiled();
       if (!enc) return attn::record_cuda_error(cudaErrorNotSupported);
     }
-    using attn::prefix::tc::launch;
-    if (plan.prefix_tc)
-      e = bf16 ? launch<true, true>(enc, p, cuts.counters, counters, st) : launch<false, true>(enc, p, cuts.counters, counters, st);
-    else
-      e = bf16 ? launch_prefix<true>(p, plan.prefix_nt, cuts.counters, counters, st)
-               : launch_prefix<false>(p, plan.prefix_nt, cuts.counters, counters, st);
-    if (e != cudaSuccess) return attn::record_cuda_error(e);
-    if (plan.suffix_tc)
-      e = bf16 ? launch<true, false>(enc, p, nullptr, 0, st) : launch<false, false>(enc, p, nullptr, 0, st);
-    else
-      e = bf16 ? launch_suffix<true>(p, plan.suffix_nt, cuts, plan.ranges, st)
-               : launch_suffix<false>(p, plan.suffix_nt, cuts, plan.ranges, st);
+    const bool shared = p.num_groups > 0;
+    if (shared) {
+      if (plan.prefix_tc) e = bf16 ? launch<true, true>(enc, p, false, st) : launch<false, true>(enc, p, false, st);
+      else e = bf16 ? launch_prefix<true>(p, plan.prefix_nt, st) : launch_prefix<false>(p, plan.prefix_nt, st);
+      if (e != cudaSuccess) return attn::record_cuda_error(e);
+    }
+    if (plan.suffix_tc) {
+      e = bf16 ? launch<true, false>(enc, p, shared, st) : launch<false, false>(enc, p, shared, st);
+    } else {
+      e = bf16 ? launch_suffix<true>(p, plan.suffix_nt, shared, st) : launch_suffix<false>(p, plan.suffix_nt, shared, st);
+      if (e == cudaSuccess) e = bf16 ? launch_join<true>(p, st) : launch_join<false>(p, st);
+    }
     return e == cudaSuccess ? ATTN_OK : attn::record_cuda_error(e);
   }
   e = dtype == ATTN_F32 ? attn::prefix::launch_dt<0>(p, st)

@@ -4,7 +4,7 @@
 namespace attn {
 namespace prefix {
 namespace rows {
-template cudaError_t launch_prefix<true>(const Params&, int, int*, int, cudaStream_t);
+template cudaError_t launch_prefix<true>(const Params&, int, cudaStream_t);
 }  // namespace rows
 }  // namespace prefix
 }  // namespace attn

@@ -4,7 +4,8 @@
 namespace attn {
 namespace prefix {
 namespace rows {
-template cudaError_t launch_suffix<true>(const Params&, int, const Cuts&, int, cudaStream_t);
+template cudaError_t launch_suffix<true>(const Params&, int, bool, cudaStream_t);
+template cudaError_t launch_join<true>(const Params&, cudaStream_t);
 }  // namespace rows
 }  // namespace prefix
 }  // namespace attn

@@ -4,7 +4,8 @@
 namespace attn {
 namespace prefix {
 namespace rows {
-template cudaError_t launch_suffix<false>(const Params&, int, const Cuts&, int, cudaStream_t);
+template cudaError_t launch_suffix<false>(const Params&, int, bool, cudaStream_t);
+template cudaError_t launch_join<false>(const Params&, cudaStream_t);
 }  // namespace rows
 }  // namespace prefix
 }  // namespace attn

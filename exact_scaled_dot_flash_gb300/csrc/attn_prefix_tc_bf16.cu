@@ -4,8 +4,8 @@
 namespace attn {
 namespace prefix {
 namespace tc {
-template cudaError_t launch<true, true>(EncodeTiledFn, const Params&, int*, int, cudaStream_t);
-template cudaError_t launch<true, false>(EncodeTiledFn, const Params&, int*, int, cudaStream_t);
+template cudaError_t launch<true, true>(EncodeTiledFn, const Params&, bool, cudaStream_t);
+template cudaError_t launch<true, false>(EncodeTiledFn, const Params&, bool, cudaStream_t);
 }  // namespace tc
 }  // namespace prefix
 }  // namespace attn

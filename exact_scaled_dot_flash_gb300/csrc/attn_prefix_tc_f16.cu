@@ -4,8 +4,8 @@
 namespace attn {
 namespace prefix {
 namespace tc {
-template cudaError_t launch<false, true>(EncodeTiledFn, const Params&, int*, int, cudaStream_t);
-template cudaError_t launch<false, false>(EncodeTiledFn, const Params&, int*, int, cudaStream_t);
+template cudaError_t launch<false, true>(EncodeTiledFn, const Params&, bool, cudaStream_t);
+template cudaError_t launch<false, false>(EncodeTiledFn, const Params&, bool, cudaStream_t);
 }  // namespace tc
 }  // namespace prefix
 }  // namespace attn

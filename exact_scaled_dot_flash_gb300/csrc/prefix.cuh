@@ -12,8 +12,11 @@
 //           keys for a block of rows and a head) of all groups, in one order, are cut into
 //           as many ranges as there are CTAs, so a row's parts are the ranges that its
 //           unit's blocks lie in (Head, Rec, parts_of).
-//   suffix: a unit is a sequence, its keys [pre, L) (all of them outside a group). It
-//           joins its own part with those of the prefix and writes out and lse.
+//   suffix: a unit is a sequence, its keys [pre, L) (all of them outside a group). For many
+//           rows it joins its own part with those of the prefix and writes out and lse;
+//           for few rows it leaves parts too, and does not need the prefix's: the stages then run side
+//           by side, the prefix on as many SMs as let it end with the suffix (share_out),
+//           and a last kernel joins the parts of each row in their order.
 #pragma once
 
 #include <atomic>
@@ -57,6 +60,14 @@ struct Params {
   Rec* rec;         // [num_groups]
   float2* ml;       // [most_parts, num_queries * Hq]
   float* o;         // [most_parts, num_queries * Hq, D]
+  // of the few-row suffix stage: blocks and ranges as above; each sequence's first block; the
+  // parts of units that lie in one range; those of units that are cut: CTA c (range, head) owns
+  // slots 2c (its first unit) and 2c + 1 (its last), suffix_rows rows each
+  int suffix_rows, suffix_ranges;
+  Head* suffix_head;
+  int64_t* suffix_first;  // [num_seqs]
+  float2 *own_ml, *cut_ml;
+  float *own_o, *cut_o;
 };
 
 __device__ __forceinline__ int capacity(const Params& p) { return p.max_pages * p.page_size; }
@@ -142,6 +153,20 @@ __device__ __forceinline__ int queries_of(const Params& p, int a, int b, int mos
   return a < b ? min(max(query_at(p, b) - q_lo, 0), most) : 0;
 }
 
+// Keys of sequence s that are its own: [start, L); `pre`: tokens its group shares.
+struct Own {
+  int group, pre, start, L;
+};
+
+__device__ __forceinline__ Own own_of(const Params& p, int s) {
+  Own o;
+  o.L = seq_len(p, s);
+  o.group = group_of(p, s);
+  o.pre = o.group >= 0 ? prefix_len(p, o.group) : 0;
+  o.start = min(o.pre, o.L);
+  return o;
+}
+
 // What a group brings to the prefix stage: `first` is filled in by the caller.
 __device__ __forceinline__ Rec rec_of(const Params& p, int g, int key_block, int row_block, bool halves) {
   int a, b;
@@ -168,18 +193,27 @@ struct Share {
   int ranges, g;
 };
 
-template <int THREADS>
+// Microseconds, measured: a block of 256 rows and 128 keys of 128 elements on an SM, and what a piece
+// costs besides; KB of keys and values that the few-row suffix stage streams in one of them, on one SM
+// and on all.
+constexpr float BLOCK_US = 1.9f, PIECE_US = 10.f, SM_KB_US = 60.f, ALL_KB_US = 6000.f;
+
+template <int THREADS, bool BESIDE>
 __device__ __forceinline__ Share share_out(const Params& p, int ctas, int key_block, int row_block, bool halves) {
   __shared__ int64_t warp_sum[THREADS / 32];
   __shared__ int most_full, most_half, found_g;
   __shared__ int64_t found_first;
+  __shared__ unsigned long long own_keys;  // of all sequences
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.num_groups + THREADS - 1) / THREADS;
   const int g0 = min(tid * per, p.num_groups), g1 = min(g0 + per, p.num_groups);
-  if (tid == 0) most_full = most_half = found_g = 0, found_first = 0;
+  if (tid == 0) most_full = most_half = found_g = 0, found_first = 0, own_keys = 0;
   __syncthreads();
-  int64_t mine = 0;
+  int64_t mine = 0, keys = 0;
   int full = 0, half = 0;
+  if constexpr (BESIDE) {
+    for (int s = tid; s < p.num_seqs; s += THREADS) keys += seq_len(p, s);
+  }
   Rec r0{};
   for (int g = g0; g < g1; ++g) {
     const Rec r = rec_of(p, g, key_block, row_block, halves);
@@ -187,6 +221,16 @@ __device__ __forceinline__ Share share_out(const Params& p, int ctas, int key_bl
     mine += blocks_of(p, r);
     if (r.rbs > r.half) full = max(full, r.nb);
     if (r.half) half = max(half, (r.nb + 1) / 2);
+    if constexpr (BESIDE) {
+      int a, b;
+      group_range(p, g, a, b);
+      keys -= static_cast<int64_t>(b - a) * prefix_len(p, g);
+    }
+  }
+  if constexpr (BESIDE) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
+    if (lane == 0) atomicAdd(&own_keys, static_cast<unsigned long long>(keys));
   }
   int64_t incl = mine;
 #pragma unroll
@@ -211,6 +255,17 @@ __device__ __forceinline__ Share share_out(const Params& p, int ctas, int key_bl
   // as many ranges as CTAs, if they leave a row no more parts than its room: n blocks lie in
   // at most n ranges / total + 1 ranges
   int64_t ranges = min(static_cast<int64_t>(ctas), s.total);
+  if constexpr (BESIDE) {
+    // Of 8, 16 .. SMs for this stage the number with which both are done first: the other one
+    // streams on the rest meanwhile, then on all.
+    const float us = static_cast<float>(s.total) * BLOCK_US * (p.D == 128 ? 1.f : 0.7f);
+    const float kb = fmaxf(static_cast<float>(static_cast<long long>(own_keys)), 0.f) * p.Hkv * p.D * (4.f / 1024.f);
+    const int n = min(8 * (lane + 1), ctas);
+    const float own = PIECE_US + us / n;
+    const float rest = fmaxf(kb - own * fminf(SM_KB_US * (SMS - n), ALL_KB_US), 0.f);
+    const uint32_t t = static_cast<uint32_t>(fminf((own + rest / ALL_KB_US) * 16.f, 1e8f)), best = __reduce_min_sync(0xffffffffu, t);
+    ranges = min(ranges, static_cast<int64_t>(min(8 * (32 - __clz(__ballot_sync(0xffffffffu, t == best))), ctas)));
+  }
   if (most_full) ranges = min(ranges, s.total * (p.most_parts - 1) / most_full);
   if (most_half) ranges = min(ranges, s.total * (p.most_parts / 2 - 1) / most_half);
   s.ranges = static_cast<int>(max(ranges, static_cast<int64_t>(1)));
@@ -278,6 +333,26 @@ cudaError_t allow_smem(K kern, int smem, int device, std::atomic<unsigned long l
   return e;
 }
 
+// A launch that may come up before the one in front of it on the stream has ended; its kernel waits
+// (griddepcontrol.wait) before it touches what that one or an earlier one has written.
+template <typename... A>
+cudaError_t launch_early(void (*kern)(A...), dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------------ few rows (prefix_rows.cuh)
 namespace rows {
 
@@ -292,28 +367,21 @@ __host__ __device__ constexpr int ctas_of_sm(int D, int nt) { return D == 128 ? 
 // Groups of 8 rows that a CTA takes.
 inline int nt_of(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }
 
-// Workspace of the sequences that are cut: CTA c (range, head) owns slots 2c (its first unit) and
-// 2c + 1 (its last), each 8 nt x D floats and 8 nt (m, l); a counter for each CTA.
-struct Cuts {
-  float* o;
-  float2* ml;
-  int* counters;
-};
-
-// counters: cleared by the prefix stage, which is always launched before the suffix stage.
 template <bool BF16>
-cudaError_t launch_prefix(const Params& p, int nt, int* counters, int num_counters, cudaStream_t st);
+cudaError_t launch_prefix(const Params& p, int nt, cudaStream_t st);
 template <bool BF16>
-cudaError_t launch_suffix(const Params& p, int nt, const Cuts& cuts, int ranges, cudaStream_t st);
+cudaError_t launch_suffix(const Params& p, int nt, bool after_prefix, cudaStream_t st);
+template <bool BF16>
+cudaError_t launch_join(const Params& p, cudaStream_t st);
 
 }  // namespace rows
 
 // ------------------------------------------------------------------ many rows (prefix_tc.cuh)
 namespace tc {
 
-// One stage; counters as above (prefix stage).
+// One stage; after_prefix: the launch before it is the prefix stage.
 template <bool BF16, bool PREFIX>
-cudaError_t launch(EncodeTiledFn enc, const Params& p, int* counters, int num_counters, cudaStream_t st);
+cudaError_t launch(EncodeTiledFn enc, const Params& p, bool after_prefix, cudaStream_t st);
 
 }  // namespace tc
 

@@ -14,9 +14,8 @@
 //
 // Suffix stage: the keys of all sequences, in blocks of 64 (16 a warp), are cut into ranges
 // of equal length, one for each group of Hkv CTAs (one a head, side by side). A CTA walks the
-// sequences of its range; a sequence wholly inside it is joined with its prefix's parts
-// and written out, a cut one leaves parts, and the CTA that finishes the last of them (a
-// counter that the prefix stage has cleared) joins all in the order of the ranges.
+// units (sequences) of its range and leaves a part for each row; join_kernel joins a
+// row's parts, those of its prefix first, then those of the ranges in their order.
 // Prefix stage: blocks of 64 keys for 8 NT rows and a head, shared out as prefix.cuh says.
 #pragma once
 
@@ -76,8 +75,7 @@ struct Shared {
   static constexpr int O = WARPS * ROWS * ROW * 4;            // the warps' outputs, in the ring's place
   static constexpr int OFF_ML = RING > O ? RING : O;
   static constexpr int OFF_LIM = OFF_ML + WARPS * ROWS * 8;
-  static constexpr int OFF_PARTS = OFF_LIM + ROWS * 4;        // parts of each row's prefix
-  static constexpr int OFF_Q = OFF_PARTS + ROWS * 4;          // query operands, in the lanes' order
+  static constexpr int OFF_Q = OFF_LIM + ROWS * 4;            // query operands, in the lanes' order
   static constexpr int BYTES = OFF_Q + NT * (D / 16) * 32 * 8;
 };
 
@@ -332,36 +330,6 @@ __device__ __forceinline__ Part of_warps(const uint8_t* smem, int r, int d4) {
   return a;
 }
 
-// Adds the prefix's parts of a row (n of them), BATCH read together: each read is a trip to L2.
-template <int D>
-__device__ __forceinline__ void add_prefix(const Params& p, Part& a, int64_t row, int d4, int n) {
-  constexpr int BATCH = 8;
-  const int64_t rows = static_cast<int64_t>(p.num_queries) * p.Hq;
-  for (int z0 = 0; z0 < n; z0 += BATCH) {
-    float2 ml[BATCH];
-    float4 x[BATCH];
-#pragma unroll
-    for (int z = 0; z < BATCH; ++z) {
-      const int64_t at = (z0 + z) * rows + row;
-      const bool is = z0 + z < n && in_bounds(p.status, at, p.most_parts * rows);
-      ml[z] = is ? __ldcg(p.ml + at) : make_float2(-INFINITY, 0.f);
-      x[z] = is ? __ldcg(reinterpret_cast<const float4*>(p.o) + at * (D / 4) + d4) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int z = 0; z < BATCH; ++z) a.add(ml[z], x[z]);
-  }
-}
-
-template <int D, bool BF16>
-__device__ __forceinline__ void write_out(const Params& p, const Part& a, int64_t row, int d4) {
-  if (!in_bounds(p.status, row, static_cast<int64_t>(p.num_queries) * p.Hq)) return;
-  const bool live = a.sum > 0.f;
-  const float inv = live ? 1.f / a.sum : __int_as_float(0x7fc00000);
-  reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D)[d4] =
-      make_uint2(pack2<BF16>(a.o.x * inv, a.o.y * inv), pack2<BF16>(a.o.z * inv, a.o.w * inv));
-  if (p.lse && d4 == 0) p.lse[row] = live ? (a.M + log2f(a.sum)) * LN2 : (a.sum == 0.f ? -INFINITY : a.sum);
-}
-
 // ------------------------------------------------------------------ prefix stage
 // Each row's limit of a group's rows (row_lo on), into shared memory.
 __device__ __forceinline__ void group_limits(const Params& p, int a, int b, int q_lo, int row_lo, int R, int rows, int* lims) {
@@ -377,14 +345,13 @@ __device__ __forceinline__ void group_limits(const Params& p, int a, int b, int 
 }
 
 template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT)) prefix_kernel(const __grid_constant__ Params p, int* counters, int num_counters) {
-  asm volatile("griddepcontrol.launch_dependents;");  // the suffix stage may come up: it waits before it reads
+__global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT)) prefix_kernel(const __grid_constant__ Params p) {
+  wait_before();
+  let_next();  // the suffix stage runs beside this one
   constexpr int ROWS = 8 * NT;
   extern __shared__ __align__(16) uint8_t smem[];
   using SH = Shared<D, NT>;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i < num_counters; i += static_cast<int64_t>(gridDim.x) * THREADS)
-    counters[i] = 0;
-  const Share sh = share_out<THREADS>(p, gridDim.x, BLOCK, ROWS, false);
+  const Share sh = share_out<THREADS, false>(p, gridDim.x, BLOCK, ROWS, false);
   const int heads = p.Hq / p.Hkv;
   int64_t u = sh.u0, first = sh.first;
   for (int g = sh.g; u < sh.u1; ++g) {
@@ -431,20 +398,6 @@ __global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT)) prefix_kernel(cons
 }
 
 // ------------------------------------------------------------------ suffix stage
-// Keys of sequence s that are its own: [start, L); `pre`: tokens its group shares.
-struct Own {
-  int group, pre, start, L;
-};
-
-__device__ __forceinline__ Own own_of(const Params& p, int s) {
-  Own o;
-  o.L = seq_len(p, s);
-  o.group = group_of(p, s);
-  o.pre = o.group >= 0 ? prefix_len(p, o.group) : 0;
-  o.start = min(o.pre, o.L);
-  return o;
-}
-
 __device__ __forceinline__ int key_blocks(int n) { return max(1, (n + BLOCK - 1) / BLOCK); }  // without keys: one
 
 __device__ __forceinline__ int row_blocks(const Params& p, int nq, int rows) {
@@ -504,17 +457,19 @@ __device__ __forceinline__ Place locate(const Params& p, int range, int ranges, 
   pl.ranges = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(ranges), most)));
   u0 = range < pl.ranges ? cut(total, range, pl.ranges) : total;
   u1 = range < pl.ranges ? cut(total, range + 1, pl.ranges) : total;
-  if (u0 >= before && u0 < before + mine) {
-    int s = s0;
+  if (blockIdx.x == 0 || (u0 >= before && u0 < before + mine)) {
     int64_t at = before;
-    for (; s < s1; ++s) {
+    for (int s = s0; s < s1; ++s) {
       const int64_t n = blocks(s, rbs);
-      if (u0 < at + n) break;
+      if (u0 >= at && u0 < at + n) {
+        found_at = at;
+        found_s = s;
+      }
+      if (blockIdx.x == 0) p.suffix_first[s] = at;
       at += n;
     }
-    found_at = at;
-    found_s = s;
   }
+  if (blockIdx.x == 0 && tid == 0) *p.suffix_head = Head{total, pl.ranges, ROWS};
   __syncthreads();
   pl.s = found_s;
   pl.at = found_at;
@@ -523,18 +478,15 @@ __device__ __forceinline__ Place locate(const Params& p, int range, int ranges, 
 
 template <int D, bool BF16, int NT>
 __global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT))
-    suffix_kernel(const __grid_constant__ Params p, const Cuts cuts, int ranges, int least) {
+    suffix_kernel(const __grid_constant__ Params p, int ranges, int least, int after_prefix) {
+  // After the prefix stage nothing is waited for: what this one reads was complete before that began.
+  if (!after_prefix) wait_before();
+  let_next();
   constexpr int ROWS = 8 * NT, G = D / 4;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ bool last_part;
   using SH = Shared<D, NT>;
   const int h = blockIdx.x % p.Hkv, range = blockIdx.x / p.Hkv;
   const int heads = p.Hq / p.Hkv;
-  bool waited = false;  // for the prefix stage: its parts and the counters
-  auto wait = [&]() {
-    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
-    waited = true;
-  };
   int64_t u0, u1;
   const Place pl = locate<ROWS>(p, range, ranges, least, u0, u1);
   int64_t begin = pl.at;  // first block of the sequence
@@ -570,110 +522,116 @@ __global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT))
       int* const lims = reinterpret_cast<int*>(smem + SH::OFF_LIM);
       for (int r = threadIdx.x; r < ROWS; r += THREADS)
         lims[r] = r < w.R ? limit_of(p, s, q_lo + (w.row_lo + r) / heads) : 0;
-      int* const parts = reinterpret_cast<int*>(smem + SH::OFF_PARTS);
-      auto count_parts = [&]() {  // of each row; by the last warp, that the limits leave idle
-        const int r = static_cast<int>(threadIdx.x) - (THREADS - 32);
-        if (r < 0 || r >= w.R) return;
-        const int q = (w.row_lo + r) / heads;
-        parts[r] = own.pre > 0 ? parts_of(p, own.group, q_lo + q, w.row_lo + r - q * heads, h) : 0;
-      };
-      const bool counted = waited;  // before the keys where the prefix stage is known to be complete
-      if (counted) count_parts();
       stream<D, BF16, NT>(p, w, smem);
-      wait();
-      if (!counted) {
-        count_parts();
-        __syncthreads();
-      }
-      const int64_t slot = 2ll * blockIdx.x + (starts ? 0 : 1), nslot = 2ll * ranges * p.Hkv * ROWS;
-      if (whole) {
-        for (int e = threadIdx.x; e < w.R * G; e += THREADS) {
-          const int r = e / G, d4 = e - r * G;
-          Part x = of_warps<D, NT>(smem, r, d4);
-          add_prefix<D>(p, x, row_at(r), d4, parts[r]);
-          write_out<D, BF16>(p, x, row_at(r), d4);
-        }
-      } else {
-        for (int e = threadIdx.x; e < w.R * G; e += THREADS) {
-          const int r = e / G, d4 = e - r * G;
-          const Part x = of_warps<D, NT>(smem, r, d4);
-          const int64_t at = slot * ROWS + r;
-          if (!in_bounds(p.status, at, nslot)) continue;
-          reinterpret_cast<float4*>(cuts.o)[at * G + d4] = x.o;
-          if (d4 == 0) cuts.ml[at] = make_float2(x.M, x.sum);
-        }
-        // the ranges rf .. rl hold the unit's blocks
-        const int64_t end = first + nb;
-        const int rf = range_of(first, pl.total, pl.ranges), rl = range_of(end - 1, pl.total, pl.ranges);
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0) {
-          const int64_t n = static_cast<int64_t>(rf) * p.Hkv + h;  // a range begins one cut unit at most
-          last_part = in_bounds(p.status, n, static_cast<int64_t>(ranges) * p.Hkv) && atomicAdd(cuts.counters + n, 1) == rl - rf;
-        }
-        __syncthreads();
-        if (last_part) {
-          __threadfence();
-          const bool starts_late = first > cut(pl.total, rf, pl.ranges);
-          for (int e = threadIdx.x; e < w.R * G; e += THREADS) {
-            const int r = e / G, d4 = e - r * G;
-            Part x;
-            constexpr int BATCH = 4;
-            for (int r0 = rf; r0 <= rl; r0 += BATCH) {
-              float2 ml[BATCH];
-              float4 y[BATCH];
-#pragma unroll
-              for (int k = 0; k < BATCH; ++k) {
-                const int64_t at = (2ll * (static_cast<int64_t>(r0 + k) * p.Hkv + h) + (r0 + k == rf && starts_late ? 1 : 0)) * ROWS + r;
-                const bool is = r0 + k <= rl && in_bounds(p.status, at, nslot);
-                ml[k] = is ? __ldcg(cuts.ml + at) : make_float2(-INFINITY, 0.f);
-                y[k] = is ? __ldcg(reinterpret_cast<const float4*>(cuts.o) + at * G + d4) : make_float4(0.f, 0.f, 0.f, 0.f);
-              }
-#pragma unroll
-              for (int k = 0; k < BATCH; ++k) x.add(ml[k], y[k]);
-            }
-            add_prefix<D>(p, x, row_at(r), d4, parts[r]);
-            write_out<D, BF16>(p, x, row_at(r), d4);
-          }
-        }
+      const int64_t slot = 2ll * blockIdx.x + (starts ? 0 : 1);
+      const int64_t rows = whole ? static_cast<int64_t>(p.num_queries) * p.Hq : 2ll * ranges * p.Hkv * ROWS;
+      float4* const to = reinterpret_cast<float4*>(whole ? p.own_o : p.cut_o);
+      float2* const to_ml = whole ? p.own_ml : p.cut_ml;
+      for (int e = threadIdx.x; e < w.R * G; e += THREADS) {
+        const int r = e / G, d4 = e - r * G;
+        const Part x = of_warps<D, NT>(smem, r, d4);
+        const int64_t at = whole ? row_at(r) : slot * ROWS + r;
+        if (!in_bounds(p.status, at, rows)) continue;
+        to[at * G + d4] = x.o;
+        if (d4 == 0) to_ml[at] = make_float2(x.M, x.sum);
       }
       __syncthreads();
     }
     begin += static_cast<int64_t>(nb) * rbs;
   }
-  wait();  // no CTA ends before the prefix stage: the next call on the stream may use the workspace
+  // the stage does not end before the prefix's: the next launch waits for this one
+  if (blockIdx.x == 0 && after_prefix) wait_before();
+}
+
+// ------------------------------------------------------------------ the parts together
+constexpr int JOIN_THREADS = 256;
+
+// A thread takes 4 elements of a row. What it reads of the metadata it reads before it waits for
+// the stages: its CTA may be on its SM long before they end.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ Params p) {
+  constexpr int G = D / 4, BATCH = 8;  // parts read together: each read is a trip to L2
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (JOIN_THREADS / G) + threadIdx.x / G;
+  const int d4 = threadIdx.x % G;
+  const int64_t rows = static_cast<int64_t>(p.num_queries) * p.Hq;
+  if (row >= rows) return;
+  const int query = static_cast<int>(row / p.Hq), head = static_cast<int>(row - static_cast<int64_t>(query) * p.Hq);
+  const int heads = p.Hq / p.Hkv, h = head / heads, hr = head - h * heads;
+  // the query's sequence: in a decode step the one of its own number
+  int s = min(query, p.num_seqs - 1);
+  if (query < query_at(p, s) || query >= query_at(p, s + 1)) s = last_at_most(p.q_offsets, 0, p.num_seqs, query);
+  int q_lo;
+  const int nq = queries_of(p, s, s + 1, p.max_queries, q_lo);
+  if (query < q_lo || query >= q_lo + nq) return;  // of no sequence
+  const Own own = own_of(p, s);
+  const int nb = key_blocks(own.L - own.start);
+  const int64_t local = static_cast<int64_t>(query - q_lo) * heads + hr;
+  const int rb = static_cast<int>(local / p.suffix_rows), r = static_cast<int>(local - static_cast<int64_t>(rb) * p.suffix_rows);
+  wait_before();
+  const int64_t total = __ldcg(reinterpret_cast<const long long*>(&p.suffix_head->total));
+  const int ranges = __ldcg(&p.suffix_head->ranges);
+  const int64_t first = __ldcg(reinterpret_cast<const long long*>(p.suffix_first + s)) + static_cast<int64_t>(rb) * nb;
+  const int n = own.pre > 0 ? parts_of(p, own.group, query, hr, h) : 0;  // of the prefix
+  const int rf = range_of(first, total, ranges), rl = range_of(first + nb - 1, total, ranges);
+  const int late = first > cut(total, rf, ranges) ? 1 : 0;
+  const int64_t slots = 2ll * p.suffix_ranges * p.Hkv * p.suffix_rows;
+  Part x;
+  for (int z0 = 0; z0 < n + rl - rf + 1; z0 += BATCH) {
+    float2 ml[BATCH];
+    float4 y[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int z = z0 + k, c = rf + z - n;  // part of the prefix, or range
+      const float2* m = p.ml;
+      const float* o = p.o;
+      int64_t at = z * rows + row, most = p.most_parts * rows;
+      if (z >= n) {
+        const bool one = rf == rl;
+        m = one ? p.own_ml : p.cut_ml;
+        o = one ? p.own_o : p.cut_o;
+        at = one ? row : (2ll * (static_cast<int64_t>(c) * p.Hkv + h) + (c == rf ? late : 0)) * p.suffix_rows + r;
+        most = one ? rows : slots;
+      }
+      const bool is = (z < n || c <= rl) && in_bounds(p.status, at, most);
+      ml[k] = is ? __ldcg(m + at) : make_float2(-INFINITY, 0.f);
+      y[k] = is ? __ldcg(reinterpret_cast<const float4*>(o) + at * G + d4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) x.add(ml[k], y[k]);
+  }
+  const bool live = x.sum > 0.f;
+  const float inv = live ? 1.f / x.sum : __int_as_float(0x7fc00000);
+  reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D)[d4] =
+      make_uint2(pack2<BF16>(x.o.x * inv, x.o.y * inv), pack2<BF16>(x.o.z * inv, x.o.w * inv));
+  if (p.lse && d4 == 0) p.lse[row] = live ? (x.M + log2f(x.sum)) * LN2 : (x.sum == 0.f ? -INFINITY : x.sum);
 }
 
 // ------------------------------------------------------------------ launches
 template <int D, bool BF16, int NT>
-cudaError_t launch_prefix_nt(const Params& p, int* counters, int num_counters, cudaStream_t st) {
+cudaError_t launch_prefix_nt(const Params& p, cudaStream_t st) {
   auto kern = prefix_kernel<D, BF16, NT>;
   constexpr int smem = Shared<D, NT>::BYTES;
   static std::atomic<unsigned long long> configured{0};
   const cudaError_t e = allow_smem(kern, smem, p.device, configured);
-  if (e != cudaSuccess) return e;
-  kern<<<SMS * ctas_of_sm(D, NT), THREADS, smem, st>>>(p, counters, num_counters);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : launch_early(kern, dim3(SMS * ctas_of_sm(D, NT)), THREADS, smem, st, p);
 }
 
 template <int D, bool BF16, int NT>
-cudaError_t launch_suffix_nt(const Params& p, const Cuts& cuts, int ranges, cudaStream_t st) {
+cudaError_t launch_suffix_nt(const Params& p, bool after_prefix, cudaStream_t st) {
   auto kern = suffix_kernel<D, BF16, NT>;
   constexpr int smem = Shared<D, NT>::BYTES;
   static std::atomic<unsigned long long> configured{0};
   const cudaError_t e = allow_smem(kern, smem, p.device, configured);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ranges) * p.Hkv);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p, cuts, ranges, LEAST_BLOCKS);
+  return launch_early(kern, dim3(static_cast<unsigned>(p.suffix_ranges) * p.Hkv), THREADS, smem, st, p, p.suffix_ranges,
+                      LEAST_BLOCKS, after_prefix ? 1 : 0);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_join_d(const Params& p, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(p.num_queries) * p.Hq, per = JOIN_THREADS / (D / 4);
+  if ((rows + per - 1) / per > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_early(join_kernel<D, BF16>, dim3(static_cast<unsigned>((rows + per - 1) / per)), JOIN_THREADS, 0, st, p);
 }
 
 #define ATTN_NT(F, NT, ...)                                        \
@@ -687,13 +645,18 @@ cudaError_t launch_suffix_nt(const Params& p, const Cuts& cuts, int ranges, cuda
                            : F<64, BF16, 4>(__VA_ARGS__)))
 
 template <bool BF16>
-cudaError_t launch_prefix(const Params& p, int nt, int* counters, int num_counters, cudaStream_t st) {
-  return ATTN_NT(launch_prefix_nt, nt, p, counters, num_counters, st);
+cudaError_t launch_prefix(const Params& p, int nt, cudaStream_t st) {
+  return ATTN_NT(launch_prefix_nt, nt, p, st);
 }
 
 template <bool BF16>
-cudaError_t launch_suffix(const Params& p, int nt, const Cuts& cuts, int ranges, cudaStream_t st) {
-  return ATTN_NT(launch_suffix_nt, nt, p, cuts, ranges, st);
+cudaError_t launch_suffix(const Params& p, int nt, bool after_prefix, cudaStream_t st) {
+  return ATTN_NT(launch_suffix_nt, nt, p, after_prefix, st);
+}
+
+template <bool BF16>
+cudaError_t launch_join(const Params& p, cudaStream_t st) {
+  return p.D == 128 ? launch_join_d<128, BF16>(p, st) : launch_join_d<64, BF16>(p, st);
 }
 #undef ATTN_NT
 

@@ -23,7 +23,7 @@
 
 #include <algorithm>
 
-#include "prefix_rows.cuh"
+#include "prefix.cuh"
 
 namespace attn {
 namespace prefix {
@@ -168,7 +168,7 @@ struct Planner {
         w.s1 = w.s0 + 1;
         w.nq = queries_of(p, w.s0, w.s1, p.max_queries, w.q_lo);
         if (w.row0 >= static_cast<int64_t>(w.nq) * heads) continue;
-        const rows::Own own = rows::own_of(p, w.s0);
+        const Own own = own_of(p, w.s0);
         w.group = own.pre > 0 ? own.group : -1;
         w.lo = own.start;
         w.to = own.L;
@@ -199,7 +199,7 @@ __device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xfffff
 template <int D, bool BF16, bool PREFIX>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-              const __grid_constant__ Params p, int qblocks, int64_t items, int* counters, int num_counters) {
+              const __grid_constant__ Params p, int qblocks, int64_t items, int after_prefix) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -208,10 +208,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   Work* const works = reinterpret_cast<Work*>(smem + C::OFF_WORK);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if constexpr (PREFIX) {
-    asm volatile("griddepcontrol.launch_dependents;");  // the suffix stage may come up: it waits before it reads
-    for (int i = blockIdx.x * NUM_THREADS + threadIdx.x; i < num_counters; i += gridDim.x * NUM_THREADS) counters[i] = 0;
-  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(bar(C::BAR_FULL + s), 1);
@@ -234,9 +230,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish();
   }
+  if (PREFIX || !after_prefix) wait_before();  // nothing before this reads what other launches have written
+  if constexpr (PREFIX) let_next();            // the suffix stage may come up
   Planner<PREFIX> plan;
   if constexpr (PREFIX) {
-    plan.sh = share_out<NUM_THREADS>(p, SMS, BN, ROWS, true);
+    plan.sh = p.suffix_rows > 0 ? share_out<NUM_THREADS, true>(p, SMS, BN, ROWS, true)
+                                : share_out<NUM_THREADS, false>(p, SMS, BN, ROWS, true);
     plan.u = plan.sh.u0;
     plan.u1 = plan.sh.u1;
     plan.first = plan.sh.first;
@@ -640,7 +639,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         if (ok) p.ml[at] = make_float2(have ? m_run : -INFINITY, l_run);
       } else {
-        if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the prefix's parts
+        if (!waited) wait_before();  // the prefix's parts
         waited = true;
         const int parts = w.group >= 0 && row_in ? parts_of(p, w.group, w.q_lo + tq, pr - tq * heads, w.h) : 0;
         float M = have ? m_run : -INFINITY;
@@ -694,7 +693,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     // the suffix stage does not end before the prefix's: the next call on the stream may use the workspace
     if constexpr (!PREFIX) {
-      if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (!waited) wait_before();
     }
   }
   tc_fence_before();
@@ -707,7 +706,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 template <int D, bool BF16, bool PREFIX>
-cudaError_t launch_d(EncodeTiledFn enc, const Params& p, int* counters, int num_counters, cudaStream_t st) {
+cudaError_t launch_d(EncodeTiledFn enc, const Params& p, bool after_prefix, cudaStream_t st) {
   const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const cuuint32_t estride[4] = {1, 1, 1, 1};
   CUtensorMap tk, tv;  // k, v viewed as [pages, page_size, Hkv, D]
@@ -731,23 +730,13 @@ cudaError_t launch_d(EncodeTiledFn enc, const Params& p, int* counters, int num_
   const int64_t items = p.num_seqs * qblocks * p.Hkv;
   const int64_t ctas = PREFIX ? SMS : std::min<int64_t>(items, SMS);
   if (ctas == 0) return cudaSuccess;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(NUM_THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = PREFIX ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, tk, tv, p, static_cast<int>(qblocks), items, counters, num_counters);
+  return launch_early(kern, dim3(static_cast<unsigned>(ctas)), NUM_THREADS, smem, st, tk, tv, p, static_cast<int>(qblocks),
+                      items, after_prefix ? 1 : 0);
 }
 
 template <bool BF16, bool PREFIX>
-cudaError_t launch(EncodeTiledFn enc, const Params& p, int* counters, int num_counters, cudaStream_t st) {
-  return p.D == 128 ? launch_d<128, BF16, PREFIX>(enc, p, counters, num_counters, st)
-                    : launch_d<64, BF16, PREFIX>(enc, p, counters, num_counters, st);
+cudaError_t launch(EncodeTiledFn enc, const Params& p, bool after_prefix, cudaStream_t st) {
+  return p.D == 128 ? launch_d<128, BF16, PREFIX>(enc, p, after_prefix, st) : launch_d<64, BF16, PREFIX>(enc, p, after_prefix, st);
 }
 
 }  // namespace tc
