@@ -196,7 +196,7 @@ struct Share {
 // Microseconds, measured: a block of 256 rows and 128 keys of 128 elements on an SM, and what a piece
 // costs besides; KB of keys and values that the few-row suffix stage streams in one of them, on one SM
 // and on all.
-constexpr float BLOCK_US = 1.9f, PIECE_US = 10.f, SM_KB_US = 60.f, ALL_KB_US = 6000.f;
+constexpr float BLOCK_US = 1.9f, PIECE_US = 10.f, SM_KB_US = 40.f, ALL_KB_US = 6000.f;
 
 template <int THREADS, bool BESIDE>
 __device__ __forceinline__ Share share_out(const Params& p, int ctas, int key_block, int row_block, bool halves) {
@@ -356,13 +356,14 @@ __device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch
 // ------------------------------------------------------------------ few rows (prefix_rows.cuh)
 namespace rows {
 
-constexpr int WARPS = 4;
+constexpr int WARPS = 2;
 constexpr int THREADS = WARPS * 32;
 constexpr int BLOCK = 16 * WARPS;  // keys of a block: 16 a warp
+
 constexpr int LEAST_BLOCKS = 4;    // of a range of the suffix stage, where units are cut
 
 // CTAs of an SM: what the shared memory holds, and enough registers for the outputs.
-__host__ __device__ constexpr int ctas_of_sm(int D, int nt) { return D == 128 ? (nt <= 2 ? 3 : 2) : nt <= 2 ? 4 : 3; }
+__host__ __device__ constexpr int ctas_of_sm(int D, int nt) { return D == 128 ? (nt <= 2 ? 6 : 4) : nt <= 2 ? 8 : 6; }
 
 // Groups of 8 rows that a CTA takes.
 inline int nt_of(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }

@@ -68,7 +68,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 template <int D, int NT>
 struct Shared {
   static constexpr int ROWS = 8 * NT;
-  static constexpr int STAGES = ctas_of_sm(D, NT) == 3 && D == 128 ? 2 : 3;
+  static constexpr int STAGES = D == 128 && NT <= 2 ? 2 : 3;
   static constexpr int TILE_BYTES = TILE * D * 2;             // K or V
   static constexpr int RING = WARPS * STAGES * 2 * TILE_BYTES;
   static constexpr int ROW = D + 4;

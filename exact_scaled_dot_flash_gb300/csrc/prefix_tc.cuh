@@ -17,7 +17,8 @@
 //    first tiles fly during the epilogue of the piece before.
 // Prefix stage: pieces of equal ranges of all groups' blocks (prefix.cuh), 128 keys for 256
 // rows. Where a unit has 128 rows or fewer (the last rows of a group), the two row tiles take the
-// same rows and every other key tile, and leave a part each: a block is 256 keys.
+// same rows and half of the key tiles each, and leave a part each: a block is 256 keys. (Halves, not
+// every other tile: the keys are then read at the time that the group's other rows read them.)
 // Suffix stage: a piece is all own keys of a sequence for 256 rows, joined with the prefix's parts.
 #pragma once
 
@@ -68,7 +69,7 @@ struct Work {
   int table;           // row of the table that names the pages
   int q_lo, nq, h, row0;
   int lo, to, j0;
-  int n[NQ];           // key tiles of each row tile; split: both have the same rows, and tiles j0, j0 + 2 ..
+  int n[NQ];           // key tiles of each row tile; split: both have the same rows, and tiles from j0 and from j0 + n[0] on
   int split, part, group;
   int state;           // 0: no more work, 1: rows may see fewer keys than [lo, to), 2: every row sees all
 };
@@ -319,10 +320,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int i = 0; ok && get_work(i, w); ++i) {
         if (w.split) {  // in the order of the MMAs
           for (int j = 0; j <= w.n[0] && ok; ++j) {
-            if (j < w.n[0]) ok = load(&tm_k, w.j0 + 2 * j);
-            if (ok && j >= 1 && j - 1 < w.n[1]) ok = load(&tm_v, w.j0 + 2 * j - 1);
-            if (ok && j < w.n[1]) ok = load(&tm_k, w.j0 + 2 * j + 1);
-            if (ok && j < w.n[0]) ok = load(&tm_v, w.j0 + 2 * j);
+            if (j < w.n[0]) ok = load(&tm_k, w.j0 + j);
+            if (ok && j >= 1 && j - 1 < w.n[1]) ok = load(&tm_v, w.j0 + w.n[0] + j - 1);
+            if (ok && j < w.n[1]) ok = load(&tm_k, w.j0 + w.n[0] + j);
+            if (ok && j < w.n[0]) ok = load(&tm_v, w.j0 + j);
           }
         } else {
           const int nmax = max(w.n[0], w.n[1]);
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             if (j >= 1 && j - 1 < n1) {
               if (!(ok = wait_full(idx))) break;
-              fix_values(w.j0 + 2 * j - 1, idx);
+              fix_values(w.j0 + n0 + j - 1, idx);
               if (!(ok = wait_p(1, j - 1))) break;
               tc_fence_after();
               issue_pv(1, j - 1, idx, j == n1);
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             if (j < n0) {
               if (!(ok = wait_full(idx))) break;
-              fix_values(w.j0 + 2 * j, idx);
+              fix_values(w.j0 + j, idx);
               if (!(ok = wait_p(0, j))) break;
               tc_fence_after();
               issue_pv(0, j, idx, j == n0 - 1);
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const bool row_ok = tq < w.nq;
       const int64_t orow = row_ok ? static_cast<int64_t>(w.q_lo + tq) * p.Hq + w.h * heads + (pr - tq * heads) : 0;
       const bool row_in = row_ok && in_bounds(p.status, orow, nrows);
-      const int n_t = w.n[t], step = w.split ? 2 : 1, jt = w.j0 + (w.split ? t : 0);
+      const int n_t = w.n[t], jt = w.j0 + (w.split && t ? w.n[0] : 0);
       if (n_t > 0) {  // the thread's row of q, into the swizzled tile
         const uint4* const src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + orow * D);
         uint8_t* const dst = smem + t * C::TILE_BYTES + row * 128;
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 128; ++k) s[k] = __uint_as_float(sr[k >> 5][k & 31]);
         }
-        const int key0 = (jt + j * step) * BN;
+        const int key0 = (jt + j) * BN;
         if (key0 + BN > least || key0 < w.lo) {
 #pragma unroll
           for (int k = 0; k < 128; ++k) {
