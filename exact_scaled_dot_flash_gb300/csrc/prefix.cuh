@@ -158,14 +158,24 @@ struct Own {
   int group, pre, start, L;
 };
 
-__device__ __forceinline__ Own own_of(const Params& p, int s) {
+__device__ __forceinline__ Own own_of(const Params& p, int s, int L) {
   Own o;
-  o.L = seq_len(p, s);
-  o.group = group_of(p, s);
-  o.pre = o.group >= 0 ? prefix_len(p, o.group) : 0;
+  o.L = L;
+  if (p.num_groups == 1) {  // the common case, without a search
+    int a, b;
+    group_range(p, 0, a, b);
+    const int pre = prefix_len(p, 0);
+    o.group = s >= a && s < b ? 0 : -1;
+    o.pre = o.group == 0 ? pre : 0;
+  } else {
+    o.group = group_of(p, s);
+    o.pre = o.group >= 0 ? prefix_len(p, o.group) : 0;
+  }
   o.start = min(o.pre, o.L);
   return o;
 }
+
+__device__ __forceinline__ Own own_of(const Params& p, int s) { return own_of(p, s, seq_len(p, s)); }
 
 // What a group brings to the prefix stage: `first` is filled in by the caller.
 __device__ __forceinline__ Rec rec_of(const Params& p, int g, int key_block, int row_block, bool halves) {
@@ -196,7 +206,7 @@ struct Share {
 // Microseconds, measured: a block of 256 rows and 128 keys of 128 elements on an SM, and what a piece
 // costs besides; KB of keys and values that the few-row suffix stage streams in one of them, on one SM
 // and on all.
-constexpr float BLOCK_US = 1.9f, PIECE_US = 10.f, SM_KB_US = 40.f, ALL_KB_US = 6000.f;
+constexpr float BLOCK_US = 2.4f, PIECE_US = 10.f, SM_KB_US = 40.f, ALL_KB_US = 5500.f;
 
 template <int THREADS, bool BESIDE>
 __device__ __forceinline__ Share share_out(const Params& p, int ctas, int key_block, int row_block, bool halves) {

@@ -102,6 +102,23 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
   int* const status = p.status;
   const int64_t nrows = static_cast<int64_t>(p.num_queries) * p.Hq;
 
+  // What the first products need comes of three trips to L2 or beyond: the page of the first keys,
+  // looked up for every key that may be seen, flies with the query's elements.
+  constexpr int PIECES = D / 8;          // 16-byte pieces of a key
+  constexpr int RPC = 32 / PIECES;       // keys that one copy of the warp covers
+  const uint32_t ring = smem_u32(smem) + warp * STAGES * 2 * SH::TILE_BYTES;
+  const int64_t ntok = static_cast<int64_t>(p.num_pages) * p.page_size;
+  const int64_t step = static_cast<int64_t>(p.Hkv) * D * 2;  // bytes from token to token
+  const uint8_t* const kb = static_cast<const uint8_t*>(p.k) + (w.h * D + lane % PIECES * 8) * 2;
+  const uint8_t* const vb = static_cast<const uint8_t*>(p.v) + (w.h * D + lane % PIECES * 8) * 2;
+  // The lane's key of the tile to copy next: its block and the row in it.
+  int ckey = w.from + warp * TILE + (lane & (TILE - 1));
+  const int tile0 = w.from + warp * TILE;
+  int cfirst = tile0;
+  int blk = ckey / p.page_size, row = ckey - blk * p.page_size;
+  const int dblk = BLOCK / p.page_size, drow = BLOCK - dblk * p.page_size;
+  auto find_page = [&]() { return ckey < w.to ? page_of(p, w.table, blk) : -1; };
+  int page = find_page();
   // query operands: of 8 rows by warp: lane (g, t) holds elements 16 k + 2 t, + 1 and + 8, + 9 of row g
   for (int i = warp; i < NT; i += WARPS) {
     const int row = 8 * i + g;
@@ -111,9 +128,11 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
       const int64_t at = static_cast<int64_t>(w.q_lo + q) * p.Hq + w.h * heads + (w.row_lo + row - q * heads);
       if (in_bounds(status, at, nrows)) src = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) + at * D);
     }
+    uint2 x[KS];
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
-      sq[(i * KS + k) * 32 + lane] = src ? make_uint2(__ldg(src + 8 * k + t), __ldg(src + 8 * k + 4 + t)) : make_uint2(0u, 0u);
+    for (int k = 0; k < KS; ++k) x[k] = src ? make_uint2(__ldg(src + 8 * k + t), __ldg(src + 8 * k + 4 + t)) : make_uint2(0u, 0u);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) sq[(i * KS + k) * 32 + lane] = x[k];
   }
   __syncthreads();
   uint2 qf[NT == 1 ? KS : 1];
@@ -148,21 +167,6 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
 #pragma unroll
     for (int k = 0; k < KS; ++k) acc[k][i][0] = acc[k][i][1] = acc[k][i][2] = acc[k][i][3] = 0.f;
   }
-  constexpr int PIECES = D / 8;          // 16-byte pieces of a key
-  constexpr int RPC = 32 / PIECES;       // keys that one copy of the warp covers
-  const uint32_t ring = smem_u32(smem) + warp * STAGES * 2 * SH::TILE_BYTES;
-  const int64_t ntok = static_cast<int64_t>(p.num_pages) * p.page_size;
-  const int64_t step = static_cast<int64_t>(p.Hkv) * D * 2;  // bytes from token to token
-  const uint8_t* const kb = static_cast<const uint8_t*>(p.k) + (w.h * D + lane % PIECES * 8) * 2;
-  const uint8_t* const vb = static_cast<const uint8_t*>(p.v) + (w.h * D + lane % PIECES * 8) * 2;
-  // The lane's key of the tile to copy next: its block and the row in it.
-  int ckey = w.from + warp * TILE + (lane & (TILE - 1));
-  const int tile0 = w.from + warp * TILE;
-  int cfirst = tile0;
-  int blk = ckey / p.page_size, row = ckey - blk * p.page_size;
-  const int dblk = BLOCK / p.page_size, drow = BLOCK - dblk * p.page_size;
-  auto find_page = [&]() { return ckey < most ? page_of(p, w.table, blk) : -1; };
-  int page = find_page();
   int64_t mine = -1;  // its row of the cache; -1: zeros
   auto copy_half = [&](uint32_t at, const uint8_t* from) {  // K or V of the tile at cfirst
     if (cfirst < most) {
@@ -177,7 +181,7 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
   };
   auto copy_keys = [&](int stage) {
     const int64_t tok = static_cast<int64_t>(page) * p.page_size + row;
-    mine = page >= 0 && in_bounds(status, tok, ntok) ? tok : -1;
+    mine = page >= 0 && ckey < most && in_bounds(status, tok, ntok) ? tok : -1;
     copy_half(ring + stage * 2 * SH::TILE_BYTES, kb);
   };
   auto copy_values = [&](int stage) {  // of the same tile; then on to the next one, whose page is looked up ahead
@@ -419,12 +423,11 @@ __device__ __forceinline__ Place locate(const Params& p, int range, int ranges, 
   const int per = (p.num_seqs + THREADS - 1) / THREADS;
   const int s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
   auto blocks = [&](int s, int& rbs) -> int64_t {
-    int q_lo;
-    const int nq = queries_of(p, s, s + 1, p.max_queries, q_lo);
+    const int end = query_at(p, s + 1), L = seq_len(p, s), q_lo = query_at(p, s);  // read together
+    const Own o = own_of(p, s, L);
+    const int nq = min(max(end - q_lo, 0), p.max_queries);
     rbs = row_blocks(p, nq, ROWS);
-    if (nq <= 0) return 0;
-    const Own o = own_of(p, s);
-    return static_cast<int64_t>(key_blocks(o.L - o.start)) * rbs;
+    return nq > 0 ? static_cast<int64_t>(key_blocks(o.L - o.start)) * rbs : 0;
   };
   int64_t mine = 0;
   int my_units = 0, rbs;

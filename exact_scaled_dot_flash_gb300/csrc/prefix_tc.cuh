@@ -209,6 +209,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   Work* const works = reinterpret_cast<Work*>(smem + C::OFF_WORK);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (PREFIX || !after_prefix) wait_before();  // nothing before this reads what other launches have written
+  Planner<PREFIX> plan;
+  if constexpr (PREFIX) {
+    let_next();  // the suffix stage may come up
+    plan.sh = p.suffix_rows > 0 ? share_out<NUM_THREADS, true>(p, SMS, BN, ROWS, true)
+                                : share_out<NUM_THREADS, false>(p, SMS, BN, ROWS, true);
+    if (static_cast<int>(blockIdx.x) >= plan.sh.ranges) return;  // the SM is the suffix stage's
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(bar(C::BAR_FULL + s), 1);
@@ -231,12 +239,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish();
   }
-  if (PREFIX || !after_prefix) wait_before();  // nothing before this reads what other launches have written
-  if constexpr (PREFIX) let_next();            // the suffix stage may come up
-  Planner<PREFIX> plan;
   if constexpr (PREFIX) {
-    plan.sh = p.suffix_rows > 0 ? share_out<NUM_THREADS, true>(p, SMS, BN, ROWS, true)
-                                : share_out<NUM_THREADS, false>(p, SMS, BN, ROWS, true);
     plan.u = plan.sh.u0;
     plan.u1 = plan.sh.u1;
     plan.first = plan.sh.first;
@@ -273,9 +276,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int i = 0;; ++i) {
         Work w{};
         const bool more = plan.next(p, w);
-        bool free = false;  // looked at now and then: the others need the issue slots
-        for (int k = 0; k < 4000000 && !(free = mbar_test_nb(bar(C::BAR_FREE + (i & 1)), ((i >> 1) & 1) ^ 1)); ++k) __nanosleep(500);
-        if (!__all_sync(0xffffffffu, free)) {
+        if (!warp_wait(bar(C::BAR_FREE + (i & 1)), ((i >> 1) & 1) ^ 1)) {
           if (lane == 0) fail();
           break;
         }
