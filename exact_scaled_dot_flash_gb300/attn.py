@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -954,34 +955,39 @@ def paged_kv8_fwd(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
 
 # ------------------------------------------------------------------ pages of a cache
 def _pool(block_table, seq_lens, refs, page_size):
-    """Checks a pool's arrays (seq_lens None: the call does not take it): its C description and its device."""
-    dev = refs.device
-    size = block_table.shape
-    if len(size) != 2 or refs.dim() != 1:
+    """Checks a pool's arrays (seq_lens None: the call does not take it): its C description, its device and
+    the addresses."""
+    dev, size, pages = refs.device, block_table.shape, refs.shape
+    if len(size) != 2 or len(pages) != 1:
         raise AttnError("block_table must be int32 [num_seqs, max_pages] and refs int32 [num_pages]")
-    _int32("block_table", block_table, size, dev)
-    _int32("refs", refs, refs.shape, dev)
-    if seq_lens is not None:
-        _int32("seq_lens", seq_lens, size[:1], dev)
-    return Pages(size[0], size[1], page_size, refs.shape[0]), dev
+    ptrs = (_int32("block_table", block_table, size, dev),
+            _int32("seq_lens", seq_lens, size[:1], dev) if seq_lens is not None else None, _int32("refs", refs, pages, dev))
+    return Pages(size[0], size[1], page_size, pages[0]), dev, ptrs
 
 
 def _buffers(caches, num_pages, dev):
     """The buffers of a call: addresses and bytes of a page of each."""
     ptrs, sizes = [], []
+    shape = dtype = None
     for t in caches:
-        if t.device != dev or t.dim() < 1 or t.shape[0] != num_pages or not t.is_contiguous():
-            raise AttnError(f"caches must be contiguous [num_pages = {num_pages}, ...] tensors on {dev}")
+        if t.shape != shape or t.dtype is not dtype:  # layers are alike
+            shape, dtype = t.shape, t.dtype
+            if len(shape) < 1 or shape[0] != num_pages:
+                raise AttnError(f"caches must be [num_pages = {num_pages}, ...] tensors")
+            page = t.nbytes // num_pages if num_pages else 1
+        if t.device != dev or not t.is_contiguous():
+            raise AttnError(f"caches must be contiguous tensors on {dev}")
         ptrs.append(t.data_ptr() or None)
-        sizes.append(t.nbytes // num_pages if num_pages else 1)
+        sizes.append(page)
     n = len(ptrs)
     return (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), n
 
 
 def _rows(name, t, dev):
-    if t.dim() != 1:
+    shape = t.shape
+    if len(shape) != 1:
         raise AttnError(f"{name} must be a one-dimensional int32 tensor on {dev}")
-    return _int32(name, t, t.shape, dev)
+    return _int32(name, t, shape, dev)
 
 
 def pages_copy(caches, src, dst, *, stream=None):
@@ -1014,29 +1020,33 @@ def pages_fork(block_table, seq_lens, refs, parents, children, *, page_size: int
     shared page before one of its sequences writes to it. The children must differ from one another and
     from the parents.
     """
-    pool, dev = _pool(block_table, seq_lens, refs, page_size)
+    pool, dev, ptrs = _pool(block_table, seq_lens, refs, page_size)
     if parents.shape != children.shape:
         raise AttnError("parents and children must have the same length")
     lib = _lib or load_library()
     st = _stream(stream, dev)
-    _launch(dev, lib.attn_pages_fork, pool, block_table.data_ptr() or None, seq_lens.data_ptr() or None,
-            refs.data_ptr() or None, _rows("parents", parents, dev), _rows("children", children, dev), parents.shape[0], st)
+    _launch(dev, lib.attn_pages_fork, pool, *ptrs, _rows("parents", parents, dev), _rows("children", children, dev),
+            parents.shape[0], st)
 
 
 def pages_free(block_table, seq_lens, refs, seqs, *, stream=None):
     """Sequences ``seqs`` (int32 [n]) give back their pages (attn_pages_free), in place:
     their rows become -1, their lengths 0. The pool's arrays as for :func:`pages_fork`."""
-    pool, dev = _pool(block_table, seq_lens, refs, 1)
+    pool, dev, ptrs = _pool(block_table, seq_lens, refs, 1)
     lib = _lib or load_library()
     st = _stream(stream, dev)
-    _launch(dev, lib.attn_pages_free, pool, block_table.data_ptr() or None, seq_lens.data_ptr() or None,
-            refs.data_ptr() or None, _rows("seqs", seqs, dev), seqs.shape[0], st)
+    _launch(dev, lib.attn_pages_free, pool, *ptrs, _rows("seqs", seqs, dev), seqs.shape[0], st)
 
 
 def pages_workspace_bytes(pool: Pages) -> int:
     """Workspace bytes attn_pages_reserve and attn_pages_compact need for ``pool``."""
+    return _pages_bytes(pool.num_seqs, pool.max_pages, pool.page_size, pool.num_pages)
+
+
+@functools.lru_cache(maxsize=256)
+def _pages_bytes(*pool):
     n = ctypes.c_size_t(0)
-    rc = (_lib or load_library()).attn_pages_workspace_bytes(pool, n)
+    rc = (_lib or load_library()).attn_pages_workspace_bytes(Pages(*pool), n)
     if rc:
         check(rc)
     return n.value
@@ -1063,7 +1073,7 @@ def pages_reserve(block_table, seq_lens, refs, new_tokens, caches=(), *, page_si
     the write that follows counts the tokens. Returns ``result``, int32 [2] on the
     device: pages taken, pages lacking (then nothing was changed).
     """
-    pool, dev = _pool(block_table, seq_lens, refs, page_size)
+    pool, dev, ptrs = _pool(block_table, seq_lens, refs, page_size)
     bufs = _buffers(caches, pool.num_pages, dev)
     made = []
     if result is None:
@@ -1071,8 +1081,7 @@ def pages_reserve(block_table, seq_lens, refs, new_tokens, caches=(), *, page_si
     ws, need = _pool_space(refs, pool, workspace, made)
     lib = _lib or load_library()
     st = _stream(stream, dev, made)
-    _launch(dev, lib.attn_pages_reserve, pool, block_table.data_ptr() or None, seq_lens.data_ptr() or None,
-            refs.data_ptr() or None, _int32("new_tokens", new_tokens, seq_lens.shape, dev), *bufs,
+    _launch(dev, lib.attn_pages_reserve, pool, *ptrs, _int32("new_tokens", new_tokens, seq_lens.shape, dev), *bufs,
             _int32("result", result, (2,), dev), ws, need, st)
     return result
 
@@ -1083,7 +1092,7 @@ def pages_compact(block_table, refs, caches, *, page_map=None, used=None, worksp
     of pages in use, in every one of ``caches``; block_table and refs follow. Returns
     (page_map, used): int32 [num_pages], where each page now is (-1: it was free),
     and int32 [1], U, on the device."""
-    pool, dev = _pool(block_table, None, refs, 1)
+    pool, dev, (bt, _, rf) = _pool(block_table, None, refs, 1)
     bufs = _buffers(caches, pool.num_pages, dev)
     made = []
     if page_map is None:
@@ -1093,7 +1102,7 @@ def pages_compact(block_table, refs, caches, *, page_map=None, used=None, worksp
     ws, need = _pool_space(refs, pool, workspace, made)
     lib = _lib or load_library()
     st = _stream(stream, dev, made)
-    _launch(dev, lib.attn_pages_compact, pool, block_table.data_ptr() or None, refs.data_ptr() or None, *bufs,
+    _launch(dev, lib.attn_pages_compact, pool, bt, rf, *bufs,
             _int32("page_map", page_map, refs.shape, dev), _int32("used", used, (1,), dev), ws, need, st)
     return page_map, used
 
@@ -1101,8 +1110,13 @@ def pages_compact(block_table, refs, caches, *, page_map=None, used=None, worksp
 # ------------------------------------------------------------------ a shared prefix
 def paged_prefix_workspace_bytes(shape: PagedShape, num_groups: int, max_group_queries: int) -> int:
     """Workspace bytes attn_paged_prefix_fwd needs."""
+    return _prefix_bytes(num_groups, max_group_queries, *(getattr(shape, name) for name, _ in PagedShape._fields_))
+
+
+@functools.lru_cache(maxsize=256)
+def _prefix_bytes(num_groups, max_group_queries, *shape):
     n = ctypes.c_size_t(0)
-    rc = (_lib or load_library()).attn_paged_prefix_workspace_bytes(shape, num_groups, max_group_queries, n)
+    rc = (_lib or load_library()).attn_paged_prefix_workspace_bytes(PagedShape(*shape), num_groups, max_group_queries, n)
     if rc:
         check(rc)
     return n.value
@@ -1161,8 +1175,8 @@ def paged_prefix_fwd(q, k_cache, v_cache, block_table, seq_lens, q_offsets, grou
             made.append(lse := q.new_empty((nq, Hq), dtype=torch.float32))
         else:
             lse = _lse_buffer(lse_out, (nq, Hq), dev)
-    shape = PagedShape(ns, nq, Hq, Hkv, D, P, pages, table[1], max_queries)
-    need = paged_prefix_workspace_bytes(shape, ng, max_group_queries)
+    shape = (ns, nq, Hq, Hkv, D, P, pages, table[1], max_queries)
+    need = _prefix_bytes(ng, max_group_queries, *shape)
     if need:
         if workspace is None:
             made.append(workspace := q.new_empty(need, dtype=torch.uint8))
@@ -1171,7 +1185,7 @@ def paged_prefix_fwd(q, k_cache, v_cache, block_table, seq_lens, q_offsets, grou
             raise AttnError(f"workspace must hold {need} contiguous bytes on q's device")
     lib = _lib or load_library()
     st = _stream(stream, dev, made)
-    _launch(dev, lib.attn_paged_prefix_fwd, shape, ng, max_group_queries, q.data_ptr() or None, k_cache.data_ptr() or None,
+    _launch(dev, lib.attn_paged_prefix_fwd, PagedShape(*shape), ng, max_group_queries, q.data_ptr() or None, k_cache.data_ptr() or None,
             v_cache.data_ptr() or None, bt, sl, qo, pos, go, pl, 1 if causal else 0,
             1.0 / math.sqrt(D) if scale is None else scale, _dtype_code(q), workspace.data_ptr() if need else None, need,
             out.data_ptr() or None, lse.data_ptr() or None if lse is not None else None, st)

@@ -16,6 +16,7 @@
 
 #include "attn.h"
 #include "host_checks.h"
+#include "launch.cuh"
 #include "params.h"
 #include "ptx.cuh"
 
@@ -43,6 +44,7 @@ __device__ __forceinline__ int tokens_of(const Pool& p, int s) {
 template <bool FORK>
 __global__ void __launch_bounds__(THREADS) rows_kernel(const __grid_constant__ Pool p, const int32_t* __restrict__ from,
                                                        const int32_t* __restrict__ rows) {
+  wait_before();
   const int s = __ldg(rows + blockIdx.x);
   if (s < 0 || s >= p.num_seqs) return;
   int parent = -1, held = 0, tokens = 0;
@@ -100,7 +102,7 @@ __device__ __forceinline__ void move_as(uint8_t* to, const uint8_t* from, int n)
 }
 
 __global__ void __launch_bounds__(THREADS) copy_kernel(const __grid_constant__ CopyParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is complete
+  wait_before();  // the plan is complete
   const int64_t items = static_cast<int64_t>(p.count ? __ldcg(p.count) : p.n) * p.pieces;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int pair = static_cast<int>(it / p.pieces), r = static_cast<int>(it - static_cast<int64_t>(pair) * p.pieces);
@@ -224,7 +226,8 @@ __device__ __forceinline__ void written(const Pool& p, const int32_t* new_tokens
 __global__ void __launch_bounds__(PLAN_THREADS) reserve_kernel(const __grid_constant__ Pool p,
                                                                const int32_t* __restrict__ new_tokens, int32_t* ws,
                                                                int32_t* result, int ctas) {
-  asm volatile("griddepcontrol.launch_dependents;");  // the copies may come up; they wait
+  wait_before();
+  let_next();  // the copies may come up; they wait
   const Space w = space_of(p.num_pages, p.num_seqs);
   int32_t *const list = ws + w.list, *const owner = ws + w.owner, *const left = ws + w.left, *const first = ws + w.first;
   const int rank = static_cast<int>(cluster_rank());
@@ -251,36 +254,56 @@ __global__ void __launch_bounds__(PLAN_THREADS) reserve_kernel(const __grid_cons
   }
   cluster_sync();
 
-  // this thread's run of candidates
+  // This thread's run of candidates, and the sequence that it begins in: the last one whose first is
+  // at most c0. Each CTA looks in a copy of its own, a search in L2 would take a trip for each step.
+  constexpr int KEPT = 4096;
+  __shared__ int kept[KEPT];
+  const bool keep = p.num_seqs <= KEPT;
+  if (keep)
+    for (int s = threadIdx.x; s < p.num_seqs; s += PLAN_THREADS) kept[s] = __ldcg(first + s);
+  __syncthreads();
+  auto first_of = [&](int s) { return keep ? kept[s] : __ldcg(first + s); };
   int c0, c1;
   run_of(cands, me, threads, c0, c1);
-  int begin = 0;  // the last sequence that begins at or before c0 (and has candidates)
+  int begin = 0;
   if (c0 < c1) {
-    int lo = 0, hi = p.num_seqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldcg(first + mid) <= c0) lo = mid;
+    int hi = p.num_seqs;
+    while (hi - begin > 1) {
+      const int mid = (begin + hi) >> 1;
+      if (first_of(mid) <= c0) begin = mid;
       else hi = mid;
     }
-    begin = lo;
   }
-  auto each = [&](auto&& f) {  // f(candidate, sequence, block, its tokens, table entry)
+  // f(candidate, block, tokens of its sequence, table entry, page): a run of one candidate is read once
+  int32_t* one = nullptr;
+  int one_block = 0, one_tokens = 0, one_page = 0;
+  if (c0 + 1 == c1) {
+    written(p, new_tokens, begin, one_tokens, b0, b1);
+    one_block = b0 + (c0 - first_of(begin));
+    one = p.table + static_cast<int64_t>(begin) * p.max_pages + one_block;
+    one_page = *one;
+  }
+  auto each = [&](auto&& f) {
+    if (one) {
+      f(c0, one_block, one_tokens, one, one_page);
+      return;
+    }
     int s = begin;
     for (int c = c0; c < c1; ++s) {
       written(p, new_tokens, s, tokens, b0, b1);
-      for (int b = b0 + (c - __ldcg(first + s)); b < b1 && c < c1; ++b, ++c)
-        f(c, s, b, tokens, p.table + static_cast<int64_t>(s) * p.max_pages + b);
+      for (int b = b0 + (c - first_of(s)); b < b1 && c < c1; ++b, ++c) {
+        int32_t* const e = p.table + static_cast<int64_t>(s) * p.max_pages + b;
+        f(c, b, tokens, e, *e);
+      }
     }
   };
-  each([&](int, int, int, int, int32_t* e) {
-    const int page = *e;
+  each([&](int, int, int, int32_t*, int page) {
     if (!in_pool(page, p.num_pages)) return;
     owner[page] = -1;
     left[page] = max(p.refs[page], 1);
   });
   cluster_sync();
-  each([&](int c, int, int, int, int32_t* e) {
-    const int page = *e;
+  each([&](int c, int, int, int32_t*, int page) {
     if (!in_pool(page, p.num_pages)) return;
     atomicMax(owner + page, c);
     atomicSub(left + page, 1);
@@ -288,7 +311,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) reserve_kernel(const __grid_cons
   cluster_sync();
   auto keeps = [&](int c, int page) { return in_pool(page, p.num_pages) && __ldcg(left + page) == 0 && __ldcg(owner + page) == c; };
   int wants = 0, need;
-  each([&](int c, int, int, int, int32_t* e) { wants += keeps(c, *e) ? 0 : 1; });
+  each([&](int c, int, int, int32_t*, int page) { wants += keeps(c, page) ? 0 : 1; });
   int next = cluster_scan(wants, ctas, rank, need);
   if (need == 0) {
     if (me == 0) result[0] = result[1] = 0;
@@ -311,8 +334,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) reserve_kernel(const __grid_cons
       if (p.refs[i] <= 0) list[place++] = i;
   cluster_sync();
 
-  each([&](int c, int, int b, int held, int32_t* e) {
-    const int page = *e;
+  each([&](int c, int b, int held, int32_t* e, int page) {
     if (keeps(c, page)) return;
     const int fresh = __ldcg(list + next++);
     *e = fresh;
@@ -333,7 +355,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) reserve_kernel(const __grid_cons
 // mover number (pages in use below it) - (pages in use below U).
 __global__ void __launch_bounds__(PLAN_THREADS) compact_kernel(const __grid_constant__ Pool p, int32_t* __restrict__ map,
                                                                int32_t* used_out, int32_t* ws, int ctas) {
-  asm volatile("griddepcontrol.launch_dependents;");
+  wait_before();
+  let_next();
   const Space w = space_of(p.num_pages, p.num_seqs);
   int32_t *const holes = ws + w.list, *const movers = ws + w.owner;
   const int rank = static_cast<int>(cluster_rank());
@@ -380,25 +403,10 @@ inline int plan_ctas(int64_t work) {
   return c;
 }
 
-template <typename... A>
-cudaError_t launch_plan(void (*kern)(A...), int ctas, cudaStream_t st, A... args) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(ctas);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(PLAN_THREADS);
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 // Launches the copies of p.src -> p.dst in all buffers, 64 of them at a time. `most`:
-// an upper bound on the pairs; `after_plan`: the launch before it is the plan.
+// an upper bound on the pairs.
 inline cudaError_t launch_copies(CopyParams p, void* const* bufs, const int64_t* page_bytes, int num_bufs, int64_t most,
-                                 bool after_plan, cudaStream_t st) {
+                                 cudaStream_t st) {
   int32_t* const table = p.table;
   for (int b0 = 0; b0 < num_bufs || (b0 == 0 && table); b0 += MAX_BUFS) {
     p.num_bufs = std::min(MAX_BUFS, num_bufs - b0);
@@ -412,16 +420,7 @@ inline cudaError_t launch_copies(CopyParams p, void* const* bufs, const int64_t*
     p.pieces = static_cast<int>(pieces);
     p.table = b0 == 0 ? table : nullptr;
     const int64_t items = std::max(most * pieces, p.table ? (p.entries + THREADS - 1) / THREADS : 1);
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(items, SMS * 8)));
-    cfg.blockDim = dim3(THREADS);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = after_plan && b0 == 0 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, copy_kernel, p);
+    const cudaError_t e = launch_early(copy_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(items, SMS * 8))), THREADS, 0, st, 0, p);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -521,7 +520,7 @@ extern "C" int attn_pages_copy(int num_pages, void* const* bufs, const int64_t* 
   p.n = n;
   p.num_pages = num_pages;
   p.status = attn::status_word(dev);
-  return done(attn::pages::launch_copies(p, bufs, page_bytes, num_bufs, n, false, static_cast<cudaStream_t>(stream)));
+  return done(attn::pages::launch_copies(p, bufs, page_bytes, num_bufs, n, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int attn_pages_fork(const attn_pages_t* pool, int32_t* block_table, int32_t* seq_lens, int32_t* refs,
@@ -540,8 +539,8 @@ extern "C" int attn_pages_fork(const attn_pages_t* pool, int32_t* block_table, i
   Pool p;
   if (const int rc = pool_of(s, block_table, seq_lens, refs, p)) return rc;
   const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(std::max(1, (s.max_pages + 255) / 256)));
-  attn::pages::rows_kernel<true><<<grid, attn::pages::THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p, parents, children);
-  return done(cudaGetLastError());
+  return done(attn::launch_early(attn::pages::rows_kernel<true>, grid, attn::pages::THREADS, 0, static_cast<cudaStream_t>(stream), 0, p,
+                                 parents, children));
 }
 
 extern "C" int attn_pages_free(const attn_pages_t* pool, int32_t* block_table, int32_t* seq_lens, int32_t* refs,
@@ -558,8 +557,8 @@ extern "C" int attn_pages_free(const attn_pages_t* pool, int32_t* block_table, i
   Pool p;
   if (const int rc = pool_of(s, block_table, seq_lens, refs, p)) return rc;
   const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(std::max(1, (s.max_pages + 255) / 256)));
-  attn::pages::rows_kernel<false><<<grid, attn::pages::THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p, nullptr, seqs);
-  return done(cudaGetLastError());
+  return done(attn::launch_early(attn::pages::rows_kernel<false>, grid, attn::pages::THREADS, 0, static_cast<cudaStream_t>(stream), 0, p,
+                                 static_cast<const int32_t*>(nullptr), seqs));
 }
 
 extern "C" int attn_pages_workspace_bytes(const attn_pages_t* pool, size_t* bytes) {
@@ -589,7 +588,7 @@ extern "C" int attn_pages_reserve(const attn_pages_t* pool, int32_t* block_table
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int32_t* const ws = static_cast<int32_t*>(workspace);
   const int ctas = attn::pages::plan_ctas(std::max(s.num_pages, s.num_seqs));
-  cudaError_t e = attn::pages::launch_plan(attn::pages::reserve_kernel, ctas, st, p, new_tokens, ws, result, ctas);
+  cudaError_t e = attn::launch_early(attn::pages::reserve_kernel, dim3(ctas), attn::pages::PLAN_THREADS, 0, st, ctas, p, new_tokens, ws, result, ctas);
   if (e != cudaSuccess || num_bufs == 0 || s.num_pages == 0) return done(e);
   const Space w = attn::pages::space_of(s.num_pages, s.num_seqs);
   CopyParams c{};
@@ -598,7 +597,7 @@ extern "C" int attn_pages_reserve(const attn_pages_t* pool, int32_t* block_table
   c.count = ws + w.counts;
   c.num_pages = s.num_pages;
   c.status = p.status;
-  return done(attn::pages::launch_copies(c, bufs, page_bytes, num_bufs, s.num_seqs, true, st));
+  return done(attn::pages::launch_copies(c, bufs, page_bytes, num_bufs, s.num_seqs, st));
 }
 
 extern "C" int attn_pages_compact(const attn_pages_t* pool, int32_t* block_table, int32_t* refs, void* const* bufs,
@@ -620,7 +619,7 @@ extern "C" int attn_pages_compact(const attn_pages_t* pool, int32_t* block_table
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int32_t* const ws = static_cast<int32_t*>(workspace);
   const int ctas = attn::pages::plan_ctas(s.num_pages);
-  const cudaError_t e = attn::pages::launch_plan(attn::pages::compact_kernel, ctas, st, p, page_map, used, ws, ctas);
+  const cudaError_t e = attn::launch_early(attn::pages::compact_kernel, dim3(ctas), attn::pages::PLAN_THREADS, 0, st, ctas, p, page_map, used, ws, ctas);
   if (e != cudaSuccess || s.num_pages == 0) return done(e);
   const Space w = attn::pages::space_of(s.num_pages, s.num_seqs);
   CopyParams c{};
@@ -633,5 +632,5 @@ extern "C" int attn_pages_compact(const attn_pages_t* pool, int32_t* block_table
   c.map = page_map;
   c.entries = static_cast<int64_t>(s.num_seqs) * s.max_pages;
   if (c.entries == 0) c.table = nullptr;
-  return done(attn::pages::launch_copies(c, bufs, page_bytes, num_bufs, s.num_pages / 2, true, st));
+  return done(attn::pages::launch_copies(c, bufs, page_bytes, num_bufs, s.num_pages / 2, st));
 }

@@ -22,6 +22,7 @@
 #include <atomic>
 
 #include "host_checks.h"
+#include "launch.cuh"
 #include "params.h"
 #include "ptx.cuh"
 
@@ -342,26 +343,6 @@ cudaError_t allow_smem(K kern, int smem, int device, std::atomic<unsigned long l
   if (e == cudaSuccess) configured.fetch_or(bit, std::memory_order_acq_rel);
   return e;
 }
-
-// A launch that may come up before the one in front of it on the stream has ended; its kernel waits
-// (griddepcontrol.wait) before it touches what that one or an earlier one has written.
-template <typename... A>
-cudaError_t launch_early(void (*kern)(A...), dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
-__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------------ few rows (prefix_rows.cuh)
 namespace rows {

@@ -616,7 +616,7 @@ cudaError_t launch_prefix_nt(const Params& p, cudaStream_t st) {
   constexpr int smem = Shared<D, NT>::BYTES;
   static std::atomic<unsigned long long> configured{0};
   const cudaError_t e = allow_smem(kern, smem, p.device, configured);
-  return e != cudaSuccess ? e : launch_early(kern, dim3(SMS * ctas_of_sm(D, NT)), THREADS, smem, st, p);
+  return e != cudaSuccess ? e : launch_early(kern, dim3(SMS * ctas_of_sm(D, NT)), THREADS, smem, st, 0, p);
 }
 
 template <int D, bool BF16, int NT>
@@ -626,7 +626,7 @@ cudaError_t launch_suffix_nt(const Params& p, bool after_prefix, cudaStream_t st
   static std::atomic<unsigned long long> configured{0};
   const cudaError_t e = allow_smem(kern, smem, p.device, configured);
   if (e != cudaSuccess) return e;
-  return launch_early(kern, dim3(static_cast<unsigned>(p.suffix_ranges) * p.Hkv), THREADS, smem, st, p, p.suffix_ranges,
+  return launch_early(kern, dim3(static_cast<unsigned>(p.suffix_ranges) * p.Hkv), THREADS, smem, st, 0, p, p.suffix_ranges,
                       LEAST_BLOCKS, after_prefix ? 1 : 0);
 }
 
@@ -634,7 +634,7 @@ template <int D, bool BF16>
 cudaError_t launch_join_d(const Params& p, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(p.num_queries) * p.Hq, per = JOIN_THREADS / (D / 4);
   if ((rows + per - 1) / per > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_early(join_kernel<D, BF16>, dim3(static_cast<unsigned>((rows + per - 1) / per)), JOIN_THREADS, 0, st, p);
+  return launch_early(join_kernel<D, BF16>, dim3(static_cast<unsigned>((rows + per - 1) / per)), JOIN_THREADS, 0, st, 0, p);
 }
 
 #define ATTN_NT(F, NT, ...)                                        \

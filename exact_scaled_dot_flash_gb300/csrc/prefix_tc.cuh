@@ -732,7 +732,7 @@ cudaError_t launch_d(EncodeTiledFn enc, const Params& p, bool after_prefix, cuda
   const int64_t items = p.num_seqs * qblocks * p.Hkv;
   const int64_t ctas = PREFIX ? SMS : std::min<int64_t>(items, SMS);
   if (ctas == 0) return cudaSuccess;
-  return launch_early(kern, dim3(static_cast<unsigned>(ctas)), NUM_THREADS, smem, st, tk, tv, p, static_cast<int>(qblocks),
+  return launch_early(kern, dim3(static_cast<unsigned>(ctas)), NUM_THREADS, smem, st, 0, tk, tv, p, static_cast<int>(qblocks),
                       items, after_prefix ? 1 : 0);
 }
 
