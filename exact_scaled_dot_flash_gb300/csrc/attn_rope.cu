@@ -21,8 +21,9 @@
 // thread working out its own for every 16 bytes, the instructions were the bound
 // (72 us for 8191 tokens of 40 F16 heads, D 128). For the 16-bit types, whose
 // vectors take twice the conversions, many threads with one vector each beat few
-// with several in flight (F16, 8 CTAs an SM and 1: 36.5 us, 4.6 TB/s; 4 and 4: 49
-// us; the 32 registers of a thread hold an F16 item, of a BF16 one 40-72 bytes spill);
+// with several in flight (F16, 8 CTAs an SM and 1: 34.8 us, 4.8 TB/s; 4 and 4: 49
+// us; the 32 registers of a thread hold an F16 item; a BF16 one spills 40-72 bytes in them, and 6
+// CTAs of 42 registers are faster: 37.1 us against 39.0 for 9416 tokens of three axes, 5 CTAs with two vectors in flight 41.9);
 // for F32 it is the other way round (16384 tokens of 64 heads: 160 us, 6.7 TB/s,
 // with 4 vectors and 2 tokens a CTA, 171 us as the 16-bit types).
 #include <math.h>
@@ -66,7 +67,7 @@ struct Params {
 template <int DT> struct Elem;
 template <> struct Elem<0> { using T = float; static constexpr int VEC = 4, BATCH = 4, CTAS = 4, TOKENS = 2; };
 template <> struct Elem<1> { using T = __half; static constexpr int VEC = 8, BATCH = 1, CTAS = 8, TOKENS = 4; };
-template <> struct Elem<2> { using T = __nv_bfloat16; static constexpr int VEC = 8, BATCH = 1, CTAS = 8, TOKENS = 4; };
+template <> struct Elem<2> { using T = __nv_bfloat16; static constexpr int VEC = 8, BATCH = 1, CTAS = 6, TOKENS = 4; };
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -92,7 +93,12 @@ __global__ void __launch_bounds__(THREADS, Elem<DT>::CTAS) rope_kernel(const __g
   constexpr int BATCH = Elem<DT>::BATCH;
   constexpr int M = HALVES || N > 1 ? N : 2;  // elements of the first access
   using V1 = Vec<T, M>;                       // (not one access where N is 1)
-  extern __shared__ float2 cs[];              // [tok][rot / 2] cos, sin times mscale
+  // [tok][rot / 2] cos, sin times mscale. Vectors: two pairs of an item in 16 bytes, those of
+  // all items side by side, so that neighbouring threads read neighbouring banks (in the order of
+  // the pairs a read of 8 threads took 4 turns, and shared memory 75% of its time: 9416 tokens of 40
+  // BF16 heads, D 128, three axes 42.4 us, 39.0 as it is).
+  extern __shared__ __align__(16) float2 cs[];
+  constexpr int PAIRS = HALVES ? N : N / 2;   // of an item
   __shared__ struct { const T* in; T* out; } row_s[MAX_ROWS];
   __shared__ int16_t tok_s[MAX_ROWS];         // token, + 256 if the tail is copied
   const int half = p.rot >> 1;
@@ -144,13 +150,17 @@ __global__ void __launch_bounds__(THREADS, Elem<DT>::CTAS) rope_kernel(const __g
       const auto w = row_s[r + u * per];
       const int tok = tok_s[r + u * per];
       const float2* const c = cs + (tok & 255) * half;
+      auto factor = [&](int k) {  // of pair k of the item
+        if constexpr (N == 1) return c[item];
+        else return c[((k >> 1) * turn + item) * 2 + (k & 1)];
+      };
       if (item >= turn) {
         if (tok & 256) *reinterpret_cast<V*>(w.out + p.rot + (item - turn) * N) = y[u];
       } else if constexpr (HALVES) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           const float a = to_f(x[u].x[k]), b = to_f(y[u].x[k]);
-          const float2 f = c[item * N + k];
+          const float2 f = factor(k);
           from_f(x[u].x[k], a * f.x - b * f.y);
           from_f(y[u].x[k], b * f.x + a * f.y);
         }
@@ -160,7 +170,7 @@ __global__ void __launch_bounds__(THREADS, Elem<DT>::CTAS) rope_kernel(const __g
 #pragma unroll
         for (int k = 0; k < M; k += 2) {
           const float a = to_f(x[u].x[k]), b = to_f(x[u].x[k + 1]);
-          const float2 f = c[(item * M + k) >> 1];
+          const float2 f = factor(k >> 1);
           from_f(x[u].x[k], a * f.x - b * f.y);
           from_f(x[u].x[k + 1], b * f.x + a * f.y);
         }
@@ -191,7 +201,12 @@ __global__ void __launch_bounds__(THREADS, Elem<DT>::CTAS) rope_kernel(const __g
     const int32_t top = static_cast<int32_t>(static_cast<uint32_t>((static_cast<uint64_t>(pos) * F) >> 32));
     float sn, cn;
     sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31
-    cs[e] = make_float2(cn * p.mscale, (p.inverse ? -sn : sn) * p.mscale);
+    int to = e;
+    if constexpr (N > 1) {
+      const int item = i / PAIRS, k = i % PAIRS;
+      to = t * half + ((k >> 1) * turn + item) * 2 + (k & 1);
+    }
+    cs[to] = make_float2(cn * p.mscale, (p.inverse ? -sn : sn) * p.mscale);
   }
   __syncthreads();
   for (int item = first; item < items; item += THREADS) {
