@@ -79,6 +79,13 @@ struct Shared {
   static constexpr int BYTES = OFF_Q + NT * (D / 16) * 32 * 8;
 };
 
+// Whether a pair holds a NaN or an infinity: all bits of an exponent set.
+template <bool BF16>
+__device__ __forceinline__ bool not_finite(uint32_t pair) {
+  constexpr uint32_t LO = BF16 ? 0x7f80u : 0x7c00u, HI = LO << 16;
+  return (pair & LO) == LO || (pair & HI) == HI;
+}
+
 // A CTA's piece of a unit: rows (queries from q_lo on, `nq` of them, times heads; row_lo the
 // first of R rows), keys [from, to), read through row `table` of the table.
 struct Piece {
@@ -275,12 +282,54 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
     }
     copy_wait<2 * STAGES - 1>();
     __syncwarp();  // its values
+    bool strange = false;  // a value that is no number, in a tile that some row sees a part of
+    if (masked) {
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      uint32_t a[4];
-      ldsm4_t(a, va + (vr * PIECES + ((2 * k + ((lane >> 3) & 1)) ^ (vr & 7))) * 16);
+      for (int k = 0; k < KS; ++k) {
+        uint32_t a[4];
+        ldsm4_t(a, va + (vr * PIECES + ((2 * k + ((lane >> 3) & 1)) ^ (vr & 7))) * 16);
 #pragma unroll
-      for (int i = 0; i < NT; ++i) mma16816<BF16>(acc[k][i], a, pf[i][0], pf[i][1]);
+        for (int e = 0; e < 4; ++e) strange |= not_finite<BF16>(a[e]);
+      }
+      strange = __any_sync(0xffffffffu, strange);
+    }
+    if (!strange) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t a[4];
+        ldsm4_t(a, va + (vr * PIECES + ((2 * k + ((lane >> 3) & 1)) ^ (vr & 7))) * 16);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) mma16816<BF16>(acc[k][i], a, pf[i][0], pf[i][1]);
+      }
+    } else {
+      // 0 times it is not 0: a row at a time, with zeros in the place of what that row does not see
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll 1
+        for (int n = 0; n < 8; ++n) {
+          const int sees = min(lims[8 * i + n], w.to) - key0;
+          const uint32_t b0 = g == n ? pf[i][0] : 0u, b1 = g == n ? pf[i][1] : 0u;
+          auto keep = [&](uint32_t x, int key) {  // of the pair of keys from `key` on
+            return (key < sees ? x & 0xffffu : 0u) | (key + 1 < sees ? x & 0xffff0000u : 0u);
+          };
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            uint32_t a[4];
+            ldsm4_t(a, va + (vr * PIECES + ((2 * k + ((lane >> 3) & 1)) ^ (vr & 7))) * 16);
+            a[0] = keep(a[0], 2 * t);
+            a[1] = keep(a[1], 2 * t);
+            a[2] = keep(a[2], 8 + 2 * t);
+            a[3] = keep(a[3], 8 + 2 * t);
+            // the other rows' columns get 0 times what this row sees, which may be no number: they keep theirs
+            float d[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[e] = acc[k][i][e];
+            mma16816<BF16>(d, a, b0, b1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (2 * t + (e & 1) == n) acc[k][i][e] = d[e];
+          }
+        }
     }
     __syncwarp();
     copy_values(stage);

@@ -75,6 +75,14 @@ struct Work {
 };
 static_assert(sizeof(Work) == 64);
 
+// The most keys that one of the queries [q, q + n) of the sequences [a, b) sees. A warp calls it.
+__device__ __forceinline__ int most_seen(const Params& p, int a, int b, int q, int n) {
+  int most = 0;
+  for (int i = q + static_cast<int>(threadIdx.x & 31); i < q + n; i += 32)
+    most = max(most, limit_of(p, last_at_most(p.q_offsets, a, b, i), i));
+  return __reduce_max_sync(0xffffffffu, most);
+}
+
 // The pieces of a CTA, one after another. A warp calls it, all lanes with the same results.
 template <bool PREFIX>
 struct Planner {
@@ -143,8 +151,12 @@ struct Planner {
       w.row0 = (w.split ? rec.rbs - 1 : unit / p.Hkv) * ROWS;
       w.lo = 0;
       w.to = to;
+      if (!open) {  // what no row of the piece sees is not there
+        const int q0 = w.row0 / heads, q1 = min(nq - 1, (w.row0 + (w.split ? BM : ROWS) - 1) / heads);
+        w.to = min(to, most_seen(p, a, b, q_lo + q0, q1 - q0 + 1));
+      }
       w.group = g;
-      const int tiles = (to + BN - 1) / BN;  // with keys; a reader shorter than the prefix has fewer than nb
+      const int tiles = (w.to + BN - 1) / BN;  // with keys; a reader shorter than the prefix has fewer than nb
       if (w.split) {
         w.part = 2 * piece;
         w.j0 = 2 * k0;
@@ -176,13 +188,17 @@ struct Planner {
         w.j0 = own.start / BN;
         w.split = w.part = 0;
         const int all = query_at(p, w.s1) - w.q_lo;
+        if (p.causal && p.positions) {  // what no row of the piece sees is not there
+          const int q0 = w.row0 / heads, q1 = min(w.nq - 1, (w.row0 + ROWS - 1) / heads);
+          w.to = min(w.to, most_seen(p, w.s0, w.s1, w.q_lo + q0, q1 - q0 + 1));
+        }
 #pragma unroll
         for (int t = 0; t < NQ; ++t) {
           const int r0 = w.row0 + t * BM;
           w.n[t] = 0;
           if (r0 >= static_cast<int64_t>(w.nq) * heads) continue;
           int end = w.to;  // keys that the tile's rows see
-          if (p.causal && !p.positions) end = min(end, w.to - all + min(w.nq - 1, (r0 + BM - 1) / heads) + 1);
+          if (p.causal && !p.positions) end = min(end, own.L - all + min(w.nq - 1, (r0 + BM - 1) / heads) + 1);
           w.n[t] = end > w.lo ? (end + BN - 1) / BN - w.j0 : 0;
         }
         w.state = 1;
@@ -196,6 +212,46 @@ struct Planner {
 
 // A value that is the same in all lanes of a warp, from a reduction, whose result is uniform.
 __device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
+// Where a row does not see a key of its tile whose value is a NaN or an infinity, the product has made
+// no number of its elements (0 times it is not 0). The warp computes the row's output once more, from the keys
+// [from, to) that it sees: lane i has elements i D / 32 ... m: the row's reference.
+template <int D, bool BF16>
+__device__ __noinline__ void mend_row(const Params& p, int table, int h, int64_t orow, int from, int to, float m, float (&acc)[D / 32]) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  auto load = [&](const void* base, int64_t row, float (&x)[E]) {
+    const uint32_t* const at = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) + row * D + lane * E);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const uint32_t u = __ldg(at + i);
+      const float2 f = BF16 ? make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u))
+                            : __half22float2(*reinterpret_cast<const __half2*>(&u));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  };
+  float q[E], k[E], v[E];
+  load(p.q, orow, q);
+#pragma unroll
+  for (int i = 0; i < E; ++i) acc[i] = 0.f;
+  for (int j = from; j < to; ++j) {
+    const int page = page_of(p, table, j / p.page_size);
+    if (page < 0) continue;  // values of zero
+    const int64_t row = (static_cast<int64_t>(page) * p.page_size + j % p.page_size) * p.Hkv + h;
+    if (!in_bounds(p.status, row, static_cast<int64_t>(p.num_pages) * p.page_size * p.Hkv)) continue;
+    load(p.k, row, k);
+    load(p.v, row, v);
+    float d = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) d = fmaf(q[i], k[i], d);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    const float w = fast_exp2(fmaf(d, p.scale_log2, -m));
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+  }
+}
 
 template <int D, bool BF16, bool PREFIX>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
@@ -615,6 +671,41 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!w.split && w.row0 + t * BM >= w.nq * heads) continue;  // no rows of this tile
       tc_fence_after();
+      const int end = min(w.to, (jt + n_t) * BN);  // of the keys that were multiplied
+      if (have && __any_sync(0xffffffffu, row_in && lim < end)) {
+        bool bad = false;  // the row has an element that is no number, and did not see all keys
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + 32 * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) bad |= (o[k] & 0x7f800000u) == 0x7f800000u;
+        }
+        for (uint32_t todo = __ballot_sync(0xffffffffu, bad && row_in && lim < end); todo; todo &= todo - 1) {
+          const int r = __ffs(todo) - 1;
+          float acc[D / 32];
+          mend_row<D, BF16>(p, w.table, w.h, __shfl_sync(0xffffffffu, orow, r), max(w.lo, jt * BN),
+                            min(end, __shfl_sync(0xffffffffu, lim, r)), __shfl_sync(0xffffffffu, m_run, r), acc);
+          // through the warp's own rows of the q tile, which no product reads any more, into row r
+          float* const mine = reinterpret_cast<float*>(smem + t * C::TILE_BYTES + (warp & 3) * 4096);
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) mine[lane * (D / 32) + k] = acc[k];
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (lane == r) o[k] = __float_as_uint(mine[32 * c + k]);
+            tmem_st32(tO + 32 * c, o);
+          }
+          tmem_wait_st();
+          __syncwarp();
+        }
+      }
       if constexpr (PREFIX) {
         const int64_t at = (w.part + (w.split ? t : 0)) * nrows + orow;
         const bool ok = row_in && in_bounds(p.status, at, p.most_parts * nrows);

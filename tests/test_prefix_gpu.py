@@ -113,6 +113,44 @@ def test_pages_outside_the_cache_read_as_zeros():
         check(b)
 
 
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: "-".join(str(v) for v in f.values()))
+@pytest.mark.parametrize("strange", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("name", ["drafts", "mixed", "prompts"])
+def test_what_a_row_does_not_see_does_not_reach_it(name, form, strange):
+    # keys and values that are no numbers at tokens that only the last rows of a sequence see: those rows are no
+    # numbers, all others as without them
+    b = Shared(37, BATCHES[name], **form)
+    ref = list(b.ref())
+    hit = np.zeros(len(b.q), bool)
+    for s in range(len(b.lens)):
+        if b.new[s] > 2:
+            j = int(b.lens[s]) - 2  # the last two queries see it
+            page = b.table[s, j // b.P]
+            b.vc[page, j % b.P] = strange
+            if s % 2:
+                b.kc[page, j % b.P] = strange
+            hit[b.offs[s + 1] - 2:b.offs[s + 1]] = True
+    assert hit.any()
+    out, lse = run(b)
+    o, z = to_f64(out), to_f64(lse)
+    assert not np.isfinite(o[hit]).any()
+    near(o[~hit], z[~hit], [x[~hit] for x in ref], b.dtype, b.D)
+
+
+@pytest.mark.parametrize("form", FORMS[:4] + FORMS[5:6], ids=lambda f: "-".join(str(v) for v in f.values()))
+def test_positions_that_leave_keys_to_no_row(form):
+    # every query stands at key 10 of its own: what lies behind it is no number
+    b = Shared(41, [(150, [(90, 70), (60, 1), (40, 33)])], **form)
+    pos = np.full(len(b.q), 160, np.int32)
+    ref = b.ref(pos)
+    for s in range(3):
+        for j in range(161, int(b.lens[s])):
+            b.vc[b.table[s, j // b.P], j % b.P] = float("nan")
+            b.kc[b.table[s, j // b.P], j % b.P] = float("inf")
+    out, lse = run(b, pos)
+    near(to_f64(out), to_f64(lse), ref, b.dtype, b.D)
+
+
 def test_the_groups_do_not_change_the_result():
     # the same batch as one group, as two, as none: equal up to the order of the sums
     import torch
