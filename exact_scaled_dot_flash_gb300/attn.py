@@ -1172,14 +1172,14 @@ def paged_prefix_fwd(q, k_cache, v_cache, block_table, seq_lens, q_offsets, grou
     lse = None
     if return_lse:
         if lse_out is None:
-            made.append(lse := q.new_empty((nq, Hq), dtype=torch.float32))
+            made.append(lse := torch.empty((nq, Hq), dtype=torch.float32, device=dev))
         else:
             lse = _lse_buffer(lse_out, (nq, Hq), dev)
     shape = (ns, nq, Hq, Hkv, D, P, pages, table[1], max_queries)
     need = _prefix_bytes(ng, max_group_queries, *shape)
     if need:
         if workspace is None:
-            made.append(workspace := q.new_empty(need, dtype=torch.uint8))
+            made.append(workspace := torch.empty(need, dtype=torch.uint8, device=dev))
         elif (workspace.device != dev or workspace.numel() * workspace.element_size() < need
               or not workspace.is_contiguous()):
             raise AttnError(f"workspace must hold {need} contiguous bytes on q's device")
@@ -1262,7 +1262,7 @@ def _rope(q, k, positions, inv_freq, layout, mscale, inverse, axes, q_out, k_out
         raise AttnError("q must be [tokens, Hq, D] or [B, Hq, S, D]")
     made = []
     if q_out is None:
-        made.append(q_out := q.new_empty(size))
+        made.append(q_out := torch.empty(size, dtype=dtype, device=dev))
     elif q_out.dtype is not dtype or q_out.device != dev or q_out.shape != size:
         raise AttnError(f"q_out must be a {dtype} {list(size)} tensor on {dev}")
 
@@ -1280,7 +1280,7 @@ def _rope(q, k, positions, inv_freq, layout, mscale, inverse, axes, q_out, k_out
         if k.dtype is not dtype or k.device != dev or ksize != ((S, Hk, D) if dim == 3 else (B, Hk, S, D)):
             raise AttnError(f"k must be a {dtype} tensor on {dev} like q but for its heads")
         if k_out is None:
-            made.append(k_out := k.new_empty(ksize))
+            made.append(k_out := torch.empty(ksize, dtype=dtype, device=dev))
         elif k_out.dtype is not dtype or k_out.device != dev or k_out.shape != ksize:
             raise AttnError(f"k_out must be a {dtype} {list(ksize)} tensor on {dev}")
         kst, kost = strides("k", k), strides("k_out", k_out)

@@ -240,6 +240,7 @@ bool takes_tc(const attn_paged_shape_t& s) {
 // How a call runs and lays out its workspace.
 struct Plan {
   int most_parts = 1;                 // parts of a row's prefix
+  bool alone = false;                 // 16-bit kernels: no prefix stage
   bool prefix_tc = false, suffix_tc = false;  // the kernel for many rows
   int prefix_nt = 0, suffix_nt = 0;   // that for few: 8-row groups of a CTA
   int ranges = 0;                     // of the suffix stage
@@ -255,6 +256,11 @@ Plan plan_of(const attn_paged_shape_t& s, int num_groups, int max_group_queries)
   const int64_t seq_rows = s.max_queries * heads;
   d.prefix_tc = group_rows > 32 && takes_tc(s) && s.Hkv * ((s.num_queries * heads + 255) / 256 + num_groups) <= 0x7fffffffLL;
   d.suffix_tc = seq_rows > 32 && takes_tc(s) && s.num_seqs * s.Hkv * ((seq_rows + 255) / 256) <= 0x7fffffffLL;
+  // Up to 8 MB of keys and values, counted for every sequence by itself, are 2 us of streaming: reading the
+  // prefix once costs a launch and a stage more (4 rows over 201 + 40 keys: 14.4 us on the GPU and 34 us for the
+  // call with it, 13.5 and 27 without).
+  d.alone = takes_rows(s) && !d.suffix_tc &&
+            static_cast<int64_t>(s.num_seqs) * s.max_pages * s.page_size <= (8ll << 20) / (4ll * s.Hkv * s.D);
   d.prefix_nt = rows::nt_of(group_rows);
   d.suffix_nt = rows::nt_of(seq_rows);
   // Room for as many parts of a row's prefix as its group's CTAs can leave (two each where they split
@@ -390,6 +396,7 @@ extern "C" int attn_paged_prefix_fwd(const attn_paged_shape_t* shape, int num_gr
       enc = attn::encode_tiled();
       if (!enc) return attn::record_cuda_error(cudaErrorNotSupported);
     }
+    if (plan.alone) p.num_groups = 0;
     const bool shared = p.num_groups > 0;
     if (shared) {
       if (plan.prefix_tc) e = bf16 ? launch<true, true>(enc, p, false, st) : launch<false, true>(enc, p, false, st);

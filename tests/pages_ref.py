@@ -164,9 +164,10 @@ def near(out, lse, ref, dtype, D, parts_round=True):
 
 class Shared:
     """A batch of groups. groups: [(prefix, [(own tokens, new tokens), ...]), ...]; a prefix of None is
-    sequences of no group. Everything that no sequence holds is NaN."""
+    sequences of no group. Everything that no sequence holds is NaN. ``wide``: a table so wide that the
+    call cannot know from its shape that there is nothing to be gained by sharing."""
 
-    def __init__(self, seed, groups, *, dtype, D, P, H, Hq, hidden=float("nan")):
+    def __init__(self, seed, groups, *, dtype, D, P, H, Hq, hidden=float("nan"), wide=True):
         import torch
         self.dtype, self.D, self.P, self.H, self.Hq = dtype, D, P, H, Hq
         r = np.random.RandomState(seed)
@@ -193,6 +194,8 @@ class Shared:
         self.lens, self.new = np.array(lens, np.int32), np.array(new, np.int32)
         self.offs = np.concatenate([[0], np.cumsum(self.new)]).astype(np.int32)
         blocks = max(1, int(-(-self.lens.max() // P))) + 1
+        if wide:
+            blocks = max(blocks, (8 << 20) // (4 * H * D * P * len(lens)) + 1)
         self.table = np.full((len(lens), blocks), -1, np.int32)
         pages = int((-(-self.lens // P)).sum()) + 3
         perm = r.permutation(pages)

@@ -55,8 +55,9 @@ FORMS = [dict(dtype="bf16", D=128, P=64, H=2, Hq=8), dict(dtype="f16", D=64, P=1
 
 @pytest.mark.parametrize("form", FORMS, ids=lambda f: "-".join(str(v) for v in f.values()))
 @pytest.mark.parametrize("name", BATCHES)
-def test_batches(name, form):
-    b = Shared(len(name), BATCHES[name], **form)
+@pytest.mark.parametrize("wide", [True, False])
+def test_batches(name, form, wide):
+    b = Shared(len(name), BATCHES[name], wide=wide, **form)
     check(b)
     check(b, causal=False, scale=0.3)
 

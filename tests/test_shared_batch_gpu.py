@@ -19,14 +19,14 @@ def i32(a):
 class Program:
     """One prompt and its answers. Rows 0 .. answers-1 of the table are the answers, the last one the prompt."""
 
-    def __init__(self, dtype, prompt, answers, P, H=2, Hq=8, D=128, pages=80, seed=0):
+    def __init__(self, dtype, prompt, answers, P, H=2, Hq=8, D=128, pages=80, seed=0, width=500):
         import torch
         from exact_scaled_dot_flash_gb300 import attn
         self.attn, self.torch = attn, torch
         self.dt = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[dtype]
         self.dtype, self.P, self.H, self.Hq, self.D, self.n = dtype, P, H, Hq, D, answers
         rows = answers + 1
-        self.table, self.lens, self.refs = i32(np.full((rows, 30), -1)), i32(np.zeros(rows)), i32(np.zeros(pages))
+        self.table, self.lens, self.refs = i32(np.full((rows, width), -1)), i32(np.zeros(rows)), i32(np.zeros(pages))
         self.cache = [torch.full((pages, P, H, D), float("nan"), dtype=self.dt, device="cuda") for _ in range(2)]
         self.gen = torch.Generator().manual_seed(seed)
         self.freq, self.axes = attn.rope_frequencies(D)[0].cuda(), attn.rope_axes([D // 8, D // 8, D // 4]).cuda()
@@ -120,7 +120,7 @@ def test_answers_to_one_prompt(dtype, prompt, answers, P):
 
 def test_calls_on_two_streams_at_once():
     import torch
-    m = Program("bf16", 400, 6, 16)
+    m = Program("bf16", 400, 6, 16, width=200)
     attn = m.attn
     attn.pages_fork(m.table, m.lens, m.refs, i32([6] * 6), i32(np.arange(6)), page_size=16)
     for r in range(6):
@@ -145,7 +145,7 @@ def test_calls_on_two_streams_at_once():
 def test_a_decode_loop_in_one_graph():
     # reserve, attention and the pool's other calls captured together and replayed, lengths moving on the device
     import torch
-    m = Program("f16", 200, 4, 16)
+    m = Program("f16", 200, 4, 16, width=30)
     attn = m.attn
     attn.pages_fork(m.table, m.lens, m.refs, i32([4] * 4), i32(np.arange(4)), page_size=16)
     for r in range(4):
