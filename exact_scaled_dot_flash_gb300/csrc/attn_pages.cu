@@ -9,9 +9,11 @@
 // reserve and compact plan on one cluster of CTAs (plan_kernel below), since what they
 // hand out depends on the order of all sequences and of all pages: two prefix
 // sums over the cluster, a few thousand instructions in all, bound by the trips to L2
-// between its barriers. The copies that follow from the plan are a kernel of their own
-// over the whole GPU, bound by the bytes of the moved pages, each read once and
-// written once.
+// between its barriers (reserve, 64 of 128 rows, 8700 pages: 19 us with cold caches, a
+// beam step with it 23 us as a graph; compact, 6000 pages: 9 us). The copies that follow
+// from the plan are a kernel of their own over the whole GPU, bound by the bytes of the
+// moved pages, each read once and written once (1.27 GB: 194 us, 6.5 TB/s, 98% of the copy
+// bandwidth).
 #include <algorithm>
 
 #include "attn.h"

@@ -20,6 +20,10 @@
 // same rows and half of the key tiles each, and leave a part each: a block is 256 keys. (Halves, not
 // every other tile: the keys are then read at the time that the group's other rows read them.)
 // Suffix stage: a piece is all own keys of a sequence for 256 rows, joined with the prefix's parts.
+// Measured (32/8 heads, D 128, BF16): the prefix of 24 prompts of 16-128 tokens behind 4096 keys 119 us, 0.97
+// PFLOP/s, their own keys 57 us; 96 rows over 60001 keys 116 us, 0.82 PFLOP/s. Bound by the softmax's latency between
+// the products of two row tiles (tensor pipe 49% active); the second case also by the keys of a head
+// being read for each of its two row blocks (477 MB instead of 246).
 #pragma once
 
 #include <algorithm>
