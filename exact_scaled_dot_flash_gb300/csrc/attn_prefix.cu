@@ -261,14 +261,29 @@ Plan plan_of(const attn_paged_shape_t& s, int num_groups, int max_group_queries)
   // call with it, 13.5 and 27 without).
   d.alone = takes_rows(s) && !d.suffix_tc &&
             static_cast<int64_t>(s.num_seqs) * s.max_pages * s.page_size <= (8ll << 20) / (4ll * s.Hkv * s.D);
+  // With many rows the prefix stage packs rows of several sequences into its row blocks and fills every SM, but
+  // each row's part goes out in FP32 and comes back, and a stage more comes up: of a pass over 256 rows, 1.85 us a
+  // key tile, that is 17 us beside 40 us once. Without it a sequence's own row blocks run over all its keys, in whole
+  // rounds of the SMs (bf16, 32/8 heads, D 128, us with the stage and without: 4 sequences of 32 queries behind
+  // 8192 tokens 67 and 104, 24 of 64 207 and 233, 8 of 128 141 and 121, 24 of 512 1348 and 1278; behind 1024 tokens
+  // 46 and 23, 83 and 51, 59 and 29, 434 and 286). The table's width stands for the lengths, and groups of one
+  // size for the call's.
+  if (d.prefix_tc && d.suffix_tc) {
+    const double tiles = 1.85 * s.max_pages * s.page_size / 128;
+    const int64_t own = s.num_seqs * s.Hkv * ((seq_rows + 255) / 256), rounds = (own + attn::SMS - 1) / attn::SMS;
+    const int64_t of_group = (s.num_queries * heads + 256ll * num_groups - 1) / (256ll * std::max(1, num_groups));
+    const int64_t packed = s.Hkv * num_groups * of_group;
+    d.alone = 8 + rounds * (tiles + 4) <= 40 + (tiles + 17) * packed / attn::SMS;
+  }
   d.prefix_nt = rows::nt_of(group_rows);
   d.suffix_nt = rows::nt_of(seq_rows);
   // Room for as many parts of a row's prefix as its group's CTAs can leave (two each where they split
-  // their keys), within 64 MB where that is enough for MIN_PARTS; a call uses what the device settles on.
+  // their keys), within 64 MB where that is enough for MIN_PARTS, or for one (FP32) of rows that 16 bits
+  // take alone; a call uses what the device settles on.
   const int64_t ctas = static_cast<int64_t>(attn::SMS) * (d.prefix_tc ? 1 : rows::ctas_of_sm(s.D, d.prefix_nt));
   const int64_t units = s.Hkv * (num_groups == 1 ? std::max<int64_t>(1, (group_rows + 255) / 256) : 1);
   const int64_t room = (64ll << 20) / std::max<int64_t>(1, rows * (4 * s.D + 8));
-  d.most_parts = static_cast<int>(std::max<int64_t>(MIN_PARTS, std::min<int64_t>({MAX_PARTS, 2 * (ctas + units - 1) / units, room})));
+  d.most_parts = static_cast<int>(std::max<int64_t>(d.alone ? 1 : MIN_PARTS, std::min<int64_t>({MAX_PARTS, 2 * (ctas + units - 1) / units, room})));
   const int suffix_ctas = attn::SMS * rows::ctas_of_sm(s.D, d.suffix_nt);
   d.ranges = std::max(1, suffix_ctas / s.Hkv);
   auto up = [](int64_t n) { return (n + 31) / 32 * 32; };  // the parts move in 32 bytes

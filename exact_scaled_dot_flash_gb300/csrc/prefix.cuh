@@ -30,7 +30,7 @@ namespace attn {
 namespace prefix {
 
 constexpr float LN2 = 0.6931471805599453f;
-constexpr int MAX_PARTS = 32, MIN_PARTS = 4;  // room for the parts of a row
+constexpr int MAX_PARTS = 32, MIN_PARTS = 2;  // room for the parts of a row
 
 // How the prefix stage was shared out, in the workspace: block total and ranges of the call; of each
 // group its first block, the blocks of one (row block, head), the row blocks, whether the last
@@ -56,7 +56,7 @@ struct Params {
   float* lse;
   int* status;
   // workspace
-  int most_parts;   // slots of a row
+  int most_parts;   // slots of a row; from 4 on, a last row block of half the rows or fewer splits its keys
   Head* head;
   Rec* rec;         // [num_groups]
   float2* ml;       // [most_parts, num_queries * Hq]

@@ -79,6 +79,8 @@ struct Work {
 };
 static_assert(sizeof(Work) == 64);
 
+__device__ __forceinline__ bool halves(const Params& p) { return p.most_parts >= 4; }
+
 // The most keys that one of the queries [q, q + n) of the sequences [a, b) sees. A warp calls it.
 __device__ __forceinline__ int most_seen(const Params& p, int a, int b, int q, int n) {
   int most = 0;
@@ -101,7 +103,7 @@ struct Planner {
   bool open;
 
   __device__ __forceinline__ void load_group(const Params& p) {
-    rec = rec_of(p, g, BN, ROWS, true);
+    rec = rec_of(p, g, BN, ROWS, halves(p));
     group_range(p, g, a, b);
     nq = queries_of(p, a, b, p.max_group_queries, q_lo);
     pre = prefix_len(p, g);
@@ -135,7 +137,7 @@ struct Planner {
           ++g;
         }
         fresh = false;
-        rec = rec_of(p, g, BN, ROWS, true);
+        rec = rec_of(p, g, BN, ROWS, halves(p));
         if (u < first + blocks_of(p, rec)) load_group(p);
       }
       const int64_t off = u - first, full = full_blocks(p, rec);
@@ -273,8 +275,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   Planner<PREFIX> plan;
   if constexpr (PREFIX) {
     let_next();  // the suffix stage may come up
-    plan.sh = p.suffix_rows > 0 ? share_out<NUM_THREADS, true>(p, SMS, BN, ROWS, true)
-                                : share_out<NUM_THREADS, false>(p, SMS, BN, ROWS, true);
+    plan.sh = p.suffix_rows > 0 ? share_out<NUM_THREADS, true>(p, SMS, BN, ROWS, halves(p))
+                                : share_out<NUM_THREADS, false>(p, SMS, BN, ROWS, halves(p));
     if (static_cast<int>(blockIdx.x) >= plan.sh.ranges) return;  // the SM is the suffix stage's
   }
   if (threadIdx.x == 0) {

@@ -195,7 +195,7 @@ class Shared:
         self.offs = np.concatenate([[0], np.cumsum(self.new)]).astype(np.int32)
         blocks = max(1, int(-(-self.lens.max() // P))) + 1
         if wide:
-            blocks = max(blocks, (8 << 20) // (4 * H * D * P * len(lens)) + 1)
+            blocks = max(blocks, (8 << 20) // (4 * H * D * P * len(lens)) + 1, 65536 // P)
         self.table = np.full((len(lens), blocks), -1, np.int32)
         pages = int((-(-self.lens // P)).sum()) + 3
         perm = r.permutation(pages)

@@ -117,10 +117,11 @@ def test_pages_outside_the_cache_read_as_zeros():
 @pytest.mark.parametrize("form", FORMS, ids=lambda f: "-".join(str(v) for v in f.values()))
 @pytest.mark.parametrize("strange", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("name", ["drafts", "mixed", "prompts"])
-def test_what_a_row_does_not_see_does_not_reach_it(name, form, strange):
+@pytest.mark.parametrize("wide", [True, False])
+def test_what_a_row_does_not_see_does_not_reach_it(name, form, strange, wide):
     # keys and values that are no numbers at tokens that only the last rows of a sequence see: those rows are no
     # numbers, all others as without them
-    b = Shared(37, BATCHES[name], **form)
+    b = Shared(37, BATCHES[name], wide=wide, **form)
     ref = list(b.ref())
     hit = np.zeros(len(b.q), bool)
     for s in range(len(b.lens)):
@@ -227,6 +228,64 @@ def test_graph_streams_and_workspace():
     torch.cuda.synchronize()
     assert torch.equal(one[0], want[0]) and torch.equal(one[1], want[1])
     assert torch.equal(two[0], attn.paged_prefix_fwd(q2, *d[1:], **kw)[0])
+
+
+@pytest.mark.parametrize("wide", [True, False])
+@pytest.mark.parametrize("name", ["short", "wide", "mixed", "prompts"])
+def test_captured_between_other_work(name, wide):
+    # in one graph: the inputs come from a memset, a copy and another stream's kernels, the results go to
+    # another stream and the inputs are overwritten right behind the call
+    import torch
+    from exact_scaled_dot_flash_gb300 import attn
+    b = Shared(47, BATCHES[name], wide=wide, **FORMS[0])
+    d = b.device()
+    kw = dict(max_queries=b.max_q, max_group_queries=b.max_gq, return_lse=True)
+    want = attn.paged_prefix_fwd(*d, **kw)
+    src = [x.clone() for x in d[:3]]
+    live = [torch.empty_like(x) for x in d[:3]]
+    got = [torch.empty_like(x) for x in want]
+    big = torch.empty(1 << 26, device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    main.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        for form in range(2):
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                big.fill_(form)  # so that the copies come late
+                live[0].copy_(src[0])
+            live[1].zero_()
+            live[1].copy_(src[1])
+            live[2].copy_(src[2])
+            if form:  # the other stream's kernel is the last before the call, or a memset of this one is
+                live[1].zero_()
+                live[1].add_(src[1])
+            else:
+                big[:5].zero_()
+            main.wait_stream(side)
+            out, lse = attn.paged_prefix_fwd(*live, *d[3:], **kw)
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                got[0].copy_(out)
+                got[1].copy_(lse)
+            for x in live:
+                x.fill_(float("nan"))
+            main.wait_stream(side)
+    for _ in range(4):
+        for x in got:
+            x.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    # without a graph, in a chain: each call reads what the one before it wrote
+    def chain(wait):
+        x = d[0]
+        for _ in range(6):
+            x = attn.paged_prefix_fwd(x, *d[1:], **kw)[0]
+            if wait:
+                torch.cuda.synchronize()
+        return x
+    assert torch.equal(chain(False), chain(True))
 
 
 def test_bounds_are_computed_when_not_given():
