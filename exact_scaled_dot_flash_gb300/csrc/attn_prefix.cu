@@ -214,7 +214,7 @@ using attn::meet;
 int check_shape(const attn_paged_shape_t& s, int num_groups, int max_group_queries) {
   if (s.num_seqs < 0 || s.num_queries < 0 || s.Hq <= 0 || s.Hkv <= 0 || s.D <= 0 || s.page_size <= 0 ||
       s.num_pages < 0 || s.max_pages < 0 || s.max_queries < 0 || s.Hq % s.Hkv != 0 || num_groups < 0 ||
-      max_group_queries < 0)
+      max_group_queries < 0 || s.num_seqs > 1 << 30 || num_groups > 1 << 30)
     return ATTN_ERR_SHAPE;
   if (!(s.D == 16 || s.D == 32 || s.D == 64 || s.D == 128)) return ATTN_ERR_HEAD_DIM;
   const int heads = s.Hq / s.Hkv;
@@ -253,7 +253,7 @@ Plan plan_of(const attn_paged_shape_t& s, int num_groups, int max_group_queries)
   Plan d;
   const int64_t heads = s.Hq / s.Hkv, rows = static_cast<int64_t>(s.num_queries) * s.Hq;
   const int64_t group_rows = std::min(max_group_queries, s.num_queries) * heads;
-  const int64_t seq_rows = s.max_queries * heads;
+  const int64_t seq_rows = std::min(s.max_queries, s.num_queries) * heads;
   d.prefix_tc = group_rows > 32 && takes_tc(s) && s.Hkv * ((s.num_queries * heads + 255) / 256 + num_groups) <= 0x7fffffffLL;
   d.suffix_tc = seq_rows > 32 && takes_tc(s) && s.num_seqs * s.Hkv * ((seq_rows + 255) / 256) <= 0x7fffffffLL;
   // Up to 8 MB of keys and values, counted for every sequence by itself, are 2 us of streaming: reading the
@@ -368,8 +368,8 @@ extern "C" int attn_paged_prefix_fwd(const attn_paged_shape_t* shape, int num_gr
   p.page_size = s.page_size;
   p.num_pages = s.num_pages;
   p.max_pages = s.max_pages;
-  p.max_queries = s.max_queries;
-  p.max_group_queries = max_group_queries;
+  p.max_queries = std::min(s.max_queries, s.num_queries);
+  p.max_group_queries = std::min(max_group_queries, s.num_queries);
   p.causal = causal;
   p.device = dev;
   p.scale_log2 = scale * 1.4426950408889634f;

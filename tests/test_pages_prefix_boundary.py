@@ -138,7 +138,7 @@ def prefix(s=None, ng=1, mgq=3, **kw):
 BAD_SHAPES = [(dict(s=dict(Hq=3)), "SHAPE"), (dict(s=dict(num_queries=-1)), "SHAPE"), (dict(s=dict(D=80)), "HEAD_DIM"),
               (dict(s=dict(page_size=0)), "SHAPE"), (dict(ng=-1), "SHAPE"), (dict(mgq=-1), "SHAPE"),
               (dict(s=dict(num_pages=(1 << 31) - 1, page_size=1 << 20, max_pages=1, Hq=1 << 15, Hkv=1 << 15, D=128)), "SHAPE"),
-              (dict(s=dict(max_pages=1 << 28)), "SHAPE"), (dict(ng=1 << 30), "SHAPE"), (dict(mgq=(1 << 31) - 1), "SHAPE")]
+              (dict(s=dict(max_pages=1 << 28)), "SHAPE"), (dict(ng=1 << 30), "SHAPE"), (dict(ng=(1 << 30) + 1, s=dict(Hkv=1)), "SHAPE"), (dict(mgq=(1 << 31) - 1), "SHAPE")]
 
 
 @no_gpu_only

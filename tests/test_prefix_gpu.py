@@ -296,6 +296,13 @@ def test_bounds_are_computed_when_not_given():
     assert torch.equal(a[0], c[0])
 
 
+@pytest.mark.parametrize("form", FORMS[:2] + FORMS[5:6], ids=lambda f: "-".join(str(v) for v in f.values()))
+def test_bounds_far_too_large(form):
+    for name in ("one", "mixed", "drafts"):
+        b = Shared(53, BATCHES[name], **form)
+        check(b, max_queries=200000, max_group_queries=500000)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_gradients_through_the_paged_backward(dtype):
     # attn_paged_bwd takes the output and lse of the shared call: a shared page gets every reader's
