@@ -12,8 +12,12 @@
 //    operand, so that 8 columns hold the rows instead of 16 or 128; K by ldmatrix, V by its
 //    transposing form, P^T from S^T by one movmatrix for 8 keys x 8 rows;
 //  - a row has a reference exponent: y = 2^(x - ref), and ref moves up only when a y passes
-//    2^15 (one vote a tile instead of a reduction), to bring the largest y to 2^8. F16
-//    probabilities then keep their full precision down to 2^-22 of the largest.
+//    2^15 (one vote a tile instead of a reduction), to bring the largest y to 2^8;
+//  - up to 16 rows a CTA, a probability meets the values as two numbers of the input type, the rounded one and
+//    what the rounding left: a second mma with the operand that is there already (64 sequences with 8 rows a kv
+//    head 78.0 us, 77.2 with the rounded one alone; with 16 rows 91.5 and 86.7; 4 rows, F16, error against
+//    64 bits 2.1e-4, the output's own rounding, instead of 2.5e-4 to 2.9e-4). With 32 rows it costs 11-20%
+//    (148 us, 124 without), and the roundings of many rows average out: there it is the rounded one alone.
 //
 // Suffix stage: the keys of all sequences, in blocks of 64 (16 a warp), are cut into ranges
 // of equal length, one for each group of Hkv CTAs (one a head, side by side). A CTA walks the
@@ -82,6 +86,12 @@ struct Shared {
   static constexpr int BYTES = OFF_Q + NT * (D / 16) * 32 * 8;
 };
 
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t u) {
+  if constexpr (BF16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+
 // Whether a pair holds a NaN or an infinity: all bits of an exponent set.
 template <bool BF16>
 __device__ __forceinline__ bool not_finite(uint32_t pair) {
@@ -101,6 +111,7 @@ template <int D, bool BF16, int NT>
 __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t* smem) {
   constexpr int KS = D / 16;       // 16-element steps of a head
   constexpr int ROWS = 8 * NT;
+  constexpr bool BOTH = NT <= 2;   // probabilities as two numbers
   using SH = Shared<D, NT>;
   constexpr int STAGES = SH::STAGES;
   float* const so = reinterpret_cast<float*>(smem);
@@ -275,13 +286,20 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
           y[i][2 + e] = fast_exp2(sc[i][2 + e] - n);
         }
     }
-    uint32_t pf[NT][2];
+    uint32_t pf[NT][2], pl[BOTH ? NT : 1][2];  // rounded, and what that left
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       l[i][0] += y[i][0] + y[i][2];
       l[i][1] += y[i][1] + y[i][3];
-      pf[i][0] = transpose8x8(pack2<BF16>(y[i][0], y[i][1]));
-      pf[i][1] = transpose8x8(pack2<BF16>(y[i][2], y[i][3]));
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t hi = pack2<BF16>(y[i][2 * e], y[i][2 * e + 1]);
+        pf[i][e] = transpose8x8(hi);
+        if constexpr (BOTH) {
+          const float2 back = unpack2<BF16>(hi);
+          pl[i][e] = transpose8x8(pack2<BF16>(y[i][2 * e] - back.x, y[i][2 * e + 1] - back.y));
+        }
+      }
     }
     copy_wait<2 * STAGES - 1>();
     __syncwarp();  // its values
@@ -302,7 +320,10 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
         uint32_t a[4];
         ldsm4_t(a, va + (vr * PIECES + ((2 * k + ((lane >> 3) & 1)) ^ (vr & 7))) * 16);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) mma16816<BF16>(acc[k][i], a, pf[i][0], pf[i][1]);
+        for (int i = 0; i < NT; ++i) {
+          if constexpr (BOTH) mma16816<BF16>(acc[k][i], a, pl[i][0], pl[i][1]);
+          mma16816<BF16>(acc[k][i], a, pf[i][0], pf[i][1]);
+        }
       }
     } else {
       // 0 times it is not 0: a row at a time, with zeros in the place of what that row does not see
@@ -327,6 +348,7 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
             float d[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) d[e] = acc[k][i][e];
+            if constexpr (BOTH) mma16816<BF16>(d, a, g == n ? pl[i][0] : 0u, g == n ? pl[i][1] : 0u);
             mma16816<BF16>(d, a, b0, b1);
 #pragma unroll
             for (int e = 0; e < 4; ++e)

@@ -660,8 +660,10 @@ ATTN_API int attn_pages_workspace_bytes(const attn_pages_t* pool, size_t* bytes)
  *   M = max(m_a, m_b),  l = 2^(m_a - M) l_a + 2^(m_b - M) l_b,
  *   out = (2^(m_a - M) O_a + 2^(m_b - M) O_b) / l;
  * parts are summed in fp32 and joined in a fixed order: repeated calls give identical
- * bits. F16/BF16 kernels round the probabilities to the input type before they meet
- * the values, as attn_paged_fwd's do.
+ * bits. For more than 16 rows (queries times heads of a kv head) of a group or of a
+ * sequence the F16/BF16 kernels round the probabilities to the input type before they
+ * meet the values, as attn_paged_fwd's do; those of fewer rows (D of 64 and 128) to
+ * twice its digits.
  *
  * max_group_queries: an upper bound on the queries of one group (as max_queries for
  * one sequence: it sizes the grid; rows beyond a bound that is too small get

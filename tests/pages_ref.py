@@ -139,12 +139,14 @@ def attention(q, kc, vc, table, lens, offs, positions, causal, scale):
     return out, lse, mass, noise
 
 
-def near(out, lse, ref, dtype, D, parts_round=True):
+def near(out, lse, ref, dtype, D, pairs=False):
     """Checks a result against attention()'s. Tolerances:
     a score is a sum of D products in fp32, off by at most (D + 4) 2^-24 noise, its exponential by
     2^-21 more (the product with log2 e, the difference to the maximum, exp2), so a weight by a
     factor 1 + 2 w, w = (D + 4) 2^-24 noise + 2^-21, the normalisation included; 16-bit kernels
-    round a weight to the type (u); sums of fp32 terms, a few thousand one after another in a
+    round a weight to the type (u), or with ``pairs`` what that leaves of it once more (u u, and half of F16's
+    smallest step, 2^-25, where a warp's largest weight is 2^8: 2^-33 of each of at most 2^12 values of 8 or
+    less); sums of fp32 terms, a few thousand one after another in a
     tile's and the tiles' order, lose 2^-18 of the mass at most; the result is rounded once (u of
     it, and half of F16's smallest step). A lse is off by w + 2^-22 of itself."""
     o_ref, l_ref, mass, noise = ref
@@ -153,8 +155,8 @@ def near(out, lse, ref, dtype, D, parts_round=True):
     seen = np.isfinite(l_ref)
     none = l_ref == -np.inf
     assert np.isnan(out[none]).all() and (lse[none] == -np.inf).all(), "rows without keys"
-    tol = u * np.abs(o_ref) + (2 * w[..., None] + 2.0 ** -18 + (u if dtype != "f32" else 0.0)) * mass
-    tol = tol + (2.0 ** -25 if dtype == "f16" else 0.0)
+    tol = u * np.abs(o_ref) + (2 * w[..., None] + 2.0 ** -18 + (0.0 if dtype == "f32" else u * u if pairs else u)) * mass
+    tol = tol + (2.0 ** -25 if dtype == "f16" else 0.0) + (2.0 ** -33 * 2 ** 12 * 8 if pairs and dtype == "f16" else 0.0)
     err = np.abs(out - o_ref)
     assert (err[seen] <= tol[seen]).all(), f"out off by {np.nanmax(err[seen] / tol[seen]):.2f} of what is allowed"
     el = np.abs(lse[seen] - l_ref[seen])

@@ -153,6 +153,17 @@ def test_positions_that_leave_keys_to_no_row(form):
     near(to_f64(out), to_f64(lse), ref, b.dtype, b.D)
 
 
+@pytest.mark.parametrize("wide", [True, False])
+@pytest.mark.parametrize("dtype,D,H,Hq,n", [("f16", 64, 1, 7, 2), ("f16", 128, 2, 2, 4), ("bf16", 128, 2, 16, 1),
+                                            ("bf16", 64, 1, 4, 4)])
+def test_few_rows_keep_their_weights(dtype, D, H, Hq, n, wide):
+    # at most 16 rows of a kv head, in the group and in each sequence
+    b = Shared(61, [(300, ones(n, 1, 500)), (77, ones(1, 20, 40))], dtype=dtype, D=D, P=16, H=H, Hq=Hq, wide=wide)
+    for causal in (True, False):
+        out, lse = run(b, causal=causal)
+        near(to_f64(out), to_f64(lse), b.ref(None, causal, None), dtype, D, pairs=True)
+
+
 def test_the_groups_do_not_change_the_result():
     # the same batch as one group, as two, as none: equal up to the order of the sums
     import torch
