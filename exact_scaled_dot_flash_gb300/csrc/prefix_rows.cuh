@@ -3,7 +3,7 @@
 // groups (F16/BF16, D in {64, 128}, any page size).
 //
 // Measured: own keys of 64 sequences, 100-2000 tokens each, 32/8 heads, D 128, BF16, by themselves: 54 us, 5.1 TB/s
-// (76% of the copy bandwidth); behind 8192 shared keys the whole call 74 us.
+// (76% of the copy bandwidth); behind 8192 shared keys the whole call 75 us.
 // Bound: the bytes of the keys and values, read once for all the rows of a kv head; then the latency
 // of a unit's beginning (metadata, query, page, first keys: a trip to L2 or beyond each) and of the join.
 // A warp streams its own 16-key tiles through buffers of cp.async copies in shared memory,
