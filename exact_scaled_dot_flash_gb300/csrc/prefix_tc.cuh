@@ -10,8 +10,9 @@
 //    to divide 128);
 //  - 128-key tiles gathered page by page, one TMA box each, from a 4-D view
 //    [pages, page_size, Hkv, D] of the cache;
-//  - values past the last key set to zero in shared memory before their product: a page's
-//    unwritten rows may hold NaN, which a probability of 0 does not remove;
+//  - values past the last key and before the first set to zero in shared memory before their
+//    product: a page's unwritten rows may hold NaN, and the prefix's last values infinities, which a
+//    probability of 0 does not remove;
 //  - one CTA an SM that goes through several pieces of work without a break: a warp works out
 //    the next piece from the metadata while the others compute, and the copies of its
 //    first tiles fly during the epilogue of the piece before.
@@ -417,13 +418,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool ok = true;
       Work w{};
       auto wait_full = [&](int idx) { return warp_wait(bar(C::BAR_FULL + idx % ST), (idx / ST) & 1); };
-      // Values past the last key (tile j of the unit, in ring slot idx): whole rows, the swizzle stays inside them.
+      // Values outside the unit's keys (tile j of the unit, in ring slot idx): whole rows, the swizzle stays inside them.
       auto fix_values = [&](int j, int idx) {
-        if ((j + 1) * BN <= w.to) return;
+        const int lo = w.lo - j * BN, hi = w.to - j * BN;  // its rows are [lo, hi)
+        if (lo <= 0 && hi >= BN) return;
         uint8_t* const v = smem + C::OFF_KV + idx % ST * C::TILE_BYTES;
-        for (int e = max(w.to - j * BN, 0) * 8 + lane; e < BN * 8; e += 32)
+        auto clear = [&](int from, int to) {
+          for (int e = from * 8 + lane; e < to * 8; e += 32)
 #pragma unroll
-          for (int c = 0; c < C::NCHUNK; ++c) *reinterpret_cast<uint4*>(v + c * C::CHUNK_BYTES + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < C::NCHUNK; ++c) *reinterpret_cast<uint4*>(v + c * C::CHUNK_BYTES + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+        };
+        clear(0, min(lo, BN));
+        clear(max(hi, 0), BN);
         fence_proxy_async_smem();
         __syncwarp();
       };
