@@ -13,8 +13,9 @@
 //    transposing form, P^T from S^T by one movmatrix for 8 keys x 8 rows;
 //  - a row has a reference exponent: y = 2^(x - ref), and ref moves up only when a y passes
 //    2^15 (one vote a tile instead of a reduction), to bring the largest y to 2^8;
-//  - up to 16 rows a CTA, a probability meets the values as two numbers of the input type, the rounded one and
-//    what the rounding left: a second mma with the operand that is there already (64 sequences with 8 rows a kv
+//  - up to 16 rows a CTA, a probability meets the values as two numbers of the input type, one below it and
+//    what that left (both above 0: the sum of their products with an infinite value is that infinity): a second
+//    mma with the operand that is there already (64 sequences with 8 rows a kv
 //    head 78.0 us, 77.2 with the rounded one alone; with 16 rows 91.5 and 86.7; 4 rows, F16, error against
 //    64 bits 2.1e-4, the output's own rounding, instead of 2.5e-4 to 2.9e-4). With 32 rows it costs 11-20%
 //    (148 us, 124 without), and the roundings of many rows average out: there it is the rounded one alone.
@@ -90,6 +91,19 @@ template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t u) {
   if constexpr (BF16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
   else return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+
+// Two weights of 0 or more as numbers of the type below them, so that what is left of a weight above 0 is above 0 too: a
+// part of 0 or less would make NaN of an infinite value. F16 stays half a step away: the rest then has a
+// number from a weight of 2^-12 on (a row's largest one is 2^8 at least).
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2_below(float lo, float hi) {
+  constexpr float LESS = BF16 ? 0x1.fffffcp-1f : 0x1.ffep-1f;  // 1 - 2^-23, 1 - 2^-12
+  const float2 x = fmul2(make_float2(lo, hi), make_float2(LESS, LESS));
+  uint32_t d;
+  if constexpr (BF16) asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(x.y), "f"(x.x));
+  else asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(x.y), "f"(x.x));
+  return d;
 }
 
 // Whether a pair holds a NaN or an infinity: all bits of an exponent set.
@@ -286,18 +300,19 @@ __device__ __forceinline__ void stream(const Params& p, const Piece& w, uint8_t*
           y[i][2 + e] = fast_exp2(sc[i][2 + e] - n);
         }
     }
-    uint32_t pf[NT][2], pl[BOTH ? NT : 1][2];  // rounded, and what that left
+    uint32_t pf[NT][2], pl[BOTH ? NT : 1][2];  // in the input type, and what that left
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       l[i][0] += y[i][0] + y[i][2];
       l[i][1] += y[i][1] + y[i][3];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint32_t hi = pack2<BF16>(y[i][2 * e], y[i][2 * e + 1]);
+        const float a = y[i][2 * e], b = y[i][2 * e + 1];
+        const uint32_t hi = BOTH ? pack2_below<BF16>(a, b) : pack2<BF16>(a, b);
         pf[i][e] = transpose8x8(hi);
         if constexpr (BOTH) {
           const float2 back = unpack2<BF16>(hi);
-          pl[i][e] = transpose8x8(pack2<BF16>(y[i][2 * e] - back.x, y[i][2 * e + 1] - back.y));
+          pl[i][e] = transpose8x8(pack2<BF16>(a - back.x, b - back.y));
         }
       }
     }
