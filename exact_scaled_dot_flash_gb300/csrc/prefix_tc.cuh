@@ -13,6 +13,10 @@
 //  - values past the last key and before the first set to zero in shared memory before their
 //    product: a page's unwritten rows may hold NaN, and the prefix's last values infinities, which a
 //    probability of 0 does not remove;
+//  - key tiles that some row of a row tile does not see in full looked through for values that are no
+//    numbers (there are one or two of them in a causal sequence): where there are some, the softmax threads
+//    add the tile's product to their rows themselves, each the keys that its row sees. The look costs 1%
+//    (24 prompts of 16-128 tokens behind 4096: 162 us, 156 without any care for such values);
 //  - one CTA an SM that goes through several pieces of work without a break: a warp works out
 //    the next piece from the metadata while the others compute, and the copies of its
 //    first tiles fly during the epilogue of the piece before.
@@ -28,6 +32,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "prefix.cuh"
 
@@ -62,8 +67,10 @@ struct Cfg {
   static constexpr int BAR_FULL = 0, BAR_EMPTY = STAGES, BAR_Q = 2 * STAGES, BAR_S = BAR_Q + NQ;
   static constexpr int BAR_P = BAR_S + NQ, BAR_O = BAR_P + NQ, BAR_DONE = BAR_O + NQ;
   static constexpr int BAR_WORK = BAR_DONE + 1, BAR_FREE = BAR_WORK + 2;  // the pieces' ring
-  static constexpr int OFF_MISC = OFF_BAR + (BAR_FREE + 2) * 8;
-  static constexpr int OFF_WORK = (OFF_MISC + 16 + 15) / 16 * 16;
+  static constexpr int BAR_TEAM = BAR_FREE + 2;                           // the four softmax warps of a row tile
+  static constexpr int OFF_MISC = OFF_BAR + (BAR_TEAM + NQ) * 8;
+  static constexpr int OFF_TEAM = OFF_MISC + 16;
+  static constexpr int OFF_WORK = (OFF_TEAM + NQ * 64 + 15) / 16 * 16;
   static constexpr int SMEM_BYTES = OFF_WORK + 2 * 64 + 1024;
 };
 
@@ -79,6 +86,16 @@ struct Work {
   int state;           // 0: no more work, 1: rows may see fewer keys than [lo, to), 2: every row sees all
 };
 static_assert(sizeof(Work) == 64);
+
+// What the softmax warps of a row tile tell one another and the issuing warp. Meetings take the two slots by
+// turns: who writes for meeting m + 2 has met the others at m + 1, and they had read those of m before.
+struct Team {
+  int least[2][4];  // fewest keys that a row of each warp sees
+  int strange[2];   // m + 1: a warp has found a value that is no number at meeting m
+  int alone;        // 1: the warps have added this tile's product themselves
+  int unused[5];    // to 64 bytes
+};
+static_assert(sizeof(Team) == 64);
 
 __device__ __forceinline__ bool halves(const Params& p) { return p.most_parts >= 4; }
 
@@ -220,44 +237,67 @@ struct Planner {
 // A value that is the same in all lanes of a warp, from a reduction, whose result is uniform.
 __device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
 
-// Where a row does not see a key of its tile whose value is a NaN or an infinity, the product has made
-// no number of its elements (0 times it is not 0). The warp computes the row's output once more, from the keys
-// [from, to) that it sees: lane i has elements i D / 32 ... m: the row's reference.
+// Whether one of the values of the rows [from, to) of a tile in shared memory is a NaN or an infinity, as far as this
+// thread (of 128) looks: 0 times it is not 0.
 template <int D, bool BF16>
-__device__ __noinline__ void mend_row(const Params& p, int table, int h, int64_t orow, int from, int to, float m, float (&acc)[D / 32]) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  auto load = [&](const void* base, int64_t row, float (&x)[E]) {
-    const uint32_t* const at = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) + row * D + lane * E);
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      const uint32_t u = __ldg(at + i);
-      const float2 f = BF16 ? make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u))
-                            : __half22float2(*reinterpret_cast<const __half2*>(&u));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
+__device__ __forceinline__ bool any_strange(const uint8_t* v, int from, int to, int thread) {
+  uint32_t sum = 0;
+  auto add = [&](uint32_t x) {
+    if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(x), "r"(0u));
+    else asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(x), "r"(0u));
   };
-  float q[E], k[E], v[E];
-  load(p.q, orow, q);
+  for (int e = from * 8 + thread; e < to * 8; e += 128)
 #pragma unroll
-  for (int i = 0; i < E; ++i) acc[i] = 0.f;
-  for (int j = from; j < to; ++j) {
-    const int page = page_of(p, table, j / p.page_size);
-    if (page < 0) continue;  // values of zero
-    const int64_t row = (static_cast<int64_t>(page) * p.page_size + j % p.page_size) * p.Hkv + h;
-    if (!in_bounds(p.status, row, static_cast<int64_t>(p.num_pages) * p.page_size * p.Hkv)) continue;
-    load(p.k, row, k);
-    load(p.v, row, v);
-    float d = 0.f;
+    for (int c = 0; c < Cfg<D>::NCHUNK; ++c) {
+      const uint4 x = *reinterpret_cast<const uint4*>(v + c * Cfg<D>::CHUNK_BYTES + e * 16);
+      add(x.x);
+      add(x.y);
+      add(x.z);
+      add(x.w);
+    }
+  return sum & 0x7fff7fffu;
+}
+
+// The product of a key tile whose values are not all numbers, with the weights that the tensor core would take: a
+// thread adds to its row of O what the row sees, keys [from, to) of the tile. (A weight of 0 does not remove what
+// is no number from the other rows of a tensor core's product.) 20 to 30 us, whatever the context's length.
+template <int D, bool BF16>
+__device__ __noinline__ void own_product(uint32_t tP, uint32_t tO, const uint8_t* v, int from, int to, bool fresh) {
+  const int first = __reduce_min_sync(0xffffffffu, to > from ? from : BN) & ~1;
+  const int last = __reduce_max_sync(0xffffffffu, to > from ? to : 0);
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t o[32];
+    tmem_ld32(tO + 32 * c, o);
+    tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < E; ++i) d = fmaf(q[i], k[i], d);
+    for (int i = 0; i < 32; ++i) o[i] = fresh ? 0u : o[i];
+    const uint8_t* const at = v + c / 2 * Cfg<D>::CHUNK_BYTES;
+#pragma unroll 1
+    for (int key = first; key < last; ++key) {
+      const uint32_t pair = tmem_ld1(tP + key / 2);
+      tmem_wait_ld();
+      const uint32_t half = key & 1 ? pair >> 16 : pair & 0xffffu;
+      const float w = BF16 ? __uint_as_float(half << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(half)));
+      if (key >= from && key < to) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    const float w = fast_exp2(fmaf(d, p.scale_log2, -m));
+        for (int u = 0; u < 4; ++u) {
+          const uint4 x = *reinterpret_cast<const uint4*>(at + key * 128 + (((c & 1) * 4 + u) ^ (key & 7)) * 16);
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = BF16 ? make_float2(__uint_as_float(y[i] << 16), __uint_as_float(y[i] & 0xffff0000u))
+                                  : __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
+            o[8 * u + 2 * i] = __float_as_uint(fmaf(w, f.x, __uint_as_float(o[8 * u + 2 * i])));
+            o[8 * u + 2 * i + 1] = __float_as_uint(fmaf(w, f.y, __uint_as_float(o[8 * u + 2 * i + 1])));
+          }
+        }
+      }
+      __syncwarp();
+    }
+    tmem_st32(tO + 32 * c, o);
   }
+  tmem_wait_st();
 }
 
 template <int D, bool BF16, bool PREFIX>
@@ -271,6 +311,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   Work* const works = reinterpret_cast<Work*>(smem + C::OFF_WORK);
+  volatile Team* const teams = reinterpret_cast<volatile Team*>(smem + C::OFF_TEAM);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (PREFIX || !after_prefix) wait_before();  // nothing before this reads what other launches have written
   Planner<PREFIX> plan;
@@ -290,6 +331,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(bar(C::BAR_S + t), 1);
       mbar_init(bar(C::BAR_P + t), BM);
       mbar_init(bar(C::BAR_O + t), 1);
+      mbar_init(bar(C::BAR_TEAM + t), 4);
+      teams[t].strange[0] = teams[t].strange[1] = teams[t].alone = 0;
     }
     mbar_init(bar(C::BAR_DONE), 1);
     for (int i = 0; i < 2; ++i) {
@@ -420,16 +463,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       auto wait_full = [&](int idx) { return warp_wait(bar(C::BAR_FULL + idx % ST), (idx / ST) & 1); };
       // Values outside the unit's keys (tile j of the unit, in ring slot idx): whole rows, the swizzle stays inside them.
       auto fix_values = [&](int j, int idx) {
-        const int lo = w.lo - j * BN, hi = w.to - j * BN;  // its rows are [lo, hi)
+        const int lo = PREFIX ? 0 : w.lo - j * BN, hi = w.to - j * BN;  // its rows are [lo, hi)
         if (lo <= 0 && hi >= BN) return;
         uint8_t* const v = smem + C::OFF_KV + idx % ST * C::TILE_BYTES;
-        auto clear = [&](int from, int to) {
-          for (int e = from * 8 + lane; e < to * 8; e += 32)
+        auto clear = [&](int e) {
 #pragma unroll
-            for (int c = 0; c < C::NCHUNK; ++c) *reinterpret_cast<uint4*>(v + c * C::CHUNK_BYTES + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+          for (int c = 0; c < C::NCHUNK; ++c) *reinterpret_cast<uint4*>(v + c * C::CHUNK_BYTES + e * 16) = make_uint4(0u, 0u, 0u, 0u);
         };
-        clear(0, min(lo, BN));
-        clear(max(hi, 0), BN);
+        if (!PREFIX && lo > 0) {
+#pragma unroll 1
+          for (int e = lane; e < min(lo, BN) * 8; e += 32) clear(e);
+        }
+        for (int e = max(hi, 0) * 8 + lane; e < BN * 8; e += 32) clear(e);
         fence_proxy_async_smem();
         __syncwarp();
       };
@@ -444,11 +489,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         __syncwarp();
       };
-      auto issue_pv = [&](int t, int j, int idx, bool last) {
+      auto issue_pv = [&](int t, int j, int idx, bool last, auto checked) {
         const uint64_t b = dv0 + (idx % ST) * TILE16;
         const uint32_t d = tmem + 256 + t * D;
         const uint32_t a = tmem + t * BN + C::COL_P;
-        if (elect_one()) {
+        // the softmax warps may have added the product themselves (a loop of its own where they never do: one for both
+        // costs the prefix stage 1%)
+        if (decltype(checked)::value && uniform(teams[t].alone)) {
+          if (last && elect_one()) umma_commit(bar(C::BAR_O + t));
+        } else if (elect_one()) {
           umma_ts(d, a, b, idesc_pv, j > 0 ? 1u : 0u);
 #pragma unroll
           for (int k = 1; k < C::KSTEPS_PV; ++k) umma_ts(d, a + k * 8, b + k * VSTEP16, idesc_pv, 1u);
@@ -470,72 +519,75 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ok = warp_wait(bar(C::BAR_Q + t), used[t] & 1);
             ++used[t];
           }
-        // every wait is bounded
-        if (split) {
-          int idx = it0;
-          for (int j = 0; j <= n0 && ok; ++j) {
-            if (j < n0) {
-              if (!(ok = wait_full(idx))) break;
-              tc_fence_after();
-              issue_s(0, idx);
-              release(idx++);
-            }
-            if (j >= 1 && j - 1 < n1) {
-              if (!(ok = wait_full(idx))) break;
-              fix_values(w.j0 + n0 + j - 1, idx);
-              if (!(ok = wait_p(1, j - 1))) break;
-              tc_fence_after();
-              issue_pv(1, j - 1, idx, j == n1);
-              release(idx++);
-            }
-            if (j < n1) {
-              if (!(ok = wait_full(idx))) break;
-              tc_fence_after();
-              issue_s(1, idx);
-              release(idx++);
-            }
-            if (j < n0) {
-              if (!(ok = wait_full(idx))) break;
-              fix_values(w.j0 + j, idx);
-              if (!(ok = wait_p(0, j))) break;
-              tc_fence_after();
-              issue_pv(0, j, idx, j == n0 - 1);
-              release(idx++);
-            }
-          }
-          it0 = idx;
-        } else {
-          for (int j = 0; j <= nmax && ok; ++j) {
-            const int idx = it0 + 2 * j;
-            if (j < nmax) {
-              if (!(ok = wait_full(idx))) break;
-              tc_fence_after();
-              if (j < n0) issue_s(0, idx);
-            }
-            if (j >= 1 && j - 1 < n1) {
-              if (j - 1 >= n0) {
-                if (!(ok = wait_full(idx - 1))) break;
-                fix_values(w.j0 + j - 1, idx - 1);
-              }
-              if (!(ok = wait_p(1, j - 1))) break;
-              tc_fence_after();
-              issue_pv(1, j - 1, idx - 1, j == n1);
-            }
-            if (j >= 1) release(idx - 1);
-            if (j < nmax) {
-              if (j < n1) issue_s(1, idx);
-              release(idx);
+        auto walk = [&](auto checked) {  // every wait is bounded
+          if (split) {
+            int idx = it0;
+            for (int j = 0; j <= n0 && ok; ++j) {
               if (j < n0) {
-                if (!(ok = wait_full(idx + 1))) break;
-                fix_values(w.j0 + j, idx + 1);
+                if (!(ok = wait_full(idx))) break;
+                tc_fence_after();
+                issue_s(0, idx);
+                release(idx++);
+              }
+              if (j >= 1 && j - 1 < n1) {
+                if (!(ok = wait_full(idx))) break;
+                fix_values(w.j0 + n0 + j - 1, idx);
+                if (!(ok = wait_p(1, j - 1))) break;
+                tc_fence_after();
+                issue_pv(1, j - 1, idx, j == n1, checked);
+                release(idx++);
+              }
+              if (j < n1) {
+                if (!(ok = wait_full(idx))) break;
+                tc_fence_after();
+                issue_s(1, idx);
+                release(idx++);
+              }
+              if (j < n0) {
+                if (!(ok = wait_full(idx))) break;
+                fix_values(w.j0 + j, idx);
                 if (!(ok = wait_p(0, j))) break;
                 tc_fence_after();
-                issue_pv(0, j, idx + 1, j == n0 - 1);
+                issue_pv(0, j, idx, j == n0 - 1, checked);
+                release(idx++);
               }
             }
+            it0 = idx;
+          } else {
+            for (int j = 0; j <= nmax && ok; ++j) {
+              const int idx = it0 + 2 * j;
+              if (j < nmax) {
+                if (!(ok = wait_full(idx))) break;
+                tc_fence_after();
+                if (j < n0) issue_s(0, idx);
+              }
+              if (j >= 1 && j - 1 < n1) {
+                if (j - 1 >= n0) {
+                  if (!(ok = wait_full(idx - 1))) break;
+                  fix_values(w.j0 + j - 1, idx - 1);
+                }
+                if (!(ok = wait_p(1, j - 1))) break;
+                tc_fence_after();
+                issue_pv(1, j - 1, idx - 1, j == n1, checked);
+              }
+              if (j >= 1) release(idx - 1);
+              if (j < nmax) {
+                if (j < n1) issue_s(1, idx);
+                release(idx);
+                if (j < n0) {
+                  if (!(ok = wait_full(idx + 1))) break;
+                  fix_values(w.j0 + j, idx + 1);
+                  if (!(ok = wait_p(0, j))) break;
+                  tc_fence_after();
+                  issue_pv(0, j, idx + 1, j == n0 - 1, checked);
+                }
+              }
+            }
+            it0 += 2 * nmax;
           }
-          it0 += 2 * nmax;
-        }
+        };
+        if (PREFIX && uniform(w.state) == 2) walk(std::false_type{});
+        else walk(std::true_type{});
         done[0] += n0;
         done[1] += n1;
       }
@@ -558,7 +610,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const float sc = p.scale_log2;
     const int heads = p.Hq / p.Hkv;
     int done = 0, used = 0;  // key tiles and pieces before
-    bool failed = false, waited = false;
+    int it0 = 0;            // ring slots of the pieces before
+    int met = 0;            // meetings of the row tile's four warps
+    volatile Team& team = teams[t];
+    bool failed = false, waited = false, alone = false;
+    auto meet = [&]() {  // all lanes
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::BAR_TEAM + t));
+      return warp_wait(bar(C::BAR_TEAM + t), met++ & 1);
+    };
     for (int i = 0; !failed; ++i) {
       Work w{};
       if (!get_work(i, w)) break;
@@ -589,11 +649,35 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         lim = min(w.to, limit_of(p, PREFIX ? last_at_most(p.q_offsets, w.s0, w.s1, q) : w.s0, q));
       }
       const int least = __reduce_min_sync(0xffffffffu, row_ok ? lim : w.to);
+      int least_t = w.to;  // of the row tile
+      if (w.state != 2 && n_t > 0) {
+        if (lane == 0) team.least[met & 1][warp & 3] = least;
+        failed = !meet();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) least_t = min(least_t, team.least[(met - 1) & 1][k]);
+      }
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = 0; j < n_t; ++j) {
+      for (int j = 0; j < n_t && !failed; ++j) {
         const bool ok = mbar_wait(bar(C::BAR_S + t), (done + j) & 1);
         if (__any_sync(0xffffffffu, !ok)) { failed = true; break; }
         tc_fence_after();
+        // Values that a row of the tile does not see have to be numbers for the tensor core: where there are such keys
+        // the four warps look through theirs. (Once S of a tile is there, so is what was in its values' slot before.)
+        const int base = (jt + j) * BN;
+        const int from = max(base, max(least_t, w.lo)), upto = min(base + BN, w.to);
+        const uint8_t* values = nullptr;  // of the tile, if one of them is none
+        if (from < upto) {
+          const int idx = it0 + (!w.split ? 2 * j + 1 : t ? 4 * j + 3 + (j + 1 < w.n[0]) : 4 * j + 1 + (j < w.n[1]));
+          const int slot = met & 1;
+          values = smem + C::OFF_KV + idx % C::STAGES * C::TILE_BYTES;
+          failed = !warp_wait(bar(C::BAR_FULL + idx % C::STAGES), (idx / C::STAGES) & 1);
+          if (failed) break;
+          const bool bad = any_strange<D, BF16>(values, from - base, upto - base, (warp & 3) * 32 + lane);
+          if (__any_sync(0xffffffffu, bad) && lane == 0) team.strange[slot] = met + 1;
+          failed = !meet();
+          if (failed) break;
+          if (team.strange[slot] != met) values = nullptr;
+        }
         float s[128];
         {
           uint32_t sr[4][32];
@@ -666,10 +750,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
         tmem_wait_st();
+        if (values) own_product<D, BF16>(tP, tO, values, max(w.lo - key0, 0), min(lim - key0, BN), j == 0);
+        if ((values != nullptr) != alone) {
+          alone = values != nullptr;
+          if (row == 0) team.alone = alone;
+        }
         tc_fence_before();
         mbar_arrive(bar(C::BAR_P + t));
       }
       done += n_t;
+      it0 += w.split ? 2 * (w.n[0] + w.n[1]) : 2 * max(w.n[0], w.n[1]);
       // -------------------------------------------------------------- epilogue
       const bool have = n_t > 0;
       if (!failed && have) {
@@ -683,41 +773,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!w.split && w.row0 + t * BM >= w.nq * heads) continue;  // no rows of this tile
       tc_fence_after();
-      const int end = min(w.to, (jt + n_t) * BN);  // of the keys that were multiplied
-      if (have && __any_sync(0xffffffffu, row_in && lim < end)) {
-        bool bad = false;  // the row has an element that is no number, and did not see all keys
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + 32 * c, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) bad |= (o[k] & 0x7f800000u) == 0x7f800000u;
-        }
-        for (uint32_t todo = __ballot_sync(0xffffffffu, bad && row_in && lim < end); todo; todo &= todo - 1) {
-          const int r = __ffs(todo) - 1;
-          float acc[D / 32];
-          mend_row<D, BF16>(p, w.table, w.h, __shfl_sync(0xffffffffu, orow, r), max(w.lo, jt * BN),
-                            min(end, __shfl_sync(0xffffffffu, lim, r)), __shfl_sync(0xffffffffu, m_run, r), acc);
-          // through the warp's own rows of the q tile, which no product reads any more, into row r
-          float* const mine = reinterpret_cast<float*>(smem + t * C::TILE_BYTES + (warp & 3) * 4096);
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) mine[lane * (D / 32) + k] = acc[k];
-          __syncwarp();
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + 32 * c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (lane == r) o[k] = __float_as_uint(mine[32 * c + k]);
-            tmem_st32(tO + 32 * c, o);
-          }
-          tmem_wait_st();
-          __syncwarp();
-        }
-      }
       if constexpr (PREFIX) {
         const int64_t at = (w.part + (w.split ? t : 0)) * nrows + orow;
         const bool ok = row_in && in_bounds(p.status, at, p.most_parts * nrows);

@@ -5,6 +5,7 @@ import pytest
 from tests.gpu_util import to_f64
 from tests.pages_ref import Shared, near
 from tests.test_prefix_gpu import BATCHES, FORMS, run
+from tests.test_prefix_long_gpu import MANY, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +62,75 @@ def test_an_infinite_value_of_few_rows(share, where, wide, strange, form):
     assert (o[rows][:, :, 3] == strange).all()
     o[rows, :, 3] = ref[0][rows, :, 3]
     near(o, z, ref, b.dtype, b.D)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("groups", [[(None, [(100000, 100)])], [(60000, [(40000, 100), (70, 60)])]])
+@pytest.mark.parametrize("strange", [float("nan"), float("inf")])
+@pytest.mark.parametrize("back", [99995, 101, 99, 64, 2])
+def test_one_value_that_is_no_number_in_a_long_context(back, strange, groups, dtype, D):
+    # 400 rows of 100000 keys; the value of the key `back` places from the end, which all rows see, or none but the last ones:
+    # the same time and the same status as without it
+    import torch
+    from exact_scaled_dot_flash_gb300 import attn
+    b = Shared(103, groups, dtype=dtype, D=D, P=64, H=1, Hq=4, wide=False)
+    d = b.device()
+    ref = list(reference(b, d))
+    j = int(b.lens[0]) - back
+    d[2][b.table[0, j // b.P], j % b.P, :, 3] = strange
+    out = torch.full_like(d[0], 768.0)
+    attn.device_status(0, clear=True)
+    times = []
+    for _ in range(2):
+        e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        e[0].record()
+        out, lse = attn.paged_prefix_fwd(*d, max_queries=b.max_q, max_group_queries=b.max_gq, return_lse=True, out=out)
+        e[1].record()
+        torch.cuda.synchronize()
+        times.append(e[0].elapsed_time(e[1]))
+    assert attn.device_status(0, clear=True) == 0
+    o, z = to_f64(out), to_f64(lse)
+    sees = np.zeros(len(b.q), bool)
+    seqs = [s for s in range(len(b.lens)) if b.table[s, j // b.P] == b.table[0, j // b.P]]
+    for s in seqs:  # the keys that query i sees: L - n + i + 1
+        n, L = int(b.new[s]), int(b.lens[s])
+        sees[b.offs[s]:b.offs[s + 1]] = j < L - n + np.arange(n) + 1
+    assert sees.sum() >= min(back, 100)
+    at = o[sees][:, :, 3]
+    assert (np.isnan(at) if np.isnan(strange) else at == strange).all()
+    o[sees, :, 3] = ref[0][sees, :, 3]
+    near(o, z, ref, dtype, D)
+    assert min(times) < 20  # ms; 0.4 to 0.6 without it
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_values_that_are_no_numbers_all_over(causal, dtype, D):
+    # rows that see anything from nothing to all of a long prefix, with such values spread over it and over the own keys: an
+    # element of a row is a number unless the row sees one of them there
+    b = Shared(107, MANY["unequal"][:2] + [(700, [(300, 200), (90, 80)])], dtype=dtype, D=D, P=64, H=8, Hq=32)
+    r = np.random.RandomState(5)
+    pos = r.randint(-2, 9100, len(b.q)).astype(np.int32) if causal else None
+    d = b.device()
+    ref = list(reference(b, d, pos, causal))
+    hit = np.zeros((len(b.q), b.H, D), bool)
+    for s in r.permutation(len(b.lens))[:12]:
+        n, L, at = int(b.new[s]), int(b.lens[s]), slice(b.offs[s], b.offs[s + 1])
+        for j in r.randint(0, L, 3):
+            h, e = int(r.randint(b.H)), int(r.randint(D))
+            page = b.table[s, j // b.P]
+            d[2][page, j % b.P, h, e] = [float("nan"), float("inf"), -float("inf")][int(r.randint(3))]
+            for s2 in np.flatnonzero(b.table[:, j // b.P] == page):
+                rows = slice(b.offs[s2], b.offs[s2 + 1])
+                if j < b.lens[s2]:
+                    hit[rows, h, e] |= pos[rows] >= j if causal else True
+    import torch
+    from exact_scaled_dot_flash_gb300 import attn
+    out, lse = attn.paged_prefix_fwd(*d, positions=torch.from_numpy(pos).cuda() if causal else None, causal=causal,
+                                     max_queries=b.max_q, max_group_queries=b.max_gq, return_lse=True)
+    assert attn.device_status(0, clear=True) == 0
+    o, z = to_f64(out), to_f64(lse)
+    hit = np.repeat(hit, b.Hq // b.H, 1)
+    assert hit.any() and not np.isfinite(o[hit]).any()
+    o[hit] = ref[0][hit]
+    near(o, z, ref, dtype, D)
