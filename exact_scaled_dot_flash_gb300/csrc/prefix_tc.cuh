@@ -260,7 +260,8 @@ __device__ __forceinline__ bool any_strange(const uint8_t* v, int from, int to, 
 
 // The product of a key tile whose values are not all numbers, with the weights that the tensor core would take: a
 // thread adds to its row of O what the row sees, keys [from, to) of the tile. (A weight of 0 does not remove what
-// is no number from the other rows of a tensor core's product.) 20 to 30 us, whatever the context's length.
+// is no number from the other rows of a tensor core's product.) Whatever the context's length: a call over 100000
+// keys 1281 us, 1349 with one such value (BF16, D 128, 400 rows, 64 keys of the tile seen by some).
 template <int D, bool BF16>
 __device__ __noinline__ void own_product(uint32_t tP, uint32_t tO, const uint8_t* v, int from, int to, bool fresh) {
   const int first = __reduce_min_sync(0xffffffffu, to > from ? from : BN) & ~1;

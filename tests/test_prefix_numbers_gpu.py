@@ -100,7 +100,7 @@ def test_one_value_that_is_no_number_in_a_long_context(back, strange, groups, dt
     assert (np.isnan(at) if np.isnan(strange) else at == strange).all()
     o[sees, :, 3] = ref[0][sees, :, 3]
     near(o, z, ref, dtype, D)
-    assert min(times) < 20  # ms; 0.4 to 0.6 without it
+    assert min(times) < 20  # ms; 0.5 to 1.3 without it
 
 
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64)])
