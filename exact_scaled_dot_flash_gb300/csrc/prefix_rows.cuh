@@ -639,14 +639,18 @@ __global__ void __launch_bounds__(THREADS, ctas_of_sm(D, NT))
 constexpr int JOIN_THREADS = 256;
 
 // A thread takes 4 elements of a row. What it reads of the metadata it reads before it waits for
-// the stages: its CTA may be on its SM long before they end.
+// the stages: its CTA may be on its SM long before they end. A thread without a row of a sequence waits too: the
+// next launch may own the workspace, and a call may have no such row at all.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ Params p) {
   constexpr int G = D / 4, BATCH = 8;  // parts read together: each read is a trip to L2
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (JOIN_THREADS / G) + threadIdx.x / G;
   const int d4 = threadIdx.x % G;
   const int64_t rows = static_cast<int64_t>(p.num_queries) * p.Hq;
-  if (row >= rows) return;
+  if (row >= rows) {
+    wait_before();
+    return;
+  }
   const int query = static_cast<int>(row / p.Hq), head = static_cast<int>(row - static_cast<int64_t>(query) * p.Hq);
   const int heads = p.Hq / p.Hkv, h = head / heads, hr = head - h * heads;
   // the query's sequence: in a decode step the one of its own number
@@ -654,7 +658,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
   if (query < query_at(p, s) || query >= query_at(p, s + 1)) s = last_at_most(p.q_offsets, 0, p.num_seqs, query);
   int q_lo;
   const int nq = queries_of(p, s, s + 1, p.max_queries, q_lo);
-  if (query < q_lo || query >= q_lo + nq) return;  // of no sequence
+  if (query < q_lo || query >= q_lo + nq) {  // of no sequence
+    wait_before();
+    return;
+  }
   const Own own = own_of(p, s);
   const int nb = key_blocks(own.L - own.start);
   const int64_t local = static_cast<int64_t>(query - q_lo) * heads + hr;
