@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const __grid_constant__ P
     parent = __ldg(from + blockIdx.x);
     if (parent < 0 || parent >= p.num_seqs || parent == s) return;
     tokens = tokens_of(p, parent);
-    held = (tokens + p.page_size - 1) / p.page_size;
+    held = tokens > 0 ? (tokens - 1) / p.page_size + 1 : 0;  // tokens may be 2^31 - 1
   }
   if (blockIdx.y == 0 && threadIdx.x == 0) p.lens[s] = tokens;
   const int b = blockIdx.y * THREADS + threadIdx.x;
