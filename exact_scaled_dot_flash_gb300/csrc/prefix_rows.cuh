@@ -34,7 +34,7 @@ namespace prefix {
 namespace rows {
 
 constexpr int TILE = 16;                  // keys of a warp's tile
-constexpr float UNSEEN = -3e38f;          // reference of a row without keys: its first one passes every range
+constexpr float UNSEEN = -3.40282347e38f; // reference of a row without keys, the least number: a first score above it passes every range
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");

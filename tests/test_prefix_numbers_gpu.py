@@ -1,4 +1,5 @@
-"""Infinite values in attention of sequences that share a prefix (attn_paged_prefix_fwd)."""
+"""Values that are no numbers, and scores near the end of fp32, in attention of sequences that share a prefix
+(attn_paged_prefix_fwd)."""
 import numpy as np
 import pytest
 
@@ -134,3 +135,28 @@ def test_values_that_are_no_numbers_all_over(causal, dtype, D):
     assert hit.any() and not np.isfinite(o[hit]).any()
     o[hit] = ref[0][hit]
     near(o, z, ref, dtype, D)
+
+
+@pytest.mark.parametrize("score", [-2.3e38, -2.2e38, -2.1e38, -1e38, -1e30])
+@pytest.mark.parametrize("form", FORMS, ids=ids)
+@pytest.mark.parametrize("new", [1, 2])
+@pytest.mark.parametrize("pre", [0, 40])
+def test_a_score_near_the_end_of_fp32(pre, new, form, score):
+    # few rows, whose scores are all the same, in log2 units down to -3.33e38: the output is the mean of the values, the lse
+    # the score itself (the log of the number of keys is far below its last bit)
+    b = Shared(97, [(40, [(new, new)] * 2), (None, [(new + 7, new)])], **form)
+    b.pre[:] = pre  # 0: all keys are the sequences' own
+    f16 = b.dtype == "f16"
+    q, k = (2.0 ** 15, -2.0 ** 15) if f16 else (2.0 ** 64, score / 2.0 ** 64)
+    b.q.zero_()
+    b.q[:, :, 0] = q
+    b.kc[..., 0] = k
+    scale = float(np.float32(score / (q * k))) if f16 else 1.0
+    exact = q * float(b.kc[0, 0, 0, 0].double()) * scale
+    out, lse = run(b, causal=False, scale=scale)
+    ref = list(b.ref(None, False, 0.0))  # equal scores
+    o, z = to_f64(out), to_f64(lse)
+    # of it: the scale and its product with log2 e, the score, the way back with ln 2, each rounded, and the two constants
+    assert np.abs(z / exact - 1).max() <= 6 * 2.0 ** -24
+    ref[1] = z
+    near(o, z, ref, b.dtype, b.D)
