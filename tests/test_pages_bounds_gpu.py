@@ -1,5 +1,8 @@
 """The pages of a cache on the GPU (attn_pages_*) at the ends of their ranges."""
+import numpy as np
 import pytest
+
+from tests.test_pages_gpu import Both
 
 pytestmark = pytest.mark.gpu
 
@@ -23,3 +26,17 @@ def test_fork_of_a_full_row(P, M):
         attn.pages_free(table, lens, refs, lens.new_tensor([1]))
     assert torch.equal(torch.bincount(table[0], minlength=N).int(), refs)
 
+
+@pytest.mark.parametrize("S,M,P,N", [(4097, 3, 4, 6000), (9000, 2, 8, 9100), (5000, 4, 3, 40000)])
+def test_more_sequences_than_a_block_keeps(S, M, P, N):
+    b = Both(S, M, P, N, [("i16", (P, 2))], seed=S)
+    r = np.random.RandomState(S)
+    for step in range(4):
+        b.reserve(np.where(r.rand(S) < 0.4, r.randint(0, 2 * P, S), 0))
+        kids = np.flatnonzero(b.ref.lens == 0)[:S // 8]
+        parents = np.flatnonzero(b.ref.lens > 0)
+        if len(kids) and len(parents):
+            b.fork(r.choice(parents, len(kids)).tolist(), kids.tolist())
+        b.reserve(r.randint(0, 2, S))
+        b.free(r.permutation(S)[:S // 3].tolist())
+        b.compact()

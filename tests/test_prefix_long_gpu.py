@@ -127,3 +127,53 @@ def test_page_sizes(name, P, dtype, D, checked_path):  # noqa: F811
               "prompts": [(901, [(80, 70), (300, 300)]), (500, [(10, 10)])]}[name]
     b = Shared(83, groups, dtype=dtype, D=D, P=P, H=2, Hq=8)
     check_both(b, checked_path)
+
+
+@pytest.mark.parametrize("dtype,D,new", [("bf16", 128, 20), ("f16", 64, 1), ("f32", 128, 2)])
+def test_a_cache_past_32_bits(dtype, D, new, checked_path):  # noqa: F811
+    # the batch's pages are the last of a cache of more than 2^32 elements
+    import torch
+    from exact_scaled_dot_flash_gb300 import attn
+    b = Shared(127, [(700, ones(5, new, 300, new=new))], dtype=dtype, D=D, P=64, H=8, Hq=32, hidden=0.0)
+    d = list(b.device())
+    kw = dict(max_queries=b.max_q, max_group_queries=b.max_gq, return_lse=True)
+    ref = reference(b, d)
+    n = len(b.kc)
+    pages = (1 << 32) // (b.P * b.H * D) + n
+    for i in (1, 2):
+        big = torch.zeros((pages, b.P, b.H, D), dtype=d[i].dtype, device="cuda")
+        big[pages - n:] = d[i]
+        d[i] = big
+    d[3] = torch.where(d[3] >= 0, d[3] + (pages - n), d[3])
+    for path in (None, checked_path):
+        if path is None:
+            out, lse = attn.paged_prefix_fwd(*d, **kw)
+        else:
+            with attn.use_library(path):
+                out, lse = attn.paged_prefix_fwd(*d, **kw)
+                torch.cuda.synchronize()
+                assert attn.device_status(0, clear=True) == 0
+        near(to_f64(out), to_f64(lse), ref, b.dtype, b.D)
+
+
+def test_calls_on_several_streams_at_once():
+    # calls with few and with many rows, each stream its own workspaces: the same bits as one after another
+    import torch
+    from exact_scaled_dot_flash_gb300 import attn
+    batches = [Shared(131, g, dtype="bf16", D=128, P=64, H=8, Hq=32)
+               for g in (MANY["one_group"], MANY["prompts"], [(3000, ones(60, 1, 900))], [(500, ones(3)), (None, ones(2, 9, 80))])]
+    d = [b.device() for b in batches]
+    kw = [dict(max_queries=b.max_q, max_group_queries=b.max_gq, return_lse=True) for b in batches]
+    want = [attn.paged_prefix_fwd(*x, **k) for x, k in zip(d, kw)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in batches]
+    got = []
+    for i in range(24):
+        s = streams[i % 4]
+        which = (i * 3 + i // 4) % 4
+        with torch.cuda.stream(s):
+            got.append((which, attn.paged_prefix_fwd(*d[which], **kw[which])))
+    torch.cuda.synchronize()
+    for which, x in got:
+        assert torch.equal(x[0], want[which][0]) and torch.equal(x[1], want[which][1])
+    assert attn.device_status(0, clear=True) == 0
