@@ -1131,7 +1131,9 @@ def paged_prefix_fwd(q, k_cache, v_cache, block_table, seq_lens, q_offsets, grou
     Sequences group_offsets[g] .. group_offsets[g+1]-1 (int32 [groups + 1]) share
     their first prefix_lens[g] tokens (int32 [groups]): the rows of the table name
     the same pages for them (:func:`pages_fork`), or copies. Their keys and values are
-    read once for the whole group. The other arguments and the results are those
+    read once for 256 rows (queries times heads of a kv head) of the group: float16 and
+    bfloat16, D of 64 or 128, page sizes that are multiples of 8 and divide 128, or multiples of
+    128. With other page sizes that is 32 rows, with float32 or D of 16 or 32 it is 64. The other arguments and the results are those
     of :func:`paged_fwd`; ``max_group_queries`` bounds the queries of one group
     (computed, with a host sync, when None), and ``workspace`` (a CUDA uint8 tensor of
     :func:`paged_prefix_workspace_bytes`) is allocated here when not given.

@@ -6,9 +6,9 @@
 // an atomic exchange wherever two rows of a call may name the same row of the
 // table, so that refs counts entries whatever the caller passes.
 //
-// reserve and compact plan on one cluster of CTAs (plan_kernel below), since what they
-// hand out depends on the order of all sequences and of all pages: two prefix
-// sums over the cluster, a few thousand instructions in all, bound by the trips to L2
+// reserve and compact plan on one cluster of CTAs (reserve_kernel, compact_kernel), since what they
+// hand out depends on the order of all sequences and of all pages: three prefix sums over
+// the cluster in reserve, two in compact, a few thousand instructions in all, bound by the trips to L2
 // between its barriers (reserve, 64 of 128 rows, 8700 pages: 19 us with cold caches, a
 // beam step with it 23 us as a graph; compact, 6000 pages: 9 us). The copies that follow
 // from the plan are a kernel of their own over the whole GPU, bound by the bytes of the
@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) compact_kernel(const __grid_cons
   }
 }
 
-// A cluster of one CTA up to 1024 pages and sequences, of eight from 8192 on: a thread
-// looks at one of each while that is possible.
+// A cluster of one CTA up to 1024 pages or sequences, of eight from 4097 on: a thread
+// looks at one of each up to 8192.
 inline int plan_ctas(int64_t work) {
   int c = 1;
   while (c < MAX_CLUSTER && static_cast<int64_t>(c) * PLAN_THREADS < work) c *= 2;

@@ -263,11 +263,13 @@ Plan plan_of(const attn_paged_shape_t& s, int num_groups, int max_group_queries)
             static_cast<int64_t>(s.num_seqs) * s.max_pages * s.page_size <= (8ll << 20) / (4ll * s.Hkv * s.D);
   // With many rows the prefix stage packs rows of several sequences into its row blocks and fills every SM, but
   // each row's part goes out in FP32 and comes back, and a stage more comes up: of a pass over 256 rows, 1.85 us a
-  // key tile, that is 17 us beside 40 us once. Without it a sequence's own row blocks run over all its keys, in whole
-  // rounds of the SMs (bf16, 32/8 heads, D 128, us with the stage and without: 4 sequences of 32 queries behind
-  // 8192 tokens 67 and 104, 24 of 64 207 and 233, 8 of 128 141 and 121, 24 of 512 1348 and 1278; behind 1024 tokens
-  // 46 and 23, 83 and 51, 59 and 29, 434 and 286). The table's width stands for the lengths, and groups of one
-  // size for the call's.
+  // key tile of D 128, that is 17 us beside 40 us once (the stages run one after another here, unlike those that
+  // prefix.cuh's constants are of). Without it a sequence's own row blocks run over all its keys, in whole
+  // rounds of the SMs. 32/8 heads, us with the stage and without, BF16 with D 128: 4 sequences of 32 queries behind
+  // 8192 tokens 65 and 106, 24 of 64 211 and 236, 8 of 128 145 and 121, 24 of 512 1346 and 1292; behind 1024 tokens
+  // 46 and 25, 84 and 53, 58 and 30, 438 and 298. F16 with D 64, where the constants of D 128 choose the faster way
+  // too: 46 and 92, 158 and 197, 111 and 102, 1123 and 1060; 35 and 21, 62 and 43, 45 and 25, 330 and 233. The
+  // table's width stands for the lengths, and groups of one size for the call's.
   if (d.prefix_tc && d.suffix_tc) {
     const double tiles = 1.85 * s.max_pages * s.page_size / 128;
     const int64_t own = s.num_seqs * s.Hkv * ((seq_rows + 255) / 256), rounds = (own + attn::SMS - 1) / attn::SMS;

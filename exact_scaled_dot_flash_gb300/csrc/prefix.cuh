@@ -204,8 +204,8 @@ struct Share {
   int ranges, g;
 };
 
-// Microseconds, measured: a block of 256 rows and 128 keys of 128 elements on an SM, and what a piece
-// costs besides; KB of keys and values that the few-row suffix stage streams in one of them, on one SM
+// Microseconds, measured where the two stages run side by side: a block of 256 rows and 128 keys of 128
+// elements on an SM, and what a piece costs besides; KB of keys and values that the few-row suffix stage streams in one of them, on one SM
 // and on all.
 constexpr float BLOCK_US = 2.4f, PIECE_US = 10.f, SM_KB_US = 40.f, ALL_KB_US = 5500.f;
 

@@ -20,11 +20,13 @@
 //    64 bits 2.1e-4, the output's own rounding, instead of 2.5e-4 to 2.9e-4). With 32 rows it costs 11-20%
 //    (148 us, 124 without), and the roundings of many rows average out: there it is the rounded one alone.
 //
-// Suffix stage: the keys of all sequences, in blocks of 64 (16 a warp), are cut into ranges
+// Suffix stage: the keys of all sequences, in blocks of 32 (16 a warp), are cut into ranges
 // of equal length, one for each group of Hkv CTAs (one a head, side by side). A CTA walks the
 // units (sequences) of its range and leaves a part for each row; join_kernel joins a
 // row's parts, those of its prefix first, then those of the ranges in their order.
-// Prefix stage: blocks of 64 keys for 8 NT rows and a head, shared out as prefix.cuh says.
+// Prefix stage: blocks of 32 keys for 8 NT rows and a head, shared out as prefix.cuh says. Groups of more rows
+// come here too where prefix_tc.cuh does not take the page size, and read their prefix once for every 32 of
+// them (384 rows a head behind 8192 keys: 123 us with pages of 48 or 96 tokens, 49 with 64).
 #pragma once
 
 #include "prefix.cuh"

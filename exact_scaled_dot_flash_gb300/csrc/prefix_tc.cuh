@@ -15,7 +15,7 @@
 //    probability of 0 does not remove;
 //  - key tiles that some row of a row tile does not see in full looked through for values that are no
 //    numbers (there are one or two of them in a causal sequence): where there are some, the softmax threads
-//    add the tile's product to their rows themselves, each the keys that its row sees. The look costs 1%
+//    add the tile's product to their rows themselves, each the keys that its row sees. That costs 4%
 //    (24 prompts of 16-128 tokens behind 4096: 162 us, 156 without any care for such values);
 //  - one CTA an SM that goes through several pieces of work without a break: a warp works out
 //    the next piece from the metadata while the others compute, and the copies of its
@@ -25,10 +25,10 @@
 // same rows and half of the key tiles each, and leave a part each: a block is 256 keys. (Halves, not
 // every other tile: the keys are then read at the time that the group's other rows read them.)
 // Suffix stage: a piece is all own keys of a sequence for 256 rows, joined with the prefix's parts.
-// Measured (32/8 heads, D 128, BF16): the prefix of 24 prompts of 16-128 tokens behind 4096 keys 119 us, 0.97
-// PFLOP/s, their own keys 57 us; 96 rows over 60001 keys 116 us, 0.82 PFLOP/s. Bound by the softmax's latency between
+// Measured (32/8 heads, D 128, BF16): the prefix of 24 prompts of 16-128 tokens behind 4096 keys 117 us, 0.99
+// PFLOP/s, their own keys 61 us; 96 rows over 60001 keys 117 us, 0.81 PFLOP/s. Bound by the softmax's latency between
 // the products of two row tiles (tensor pipe 49% active); the second case also by the keys of a head
-// being read for each of its two row blocks (477 MB instead of 246).
+// being read for each of its two row blocks (475 MB instead of 246).
 #pragma once
 
 #include <algorithm>
@@ -717,6 +717,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         const float neg_m = (m_run == -INFINITY) ? 0.f : -m_run;
         float2 sum_a = make_float2(0.f, 0.f), sum_b = make_float2(0.f, 0.f);
+        // The product takes the weights rounded to the input type; their sum is of the unrounded ones. Error against 64
+        // bits, relative to the output's norm, BF16: 2.2e-3 to 2.3e-3, of which 1.7e-3 are the output's own rounding (F16 2.7e-4,
+        // 2.1e-4). As two numbers each, with a second product, the error is the output's rounding alone, and the calls take 21 to 36%
+        // longer (96 rows behind 60001 keys 170 us, 140 as it is; 24 prompts behind 4096 220 and 161; 8 groups of 7 heads 76 and 60).
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           uint32_t pk[32];

@@ -640,10 +640,13 @@ ATTN_API int attn_pages_workspace_bytes(const attn_pages_t* pool, size_t* bytes)
 /* ------------------------------------------------------------ a shared prefix
  * attn_paged_prefix_fwd - attn_paged_fwd for a batch in which groups of sequences
  * begin with the same tokens (a system prompt, a document with many questions, the
- * answers to one request): the keys and values that a group shares are read once
- * for all of its queries, except in calls whose sizes (max_pages stands for the
- * lengths: a table wider than they need hides such a call) say that each sequence by
- * itself is done sooner. (The pages have no counterpart.)
+ * answers to one request): the keys and values that a group shares are read for
+ * blocks of its rows (queries times heads of a kv head) instead of for each sequence:
+ * once for 256 rows with F16/BF16, D of 64 or 128 and a page_size that is a multiple of 8
+ * and divides 128, or a multiple of 128; for 32 rows with other page sizes; for 64
+ * with F32 or D of 16 or 32. Calls whose sizes (max_pages stands for the lengths: a
+ * table wider than they need hides such a call) say that each sequence by
+ * itself is done sooner go without. (The pages have no counterpart.)
  *
  * Group g is the sequences group_offsets[g] .. group_offsets[g+1]-1 (device int32
  * [num_groups + 1], clamped to [0, num_seqs], not decreasing), and their first
